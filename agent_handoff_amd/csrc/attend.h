@@ -1,0 +1,101 @@
+// attend.h - internal launchers of the operators of kvattend.h (host side),
+// and the layout of a paged cache.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "layout.h"
+
+namespace kvc {
+
+// bf16 head vectors: element (n, h, c) at data[n * ts + h * hs + c].
+struct RowsDev {
+    uint16_t* data;
+    uint64_t ts, hs;
+};
+
+// Byte layout of one page (see kvattend.h): codes, then (8-bit formats) steps.
+struct PageLayout {
+    uint32_t num_pages, H, P, d, format;
+    uint32_t esize;        // bytes of one code
+    uint64_t steps;        // offset of the steps in a page
+    uint64_t page_bytes;
+};
+
+inline bool page_spec_ok(uint32_t num_pages, uint32_t H, uint32_t P, uint32_t d, uint32_t format) {
+    return num_pages >= 1 && num_pages <= 0x7FFFFFFFu && H >= 1 && H <= (1u << 16) &&
+           (P == 16 || P == 32 || P == 64 || P == 128 || P == 256) && (d == 64 || d == 128) && format <= 2;
+}
+
+inline PageLayout page_layout(uint32_t num_pages, uint32_t H, uint32_t P, uint32_t d, uint32_t format) {
+    PageLayout l;
+    l.num_pages = num_pages;
+    l.H = H;
+    l.P = P;
+    l.d = d;
+    l.format = format;
+    l.esize = format == 0 ? 2 : 1;
+    l.steps = 2ull * H * P * d * l.esize;
+    l.page_bytes = align_up(l.steps + (format == 0 ? 0 : 2ull * H * P * 4), 256);
+    return l;
+}
+
+constexpr int kMaxPairs = 64;
+struct RotateArgs {
+    uint32_t n, Hq, Hk, d;
+    RowsDev q_in, k_in, q_out, k_out;
+    const void *q_weight, *k_weight;
+    float eps;
+    const int64_t* positions;
+    const float* inv_freq;  // host
+    uint32_t n_pairs, pairing;
+};
+hipError_t launch_norm_rotate(const RotateArgs& a, hipStream_t stream);
+
+hipError_t launch_page_write(const PageLayout& l, void* pages, uint32_t n, const RowsDev& k, const RowsDev& v,
+                             const int64_t* slots, int32_t* dev_status, hipStream_t stream);
+hipError_t launch_page_read(const PageLayout& l, const void* pages, uint32_t n, const int64_t* slots,
+                            const RowsDev& k_out, const RowsDev& v_out, int32_t* dev_status, hipStream_t stream);
+
+// How an attention call is cut up: workgroups of kAttendWaves waves take
+// `chunk` tokens of one source for rt * 16 query rows of one kv head;
+// `chunks` of them cover the longest sequence.
+struct AttendPlan {
+    uint32_t rows;        // query rows that share a kv head's tokens
+    uint32_t rt;          // row tiles of 16 of one workgroup: 1, 2 or 4
+    uint32_t row_blocks;  // workgroups that share tokens, ceil(rows / (16 rt))
+    uint32_t chunk, chunks;
+};
+AttendPlan page_attend_plan(uint32_t n_seqs, uint32_t H, uint32_t Hq, uint64_t max_tokens);
+AttendPlan pool_attend_plan(uint32_t H, uint32_t n_agents, uint32_t Hq, uint32_t T);
+// Partial results of `splits` parts of rows x d outputs: f32 sums [rows][splits][d],
+// then f32 {maximum, sum} [rows][splits].
+inline uint64_t attend_ws_bytes(uint64_t rows, uint64_t splits, uint32_t d) {
+    return align_up(rows * splits * (d + 2) * 4, 256);
+}
+
+struct TailArgs {
+    PageLayout lay;
+    const uint8_t* pages;
+    const int32_t* table;
+    uint32_t table_cols;
+    uint64_t table_stride;
+    const int32_t* lens;
+};
+struct AttendArgs {
+    uint32_t n, H, Hq, d;  // sequences (agents), kv heads, query heads, channels
+    RowsDev q, out;
+    float scale;
+    float* lse;
+    float* ws;
+    int32_t* status;
+    // pool (pool != nullptr)
+    const uint8_t* pool;
+    uint32_t L, T, layer;
+    // pages (table != nullptr)
+    TailArgs tail;
+};
+hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
+
+}  // namespace kvc

@@ -408,6 +408,24 @@ class SharedKVPool:
         kvpool_decode(self.shape, self.pool, layer_begin, layer_end, k_outs, v_outs, dev_status)
         return k_outs, v_outs
 
+    def attend(self, layer, q, tail=None, out=None, lse=None, scale=None, dev_status=None):
+        """Attention of one new token of each agent over one layer of the pool,
+        without decoding it, and over the agents' own pages (PooledAgent): q:
+        bf16 [n_agents, q_heads, d]; tail: None or (PagedKV, table, lens).
+        Returns out (a new tensor when None). See kvattend.kvpool_attend."""
+        from . import kvattend
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        spec, most, t = None, 0, None
+        if tail is not None:
+            cache, table, lens = tail
+            spec, most = cache.spec, table.shape[1] * cache.spec.page_tokens
+            t = (spec, cache.pages, table, lens)
+        need = kvattend.kvpool_attend_workspace_bytes(self.shape, q.shape[0], q.shape[1], spec, most)
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        kvattend.kvpool_attend(self.shape, self.pool, layer, q, out, ws, t, lse, scale, dev_status)
+        return out
+
 
 class CacheCard:
     """A CacheCard (QKVShare: quantised groups, per-token widths and

@@ -1,0 +1,262 @@
+"""Host-side checks of the operators of include/kvattend.h: exported symbols,
+sizes and layout against the oracle, and every refusal, all before any device
+work (no GPU calls are made)."""
+
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+from agent_handoff_amd import kvattend as ka
+from agent_handoff_amd import kvcodec as kv
+from oracle import attend as oa
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_every_declared_symbol_is_exported():
+    text = open(os.path.join(ROOT, "include", "kvattend.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = sorted(set(re.findall(r"^(?:int|size_t)\s+([a-z_0-9]+)\s*\(", text, flags=re.M)))
+    assert names == sorted(ka.EXPORTED)
+    lib = ctypes.CDLL(kv.LIB_PATH)
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+@pytest.mark.parametrize("spec", [(1, 1, 16, 64, 0), (7, 3, 16, 64, 1), (960, 8, 16, 128, 1), (5, 8, 256, 128, 2),
+                                  (3, 5, 32, 128, 0)])
+def test_page_bytes_agree_with_oracle(spec):
+    assert ka.kvpage_bytes(spec) == oa.page_bytes(spec)
+
+
+def test_invalid_page_descriptions_give_zero():
+    good = (4, 2, 16, 64, 1)
+    for i, bad in [(0, 0), (0, 1 << 31), (1, 0), (1, (1 << 16) + 1), (2, 0), (2, 8), (2, 24), (2, 512), (3, 96), (3, 256),
+                   (4, 3)]:
+        spec = list(good)
+        spec[i] = bad
+        assert ka.kvpage_bytes(spec) == 0, spec
+        assert ka.kvpage_attend_workspace_bytes(spec, 1, 4, 64) == 0, spec
+
+
+def test_workspace_sizes():
+    spec = (4, 2, 16, 64, 1)
+    assert ka.kvpage_attend_workspace_bytes(spec, 3, 4, 64) > 0
+    assert ka.kvpage_attend_workspace_bytes(spec, 3, 5, 64) == 0          # 5 heads over 2
+    assert ka.kvpage_attend_workspace_bytes(spec, 0, 4, 64) > 0
+    assert ka.kvpage_attend_workspace_bytes(spec, 1, 4, 1 << 31) == 0
+    assert ka.kvpage_attend_workspace_bytes(spec, 1 << 28, 4, 64) == 0
+    # long contexts: parts of several sequences, growing with the length
+    small, large = (ka.kvpage_attend_workspace_bytes(spec, 2, 4, n) for n in (100, 1 << 20))
+    assert large > small
+    shape = (2, 2, 1000, 64)
+    assert ka.kvpool_attend_workspace_bytes(shape, 3, 4) > 0
+    assert ka.kvpool_attend_workspace_bytes(shape, 3, 4, spec, 64) > ka.kvpool_attend_workspace_bytes(shape, 3, 4)
+    assert ka.kvpool_attend_workspace_bytes(shape, 3, 5) == 0
+    assert ka.kvpool_attend_workspace_bytes(shape, 3, 4, (4, 1, 16, 64, 1), 64) == 0     # other heads
+    assert ka.kvpool_attend_workspace_bytes(shape, 3, 4, (4, 2, 16, 128, 1), 64) == 0    # other head_dim
+    assert ka.kvpool_attend_workspace_bytes((2, 2, 0, 64), 3, 4) == 0
+
+
+# ---------------------------------------------------------------- refusals
+# Raw C calls with fake (never dereferenced) device addresses, on hosts
+# without a GPU only, so that a missing check can never launch a kernel on
+# fake memory.
+
+fake_addresses = pytest.mark.skipif(torch.cuda.device_count() != 0, reason="fake device addresses: CPU-only host")
+
+L = kv.library()
+A = 1 << 40  # addresses 1 TiB apart, 256-aligned
+N, HQ, HK, D = 5, 8, 2, 64
+
+
+def rows(base, ts=None, hs=D, heads=HK):
+    return ka.kvc_rows(base, heads * D if ts is None else ts, hs)
+
+
+def _rotate(n=N, hq=HQ, hk=HK, d=D, q=None, k=None, qw=5 * A, kw=6 * A, eps=1e-6, pos=7 * A, pairs=32, pairing=0,
+            qo=None, ko=None, f=True):
+    q = rows(A, heads=HQ) if q is None else q
+    k = rows(2 * A) if k is None else k
+    qo = rows(3 * A, heads=HQ) if qo is None else qo
+    ko = rows(4 * A) if ko is None else ko
+    fr = np.ones(64, np.float32)
+    return L.kvc_norm_rotate(n, hq, hk, d, q or None, k or None, qw, kw, eps, pos, fr.ctypes.data if f else None, pairs,
+                             pairing, qo or None, ko or None, None)
+
+
+@fake_addresses
+def test_rotate_refusals():
+    assert _rotate(n=0) == kv.KVC_OK and _rotate(hq=0, hk=0) == kv.KVC_OK
+    assert _rotate(d=96) == kv.KVC_E_SHAPE and _rotate(hq=(1 << 16) + 1) == kv.KVC_E_SHAPE
+    assert _rotate(n=(1 << 26) + 1) == kv.KVC_E_SHAPE
+    assert _rotate(q=rows(A, ts=1 << 62)) == kv.KVC_E_SHAPE
+    for bad in ({"pairs": 4}, {"pairs": 40}, {"pairing": 2}, {"eps": -1e-6}, {"eps": float("nan")}, {"eps": float("inf")}):
+        assert _rotate(**bad) == kv.KVC_E_RANGE, bad
+    assert _rotate(q=False) == kv.KVC_E_NULL and _rotate(ko=False) == kv.KVC_E_NULL
+    assert _rotate(pos=None) == kv.KVC_E_NULL and _rotate(f=False) == kv.KVC_E_NULL
+    assert _rotate(qo=rows(0)) == kv.KVC_E_NULL
+    for bad in ({"q": rows(A + 2)}, {"ko": rows(4 * A, ts=HK * D + 4)}, {"k": rows(2 * A, hs=D + 1)}, {"qw": 5 * A + 8},
+                {"pos": 7 * A + 4}):
+        assert _rotate(**bad) == kv.KVC_E_ALIGN, bad
+    for bad in ({"qo": rows(A + 2 * D, heads=HQ)},             # shifted over its own input
+                {"ko": rows(3 * A)},                           # both outputs at one place
+                {"qo": rows(3 * A, ts=HQ * D - 8, heads=HQ)},  # tokens run into one another
+                {"qo": rows(3 * A, ts=0)},                     # one row for all tokens
+                {"qo": rows(3 * A, hs=D // 2)},                # heads run into one another
+                {"ko": rows(A)},                               # an output over the other's input
+                {"qo": rows(5 * A)}, {"qo": rows(7 * A)}):     # over a weight, over the positions
+        assert _rotate(**bad) == kv.KVC_E_ALIAS, bad
+    # query and key rows of one projection buffer, whose key rows start inside the queries
+    assert _rotate(q=rows(A, ts=1024), qo=rows(A, ts=1024), k=rows(A + 2 * (HQ * D - 8), ts=1024),
+                   ko=rows(A + 2 * (HQ * D - 8), ts=1024)) == kv.KVC_E_ALIAS
+
+
+SPEC = ka.kvc_pages(6, HK, 16, D, ka.KVC_PAGE_INT8)
+PB = ka.kvpage_bytes(SPEC)
+
+
+def _copy(f, spec=SPEC, pages=A, size=PB, n=N, k=None, v=None, slots=4 * A, status=5 * A):
+    k = rows(2 * A) if k is None else k
+    v = rows(3 * A) if v is None else v
+    head = (spec, pages, size, n)
+    args = (k or None, v or None, slots) if f is L.kvpage_write else (slots, k or None, v or None)
+    return f(*head, *args, status, None)
+
+
+@fake_addresses
+@pytest.mark.parametrize("f", [L.kvpage_write, L.kvpage_read])
+def test_page_copy_refusals(f):
+    assert _copy(f, n=0) == kv.KVC_OK
+    assert _copy(f, spec=None) == kv.KVC_E_NULL
+    assert _copy(f, spec=ka.kvc_pages(6, HK, 24, D, 1)) == kv.KVC_E_SHAPE
+    assert _copy(f, n=(1 << 26) + 1) == kv.KVC_E_SHAPE
+    for bad in ({"pages": None}, {"k": False}, {"v": rows(0)}, {"slots": None}):
+        assert _copy(f, **bad) == kv.KVC_E_NULL, bad
+    assert _copy(f, size=PB - 1) == kv.KVC_E_SIZE
+    for bad in ({"pages": A + 128}, {"k": rows(2 * A + 8)}, {"v": rows(3 * A, ts=HK * D + 1)}, {"slots": 4 * A + 4},
+                {"status": 5 * A + 2}):
+        assert _copy(f, **bad) == kv.KVC_E_ALIGN, bad
+    for bad in ({"k": rows(A + 256)}, {"v": rows(A + PB - 256)}, {"status": A + 64}, {"status": 4 * A + 8},
+                {"status": 2 * A}):
+        assert _copy(f, **bad) == kv.KVC_E_ALIAS, bad
+    if f is L.kvpage_write:
+        assert _copy(f, slots=A + 64) == kv.KVC_E_ALIAS
+    else:
+        for bad in ({"k": rows(2 * A, ts=0)}, {"v": rows(2 * A)}, {"v": rows(4 * A)}, {"k": rows(2 * A, hs=0)}):
+            assert _copy(f, **bad) == kv.KVC_E_ALIAS, bad
+
+
+WS = ka.kvpage_attend_workspace_bytes(SPEC, N, HQ, 4 * 16)
+
+
+def _attend(spec=SPEC, pages=A, size=PB, n=N, hq=HQ, q=None, table=3 * A, cols=4, stride=4, lens=4 * A, scale=0.125,
+            out=None, lse=6 * A, ws=7 * A, ws_bytes=WS, status=8 * A):
+    q = rows(2 * A, heads=HQ) if q is None else q
+    out = rows(5 * A, heads=HQ) if out is None else out
+    return L.kvpage_attend(spec, pages, size, n, hq, q or None, table, cols, stride, lens, scale, out or None, lse, ws,
+                           ws_bytes, status, None)
+
+
+@fake_addresses
+def test_page_attend_refusals():
+    assert _attend(n=0) == kv.KVC_OK
+    for bad in ({"spec": None}, {"pages": None}, {"q": False}, {"table": None}, {"lens": None}, {"out": rows(0)},
+                {"ws": None}):
+        assert _attend(**bad) == kv.KVC_E_NULL, bad
+    for bad in ({"spec": ka.kvc_pages(6, HK, 16, 96, 1)}, {"hq": 7}, {"hq": 0}, {"cols": 0}, {"cols": 1 << 27},
+                {"n": 1 << 27}, {"q": rows(2 * A, ts=1 << 62)}):
+        assert _attend(**bad) == kv.KVC_E_SHAPE, bad
+    for bad in ({"scale": float("inf")}, {"scale": float("nan")}, {"stride": 3}, {"stride": 1 << 31}):
+        assert _attend(**bad) == kv.KVC_E_RANGE, bad
+    assert _attend(size=PB - 1) == kv.KVC_E_SIZE and _attend(ws_bytes=WS - 1) == kv.KVC_E_SIZE
+    for bad in ({"pages": A + 16}, {"q": rows(2 * A + 8)}, {"out": rows(5 * A, hs=D + 4)}, {"table": 3 * A + 2},
+                {"lens": 4 * A + 1}, {"lse": 6 * A + 2}, {"ws": 7 * A + 64}, {"status": 8 * A + 1}):
+        assert _attend(**bad) == kv.KVC_E_ALIGN, bad
+    for bad in ({"out": rows(2 * A, heads=HQ)}, {"out": rows(A, heads=HQ)}, {"out": rows(3 * A, heads=HQ)},
+                {"out": rows(5 * A, ts=0)}, {"lse": 5 * A}, {"ws": A}, {"ws": 2 * A}, {"status": 7 * A + 16},
+                {"lse": 4 * A}, {"status": 3 * A}):
+        assert _attend(**bad) == kv.KVC_E_ALIAS, bad
+
+
+SHAPE = kv.kvc_shape(2, HK, 100, D)
+POOL = kv.kvpool_bytes(SHAPE)
+PWS = ka.kvpool_attend_workspace_bytes(SHAPE, N, HQ, SPEC, 64)
+
+
+def _tail(**change):
+    t = dict(spec=ctypes.pointer(SPEC), pages=A, pages_bytes=PB, table=3 * A, table_cols=4, table_stride=4, lens=4 * A)
+    t.update(change)
+    return ka.kvc_tail(**t)
+
+
+def _pool(shape=SHAPE, pool=9 * A, size=POOL, layer=1, n=N, hq=HQ, q=None, scale=0.125, tail=None, out=None, lse=6 * A,
+          ws=7 * A, ws_bytes=PWS, status=8 * A):
+    q = rows(2 * A, heads=HQ) if q is None else q
+    out = rows(5 * A, heads=HQ) if out is None else out
+    tail = _tail() if tail is None else tail
+    return L.kvpool_attend(shape, pool, size, layer, n, hq, q or None, scale, tail or None, out or None, lse, ws, ws_bytes,
+                           status, None)
+
+
+@fake_addresses
+def test_pool_attend_refusals():
+    assert _pool(n=0) == kv.KVC_OK
+    for bad in ({"shape": None}, {"pool": None}, {"q": False}, {"out": rows(0)}, {"ws": None}, {"tail": _tail(pages=None)},
+                {"tail": _tail(lens=None)}, {"tail": _tail(spec=None)}):
+        assert _pool(**bad) == kv.KVC_E_NULL, bad
+    for bad in ({"shape": kv.kvc_shape(2, HK, 0, D)}, {"hq": 9}, {"tail": _tail(table_cols=0)},
+                {"tail": _tail(spec=ctypes.pointer(ka.kvc_pages(6, HK, 16, 128, 1)), pages_bytes=1 << 30)},
+                {"tail": _tail(spec=ctypes.pointer(ka.kvc_pages(6, 1, 16, D, 1)), pages_bytes=1 << 30)}):
+        assert _pool(**bad) == kv.KVC_E_SHAPE, bad
+    for bad in ({"layer": 2}, {"scale": float("nan")}, {"tail": _tail(table_stride=2)}):
+        assert _pool(**bad) == kv.KVC_E_RANGE, bad
+    for bad in ({"size": POOL - 1}, {"ws_bytes": PWS - 1}, {"tail": _tail(pages_bytes=PB - 1)}):
+        assert _pool(**bad) == kv.KVC_E_SIZE, bad
+    for bad in ({"pool": 9 * A + 16}, {"tail": _tail(pages=A + 16)}, {"q": rows(2 * A + 2)}, {"ws": 7 * A + 16}):
+        assert _pool(**bad) == kv.KVC_E_ALIGN, bad
+    for bad in ({"out": rows(9 * A, heads=HQ)}, {"out": rows(A, heads=HQ)}, {"ws": 9 * A}, {"lse": 3 * A},
+                {"status": 9 * A}, {"out": rows(2 * A, heads=HQ)}, {"lse": 2 * A}):
+        assert _pool(**bad) == kv.KVC_E_ALIAS, bad
+
+
+# ---------------------------------------------------------------- the binding's own checks
+
+def test_binding_refuses_wrong_tensors():
+    b = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    i64 = torch.zeros(3, dtype=torch.int64)
+    f = np.ones(32, np.float32)
+    for bad in (dict(q=b.float()), dict(q_out=b[:2]), dict(positions=i64.int()), dict(positions=None),
+                dict(q=b.transpose(1, 2).contiguous().transpose(1, 2)), dict(k_out=None), dict(q_weight=b[0, 0, :32])):
+        args = dict(q=b, k=b, positions=i64, inv_freq=f, q_out=b, k_out=b)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            ka.kvc_norm_rotate(**args)
+    with pytest.raises(ValueError, match="GPU"):
+        ka.kvc_norm_rotate(b, b.clone(), i64, f, b, b)
+    spec = (4, 2, 16, 64, 1)
+    pages = torch.zeros(ka.kvpage_bytes(spec), dtype=torch.uint8)
+    for bad in (dict(k=b[:2]), dict(slots=i64.int()), dict(pages=pages.view(torch.int32)), dict(v=b.half())):
+        args = dict(spec=spec, pages=pages, k=b, v=b, slots=i64)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            ka.kvpage_write(**args)
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    table, lens = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    for bad in (dict(table=table[:2]), dict(table=table.long()), dict(table=table.t().contiguous().t()), dict(lens=lens[:2]),
+                dict(out=q[:, :2]), dict(lse=torch.zeros(3, 2)), dict(q=q[0]), dict(q=q[..., :32]), dict(ws=ws.float())):
+        args = dict(spec=spec, pages=pages, q=q, table=table, lens=lens, out=q.clone(), ws=ws)
+        args.update(bad)
+        with pytest.raises(ValueError):
+            ka.kvpage_attend(**args)
+    with pytest.raises(ValueError, match="GPU"):
+        ka.kvpage_attend(spec, pages, q, table, lens, q.clone(), ws)
+    with pytest.raises(ValueError, match="head_dim"):
+        ka.kvpool_attend((1, 2, 8, 128), pages, 0, q, q.clone(), ws)
+    with pytest.raises(ValueError):
+        ka.PagedKV(4, 2, 24, 64, device="cpu")
