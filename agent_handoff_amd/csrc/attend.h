@@ -58,22 +58,22 @@ hipError_t launch_page_write(const PageLayout& l, void* pages, uint32_t n, const
 hipError_t launch_page_read(const PageLayout& l, const void* pages, uint32_t n, const int64_t* slots,
                             const RowsDev& k_out, const RowsDev& v_out, int32_t* dev_status, hipStream_t stream);
 
-// How an attention call is cut up: workgroups of kAttendWaves waves take
-// `chunk` tokens of one source for rt * 16 query rows of one kv head;
-// `chunks` of them cover the longest sequence.
+// How the tokens of one source (a pool's layer, or pages) are shared out among
+// workgroups. A unit is the work of one kv head of one sequence (of all
+// agents for a pool) for 16 rt query rows.
 struct AttendPlan {
     uint32_t rows;        // query rows that share a kv head's tokens
-    uint32_t rt;          // row tiles of 16 of one workgroup: 1, 2 or 4
-    uint32_t row_blocks;  // workgroups that share tokens, ceil(rows / (16 rt))
-    uint32_t chunk, chunks;
+    uint32_t rt;          // row tiles of 16 of one workgroup: 1 or 2
+    uint32_t row_blocks;  // units that share tokens, ceil(rows / (16 rt))
+    bool whole;           // each workgroup takes one unit
+    uint64_t units, W;    // W: workgroups
+    uint64_t slots;       // places for partial results: 16 rt rows of d sums, a maximum and a sum
+    uint64_t part_bytes(uint32_t d) const { return slots * 16 * rt * (d + 2) * 4; }
+    uint64_t bytes(uint32_t d) const { return align_up(part_bytes(d) + units * 8, 256); }
 };
-AttendPlan page_attend_plan(uint32_t n_seqs, uint32_t H, uint32_t Hq, uint64_t max_tokens);
-AttendPlan pool_attend_plan(uint32_t H, uint32_t n_agents, uint32_t Hq, uint32_t T);
-// Partial results of `splits` parts of rows x d outputs: f32 sums [rows][splits][d],
-// then f32 {maximum, sum} [rows][splits].
-inline uint64_t attend_ws_bytes(uint64_t rows, uint64_t splits, uint32_t d) {
-    return align_up(rows * splits * (d + 2) * 4, 256);
-}
+// tail: pages behind a pool (all parts are joined, none is written as output).
+AttendPlan page_attend_plan(uint32_t n_seqs, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens, bool tail);
+AttendPlan pool_attend_plan(uint32_t H, uint32_t n_agents, uint32_t Hq, uint32_t d, uint32_t T, bool tail);
 
 struct TailArgs {
     PageLayout lay;
@@ -88,7 +88,7 @@ struct AttendArgs {
     RowsDev q, out;
     float scale;
     float* lse;
-    float* ws;
+    void* ws;
     int32_t* status;
     // pool (pool != nullptr)
     const uint8_t* pool;

@@ -36,6 +36,8 @@
 #include "codebook.h"
 #include "kernels_common.h"
 
+#include <type_traits>
+
 namespace kvc {
 namespace {
 
@@ -43,9 +45,11 @@ constexpr int kDevBadHeader = 1, kDevBadPage = 32, kDevBadLength = 64;  // KVC_D
 constexpr int kFmtBf16 = 0, kFmtInt8 = 1, kFmtFp8 = 2, kFmtPool = 3;
 constexpr int kWaves = 4;
 constexpr uint32_t kTile = 32;
-constexpr uint32_t kMaxChunk = 4096;  // 32 tiles a wave: one page number of 16 tokens in each of 64 lanes
+constexpr uint32_t kBlock = kWaves * kTile;  // tokens of one step of a workgroup
+constexpr uint32_t kPageRun = 32 * kBlock;   // 32 tiles a wave: a page number for 16 tokens in each of 64 lanes
 constexpr float kSlack = 3.0f;
 constexpr int kWeightExp = 12;
+constexpr int kMinExp = -100;  // steps below 2^-100 are taken with this exponent
 constexpr float kNegInf = -__builtin_inff();
 
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
@@ -54,17 +58,26 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-struct AttendParams {
+struct Common {
     RowsDev q, out;
     float* lse;
-    float* part;    // f32 sums [Hq * n][splits][d], then {m, l} [Hq * n][splits]
     int32_t* status;
-    uint32_t n, H, Hq, group;   // sequences (or agents), kv heads, query heads, Hq / H
-    uint32_t rows, row_blocks;  // query rows of one unit, workgroups of it
-    uint32_t chunk, chunks;
-    uint32_t splits, split0;    // parts of a row in all, and this launch's first
-    uint32_t direct;            // one part: outputs are final
+    uint32_t n, H, Hq, group;  // sequences (or agents), kv heads, query heads, Hq / H
+    uint32_t direct;           // one source: what needs no joining is written as output
     float scale_log2;
+};
+
+// One source of tokens: a pool's layer, or pages. Its units are (sequence, kv
+// head, row block), the pool's (kv head, row block); a unit's tokens come
+// in blocks of kBlock. Workgroup w of W takes an equal share of all blocks in
+// unit order; with `whole`, workgroup w is unit w.
+struct Source {
+    uint32_t rows, row_blocks, W, whole;
+    // partial results: slots of 16 RT rows x (d sums, then {m, l}). The part of a unit that workgroup w starts is
+    // slot 2w + 1, one that it continues slot 2w; whole units (where they are joined at all) come behind, at 2W
+    // (at 0 with `whole`).
+    float* part;
+    uint2* info;  // of each unit: first slot, number of parts (0: written as output)
     // pool
     const uint8_t* pool;
     PoolLayout lay;
@@ -142,9 +155,34 @@ struct Raw {
 template <int D>
 struct Raw<kFmtPool, D> {
     uint4 k[2][D / 64];
-    uint32_t v[8];   // three plane bytes (d = 128) or nibbles' bytes (d = 64)
-    uint32_t vs[4];  // eight binary16 sizes
+    uint32_t v[2][3];  // one word of each plane of one token per run of 16 (see gather_bytes)
+    uint2 vs[2];       // four binary16 sizes per run
 };
+
+// Bytes of four tokens, from four lanes that each hold a word of one: lane
+// 4 b + w of 16 gets byte b of word w of tokens 0..3, whose words are in
+// lanes w, 4 + w, 8 + w, 12 + w. Rotations by 4, 8 and 12 lanes bring the words
+// of tokens b - 1, b - 2 and b - 3 (mod 4); the selectors, which depend on b,
+// place one byte of each.
+__device__ __forceinline__ void gather_selectors(uint32_t b, uint32_t& sel_a, uint32_t& sel_b) {
+    const auto at = [](uint32_t token, uint32_t byte) { return (byte ^ 0x0Cu) << (8 * (token & 3)); };
+    sel_a = 0x0C0C0C0Cu ^ at(b, b) ^ at(b - 1, 4 + b);
+    sel_b = 0x0C0C0C0Cu ^ at(b - 2, b) ^ at(b - 3, 4 + b);
+}
+__device__ __forceinline__ uint32_t gather_bytes(uint32_t own, uint32_t sel_a, uint32_t sel_b) {
+    const uint32_t r4 = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0x124, 0xF, 0xF, true);
+    const uint32_t r8 = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0x128, 0xF, 0xF, true);
+    const uint32_t r12 = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0x12C, 0xF, 0xF, true);
+    return __builtin_amdgcn_perm(r4, own, sel_a) | __builtin_amdgcn_perm(r12, r8, sel_b);
+}
+
+// First channel of matrix row 4 g + r of the value products.
+template <int FMT, int D>
+__device__ __forceinline__ uint32_t channel_of(uint32_t g, uint32_t r) {
+    if (FMT != kFmtPool) return (4 * g + r) * (D / 16);
+    // lane 4 g + r holds byte g of word r (d = 128), or a nibble of it
+    return D == 128 ? 32 * r + 8 * g : 32 * (r & 1) + 8 * g + 4 * (r >> 1);
+}
 
 template <int W>
 __device__ __forceinline__ void load_words(const uint8_t* a, uint32_t (&w)[W]) {
@@ -163,27 +201,27 @@ __device__ __forceinline__ void load_words(const uint8_t* a, uint32_t (&w)[W]) {
     }
 }
 
-__device__ __forceinline__ bool pool_header_ok(const AttendParams& p, uint32_t D) {
+__device__ __forceinline__ bool pool_header_ok(const Source& p, uint32_t H, uint32_t D) {
     const uint32_t* hd = reinterpret_cast<const uint32_t*>(p.pool);
     const uint64_t t = (uint64_t)hd[14] | ((uint64_t)hd[15] << 32);
-    return hd[0] == kPoolMagic && hd[1] == (1u | (1u << 16)) && hd[2] == p.L && hd[3] == p.H && hd[4] == p.T &&
+    return hd[0] == kPoolMagic && hd[1] == (1u | (1u << 16)) && hd[2] == p.L && hd[3] == H && hd[4] == p.T &&
            hd[5] == D && t == p.lay.total;
 }
 
-// The sequence's length, within what its table's row holds.
-__device__ __forceinline__ uint32_t length_of(const AttendParams& p, uint32_t b, bool tell) {
-    const int32_t len = p.lens[b];
+// A sequence's length, within what its table's row holds.
+__device__ __forceinline__ uint32_t clamp_length(const Source& p, int32_t len) {
     const uint32_t most = p.table_cols << p.page_shift;
-    if (len < 0 || (uint32_t)len > most) {
-        if (tell && p.status) atomicOr(p.status, kDevBadLength);
-        return len < 0 ? 0 : most;
-    }
-    return (uint32_t)len;
+    return len < 0 ? 0 : (uint32_t)len > most ? most : (uint32_t)len;
 }
+__device__ __forceinline__ bool bad_length(const Source& p, int32_t len) {
+    return len < 0 || (uint32_t)len > p.table_cols << p.page_shift;
+}
+// Blocks of a length; an empty sequence has one, without tokens.
+__device__ __forceinline__ uint32_t blocks_of(uint32_t len) { return len <= kBlock ? 1 : (len + kBlock - 1) / kBlock; }
 
 // Query row r (of the unit's rows) -> sequence and query head.
 template <int FMT>
-__device__ __forceinline__ void row_of(const AttendParams& p, uint32_t b, uint32_t h, uint32_t r, uint32_t& seq,
+__device__ __forceinline__ void row_of(const Common& p, uint32_t b, uint32_t h, uint32_t r, uint32_t& seq,
                                        uint32_t& qh) {
     if (FMT == kFmtPool) {
         seq = r / p.group;
@@ -192,6 +230,11 @@ __device__ __forceinline__ void row_of(const AttendParams& p, uint32_t b, uint32
         seq = b;
         qh = h * p.group + r;
     }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
 
 // In-place Walsh-Hadamard transform of the C channels of a thread and of the
@@ -209,136 +252,187 @@ __device__ __forceinline__ void fwht_row(float (&y)[C], uint32_t lane) {
             }
         }
     }
-#pragma unroll
-    for (int h = 1; h < 16; h *= 2) {
+    // partners lane ^ 1, 2, 4, 8 by DPP: quad permutes, a mirror of 8 and then of
+    // 4, a rotation by 8 of 16
+    const auto step = [&](int h, auto partner) {
         const float s = (lane & h) ? -1.0f : 1.0f;
 #pragma unroll
-        for (int i = 0; i < C; ++i) y[i] = fmaf(s, y[i], __shfl_xor(y[i], h));
-    }
+        for (int i = 0; i < C; ++i) y[i] = fmaf(s, y[i], partner(y[i]));
+    };
+    step(1, [](float v) { return dpp_xor1(v); });
+    step(2, [](float v) { return dpp_xor2(v); });
+    step(4, [](float v) { return dpp_move<0x1B>(dpp_move<0x141>(v)); });
+    step(8, [](float v) { return dpp_move<0x128>(v); });
 }
 
+// Waves of a SIMD, which sets the register budget (512 / waves) and how many
+// workgroups a CU holds.
+constexpr int waves_per_simd(int d, int rt) { return d == 64 ? (rt == 1 ? 3 : 2) : 2; }
+
+// LDS of a workgroup.
+template <int D, int RT>
+struct Shared {
+    float ml[kWaves][RT * 16][2];
+    float os[kWaves][16][D + 4];
+    uint32_t sums[kWaves];
+    uint32_t found[3];  // sequence, blocks before it, its blocks
+};
+
+// Sum over the workgroup's threads before this one, and the sum of all.
+__device__ __forceinline__ uint32_t scan_threads(uint32_t v, uint32_t* sums, uint32_t& all) {
+    const uint32_t lane = lane_id(), wave = threadIdx.x / kWave;
+    uint32_t s = v;
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) {
+        const uint32_t o = __shfl_up(s, i);
+        if (lane >= (uint32_t)i) s += o;
+    }
+    if (lane == 63) sums[wave] = s;
+    __syncthreads();
+    uint32_t before = 0;
+    all = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        if ((uint32_t)i < wave) before += sums[i];
+        all += sums[i];
+    }
+    return before + s - v;
+}
+
+// The share of workgroup w.
 template <int FMT, int D, int RT>
-__global__ __launch_bounds__(kWaves* kWave) void attend_kernel(AttendParams p) {
+__device__ __forceinline__ void attend_share(const Common& p, const Source& src, uint32_t w, Shared<D, RT>& sh) {
     constexpr int KS = D / 32;   // key product steps
     constexpr int NC = D / 16;   // channels of a lane, value products
     constexpr bool HALF = FMT != kFmtBf16;
     using R = Raw<FMT, D>;
     const uint32_t lane = lane_id(), c = lane & 15, g = lane >> 4;
     const uint32_t wave = wave_uniform(threadIdx.x / kWave);
+    const uint32_t per_seq = p.H * src.row_blocks;  // units of a sequence
 
-    // workgroup -> (row block, chunk, kv head, sequence); the row blocks of a
-    // chunk, which read the same tokens, sit 8 workgroups apart: on one XCD
-    uint32_t rb = 0, u = blockIdx.x;
-    if (p.row_blocks > 1) {
-        const uint32_t span = 8 * p.row_blocks;
-        rb = (blockIdx.x % span) / 8;
-        u = blockIdx.x / span * 8 + blockIdx.x % 8;
-    }
-    const uint32_t ck = u % p.chunks;
-    const uint32_t h = u / p.chunks % p.H;
-    const uint32_t b = u / p.chunks / p.H;
-    if (b >= (FMT == kFmtPool ? 1u : p.n)) return;  // the padding of the last 8
-
-    uint32_t len;
+    // ---- this workgroup's blocks: `left` of them, from block `off` of unit (b, hr)
+    uint32_t b = 0, hr = 0, off = 0;
+    // shares of `each` blocks, the first `more` of them one larger; this one begins at x0
+    uint64_t each = 0, x0 = 0, left;
+    uint32_t more = 0;
+    const auto share = [&](uint64_t total) {
+        // no empty shares
+        if (w >= total) return false;
+        const uint32_t W = total < src.W ? (uint32_t)total : src.W;
+        if (w >= W) return false;
+        divmod_u64(total, W, each, more);
+        x0 = each * w + (w < more ? w : more);
+        left = each + (w < more);
+        return true;
+    };
+    bool header = true;
     if (FMT == kFmtPool) {
-        if (!pool_header_ok(p, D)) {
-            if (threadIdx.x == 0 && p.status) atomicOr(p.status, kDevBadHeader);
-            return;
+        // (looked at before anything is written: the loads do not depend on it)
+        header = pool_header_ok(src, p.H, D);
+        const uint32_t nb = blocks_of(src.T);
+        if (src.whole) {
+            hr = w;
+            left = nb;
+        } else {
+            if (!share((uint64_t)per_seq * nb)) return;
+            uint64_t q;
+            divmod_u64(x0, nb, q, off);
+            hr = (uint32_t)q;
         }
-        len = p.T;
+    } else if (src.whole) {
+        b = w / per_seq;
+        hr = w % per_seq;
+        left = 1u << 31;
     } else {
-        len = wave_uniform(length_of(p, b, threadIdx.x == 0 && ck == 0 && h == 0 && rb == 0));
-    }
-    const uint32_t begin = ck * p.chunk;
-    if (begin >= len && !(p.direct && ck == 0)) return;
-    const uint32_t end = len - begin < p.chunk ? len : begin + p.chunk;  // begin <= len here
-
-    // page numbers of this wave's 16-token runs: run i of tile t in lane 2t + i
-    uint32_t my_page = 0;
-    if (FMT != kFmtPool) {
-        const uint32_t t = begin + ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
-        if (t < end) {
-            const int32_t pg = p.table[b * p.table_stride + (t >> p.page_shift)];
-            const bool ok = (uint32_t)pg < p.num_pages;
-            if (!ok && p.status) atomicOr(p.status, kDevBadPage);
-            my_page = ok ? (uint32_t)pg : 0;
+        // every thread counts the blocks of a run of sequences; then the thread whose run holds the first block finds it
+        const uint32_t run = (p.n + kWaves * kWave - 1) / (kWaves * kWave);
+        const uint32_t s0 = threadIdx.x * run, s1 = s0 + run < p.n ? s0 + run : p.n;
+        uint32_t mine = 0, all;
+        for (uint32_t s = s0; s < s1; ++s) mine += blocks_of(clamp_length(src, src.lens[s]));
+        const uint32_t before = scan_threads(mine, sh.sums, all);
+        if (!share((uint64_t)wave_uniform(all) * per_seq)) return;
+        uint64_t q64;
+        uint32_t part;
+        divmod_u64(x0, per_seq, q64, part);
+        const uint32_t q = (uint32_t)q64;  // sequences' blocks before
+        if (q >= before && q - before < mine) {
+            uint32_t at = before, s = s0, nb = 0;
+            for (; s < s1; ++s) {
+                nb = blocks_of(clamp_length(src, src.lens[s]));
+                if (q - at < nb) break;
+                at += nb;
+            }
+            sh.found[0] = s;
+            sh.found[1] = at;
+            sh.found[2] = nb;
         }
+        __syncthreads();
+        b = wave_uniform(sh.found[0]);
+        divmod_u64(x0 - (uint64_t)wave_uniform(sh.found[1]) * per_seq, wave_uniform(sh.found[2]), q64, off);
+        hr = (uint32_t)q64;
     }
 
-    // queries: row 16 rt + c, channels as the key loads have them
-    u32x4 qf[RT][KS];
-    float qscale[RT];
+    uint64_t first = x0 - off;  // the unit's first block
+    for (uint32_t nb = 0; left != 0; off = 0, ++hr, first += nb) {
+    if (FMT != kFmtPool && hr == per_seq) {
+        hr = 0;
+        ++b;
+    }
+    if (FMT == kFmtPool ? hr >= per_seq : b >= p.n) break;
+    const uint32_t h = hr / src.row_blocks, rb = hr % src.row_blocks;
+
+    // everything that can be asked for at once: the queries (row 16 rt + c,
+    // channels as the key loads have them), the length, the first page numbers
+    uint32_t qw[RT][KS][4];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const uint32_t r = (rb * RT + rt) * 16 + c;
-        uint32_t w[KS][4];
         uint32_t seq, qh;
-        row_of<FMT>(p, b, h, r < p.rows ? r : 0, seq, qh);
+        row_of<FMT>(p, b, h, r < src.rows ? r : 0, seq, qh);
         const uint8_t* qp = reinterpret_cast<const uint8_t*>(p.q.data + (uint64_t)seq * p.q.ts + (uint64_t)qh * p.q.hs);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const uint32_t ch = HALF ? (s / 2) * 64 + g * 16 + (s % 2) * 8 : s * 32 + g * 8;
-            load_words(qp + 2 * ch, w[s]);
-            if (r >= p.rows) w[s][0] = w[s][1] = w[s][2] = w[s][3] = 0;
-        }
-        qscale[rt] = p.scale_log2;
-        if (HALF) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t lo = w[s][i] & 0x7FFFu, hi = (w[s][i] >> 16) & 0x7FFFu;
-                    m = lo > m ? lo : m;
-                    m = hi > m ? hi : m;
-                }
-            uint32_t o = __shfl_xor(m, 16);
-            m = o > m ? o : m;
-            o = __shfl_xor(m, 32);
-            m = o > m ? o : m;
-            // largest magnitude to [2^14, 2^15); Inf and NaN stay what they are
-            const int e = (m == 0 || m >= 0x7F80u) ? 0 : 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(m << 16));
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    qf[rt][s][i] = pack_half2(__builtin_amdgcn_ldexpf(bf16_lo(w[s][i]), e),
-                                              __builtin_amdgcn_ldexpf(bf16_hi(w[s][i]), e));
-            qscale[rt] = __builtin_amdgcn_ldexpf(qscale[rt], -e);
-        } else {
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qf[rt][s][i] = w[s][i];
+            load_words(qp + 2 * ch, qw[rt][s]);
         }
     }
-    if (FMT == kFmtPool) {
-        const float step = reinterpret_cast<const float*>(p.pool + p.lay.k_scale)[p.layer];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) qscale[rt] *= step;
+    // page numbers of this wave's 16-token runs: run i of tile t in lane 2t + i
+    // (whole rows of the table can be read, whatever the length)
+    const uint32_t run0 = ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
+    const auto load_pages = [&](uint32_t base) {
+        const uint32_t t = (base + run0) >> src.page_shift;
+        return src.table[b * src.table_stride + (t < src.table_cols ? t : 0)];
+    };
+    int32_t given = 0, page = 0;
+    if (FMT != kFmtPool) {
+        given = src.lens[b];
+        page = load_pages(off * kBlock);
     }
+    const uint32_t len = FMT == kFmtPool ? src.T : wave_uniform(clamp_length(src, given));
+    if (FMT != kFmtPool && hr == 0 && off == 0 && threadIdx.x == 0 && bad_length(src, given) && p.status)
+        atomicOr(p.status, kDevBadLength);
+    nb = blocks_of(len);
+    const uint32_t take = nb - off < left ? nb - off : (uint32_t)left;
+    left -= take;
+    if (FMT != kFmtPool && src.whole) left = 0;
+    const uint32_t begin = off * kBlock;
+    const uint32_t end = off + take == nb ? len : begin + take * kBlock;
 
-    // running state
-    f32x4 o[RT][NC];
-    float m[RT], mu[RT], l[RT];
-    int E = -1000;  // exponent taken out of the weights (HALF)
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = kNegInf;
-        mu[rt] = 0.0f;
-        l[rt] = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NC; ++n) o[rt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-
-    const uint64_t vec0 = FMT == kFmtPool ? ((uint64_t)p.layer * p.H + h) * p.T : 0;  // the head's first vector
+    const uint64_t vec0 = FMT == kFmtPool ? ((uint64_t)src.layer * p.H + h) * src.T : 0;  // the head's first vector
+    uint32_t my_page = 0;
+    const auto take_pages = [&](uint32_t base) {
+        const bool counts = base + run0 < end, ok = (uint32_t)page < src.num_pages;
+        if (counts && !ok && p.status) atomicOr(p.status, kDevBadPage);
+        my_page = counts && ok ? (uint32_t)page : 0;
+    };
+    if (FMT != kFmtPool) take_pages(begin);
     const auto load = [&](uint32_t t0, uint32_t it, R& x) {
         if constexpr (FMT == kFmtPool) {
             const uint64_t vec = vec0 + t0;
-            const uint32_t last = p.T - t0 - 1;  // tokens behind the last are the last again (masked below)
-            const uint8_t* kb = p.pool + p.lay.k_codes + vec * D;
-            const uint8_t* vb = p.pool + p.lay.v_codes + vec * (3 * D / 8);
-            const uint8_t* sb = p.pool + p.lay.v_scale + vec * 2;
+            const uint32_t last = src.T - t0 - 1;  // tokens behind the last are the last again (masked below)
+            const uint8_t* kb = src.pool + src.lay.k_codes + vec * D;
+            const uint8_t* vb = src.pool + src.lay.v_codes + vec * (3 * D / 8);
+            const uint8_t* sb = src.pool + src.lay.v_scale + vec * 2;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t t = 16 * i + c < last ? 16 * i + c : last;
@@ -346,26 +440,32 @@ __global__ __launch_bounds__(kWaves* kWave) void attend_kernel(AttendParams p) {
                 for (int s = 0; s < D / 64; ++s)
                     x.k[i][s] = *reinterpret_cast<const uint4*>(kb + t * D + 64 * s + 16 * g);
             }
-            const uint32_t at = D == 128 ? c : c >> 1;
+            const uint32_t word = 4 * (D == 128 ? c & 3 : c & 1);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t t0j = (j < 4 ? 0 : 16) + 4 * g + (j & 3);
-                const uint32_t t = t0j < last ? t0j : last;
-                const uint8_t* a = vb + t * (3 * D / 8) + at;
-                x.v[j] = (uint32_t)a[0] | (uint32_t)a[D / 8] << 8 | (uint32_t)a[2 * D / 8] << 16;
-                const uint32_t sz = *reinterpret_cast<const uint16_t*>(sb + 2 * t);
-                if (j & 1)
-                    x.vs[j >> 1] |= sz << 16;
-                else
-                    x.vs[j >> 1] = sz;
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t t1 = 16 * i + 4 * g + (c >> 2), t = t1 < last ? t1 : last;
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                    x.v[i][q] = *reinterpret_cast<const uint32_t*>(vb + t * (3 * D / 8) + q * (D / 8) + word);
+                // sizes of four tokens; behind the last token, the same bytes of the pool's last four (masked below)
+                const uint32_t s1 = 16 * i + 4 * g;
+                if (s1 + 3 <= last) {
+                    __builtin_memcpy(&x.vs[i], sb + 2 * s1, 8);
+                } else {
+                    uint32_t z[4];
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j)
+                        z[j] = *reinterpret_cast<const uint16_t*>(sb + 2 * (s1 + j < last ? s1 + j : last));
+                    x.vs[i] = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
+                }
             }
         } else {
             constexpr uint32_t ROW = FMT == kFmtBf16 ? 2 * D : D;
-            const uint32_t P = 1u << p.page_shift;
+            const uint32_t P = 1u << src.page_shift;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t pg = __builtin_amdgcn_readlane(my_page, (2 * it + i) & 63);
-                const uint8_t* pb = p.pages + (uint64_t)pg * p.page_bytes;
+                const uint8_t* pb = src.pages + (uint64_t)pg * src.page_bytes;
                 const uint32_t at = (t0 + 16 * i) & (P - 1);
                 const uint32_t kl = h * P + at, vl = (p.H + h) * P + at;  // rows inside the page
                 const uint8_t* kb = pb + (uint64_t)kl * ROW;
@@ -376,8 +476,8 @@ __global__ __launch_bounds__(kWaves* kWave) void attend_kernel(AttendParams p) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) load_words(vb + (4 * g + j) * ROW + c * (ROW / 16), x.v[4 * i + j]);
                 if (FMT != kFmtBf16) {
-                    const float4 a = *reinterpret_cast<const float4*>(pb + p.steps + (uint64_t)(kl + 4 * g) * 4);
-                    const float4 w = *reinterpret_cast<const float4*>(pb + p.steps + (uint64_t)(vl + 4 * g) * 4);
+                    const float4 a = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(kl + 4 * g) * 4);
+                    const float4 w = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(vl + 4 * g) * 4);
                     x.ks[4 * i] = a.x;
                     x.ks[4 * i + 1] = a.y;
                     x.ks[4 * i + 2] = a.z;
@@ -390,69 +490,153 @@ __global__ __launch_bounds__(kWaves* kWave) void attend_kernel(AttendParams p) {
             }
         }
     };
+    R x;
+    if (begin + wave * kTile < end) load(begin + wave * kTile, 0, x);
 
-    const auto tile = [&](uint32_t t0, R& x) {
-        const uint32_t live = end - t0;  // tokens of this tile that count, if below 32
-        // key operands
-        u32x4 kf[2][KS];
+    u32x4 qf[RT][KS];
+    float qscale[RT];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+    for (int rt = 0; rt < RT; ++rt) {
+        uint32_t(&z)[KS][4] = qw[rt];
+        const uint32_t r = (rb * RT + rt) * 16 + c;
+        // a row that is none is a zero; the factor of a row's logits is kept
+        // >= 0, so that the largest product is the largest logit: a negative
+        // scale turns the queries' signs
+        const uint32_t turn = p.scale_log2 < 0.0f ? 0x80008000u : 0;
+        qscale[rt] = fabsf(p.scale_log2);
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                if (HALF) {
-                    const uint4& y = x.k[i][s / 2];
-                    uint32_t a = s % 2 ? y.z : y.x, d = s % 2 ? y.w : y.y;
-                    if (FMT != kFmtFp8) {
-                        a ^= 0x80808080u;
-                        d ^= 0x80808080u;
-                    }
-                    constexpr int F = FMT == kFmtFp8 ? kFmtFp8 : kFmtInt8;
-                    kf[i][s] = u32x4{widen<F, false>(a), widen<F, true>(a), widen<F, false>(d), widen<F, true>(d)};
-                } else {
-                    const uint4& y = x.k[i][s];
-                    kf[i][s] = u32x4{y.x, y.y, y.z, y.w};
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[s][i] = r < src.rows ? z[s][i] ^ turn : 0;
+        if (HALF) {
+            uint32_t big = 0;
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t lo = z[s][i] & 0x7FFFu, hi = (z[s][i] >> 16) & 0x7FFFu;
+                    big = lo > big ? lo : big;
+                    big = hi > big ? hi : big;
                 }
-            }
+            uint32_t other = __shfl_xor(big, 16);
+            big = other > big ? other : big;
+            other = __shfl_xor(big, 32);
+            big = other > big ? other : big;
+            // largest magnitude to [2^14, 2^15); Inf and NaN stay what they are
+            const int e = (big == 0 || big >= 0x7F80u) ? 0 : 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(big << 16));
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    qf[rt][s][i] = pack_half2(__builtin_amdgcn_ldexpf(bf16_lo(z[s][i]), e),
+                                              __builtin_amdgcn_ldexpf(bf16_hi(z[s][i]), e));
+            qscale[rt] = __builtin_amdgcn_ldexpf(qscale[rt], -e);
+        } else {
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qf[rt][s][i] = z[s][i];
         }
-        // value operands: token pairs of one channel
-        u32x4 vf[NC];
-        float vs[8];
-        if constexpr (FMT == kFmtPool) {
-            // plane words: byte j of pl[half][q] is plane q of token j
-            uint32_t pl[2][3];
+    }
+    if (FMT == kFmtPool) {
+        const float step = reinterpret_cast<const float*>(src.pool + src.lay.k_scale)[src.layer];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) qscale[rt] *= step;
+    }
+
+    // running state
+    f32x4 o[RT][NC];
+    float m[RT], mu[RT], l[RT];
+    int E = kMinExp;  // exponent taken out of the weights (HALF)
+    float elimit = __builtin_amdgcn_ldexpf(1.0f, kMinExp);  // 2^E, which no step so far has reached
+    float wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - kMinExp);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = kNegInf;
+        mu[rt] = 0.0f;
+        l[rt] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) o[rt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    uint32_t sel_a = 0, sel_b = 0;
+    if (FMT == kFmtPool) gather_selectors(c >> 2, sel_a, sel_b);
+
+    // One tile: its loads are in x; those of the next one (at t_next, if
+    // below end) go out as soon as x has been widened. PART: the tile ends
+    // behind `end`.
+    const auto tile = [&](auto part, uint32_t t0, uint32_t t_next, uint32_t it, R& x) {
+        constexpr bool PART = decltype(part)::value;
+        const uint32_t live = end - t0;
+        f32x4 s[RT][2];
+        {
+            u32x4 kf[2][KS];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                for (int q = 0; q < 3; ++q) {
-                    const uint32_t lo = __builtin_amdgcn_perm(x.v[4 * i + 1], x.v[4 * i], 0x0C0C0400u + 0x0101u * q);
-                    const uint32_t hi = __builtin_amdgcn_perm(x.v[4 * i + 3], x.v[4 * i + 2], 0x04000C0Cu + 0x01010000u * q);
-                    pl[i][q] = lo | hi;
-                    if (D == 64) pl[i][q] = pl[i][q] >> ((c & 1) * 4) & 0x0F0F0F0Fu;
+                for (int k = 0; k < KS; ++k) {
+                    if (HALF) {
+                        const uint4& y = x.k[i][k / 2];
+                        uint32_t a = k % 2 ? y.z : y.x, d = k % 2 ? y.w : y.y;
+                        if (FMT != kFmtFp8) {
+                            a ^= 0x80808080u;
+                            d ^= 0x80808080u;
+                        }
+                        constexpr int F = FMT == kFmtFp8 ? kFmtFp8 : kFmtInt8;
+                        kf[i][k] = u32x4{widen<F, false>(a), widen<F, true>(a), widen<F, false>(d), widen<F, true>(d)};
+                    } else {
+                        const uint4& y = x.k[i][k];
+                        kf[i][k] = u32x4{y.x, y.y, y.z, y.w};
+                    }
                 }
             }
-            // levels as binary16: a byte table of the low and of the high halves
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    s[rt][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) s[rt][i] = mfma<FMT>(kf[i][k], qf[rt][k], s[rt][i]);
+                }
+        }
+        // value operands: token pairs of one channel
+        u32x4 vf[NC];
+        float vs[8], ks[8];
+        if constexpr (FMT == kFmtPool) {
             constexpr uint32_t l0 = level_bytes(0, 0), l1 = level_bytes(4, 0);
             constexpr uint32_t h0 = level_bytes(0, 8), h1 = level_bytes(4, 8);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
+            for (int i = 0; i < 2; ++i) {
+                uint32_t pl[3];  // byte j: the lane's byte of the plane of token j
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t sel = pl[i][0] >> n & 0x01010101u;
-                    sel |= (n >= 1 ? pl[i][1] >> (n >= 1 ? n - 1 : 0) : pl[i][1] << 1) & 0x02020202u;
-                    sel |= (n >= 2 ? pl[i][2] >> (n >= 2 ? n - 2 : 0) : pl[i][2] << (n >= 2 ? 0 : 2 - n)) & 0x04040404u;
-                    const uint32_t lo = __builtin_amdgcn_perm(l1, l0, sel), hi = __builtin_amdgcn_perm(h1, h0, sel);
-                    vf[n][2 * i] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-                    vf[n][2 * i + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+                for (int q = 0; q < 3; ++q) {
+                    pl[q] = gather_bytes(x.v[i][q], sel_a, sel_b);
+                    if (D == 64) pl[q] = pl[q] >> ((c >> 1 & 1) * 4) & 0x0F0F0F0Fu;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // the codes of channels k and k + 4, a nibble each
+                    uint32_t code = pl[0] >> k & 0x11111111u;
+                    code |= (k >= 1 ? pl[1] >> (k >= 1 ? k - 1 : 0) : pl[1] << 1) & 0x22222222u;
+                    code |= (k >= 2 ? pl[2] >> (k >= 2 ? k - 2 : 0) : pl[2] << (k >= 2 ? 0 : 2 - k)) & 0x44444444u;
+#pragma unroll
+                    for (int n = k; n < NC; n += 4) {
+                        const uint32_t sel = (n == k ? code : code >> 4) & 0x07070707u;
+                        const uint32_t lo = __builtin_amdgcn_perm(l1, l0, sel), hi = __builtin_amdgcn_perm(h1, h0, sel);
+                        vf[n][2 * i] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
+                        vf[n][2 * i + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+                    }
+                }
+                const uint32_t w[2] = {x.vs[i].x, x.vs[i].y};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const half2_t s2 = __builtin_bit_cast(half2_t, w[j]);
+                    vs[4 * i + 2 * j] = (float)s2.x;
+                    vs[4 * i + 2 * j + 1] = (float)s2.y;
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const half2_t s2 = __builtin_bit_cast(half2_t, x.vs[j]);
-                vs[2 * j] = (float)s2.x;
-                vs[2 * j + 1] = (float)s2.y;
-            }
         } else {
-            if (live < kTile) {
+            if (PART) {
                 // rows behind the end may hold anything: NaN times a weight of 0 would stay
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -484,64 +668,58 @@ __global__ __launch_bounds__(kWaves* kWave) void attend_kernel(AttendParams p) {
                     }
                 }
             }
-            if (FMT != kFmtBf16) {
+            if constexpr (FMT != kFmtBf16) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) vs[j] = x.vs[j];
-            }
-        }
-        if (HALF) {
-            // step exponents: all weights are divided by 2^E
-            float big = vs[0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) big = fmaxf(big, vs[j]);
-            const int e = big > 0.0f ? __builtin_amdgcn_frexp_expf(big) : -1000;
-            if (__ballot(e > E) != 0) {
-                int ne = e > E ? e : E;
-                int other = __shfl_xor(ne, 16);
-                ne = other > ne ? other : ne;
-                other = __shfl_xor(ne, 32);
-                ne = other > ne ? other : ne;
-                if (E > -1000) {
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                        for (int n = 0; n < NC; ++n)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) o[rt][n][r] = __builtin_amdgcn_ldexpf(o[rt][n][r], E - ne);
+                for (int j = 0; j < 8; ++j) {
+                    vs[j] = x.vs[j];
+                    ks[j] = x.ks[j];
                 }
-                E = ne;
             }
-            const int shift = E > -1000 ? kWeightExp - E : 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) vs[j] = __builtin_amdgcn_ldexpf(vs[j], shift);
         }
+        if (t_next < end) load(t_next, it + 1, x);
+
+        // logits (before the row's factor), their maxima, and the steps' largest
+        float y[RT][8], top[RT];
+        bool move = false;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            f32x4 s[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                s[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int k = 0; k < KS; ++k) s[i] = mfma<FMT>(kf[i][k], qf[rt][k], s[i]);
-            }
-            float y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                y[j] = s[j >> 2][j & 3] * qscale[rt];
-                if constexpr (FMT == kFmtInt8 || FMT == kFmtFp8) y[j] *= x.ks[j];
+                y[rt][j] = s[rt][j >> 2][j & 3];
+                if constexpr (FMT == kFmtInt8 || FMT == kFmtFp8) y[rt][j] *= ks[j];
+                if (PART) y[rt][j] = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? y[rt][j] : kNegInf;
             }
-            if (live < kTile) {
+            top[rt] = y[rt][0];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    y[j] = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? y[j] : kNegInf;
+            for (int j = 1; j < 8; ++j) top[rt] = fmaxf(top[rt], y[rt][j]);
+            top[rt] *= qscale[rt];
+            move |= top[rt] > m[rt] + kSlack;
+        }
+        float big = 0.0f;
+        if (HALF) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) big = fmaxf(big, vs[j]);
+            move |= big >= elimit;
+        }
+        if (__ballot(move) != 0) {
+            if (HALF) {
+                big = fmaxf(big, __shfl_xor(big, 16));
+                big = fmaxf(big, __shfl_xor(big, 32));
+                const int e = __builtin_amdgcn_frexp_expf(big), ne = big >= elimit ? e : E;
+                const float a = __builtin_amdgcn_ldexpf(1.0f, E - ne);
+                E = ne;
+                elimit = __builtin_amdgcn_ldexpf(1.0f, E);
+                wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - E);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) o[rt][n] *= a;
             }
-            float top = y[0];
 #pragma unroll
-            for (int j = 1; j < 8; ++j) top = fmaxf(top, y[j]);
-            if (__ballot(top > m[rt] + kSlack) != 0) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float nm = fmaxf(m[rt], top);
+            for (int rt = 0; rt < RT; ++rt) {
+                float x2 = fmaxf(top[rt], __shfl_xor(top[rt], 16));
+                x2 = fmaxf(x2, __shfl_xor(x2, 32));
+                const float nm = fmaxf(m[rt], x2);
                 const float a = nm == kNegInf ? 1.0f : exp2_fast(m[rt] - nm);
                 m[rt] = nm;
                 mu[rt] = nm == kNegInf ? 0.0f : nm;
@@ -549,10 +727,19 @@ __global__ __launch_bounds__(kWaves* kWave) void attend_kernel(AttendParams p) {
 #pragma unroll
                 for (int n = 0; n < NC; ++n) o[rt][n] *= a;
             }
+        }
+        if (HALF) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) vs[j] *= wmul;
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
             float w[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float e = exp2_fast(y[j] - mu[rt]);
+                float e = exp2_fast(fmaf(y[rt][j], qscale[rt], -mu[rt]));
+                // by the token, not by its logit: -inf * 0 has no sign
+                if (PART) e = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? e : 0.0f;
                 l[rt] += e;
                 w[j] = HALF ? e * vs[j] : e;
             }
@@ -570,65 +757,90 @@ __global__ __launch_bounds__(kWaves* kWave) void attend_kernel(AttendParams p) {
                     lo[j] = pack_bf16x2(w[2 * j] - bf16_lo(hi[j]), w[2 * j + 1] - bf16_hi(hi[j]));
                 }
 #pragma unroll
-                for (int n = 0; n < NC; ++n) o[rt][n] = mfma_bf16(vf[n], lo, mfma_bf16(vf[n], hi, o[rt][n]));
+                for (int n = 0; n < NC; ++n) o[rt][n] = mfma_bf16(vf[n], hi, o[rt][n]);
+#pragma unroll
+                for (int n = 0; n < NC; ++n) o[rt][n] = mfma_bf16(vf[n], lo, o[rt][n]);
             }
         }
     };
 
-    {
-        uint32_t it = 0;
-        for (uint32_t t0 = begin + wave * kTile; t0 < end; t0 += kWaves * kTile, ++it) {
-            R x;
-            load(t0, it, x);
-            tile(t0, x);
+    for (uint32_t base = begin; base < end; base += kPageRun) {
+        if (base != begin) {  // the next page numbers (the pool needs none: one round)
+            page = load_pages(base);
+            take_pages(base);
+            if (base + wave * kTile < end) load(base + wave * kTile, 0, x);
         }
+        const uint32_t stop = FMT == kFmtPool || end - base <= kPageRun ? end : base + kPageRun;
+        uint32_t it = 0, t0 = base + wave * kTile;
+        for (; t0 + kTile <= stop; t0 += kBlock, ++it)
+            tile(std::false_type{}, t0, t0 + kBlock < stop ? t0 + kBlock : end, it, x);
+        if (t0 < stop) tile(std::true_type{}, t0, end, it, x);
+        if (FMT == kFmtPool) break;
+    }
+    if (FMT == kFmtPool && !header) {
+        if (threadIdx.x == 0 && p.status) atomicOr(p.status, kDevBadHeader);
+        return;
     }
 
     // ---- join the waves: m and l first, then the sums, 16 rows at a time
-    __shared__ float ml[kWaves][RT * 16][2];
-    __shared__ float os[kWaves][16][D + 4];
+    const bool whole = take == nb;
+    const uint32_t slot = whole ? (src.whole ? 0 : 2 * src.W) + b * per_seq + hr : off ? 2 * w : 2 * w + 1;
+    if (off == 0 && threadIdx.x == 0 && !(src.whole && p.direct)) {
+        // parts: up to the workgroup whose share has the unit's last block
+        uint32_t parts = p.direct ? 0 : 1;
+        if (!whole) {
+            const uint64_t last = first + nb - 1, large = (each + 1) * more;
+            uint64_t at;
+            uint32_t rest;
+            if (last < large)
+                divmod_u64(last, (uint32_t)each + 1, at, rest);
+            else
+                divmod_u64(last - large, (uint32_t)each, at, rest);
+            parts = (uint32_t)at + (last < large ? 0 : more) - w + 1;
+        }
+        src.info[b * per_seq + hr] = make_uint2(slot, parts);
+    }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         float s = l[rt];
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (g == 0) {
-            ml[wave][rt * 16 + c][0] = m[rt];
-            ml[wave][rt * 16 + c][1] = s;
+            sh.ml[wave][rt * 16 + c][0] = m[rt];
+            sh.ml[wave][rt * 16 + c][1] = s;
         }
     }
     __syncthreads();
     const uint32_t row = threadIdx.x / 16, ch = threadIdx.x % 16 * NC;  // the thread's part of the outputs
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        float M = ml[0][rt * 16 + c][0];
+        float M = sh.ml[0][rt * 16 + c][0];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) M = fmaxf(M, ml[w][rt * 16 + c][0]);
+        for (int v = 1; v < kWaves; ++v) M = fmaxf(M, sh.ml[v][rt * 16 + c][0]);
         const float Mu = M == kNegInf ? 0.0f : M;
-        float a = exp2_fast(m[rt] - Mu);
-        const int sh = HALF && E > -1000 ? E - kWeightExp : 0;
+        const float a = exp2_fast(m[rt] - Mu);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
                 float v = o[rt][n][r];
-                if (HALF) v = __builtin_amdgcn_ldexpf(v, sh);
-                os[wave][c][(4 * g + r) * NC + n] = v * a;
+                if (HALF) v = __builtin_amdgcn_ldexpf(v, E - kWeightExp);
+                sh.os[wave][c][channel_of<FMT, D>(g, r) + n] = v * a;
             }
         __syncthreads();
         const uint32_t r = (rb * RT + rt) * 16 + row;
-        float Mr = ml[0][rt * 16 + row][0];
+        float Mr = sh.ml[0][rt * 16 + row][0];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) Mr = fmaxf(Mr, ml[w][rt * 16 + row][0]);
+        for (int v = 1; v < kWaves; ++v) Mr = fmaxf(Mr, sh.ml[v][rt * 16 + row][0]);
         const float Mru = Mr == kNegInf ? 0.0f : Mr;
-        float total = 0.0f, y[NC];
+        float sum = 0.0f, y[NC];
 #pragma unroll
         for (int n = 0; n < NC; ++n) y[n] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            total = fmaf(ml[w][rt * 16 + row][1], exp2_fast(ml[w][rt * 16 + row][0] - Mru), total);
+        for (int v = 0; v < kWaves; ++v) {
+            sum = fmaf(sh.ml[v][rt * 16 + row][1], exp2_fast(sh.ml[v][rt * 16 + row][0] - Mru), sum);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) y[n] += os[w][row][ch + n];
+            for (int n = 0; n < NC; ++n) y[n] += sh.os[v][row][ch + n];
         }
         if (FMT == kFmtPool) {
             fwht_row<NC>(y, lane);
@@ -636,190 +848,288 @@ __global__ __launch_bounds__(kWaves* kWave) void attend_kernel(AttendParams p) {
 #pragma unroll
             for (int n = 0; n < NC; ++n) y[n] *= k;
         }
-        if (r < p.rows) {
-            uint32_t seq, qh;
-            row_of<FMT>(p, b, h, r, seq, qh);
-            const uint64_t at = (uint64_t)seq * p.Hq + qh;
-            if (p.direct) {
+        if (r < src.rows) {
+            if (whole && p.direct) {
+                uint32_t seq, qh;
+                row_of<FMT>(p, b, h, r, seq, qh);
                 // a row without tokens: zeros, and ln 0
-                const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 uint16_t* to = p.out.data + (uint64_t)seq * p.out.ts + (uint64_t)qh * p.out.hs + ch;
-                uint32_t w[NC / 2];
+                uint32_t z[NC / 2];
 #pragma unroll
-                for (int n = 0; n < NC / 2; ++n) w[n] = pack_bf16x2(y[2 * n] * inv, y[2 * n + 1] * inv);
+                for (int n = 0; n < NC / 2; ++n) z[n] = pack_bf16x2(y[2 * n] * inv, y[2 * n + 1] * inv);
                 if constexpr (NC == 8)
-                    *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(to) = make_uint4(z[0], z[1], z[2], z[3]);
                 else
-                    *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-                if (p.lse && threadIdx.x % 16 == 0) p.lse[at] = (Mr + log2f(total)) * 0.69314718055994531f;
+                    *reinterpret_cast<uint2*>(to) = make_uint2(z[0], z[1]);
+                if (p.lse && threadIdx.x % 16 == 0)
+                    p.lse[(uint64_t)seq * p.Hq + qh] = (Mr + log2f(sum)) * 0.69314718055994531f;
             } else {
-                const uint64_t part = at * p.splits + p.split0 + ck;
-                float* to = p.part + part * D + ch;
+                float* to = src.part + (uint64_t)slot * (16 * RT * (D + 2));
 #pragma unroll
-                for (int n = 0; n < NC; n += 4) *reinterpret_cast<f32x4*>(to + n) = f32x4{y[n], y[n + 1], y[n + 2], y[n + 3]};
-                if (threadIdx.x % 16 == 0) {
-                    float* t2 = p.part + (uint64_t)p.n * p.Hq * p.splits * D + part * 2;
-                    t2[0] = Mr;
-                    t2[1] = total;
-                }
+                for (int n = 0; n < NC; n += 4)
+                    *reinterpret_cast<f32x4*>(to + (rt * 16 + row) * D + ch + n) = f32x4{y[n], y[n + 1], y[n + 2], y[n + 3]};
+                if (threadIdx.x % 16 == 0)
+                    *reinterpret_cast<float2*>(to + 16 * RT * D + 2 * (rt * 16 + row)) = make_float2(Mr, sum);
             }
         }
         __syncthreads();
     }
+    }
 }
 
-// Joins the parts of a row: one wave per row, d / 64 channels a lane.
+template <int FMT, int D, int RT>
+__global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_kernel(Common p, Source src) {
+    __shared__ Shared<D, RT> sh;
+    attend_share<FMT, D, RT>(p, src, blockIdx.x, sh);
+}
+
+// A pool's workgroups and those of the tails behind it, in one launch.
+template <int FMT, int D, int RT>
+__global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_both_kernel(Common p, Source pool, Source tail) {
+    __shared__ union {
+        Shared<D, RT> a;
+        Shared<D, 1> b;
+    } sh;
+    if (blockIdx.x < pool.W)
+        attend_share<kFmtPool, D, RT>(p, pool, blockIdx.x, sh.a);
+    else
+        attend_share<FMT, D, 1>(p, tail, blockIdx.x - pool.W, sh.b);
+}
+
+// Joins the parts of a row: V waves a row, which take its parts in turn, d / 64
+// channels a lane. What bounds it is latency, so a lane loads the maximum and
+// sum of one part, and the parts' sums come eight at a time.
 struct JoinParams {
-    RowsDev out;
-    float* lse;
-    const float* part;
-    uint32_t n, Hq, splits;
-    uint32_t pool_splits;     // parts that are always there
-    uint32_t chunk;           // tokens of a tail's part
-    AttendParams src;         // header and lengths
+    Common c;
+    Source src[2];
+    uint32_t rt[2];
+    uint32_t sources;
 };
 
-template <int D>
+template <int D, int V>
 __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p) {
-    constexpr int C = D / 64;
+    constexpr int C = D / 64, U = 8;
+    constexpr int RPB = kBlockThreads / kWave / V;  // rows of a workgroup
+    typedef float vec __attribute__((ext_vector_type(C)));
     const uint32_t lane = lane_id();
-    const uint64_t row = (uint64_t)blockIdx.x * (kBlockThreads / kWave) + wave_uniform(threadIdx.x / kWave);
-    if (row >= (uint64_t)p.n * p.Hq) return;
-    if (p.src.pool && !pool_header_ok(p.src, D)) return;
-    const uint32_t seq = (uint32_t)(row / p.Hq), qh = (uint32_t)(row % p.Hq);
-    uint32_t parts = p.pool_splits;
-    if (p.src.table) parts += (length_of(p.src, seq, false) + p.chunk - 1) / p.chunk;
-    const float* o = p.part + row * p.splits * D;
-    const float* ml = p.part + (uint64_t)p.n * p.Hq * p.splits * D + row * p.splits * 2;
-    float M = kNegInf;
-    for (uint32_t s = lane; s < parts; s += kWave) M = fmaxf(M, ml[2 * s]);
+    const uint32_t wave = wave_uniform(threadIdx.x / kWave), w = wave % V;
+    const uint64_t row = (uint64_t)blockIdx.x * RPB + wave / V;
+    if (row >= (uint64_t)p.c.n * p.c.Hq) return;
+    const uint32_t seq = (uint32_t)(row / p.c.Hq), qh = (uint32_t)(row % p.c.Hq);
+    const uint32_t h = qh / p.c.group, i = qh % p.c.group;
+    // this row's place in each source: its part k at from[s] + stride[s] * slot
+    const float *from[2], *ml[2];
+    uint64_t stride[2];
+    uint32_t slot[2], parts[2] = {0, 0};
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if ((uint32_t)s >= p.sources) break;
+        const Source& x = p.src[s];
+        const uint32_t tile = 16 * p.rt[s], r = x.pool ? seq * p.c.group + i : i;
+        const uint2 info = x.info[(x.pool ? 0 : (uint64_t)seq * p.c.H * x.row_blocks) + h * x.row_blocks + r / tile];
+        slot[s] = wave_uniform(info.x);
+        parts[s] = wave_uniform(info.y);
+        stride[s] = (uint64_t)tile * (D + 2);
+        from[s] = x.part + r % tile * D;
+        ml[s] = x.part + tile * D + r % tile * 2;
+    }
+    if (p.src[0].pool && !pool_header_ok(p.src[0], p.c.H, D)) return;
+    const uint32_t n0 = parts[0], n = n0 + parts[1];
+    if (n == 0) return;  // written already
+    const auto at = [&](const float* const (&base)[2], uint32_t k) {
+        const int s = k >= n0;
+        const uint32_t j = s ? k - n0 : k;
+        return base[s] + stride[s] * (j ? slot[s] - 1 + 2 * j : slot[s]);
+    };
+    float M = kNegInf, total = 0.0f;
+    for (uint32_t k = w + V * lane; k < n; k += V * kWave) M = fmaxf(M, at(ml, k)[0]);
 #pragma unroll
     for (int x = 1; x < 64; x *= 2) M = fmaxf(M, __shfl_xor(M, x));
     const float Mu = M == kNegInf ? 0.0f : M;
-    float total = 0.0f, y[C];
+    vec y = 0.0f;
+    for (uint32_t base = w; base < n; base += V * kWave) {
+        const uint32_t k = base + V * lane;
+        const float2 v = *reinterpret_cast<const float2*>(at(ml, k < n ? k : base));
+        const float a = exp2_fast(v.x - Mu);
+        total = k < n ? fmaf(v.y, a, total) : total;
+        const uint32_t rest = (n - base + V - 1) / V, count = rest < kWave ? rest : kWave;
+        for (uint32_t j = 0; j < count; j += U) {
+            vec x[U];
 #pragma unroll
-    for (int i = 0; i < C; ++i) y[i] = 0.0f;
-    for (uint32_t s = 0; s < parts; ++s) {
-        const float a = exp2_fast(ml[2 * s] - Mu);
-        total = fmaf(ml[2 * s + 1], a, total);
+            for (int u = 0; u < U; ++u) {
+                const uint32_t q = j + u < count ? j + u : count - 1;
+                x[u] = *reinterpret_cast<const vec*>(at(from, base + V * q) + C * lane);
+            }
 #pragma unroll
-        for (int i = 0; i < C; ++i) y[i] = fmaf(o[(uint64_t)s * D + C * lane + i], a, y[i]);
+            for (int u = 0; u < U; ++u) {
+                const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, a), (j + u) & 63));
+                if (j + u < count) y += x[u] * f;
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) total += __shfl_xor(total, x);
+    if constexpr (V > 1) {
+        __shared__ float mt[V][2];
+        __shared__ vec ys[V][kWave];
+        if (lane == 0) {
+            mt[w][0] = M;
+            mt[w][1] = total;
+        }
+        ys[w][lane] = y;
+        __syncthreads();
+        if (w) return;
+        float all = M;
+#pragma unroll
+        for (int x = 1; x < V; ++x) all = fmaxf(all, mt[x][0]);
+        const float allu = all == kNegInf ? 0.0f : all;
+        total = 0.0f;
+        y = 0.0f;
+#pragma unroll
+        for (int x = 0; x < V; ++x) {
+            const float a = exp2_fast(mt[x][0] - allu);
+            total = fmaf(mt[x][1], a, total);
+            y += ys[x][lane] * a;
+        }
+        M = all;
     }
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    uint16_t* to = p.out.data + (uint64_t)seq * p.out.ts + (uint64_t)qh * p.out.hs;
+    uint16_t* to = p.c.out.data + (uint64_t)seq * p.c.out.ts + (uint64_t)qh * p.c.out.hs;
     if constexpr (C == 2)
-        reinterpret_cast<uint32_t*>(to)[lane] = pack_bf16x2(y[0] * inv, y[1] * inv);
+        reinterpret_cast<uint32_t*>(to)[lane] = pack_bf16x2(y.x * inv, y.y * inv);
     else
-        to[lane] = (uint16_t)pack_bf16x2(y[0] * inv, 0.0f);
-    if (p.lse && lane == 0) p.lse[row] = (M + log2f(total)) * 0.69314718055994531f;
+        to[lane] = (uint16_t)pack_bf16x2(y.x * inv, 0.0f);
+    if (p.c.lse && lane == 0) p.c.lse[row] = (M + log2f(total)) * 0.69314718055994531f;
 }
 
-template <int FMT, int D>
-hipError_t launch_rt(uint32_t rt, uint32_t grid, const AttendParams& p, hipStream_t stream) {
-    return launch_kernel(rt == 1   ? attend_kernel<FMT, D, 1>
-                         : rt == 2 ? attend_kernel<FMT, D, 2>
-                                   : attend_kernel<FMT, D, 4>,
-                         dim3(grid), dim3(kWaves * kWave), stream, p);
-}
+// A workgroup gets at least kMinBlocks blocks: half a launch's latency goes
+// into starting a share and joining it (a 4096-token pool for 15 agents with
+// tails: 20 us with 1, 14.4 with 2, 15.8 with 4). Up to kWholeTokens tokens a
+// unit stays whole and its outputs need no second launch.
+constexpr uint64_t kMinBlocks = 2, kWholeTokens = 512;
 
-template <int FMT>
-hipError_t launch_source(uint32_t d, const AttendPlan& plan, AttendParams& p, uint32_t units, hipStream_t stream) {
-    p.rows = plan.rows;
-    p.row_blocks = plan.row_blocks;
-    p.chunk = plan.chunk;
-    p.chunks = plan.chunks;
-    uint64_t blocks = (uint64_t)units * plan.chunks;
-    if (plan.row_blocks > 1) blocks = (blocks + 7) / 8 * 8 * plan.row_blocks;
-    return d == 64 ? launch_rt<FMT, 64>(plan.rt, (uint32_t)blocks, p, stream)
-                   : launch_rt<FMT, 128>(plan.rt, (uint32_t)blocks, p, stream);
-}
-
-uint32_t tiles_of(uint32_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-
-AttendPlan make_plan(uint64_t units, uint32_t rows, uint64_t max_tokens) {
+AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens, uint32_t d, uint32_t most_rt, bool direct) {
     AttendPlan a;
     a.rows = rows;
-    a.rt = tiles_of(rows);
+    a.rt = rows > 16 ? most_rt : 1;
     a.row_blocks = (rows + 16 * a.rt - 1) / (16 * a.rt);
-    const uint64_t groups = units * a.row_blocks;
-    uint64_t chunk = max_tokens * groups / 1024;
-    chunk = chunk < 256 ? 256 : (chunk + 127) / 128 * 128;
-    a.chunk = (uint32_t)(chunk > kMaxChunk ? kMaxChunk : chunk);
-    a.chunks = (uint32_t)((max_tokens + a.chunk - 1) / a.chunk);
-    if (a.chunks == 0) a.chunks = 1;
+    a.units = units_of_rows * a.row_blocks;
+    const uint64_t slots = 256ull * waves_per_simd(d, a.rt);
+    const uint64_t blocks = a.units * ((max_tokens + kBlock - 1) / kBlock);
+    a.whole = max_tokens <= kWholeTokens || a.units >= 8 * slots;
+    uint64_t w = blocks / kMinBlocks < slots ? blocks / kMinBlocks : slots;
+    if (w < 1) w = 1;
+    a.W = a.whole ? a.units : w;
+    a.slots = a.whole ? (direct ? 0 : a.units) : 2 * w + (direct ? 0 : a.units);
     return a;
+}
+
+template <int D>
+hipError_t launch_pages(uint32_t format, uint32_t rt, uint32_t grid, const Common& p, const Source& s, hipStream_t stream) {
+    const auto f = format == 0   ? (rt == 1 ? attend_kernel<kFmtBf16, D, 1> : attend_kernel<kFmtBf16, D, 2>)
+                   : format == 1 ? (rt == 1 ? attend_kernel<kFmtInt8, D, 1> : attend_kernel<kFmtInt8, D, 2>)
+                                 : (rt == 1 ? attend_kernel<kFmtFp8, D, 1> : attend_kernel<kFmtFp8, D, 2>);
+    return launch_kernel(f, dim3(grid), dim3(kWaves * kWave), stream, p, s);
+}
+template <int D>
+hipError_t launch_both(uint32_t format, uint32_t rt, uint32_t grid, const Common& p, const Source& a, const Source& b,
+                       hipStream_t stream) {
+    const auto f = format == 0   ? (rt == 1 ? attend_both_kernel<kFmtBf16, D, 1> : attend_both_kernel<kFmtBf16, D, 2>)
+                   : format == 1 ? (rt == 1 ? attend_both_kernel<kFmtInt8, D, 1> : attend_both_kernel<kFmtInt8, D, 2>)
+                                 : (rt == 1 ? attend_both_kernel<kFmtFp8, D, 1> : attend_both_kernel<kFmtFp8, D, 2>);
+    return launch_kernel(f, dim3(grid), dim3(kWaves * kWave), stream, p, a, b);
+}
+
+// The source's share of the workspace, and the bytes it takes.
+uint64_t place_source(Source& s, const AttendPlan& plan, uint32_t d, uint8_t* ws) {
+    s.rows = plan.rows;
+    s.row_blocks = plan.row_blocks;
+    s.W = (uint32_t)plan.W;
+    s.whole = plan.whole;
+    s.part = reinterpret_cast<float*>(ws);
+    s.info = reinterpret_cast<uint2*>(ws + plan.part_bytes(d));
+    return plan.bytes(d);
 }
 
 }  // namespace
 
-AttendPlan page_attend_plan(uint32_t n_seqs, uint32_t H, uint32_t Hq, uint64_t max_tokens) {
-    return make_plan((uint64_t)n_seqs * H, Hq / H, max_tokens);
+AttendPlan page_attend_plan(uint32_t n_seqs, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens, bool tail) {
+    return make_plan((uint64_t)n_seqs * H, Hq / H, max_tokens, d, tail ? 1 : 2, !tail);
 }
 
-AttendPlan pool_attend_plan(uint32_t H, uint32_t n_agents, uint32_t Hq, uint32_t T) {
-    return make_plan(H, n_agents * (Hq / H), T);
+AttendPlan pool_attend_plan(uint32_t H, uint32_t n_agents, uint32_t Hq, uint32_t d, uint32_t T, bool tail) {
+    return make_plan(H, n_agents * (Hq / H), T, d, 2, !tail);
 }
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
-    AttendParams p{};
+    Common p{};
     p.q = a.q;
     p.out = a.out;
     p.lse = a.lse;
-    p.part = a.ws;
     p.status = a.status;
     p.n = a.n;
     p.H = a.H;
     p.Hq = a.Hq;
     p.group = a.Hq / a.H;
     p.scale_log2 = a.scale * 1.4426950408889634f;
-    AttendPlan pool_plan{}, page_plan{};
     const bool has_pool = a.pool != nullptr, has_pages = a.tail.table != nullptr;
+    p.direct = !(has_pool && has_pages);
+    uint8_t* ws = static_cast<uint8_t*>(a.ws);
+    AttendPlan pool_plan{}, page_plan{};
+    Source pool{}, pages{};
     if (has_pool) {
-        pool_plan = pool_attend_plan(a.H, a.n, a.Hq, a.T);
-        p.pool = a.pool;
-        p.lay = pool_layout(a.L, a.H, a.T, a.d);
-        p.L = a.L;
-        p.T = a.T;
-        p.layer = a.layer;
+        pool_plan = pool_attend_plan(a.H, a.n, a.Hq, a.d, a.T, has_pages);
+        ws += place_source(pool, pool_plan, a.d, ws);
+        pool.pool = a.pool;
+        pool.lay = pool_layout(a.L, a.H, a.T, a.d);
+        pool.L = a.L;
+        pool.T = a.T;
+        pool.layer = a.layer;
     }
     if (has_pages) {
         const PageLayout& lay = a.tail.lay;
-        page_plan = page_attend_plan(a.n, a.H, a.Hq, (uint64_t)a.tail.table_cols * lay.P);
-        p.pages = a.tail.pages;
-        p.table = a.tail.table;
-        p.table_stride = a.tail.table_stride;
-        p.lens = a.tail.lens;
-        p.table_cols = a.tail.table_cols;
-        p.num_pages = lay.num_pages;
-        p.page_shift = 31 - __builtin_clz(lay.P);
-        p.page_bytes = lay.page_bytes;
-        p.steps = lay.steps;
+        page_plan = page_attend_plan(a.n, a.H, a.Hq, a.d, (uint64_t)a.tail.table_cols * lay.P, has_pool);
+        ws += place_source(pages, page_plan, a.d, ws);
+        pages.pages = a.tail.pages;
+        pages.table = a.tail.table;
+        pages.table_stride = a.tail.table_stride;
+        pages.lens = a.tail.lens;
+        pages.table_cols = a.tail.table_cols;
+        pages.num_pages = lay.num_pages;
+        pages.page_shift = 31 - __builtin_clz(lay.P);
+        pages.page_bytes = lay.page_bytes;
+        pages.steps = lay.steps;
     }
-    p.splits = (has_pool ? pool_plan.chunks : 0) + (has_pages ? page_plan.chunks : 0);
-    p.direct = p.splits == 1;
-    hipError_t e = hipSuccess;
-    if (has_pool) e = launch_source<kFmtPool>(a.d, pool_plan, p, a.H, stream);
-    if (has_pages && e == hipSuccess) {
-        p.split0 = has_pool ? pool_plan.chunks : 0;
-        const uint32_t units = a.n * a.H;
-        e = a.tail.lay.format == 0   ? launch_source<kFmtBf16>(a.d, page_plan, p, units, stream)
-            : a.tail.lay.format == 1 ? launch_source<kFmtInt8>(a.d, page_plan, p, units, stream)
-                                     : launch_source<kFmtFp8>(a.d, page_plan, p, units, stream);
+    hipError_t e;
+    if (has_pool && has_pages) {
+        const uint32_t grid = pool.W + pages.W;
+        e = a.d == 64 ? launch_both<64>(a.tail.lay.format, pool_plan.rt, grid, p, pool, pages, stream)
+                      : launch_both<128>(a.tail.lay.format, pool_plan.rt, grid, p, pool, pages, stream);
+    } else if (has_pool) {
+        const auto f = a.d == 64 ? (pool_plan.rt == 1 ? attend_kernel<kFmtPool, 64, 1> : attend_kernel<kFmtPool, 64, 2>)
+                                 : (pool_plan.rt == 1 ? attend_kernel<kFmtPool, 128, 1> : attend_kernel<kFmtPool, 128, 2>);
+        e = launch_kernel(f, dim3(pool.W), dim3(kWaves * kWave), stream, p, pool);
+    } else {
+        e = a.d == 64 ? launch_pages<64>(a.tail.lay.format, page_plan.rt, pages.W, p, pages, stream)
+                      : launch_pages<128>(a.tail.lay.format, page_plan.rt, pages.W, p, pages, stream);
     }
-    if (p.direct || e != hipSuccess) return e;
+    const AttendPlan& first = has_pool ? pool_plan : page_plan;
+    if (e != hipSuccess || (p.direct && first.whole)) return e;
     JoinParams j{};
-    j.out = a.out;
-    j.lse = a.lse;
-    j.part = a.ws;
-    j.n = a.n;
-    j.Hq = a.Hq;
-    j.splits = p.splits;
-    j.pool_splits = has_pool ? pool_plan.chunks : 0;
-    j.chunk = has_pages ? page_plan.chunk : 1;
-    j.src = p;
+    j.c = p;
+    j.src[0] = has_pool ? pool : pages;
+    j.rt[0] = first.rt;
+    j.src[1] = pages;
+    j.rt[1] = has_pages ? page_plan.rt : 1;
+    j.sources = p.direct ? 1 : 2;
     const uint64_t rows = (uint64_t)a.n * a.Hq;
-    return launch_kernel(a.d == 64 ? attend_join_kernel<64> : attend_join_kernel<128>,
-                         dim3((uint32_t)((rows + 3) / 4)), dim3(kBlockThreads), stream, j);
+    const bool few = first.whole || first.W <= 6 * first.units;
+    if (few)
+        return launch_kernel(a.d == 64 ? attend_join_kernel<64, 1> : attend_join_kernel<128, 1>,
+                             dim3((uint32_t)((rows + 3) / 4)), dim3(kBlockThreads), stream, j);
+    return launch_kernel(a.d == 64 ? attend_join_kernel<64, 4> : attend_join_kernel<128, 4>, dim3((uint32_t)rows),
+                         dim3(kBlockThreads), stream, j);
 }
 
 }  // namespace kvc

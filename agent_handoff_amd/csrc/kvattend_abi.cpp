@@ -117,9 +117,9 @@ int page_copy(bool write, const kvc_pages* spec, const void* pages, size_t pages
 bool heads_ok(uint64_t n, uint32_t H, uint32_t Hq) {
     return H >= 1 && Hq >= 1 && Hq % H == 0 && Hq <= (1u << 16) && n * Hq < (1ull << 29);
 }
-bool plan_ok(const kvc::AttendPlan& p, uint64_t units) {
-    return (units * p.chunks + 8) * p.row_blocks < (1ull << 31);
-}
+// tokens of all sequences, in the 128-token blocks that the kernels count
+bool tokens_ok(uint64_t n, uint64_t max_tokens) { return max_tokens < (1ull << 31) && n * (max_tokens / 128 + 1) < (1ull << 31); }
+bool plan_ok(const kvc::AttendPlan& p) { return p.units < (1ull << 30) && p.slots < (1ull << 31); }
 
 // Checks of a page source; `most`: table_cols * page_tokens.
 int check_tail(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n, const int32_t* table,
@@ -215,11 +215,11 @@ int kvpage_read(const kvc_pages* spec, const void* pages, size_t pages_bytes, ui
 }
 
 size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uint32_t q_heads, uint32_t max_tokens) {
-    if (!spec_ok(spec) || !heads_ok(n_seqs, spec->num_kv_heads, q_heads) || max_tokens >= (1u << 31)) return 0;
+    if (!spec_ok(spec) || !heads_ok(n_seqs, spec->num_kv_heads, q_heads) || !tokens_ok(n_seqs, max_tokens)) return 0;
     if (n_seqs == 0) return 256;
-    const kvc::AttendPlan p = kvc::page_attend_plan(n_seqs, spec->num_kv_heads, q_heads, max_tokens);
-    if (!plan_ok(p, (uint64_t)n_seqs * spec->num_kv_heads)) return 0;
-    return (size_t)kvc::attend_ws_bytes((uint64_t)n_seqs * q_heads, p.chunks, spec->head_dim);
+    const kvc::AttendPlan p =
+        kvc::page_attend_plan(n_seqs, spec->num_kv_heads, q_heads, spec->head_dim, max_tokens, false);
+    return plan_ok(p) ? (size_t)p.bytes(spec->head_dim) : 0;
 }
 
 int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs, uint32_t q_heads,
@@ -233,10 +233,8 @@ int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, 
     if (!q || !out || !q->data || !out->data || !ws) return KVC_E_NULL;
     const int rc = check_tail(spec, pages, pages_bytes, n_seqs, table, table_cols, table_stride, lens);
     if (rc != KVC_OK) return rc;
-    const uint64_t most = (uint64_t)table_cols * spec->page_tokens;
-    const kvc::AttendPlan plan = kvc::page_attend_plan(n_seqs, spec->num_kv_heads, q_heads, most);
-    if (!plan_ok(plan, (uint64_t)n_seqs * spec->num_kv_heads)) return KVC_E_SHAPE;
-    const uint64_t need = kvc::attend_ws_bytes((uint64_t)n_seqs * q_heads, plan.chunks, spec->head_dim);
+    const uint64_t need = kvpage_attend_workspace_bytes(spec, n_seqs, q_heads, table_cols * spec->page_tokens);
+    if (need == 0) return KVC_E_SHAPE;
     if (ws_bytes < need) return KVC_E_SIZE;
     View qv, ov;
     if (!view_of(q, n_seqs, q_heads, spec->head_dim, qv) || !view_of(out, n_seqs, q_heads, spec->head_dim, ov))
@@ -267,7 +265,7 @@ int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, 
     a.out = rows_dev(ov);
     a.scale = scale;
     a.lse = lse;
-    a.ws = static_cast<float*>(ws);
+    a.ws = ws;
     a.status = dev_status;
     a.tail = kvc::TailArgs{layout_of(spec), static_cast<const uint8_t*>(pages), table, table_cols, table_stride, lens};
     return kvc::launch_attend(a, stream) == hipSuccess ? KVC_OK : KVC_E_HIP;
@@ -279,19 +277,20 @@ size_t kvpool_attend_workspace_bytes(const kvc_shape* shape, uint32_t n_agents, 
         !heads_ok(n_agents, shape->num_kv_heads, q_heads))
         return 0;
     if (tail_spec && (!spec_ok(tail_spec) || tail_spec->num_kv_heads != shape->num_kv_heads ||
-                      tail_spec->head_dim != shape->head_dim || max_tail_tokens >= (1u << 31)))
+                      tail_spec->head_dim != shape->head_dim || !tokens_ok(n_agents, max_tail_tokens)))
         return 0;
     if (n_agents == 0) return 256;
     const uint32_t H = shape->num_kv_heads;
-    const kvc::AttendPlan p = kvc::pool_attend_plan(H, n_agents, q_heads, shape->num_tokens);
-    if (!plan_ok(p, H)) return 0;
-    uint64_t splits = p.chunks;
+    const uint32_t d = shape->head_dim;
+    const kvc::AttendPlan p = kvc::pool_attend_plan(H, n_agents, q_heads, d, shape->num_tokens, tail_spec != nullptr);
+    if (!plan_ok(p)) return 0;
+    uint64_t bytes = p.bytes(d);
     if (tail_spec) {
-        const kvc::AttendPlan t = kvc::page_attend_plan(n_agents, H, q_heads, max_tail_tokens);
-        if (!plan_ok(t, (uint64_t)n_agents * H)) return 0;
-        splits += t.chunks;
+        const kvc::AttendPlan t = kvc::page_attend_plan(n_agents, H, q_heads, d, max_tail_tokens, true);
+        if (!plan_ok(t) || t.W + p.W >= (1ull << 31)) return 0;
+        bytes += t.bytes(d);
     }
-    return (size_t)kvc::attend_ws_bytes((uint64_t)n_agents * q_heads, splits, shape->head_dim);
+    return (size_t)bytes;
 }
 
 int kvpool_attend(const kvc_shape* shape, const void* pool, size_t pool_bytes, uint32_t layer, uint32_t n_agents,
@@ -346,7 +345,7 @@ int kvpool_attend(const kvc_shape* shape, const void* pool, size_t pool_bytes, u
     a.out = rows_dev(ov);
     a.scale = scale;
     a.lse = lse;
-    a.ws = static_cast<float*>(ws);
+    a.ws = ws;
     a.status = dev_status;
     a.pool = static_cast<const uint8_t*>(pool);
     a.L = shape->num_layers;

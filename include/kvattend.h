@@ -147,7 +147,8 @@ size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uin
  *   dev_status device int32 or NULL; KVC_DEV_BAD_PAGE, KVC_DEV_BAD_LENGTH: the
  *              sequence's output is then unspecified (lengths are clamped, a
  *              page that is none is taken as page 0)
- * q_heads * n_seqs < 2^31 / 4; table_cols * page_tokens < 2^31.
+ * q_heads * n_seqs < 2^29; table_cols * page_tokens < 2^31, and n_seqs times
+ * (table_cols * page_tokens / 128 + 1) < 2^31.
  * The 8-bit formats' weights p_t * step are rounded to binary16 after division
  * by a power of two (about the largest step) for the matrix cores, bf16's are
  * split into two bf16 terms; products and sums are binary32.
