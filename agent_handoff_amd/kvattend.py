@@ -68,25 +68,26 @@ def _spec(spec):
     return spec if isinstance(spec, kvc_pages) else kvc_pages(*spec)
 
 
-def _rows(t, n, heads, d, what):
-    """[n, heads, d] bf16 rows of a GPU tensor; strides of dimensions of size 1 are not used."""
-    if t.dtype is not torch.bfloat16:
-        raise ValueError(f"{what}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.shape != (n, heads, d):
-        raise ValueError(f"{what}: expected shape {(n, heads, d)}, got {tuple(t.shape)}")
+_BF16 = torch.bfloat16
+
+
+def _rows(t, shape, what):
+    """bf16 rows of this shape (n, heads, d) of a GPU tensor; strides of dimensions of size 1 are not used."""
+    if t.dtype is not _BF16:
+        raise ValueError(f"{what}: expected {_BF16}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     ts, hs, cs = t.stride()
-    if cs != 1 and n:
+    if cs != 1 and shape[0]:
         raise ValueError(f"{what}: the last dimension must be contiguous")
     return kvc_rows(t.data_ptr(), ts, hs)
 
 
 def _plain(t, dtype, shape, what):
-    """Address of a contiguous GPU tensor of this type and shape (None: NULL)."""
-    if t is None:
-        return None
+    """Address of a contiguous GPU tensor of this type and shape."""
     if t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor")
@@ -96,23 +97,28 @@ def _plain(t, dtype, shape, what):
 def _bytes(t, what):
     if t.dtype is not torch.uint8 or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous uint8 tensor")
-    return t.data_ptr(), t.numel()
+    return t.data_ptr()
+
+
+def _status(t):
+    return None if t is None else _plain(t, torch.int32, (1,), "dev_status")
 
 
 def _call(what, function, args, tensors, stream):
-    """function(*args, stream) with the tensors' device current."""
-    device = tensors[0].device
+    """function(*args, stream) with the tensors' device current (tensors may hold None)."""
+    device = tensors[0].get_device()  # -1: not on a GPU
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{what}: tensors are on {device} and {t.device}")
-    if device.type != "cuda":
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{what}: tensors are on different devices")
+    if device < 0:
         raise ValueError("expected a GPU tensor")
-    if device.index == torch.cuda.current_device():
-        rc = function(*args, _kv._stream(stream))
+    if device == torch._C._cuda_getDevice():
+        # the current stream's handle without a Stream object: a call takes a few microseconds in all
+        rc = function(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _kv._stream(stream))
     else:
         with torch.cuda.device(device):
             rc = function(*args, _kv._stream(stream))
-    if rc != _kv.KVC_OK:
+    if rc != 0:
         raise KvcError(rc, what)
 
 
@@ -128,19 +134,28 @@ def kvc_norm_rotate(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_we
     if (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("each input needs its output")
     n, _, d = first.shape
-    hq = 0 if q is None else q.shape[1]
-    hk = 0 if k is None else k.shape[1]
+    hq = hk = 0
+    qi = qo = ki = ko = qw = kw = at = None
+    if q is not None:
+        hq = q.shape[1]
+        qi, qo = _rows(q, (n, hq, d), "q"), _rows(q_out, (n, hq, d), "q_out")
+        if q_weight is not None:
+            qw = _plain(q_weight, _BF16, (d,), "q_weight")
+    if k is not None:
+        hk = k.shape[1]
+        ki, ko = _rows(k, (n, hk, d), "k"), _rows(k_out, (n, hk, d), "k_out")
+        if k_weight is not None:
+            kw = _plain(k_weight, _BF16, (d,), "k_weight")
     f = np.ascontiguousarray(inv_freq, np.float32)
-    rows = [None if t is None else _rows(t, n, h, d, what) for t, h, what in
-            ((q, hq, "q"), (k, hk, "k"), (q_out, hq, "q_out"), (k_out, hk, "k_out"))]
-    at = _plain(positions, torch.int64, (n,), "positions")
-    if f.size and at is None:
+    if not f.flags.writeable:
+        f = f.copy()  # only for the cheap way to its address
+    if positions is not None:
+        at = _plain(positions, torch.int64, (n,), "positions")
+    elif f.size:
         raise ValueError("positions: tensor required")
     _call("kvc_norm_rotate", _lib.kvc_norm_rotate,
-          (n, hq, hk, d, rows[0], rows[1], _plain(q_weight, torch.bfloat16, (d,), "q_weight"),
-           _plain(k_weight, torch.bfloat16, (d,), "k_weight"), eps, at, f.ctypes.data if f.size else None, f.size,
-           pairing, rows[2], rows[3]),
-          [t for t in (first, q, k, q_out, k_out, positions, q_weight, k_weight) if t is not None], stream)
+          (n, hq, hk, d, qi, ki, qw, kw, eps, at, ctypes.addressof(ctypes.c_char.from_buffer(f)) if f.size else None, f.size, pairing, qo, ko),
+          (first, q, k, q_out, k_out, positions, q_weight, k_weight), stream)
 
 
 # ------------------------------------------------------------------ paged cache
@@ -152,13 +167,13 @@ def kvpage_bytes(spec):
 def _page_copy(what, function, write, spec, pages, k, v, slots, dev_status, stream):
     s = _spec(spec)
     n = slots.numel()
-    at, size = _bytes(pages, "pages")
-    kr = _rows(k, n, s.num_kv_heads, s.head_dim, "k")
-    vr = _rows(v, n, s.num_kv_heads, s.head_dim, "v")
+    shape = (n, s.num_kv_heads, s.head_dim)
+    at, size = _bytes(pages, "pages"), pages.numel()
+    kr, vr = _rows(k, shape, "k"), _rows(v, shape, "v")
     sl = _plain(slots, torch.int64, (n,), "slots")
-    st = _plain(dev_status, torch.int32, (1,), "dev_status")
+    st = _status(dev_status)
     args = (s, at, size, n, kr, vr, sl, st) if write else (s, at, size, n, sl, kr, vr, st)
-    _call(what, function, args, (pages, k, v, slots) if dev_status is None else (pages, k, v, slots, dev_status), stream)
+    _call(what, function, args, (pages, k, v, slots, dev_status), stream)
 
 
 def kvpage_write(spec, pages, k, v, slots, dev_status=None, stream=None):
@@ -186,12 +201,16 @@ def _table(table, lens, n):
     return table.data_ptr(), table.shape[1], table.stride(0), _plain(lens, torch.int32, (n,), "lens")
 
 
-def _attend_args(q, out, lse, scale):
-    if q.dim() != 3:
+def _attend_args(q, out, lse, scale, head_dim):
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q: expected rows [sequences, heads, head_dim]")
-    n, hq, d = q.shape
-    return (n, hq, _rows(q, n, hq, d, "q"), _rows(out, n, hq, d, "out"),
-            _plain(lse, torch.float32, (n, hq), "lse"), 1.0 / math.sqrt(d) if scale is None else scale)
+    n, hq, d = shape
+    if d != head_dim:
+        raise ValueError(f"q: expected head_dim {head_dim}, got {d}")
+    return (n, hq, _rows(q, shape, "q"), _rows(out, shape, "out"),
+            None if lse is None else _plain(lse, torch.float32, (n, hq), "lse"),
+            1.0 / math.sqrt(d) if scale is None else scale)
 
 
 def kvpage_attend(spec, pages, q, table, lens, out, ws, lse=None, scale=None, dev_status=None, stream=None):
@@ -200,16 +219,12 @@ def kvpage_attend(spec, pages, q, table, lens, out, ws, lse=None, scale=None, de
     (kvpage_attend_workspace_bytes of columns * page_tokens); lse: float32
     [n, q_heads] or None; scale: 1 / sqrt(head_dim) if None."""
     s = _spec(spec)
-    n, hq, qr, outr, lp, scale = _attend_args(q, out, lse, scale)
-    if q.shape[2] != s.head_dim:
-        raise ValueError(f"q: expected head_dim {s.head_dim}, got {q.shape[2]}")
-    at, size = _bytes(pages, "pages")
-    wp, wsize = _bytes(ws, "ws")
+    n, hq, qr, outr, lp, scale = _attend_args(q, out, lse, scale, s.head_dim)
     tab, cols, stride, lens_p = _table(table, lens, n)
-    st = _plain(dev_status, torch.int32, (1,), "dev_status")
     _call("kvpage_attend", _lib.kvpage_attend,
-          (s, at, size, n, hq, qr, tab, cols, stride, lens_p, scale, outr, lp, wp, wsize, st),
-          [t for t in (pages, q, table, lens, out, ws, lse, dev_status) if t is not None], stream)
+          (s, _bytes(pages, "pages"), pages.numel(), n, hq, qr, tab, cols, stride, lens_p, scale, outr, lp,
+           _bytes(ws, "ws"), ws.numel(), _status(dev_status)),
+          (pages, q, table, lens, out, ws, lse, dev_status), stream)
 
 
 def kvpool_attend_workspace_bytes(shape, n_agents, q_heads, tail_spec=None, max_tail_tokens=0):
@@ -222,24 +237,17 @@ def kvpool_attend(shape, pool, layer, q, out, ws, tail=None, lse=None, scale=Non
     """q, out: rows [n_agents, q_heads, head_dim]; pool: uint8 tensor as
     kvpool_encode wrote it; tail: (spec, pages, table, lens) of the agents' own
     pages or None; the rest as for kvpage_attend."""
-    sh = _kv._shape(shape)
-    n, hq, qr, outr, lp, scale = _attend_args(q, out, lse, scale)
-    if q.shape[2] != sh.head_dim:
-        raise ValueError(f"q: expected head_dim {sh.head_dim}, got {q.shape[2]}")
-    at, size = _bytes(pool, "pool")
-    wp, wsize = _bytes(ws, "ws")
-    st = _plain(dev_status, torch.int32, (1,), "dev_status")
-    tensors = [t for t in (pool, q, out, ws, lse, dev_status) if t is not None]
-    tp = None
+    sh = shape if isinstance(shape, kvc_shape) else kvc_shape(*shape)
+    n, hq, qr, outr, lp, scale = _attend_args(q, out, lse, scale, sh.head_dim)
+    tensors, tp = (pool, q, out, ws, lse, dev_status), None
     if tail is not None:
         spec, pages, table, lens = tail
-        s = _spec(spec)
-        pat, psize = _bytes(pages, "tail pages")
         tab, cols, stride, lens_p = _table(table, lens, n)
-        tp = kvc_tail(ctypes.pointer(s), pat, psize, tab, cols, stride, lens_p)
-        tensors += [pages, table, lens]
+        tp = kvc_tail(ctypes.pointer(_spec(spec)), _bytes(pages, "tail pages"), pages.numel(), tab, cols, stride, lens_p)
+        tensors += (pages, table, lens)
     _call("kvpool_attend", _lib.kvpool_attend,
-          (sh, at, size, layer, n, hq, qr, scale, tp, outr, lp, wp, wsize, st), tensors, stream)
+          (sh, _bytes(pool, "pool"), pool.numel(), layer, n, hq, qr, scale, tp, outr, lp, _bytes(ws, "ws"), ws.numel(),
+           _status(dev_status)), tensors, stream)
 
 
 # ------------------------------------------------------------------ object wrapper
