@@ -67,6 +67,7 @@ struct AttendPlan {
     uint32_t row_blocks;  // units that share tokens, ceil(rows / (16 rt))
     bool whole;           // each workgroup takes one unit
     uint64_t units, W;    // W: workgroups
+    uint64_t blocks;      // blocks of tokens of all units, at most
     uint64_t slots;       // places for partial results: 16 rt rows of d sums, a maximum and a sum
     uint64_t part_bytes(uint32_t d) const { return slots * 16 * rt * (d + 2) * 4; }
     uint64_t bytes(uint32_t d) const { return align_up(part_bytes(d) + units * 8, 256); }
@@ -97,5 +98,19 @@ struct AttendArgs {
     TailArgs tail;
 };
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
+
+#ifdef __HIPCC__
+// Asks for every 64-byte line of the kernel's arguments (BYTES of them) at
+// once. They lie in host memory: read where they are first used, each line
+// costs a latency of its own, one after another.
+template <int BYTES>
+__device__ __forceinline__ void fetch_arguments() {
+    const auto* a = (const __attribute__((address_space(4))) uint32_t*)__builtin_amdgcn_kernarg_segment_ptr();
+    uint32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < BYTES / 4; i += 16) all |= a[i];
+    asm volatile("" ::"s"(all));
+}
+#endif
 
 }  // namespace kvc

@@ -273,20 +273,26 @@ constexpr int waves_per_simd(int d, int rt) { return d == 64 ? (rt == 1 ? 3 : 2)
 template <int D, int RT>
 struct Shared {
     float ml[kWaves][RT * 16][2];
-    float os[kWaves][16][D + 4];
+    float os[RT][kWaves][16][D + 4];
     uint32_t sums[kWaves];
     uint32_t found[3];  // sequence, blocks before it, its blocks
 };
 
+// Sum over the wave's lanes up to this one.
+__device__ __forceinline__ uint32_t scan_lanes(uint32_t v) {
+    const uint32_t lane = lane_id();
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) {
+        const uint32_t o = __shfl_up(v, i);
+        if (lane >= (uint32_t)i) v += o;
+    }
+    return v;
+}
+
 // Sum over the workgroup's threads before this one, and the sum of all.
 __device__ __forceinline__ uint32_t scan_threads(uint32_t v, uint32_t* sums, uint32_t& all) {
     const uint32_t lane = lane_id(), wave = threadIdx.x / kWave;
-    uint32_t s = v;
-#pragma unroll
-    for (int i = 1; i < 64; i *= 2) {
-        const uint32_t o = __shfl_up(s, i);
-        if (lane >= (uint32_t)i) s += o;
-    }
+    const uint32_t s = scan_lanes(v);
     if (lane == 63) sums[wave] = s;
     __syncthreads();
     uint32_t before = 0;
@@ -344,31 +350,46 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         hr = w % per_seq;
         left = 1u << 31;
     } else {
-        // every thread counts the blocks of a run of sequences; then the thread whose run holds the first block finds it
-        const uint32_t run = (p.n + kWaves * kWave - 1) / (kWaves * kWave);
-        const uint32_t s0 = threadIdx.x * run, s1 = s0 + run < p.n ? s0 + run : p.n;
-        uint32_t mine = 0, all;
-        for (uint32_t s = s0; s < s1; ++s) mine += blocks_of(clamp_length(src, src.lens[s]));
-        const uint32_t before = scan_threads(mine, sh.sums, all);
-        if (!share((uint64_t)wave_uniform(all) * per_seq)) return;
+        // the sequence that holds block x0, the blocks before it and its own
+        uint32_t before, mine;
         uint64_t q64;
         uint32_t part;
-        divmod_u64(x0, per_seq, q64, part);
-        const uint32_t q = (uint32_t)q64;  // sequences' blocks before
-        if (q >= before && q - before < mine) {
-            uint32_t at = before, s = s0, nb = 0;
-            for (; s < s1; ++s) {
-                nb = blocks_of(clamp_length(src, src.lens[s]));
-                if (q - at < nb) break;
-                at += nb;
+        if (p.n <= kWave) {
+            // a sequence a lane, in every wave for itself
+            const uint32_t v = lane < p.n ? blocks_of(clamp_length(src, src.lens[lane])) : 0;
+            const uint32_t up = scan_lanes(v);
+            if (!share((uint64_t)__builtin_amdgcn_readlane(up, 63) * per_seq)) return;
+            divmod_u64(x0, per_seq, q64, part);
+            b = __builtin_popcountll(__ballot(up <= (uint32_t)q64));  // sequences that end before
+            mine = __builtin_amdgcn_readlane(v, b & 63);
+            before = __builtin_amdgcn_readlane(up, b & 63) - mine;
+        } else {
+            // every thread counts a run of sequences; the one whose run holds the block then finds it
+            const uint32_t run = (p.n + kWaves * kWave - 1) / (kWaves * kWave);
+            const uint32_t s0 = threadIdx.x * run, s1 = s0 + run < p.n ? s0 + run : p.n;
+            uint32_t v = 0, all;
+            for (uint32_t s = s0; s < s1; ++s) v += blocks_of(clamp_length(src, src.lens[s]));
+            const uint32_t at0 = scan_threads(v, sh.sums, all);
+            if (!share((uint64_t)wave_uniform(all) * per_seq)) return;
+            divmod_u64(x0, per_seq, q64, part);
+            const uint32_t q = (uint32_t)q64;
+            if (q >= at0 && q - at0 < v) {
+                uint32_t at = at0, s = s0, nb = 0;
+                for (; s < s1; ++s) {
+                    nb = blocks_of(clamp_length(src, src.lens[s]));
+                    if (q - at < nb) break;
+                    at += nb;
+                }
+                sh.found[0] = s;
+                sh.found[1] = at;
+                sh.found[2] = nb;
             }
-            sh.found[0] = s;
-            sh.found[1] = at;
-            sh.found[2] = nb;
+            __syncthreads();
+            b = wave_uniform(sh.found[0]);
+            before = wave_uniform(sh.found[1]);
+            mine = wave_uniform(sh.found[2]);
         }
-        __syncthreads();
-        b = wave_uniform(sh.found[0]);
-        divmod_u64(x0 - (uint64_t)wave_uniform(sh.found[1]) * per_seq, wave_uniform(sh.found[2]), q64, off);
+        divmod_u64(x0 - (uint64_t)before * per_seq, mine, q64, off);
         hr = (uint32_t)q64;
     }
 
@@ -782,7 +803,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         return;
     }
 
-    // ---- join the waves: m and l first, then the sums, 16 rows at a time
+    // ---- join the waves: m and l first, then the sums
     const bool whole = take == nb;
     const uint32_t slot = whole ? (src.whole ? 0 : 2 * src.W) + b * per_seq + hr : off ? 2 * w : 2 * w + 1;
     if (off == 0 && threadIdx.x == 0 && !(src.whole && p.direct)) {
@@ -811,23 +832,24 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         }
     }
     __syncthreads();
-    const uint32_t row = threadIdx.x / 16, ch = threadIdx.x % 16 * NC;  // the thread's part of the outputs
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         float M = sh.ml[0][rt * 16 + c][0];
 #pragma unroll
         for (int v = 1; v < kWaves; ++v) M = fmaxf(M, sh.ml[v][rt * 16 + c][0]);
-        const float Mu = M == kNegInf ? 0.0f : M;
-        const float a = exp2_fast(m[rt] - Mu);
+        float a = exp2_fast(m[rt] - (M == kNegInf ? 0.0f : M));
+        if (HALF) a *= __builtin_amdgcn_ldexpf(1.0f, E - kWeightExp);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                float v = o[rt][n][r];
-                if (HALF) v = __builtin_amdgcn_ldexpf(v, E - kWeightExp);
-                sh.os[wave][c][channel_of<FMT, D>(g, r) + n] = v * a;
-            }
-        __syncthreads();
+            for (int n = 0; n < NC; n += 4)
+                *reinterpret_cast<f32x4*>(&sh.os[rt][wave][c][channel_of<FMT, D>(g, r) + n]) =
+                    f32x4{o[rt][n][r], o[rt][n + 1][r], o[rt][n + 2][r], o[rt][n + 3][r]} * a;
+    }
+    __syncthreads();
+    const uint32_t row = threadIdx.x / 16, ch = threadIdx.x % 16 * NC;  // the thread's part of the outputs
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
         const uint32_t r = (rb * RT + rt) * 16 + row;
         float Mr = sh.ml[0][rt * 16 + row][0];
 #pragma unroll
@@ -840,7 +862,13 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         for (int v = 0; v < kWaves; ++v) {
             sum = fmaf(sh.ml[v][rt * 16 + row][1], exp2_fast(sh.ml[v][rt * 16 + row][0] - Mru), sum);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) y[n] += sh.os[v][row][ch + n];
+            for (int n = 0; n < NC; n += 4) {
+                const f32x4 z = *reinterpret_cast<const f32x4*>(&sh.os[rt][v][row][ch + n]);
+                y[n] += z.x;
+                y[n + 1] += z.y;
+                y[n + 2] += z.z;
+                y[n + 3] += z.w;
+            }
         }
         if (FMT == kFmtPool) {
             fwht_row<NC>(y, lane);
@@ -873,13 +901,14 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                     *reinterpret_cast<float2*>(to + 16 * RT * D + 2 * (rt * 16 + row)) = make_float2(Mr, sum);
             }
         }
-        __syncthreads();
     }
+    if (left) __syncthreads();  // the next unit writes the same LDS
     }
 }
 
 template <int FMT, int D, int RT>
 __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_kernel(Common p, Source src) {
+    fetch_arguments<sizeof(Common) + sizeof(Source)>();
     __shared__ Shared<D, RT> sh;
     attend_share<FMT, D, RT>(p, src, blockIdx.x, sh);
 }
@@ -887,6 +916,7 @@ __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_k
 // A pool's workgroups and those of the tails behind it, in one launch.
 template <int FMT, int D, int RT>
 __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_both_kernel(Common p, Source pool, Source tail) {
+    fetch_arguments<sizeof(Common) + 2 * sizeof(Source)>();
     __shared__ union {
         Shared<D, RT> a;
         Shared<D, 1> b;
@@ -909,6 +939,7 @@ struct JoinParams {
 
 template <int D, int V>
 __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p) {
+    fetch_arguments<sizeof(JoinParams)>();
     constexpr int C = D / 64, U = 8;
     constexpr int RPB = kBlockThreads / kWave / V;  // rows of a workgroup
     typedef float vec __attribute__((ext_vector_type(C)));
@@ -1012,11 +1043,16 @@ constexpr uint64_t kMinBlocks = 2, kWholeTokens = 512;
 AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens, uint32_t d, uint32_t most_rt, bool direct) {
     AttendPlan a;
     a.rows = rows;
-    a.rt = rows > 16 ? most_rt : 1;
+    // two row tiles share the widening of the tokens (131071-token pool, 60
+    // rows: 80 us, with one 112), but start and join later (a 1024-token one:
+    // 11.7 us, with one 8.8): taken where every workgroup has a block to do
+    const uint64_t most_blocks = (max_tokens + kBlock - 1) / kBlock;
+    a.rt = rows > 16 && units_of_rows * ((rows + 31) / 32) * most_blocks >= 256 * waves_per_simd(d, most_rt) ? most_rt : 1;
     a.row_blocks = (rows + 16 * a.rt - 1) / (16 * a.rt);
     a.units = units_of_rows * a.row_blocks;
     const uint64_t slots = 256ull * waves_per_simd(d, a.rt);
-    const uint64_t blocks = a.units * ((max_tokens + kBlock - 1) / kBlock);
+    const uint64_t blocks = a.units * most_blocks;
+    a.blocks = blocks;
     a.whole = max_tokens <= kWholeTokens || a.units >= 8 * slots;
     uint64_t w = blocks / kMinBlocks < slots ? blocks / kMinBlocks : slots;
     if (w < 1) w = 1;

@@ -119,7 +119,9 @@ bool heads_ok(uint64_t n, uint32_t H, uint32_t Hq) {
 }
 // tokens of all sequences, in the 128-token blocks that the kernels count
 bool tokens_ok(uint64_t n, uint64_t max_tokens) { return max_tokens < (1ull << 31) && n * (max_tokens / 128 + 1) < (1ull << 31); }
-bool plan_ok(const kvc::AttendPlan& p) { return p.units < (1ull << 30) && p.slots < (1ull << 31); }
+bool plan_ok(const kvc::AttendPlan& p) {
+    return p.units < (1ull << 30) && p.slots < (1ull << 31) && p.blocks < (1ull << 40);
+}
 
 // Checks of a page source; `most`: table_cols * page_tokens.
 int check_tail(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n, const int32_t* table,

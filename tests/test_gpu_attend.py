@@ -490,3 +490,21 @@ def test_holders_attend():
     e = torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV)
     assert cache.attend(e, _i32(np.zeros((0, 2))), _i32([])).shape == e.shape
     assert pool.attend(0, e).shape == e.shape
+
+
+@pytest.mark.parametrize("seqs, heads", [(64, 2), (65, 1), (257, 1), (700, 1)])
+def test_many_ragged_sequences(seqs, heads):
+    """Work shared out over many sequences, empty ones among them, with tables wide enough that it is shared
+    (not one workgroup each)."""
+    rng = np.random.default_rng(seqs)
+    d, page = 64, 16
+    lens = rng.choice([0, 1, 127, 128, 129, 200, 640], seqs, p=[0.3, 0.2, 0.1, 0.1, 0.1, 0.15, 0.05])
+    lens[0], lens[-1] = 0, 641
+    spec = (int(np.sum(-(-lens // page))) + 1, heads, page, d, ka.KVC_PAGE_INT8)
+    store, table = random_sequences(rng, spec, lens, cols=1024 // page)
+    q = bits(rng, (seqs, 2 * heads, d))
+    out, lse = _pages_attend(spec, store.dev(), q, table, lens)
+    o, l = host_f64(out), host_f64(lse)
+    for b, n in enumerate(lens):
+        k, v = sequence(store, table, b, n)
+        check_attend(o[b], l[b], oa.f64(q)[b], k, v, 1 / math.sqrt(d), True, _steps(store), (b, n))
