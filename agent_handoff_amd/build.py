@@ -1,9 +1,12 @@
-"""Build libkvcodec.so in-tree with hipcc for gfx950 (no GPU needed)."""
+"""Build libkvcodec.so and the modules around it in-tree with hipcc for gfx950 (no GPU needed)."""
 
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,7 +18,7 @@ LIB_PATH = os.path.join(PKG, "libkvcodec.so")
 # operation; no multiply-add may be fused behind our back.
 # -packed-fp32-ops off: no packed fp32 instructions are generated.
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-ffp-contract=off", "-fno-fast-math",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
@@ -35,7 +38,7 @@ PROBE_LIB = os.path.join(PKG, "libkvprobe.so")
 def _hipcc(srcs, out, verbose, extra=()):
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     tmp = out + ".tmp"
-    cmd = [hipcc] + HIPCC_FLAGS + list(extra) + list(srcs) + ["-o", tmp]
+    cmd = [hipcc] + HIPCC_FLAGS + ([] if "-c" in extra else ["-shared"]) + list(extra) + list(srcs) + ["-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -50,10 +53,32 @@ def _hipcc(srcs, out, verbose, extra=()):
     return out
 
 
+# Python module of the operators of kvattend.h: tensors in, C calls out
+BINDING_SRC = os.path.join(PKG, "binding", "kvattend_py.cpp")
+BINDING_LIB = os.path.join(PKG, "_kvattend.so")
+
+
+def _binding(verbose):
+    import torch
+    base = os.path.dirname(torch.__file__)
+    _hipcc([BINDING_SRC], BINDING_LIB, verbose,
+           ["-isystem", os.path.join(base, "include"), "-I", sysconfig.get_paths()["include"],
+            "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+
+
 def build(verbose=False, extra=()):
-    """libkvcodec.so (the codec) and libkvprobe.so (the benchmark's probes)."""
-    _hipcc(sources(), LIB_PATH, verbose, extra)
-    _hipcc([PROBE_SRC], PROBE_LIB, verbose)
+    """libkvcodec.so (the codec), libkvprobe.so (the benchmark's probes) and _kvattend.so (a binding),
+    every source compiled anew, a few at a time."""
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(6) as pool:
+        compiled = [os.path.join(tmp, os.path.basename(s) + ".o") for s in sources()]
+        # the slowest first
+        order = sorted(zip(sources(), compiled), key=lambda x: -os.path.getsize(x[0]))
+        jobs = [pool.submit(_binding, verbose)]
+        jobs += [pool.submit(_hipcc, [s], o, verbose, ["-c"] + list(extra)) for s, o in order]
+        jobs.append(pool.submit(_hipcc, [PROBE_SRC], PROBE_LIB, verbose))
+        for j in jobs:
+            j.result()
+        _hipcc(compiled, LIB_PATH, verbose, extra)
     return LIB_PATH
 
 
