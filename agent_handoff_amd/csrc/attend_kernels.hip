@@ -965,33 +965,43 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
         from[s] = x.part + r % tile * D;
         ml[s] = x.part + tile * D + r % tile * 2;
     }
-    if (p.src[0].pool && !pool_header_ok(p.src[0], p.c.H, D)) return;
+    const bool header = !p.src[0].pool || pool_header_ok(p.src[0], p.c.H, D);
     const uint32_t n0 = parts[0], n = n0 + parts[1];
-    if (n == 0) return;  // written already
+    if (n == 0 || !header) return;  // written already, or never to be
     const auto at = [&](const float* const (&base)[2], uint32_t k) {
         const int s = k >= n0;
         const uint32_t j = s ? k - n0 : k;
         return base[s] + stride[s] * (j ? slot[s] - 1 + 2 * j : slot[s]);
     };
-    float M = kNegInf, total = 0.0f;
-    for (uint32_t k = w + V * lane; k < n; k += V * kWave) M = fmaxf(M, at(ml, k)[0]);
+    // this wave's parts w, w + V, ...: a lane has the maximum and sum of one of
+    // each 64, and the first U parts' sums are on their way before the maxima
+    // are needed (parts behind the last are read as the wave's first, or the row's)
+    const uint32_t safe = w < n ? w : 0;
+    const auto ml_of = [&](uint32_t k) { return *reinterpret_cast<const float2*>(at(ml, k < n ? k : safe)); };
+    vec x[U];
+    const auto load = [&](uint32_t base, uint32_t j) {
 #pragma unroll
-    for (int x = 1; x < 64; x *= 2) M = fmaxf(M, __shfl_xor(M, x));
+        for (int u = 0; u < U; ++u) {
+            const uint32_t k = base + V * (j + u);
+            x[u] = *reinterpret_cast<const vec*>(at(from, k < n ? k : safe) + C * lane);
+        }
+    };
+    float2 v = ml_of(w + V * lane);
+    load(w, 0);
+    float M = w + V * lane < n ? v.x : kNegInf, total = 0.0f;
+    for (uint32_t k = w + V * (lane + kWave); k < n; k += V * kWave) M = fmaxf(M, at(ml, k)[0]);
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) M = fmaxf(M, __shfl_xor(M, i));
     const float Mu = M == kNegInf ? 0.0f : M;
     vec y = 0.0f;
     for (uint32_t base = w; base < n; base += V * kWave) {
         const uint32_t k = base + V * lane;
-        const float2 v = *reinterpret_cast<const float2*>(at(ml, k < n ? k : base));
+        if (base != w) v = ml_of(k);
         const float a = exp2_fast(v.x - Mu);
         total = k < n ? fmaf(v.y, a, total) : total;
         const uint32_t rest = (n - base + V - 1) / V, count = rest < kWave ? rest : kWave;
         for (uint32_t j = 0; j < count; j += U) {
-            vec x[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t q = j + u < count ? j + u : count - 1;
-                x[u] = *reinterpret_cast<const vec*>(at(from, base + V * q) + C * lane);
-            }
+            if (j || base != w) load(base, j);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, a), (j + u) & 63));

@@ -508,3 +508,24 @@ def test_many_ragged_sequences(seqs, heads):
     for b, n in enumerate(lens):
         k, v = sequence(store, table, b, n)
         check_attend(o[b], l[b], oa.f64(q)[b], k, v, 1 / math.sqrt(d), True, _steps(store), (b, n))
+
+
+@pytest.mark.parametrize("shape, agents, group", [((1, 2, 8200, 64), 15, 4), ((1, 1, 16500, 128), 40, 2), ((1, 1, 8321, 128), 33, 4),
+                                                  ((1, 1, 9001, 64), 64, 4)])
+def test_pool_many_rows(shape, agents, group):
+    """Pools long enough that several row groups of a workgroup share the widened tokens; ends inside a step."""
+    rng = np.random.default_rng(agents)
+    k, v = synth.kv_bits(synth.WORKLOADS[3], 8, shape=shape)
+    pool = oracle.pool_encode(k, v)
+    q = bits(rng, (agents, shape[1] * group, shape[3]), 1.0)
+    out, lse = _pool_attend(shape, torch.from_numpy(pool).to(DEV), 0, q)
+    pick = [0, agents // 2, agents - 1]
+    _pool_check(host_f64(out)[pick], host_f64(lse)[pick], oa.f64(q)[pick], pool, shape, 0, 1 / math.sqrt(shape[3]), None,
+                (shape, agents))
+    spec = (agents + 2, shape[1], 16, shape[3], ka.KVC_PAGE_FP8)
+    lens = [i % 17 for i in range(agents)]
+    store, table = random_sequences(rng, spec, lens)
+    out, lse = _pool_attend(shape, torch.from_numpy(pool).to(DEV), 0, q, (spec, store.dev(), _i32(table), _i32(lens)))
+    tails = [(*sequence(store, table, a, lens[a]), _steps(store)) for a in pick]
+    _pool_check(host_f64(out)[pick], host_f64(lse)[pick], oa.f64(q)[pick], pool, shape, 0, 1 / math.sqrt(shape[3]), tails,
+                (shape, agents, "tails"))
