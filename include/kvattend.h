@@ -75,7 +75,8 @@ enum {
  * Pair j is (j, j + n_pairs) or (2j, 2j + 1) (KVC_ROPE_*); channels from
  * 2 * n_pairs on are not turned. The angle is the binary64 product, reduced
  * to a turn in binary64; everything else is binary32, rounded once to bf16.
- *   q_in, k_in     rows of n_tokens x q_heads and n_tokens x kv_heads
+ *   q_in, k_in     rows of n_tokens x q_heads and n_tokens x kv_heads;
+ *                  n_tokens < 2^26
  *   q_weight, k_weight  device bf16 [head_dim], 16-byte aligned, or NULL: no norm
  *   eps            >= 0 and finite
  *   positions      device int64 [n_tokens], 8-byte aligned (not used, may be
@@ -100,7 +101,7 @@ int kvc_norm_rotate(uint32_t n_tokens, uint32_t q_heads, uint32_t kv_heads, uint
 size_t kvpage_bytes(const kvc_pages* spec);
 
 /* Write keys and values of n_tokens tokens into their slots.
- *   k, v     rows of n_tokens x num_kv_heads
+ *   k, v     rows of n_tokens x num_kv_heads; n_tokens < 2^26
  *   slots    device int64 [n_tokens], 8-byte aligned: page * page_tokens +
  *            offset; a negative slot is skipped (padding). Slots of one call
  *            are distinct: a slot that is given twice holds codes and steps
@@ -136,9 +137,11 @@ size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uin
  * Keys and values are code * step as real numbers. A sequence of length 0
  * gives zeros and lse = -inf. What lies behind a sequence's length is not
  * used, whatever it holds.
- *   q, out     rows of n_seqs x q_heads; q_heads a multiple of num_kv_heads
- *   table      device int32, row b at table + b * table_stride, table_cols
- *              entries (only those that lens[b] reaches are read)
+ *   q, out     rows of n_seqs x q_heads (out elsewhere than q); q_heads a
+ *              multiple of num_kv_heads
+ *   table      device int32, row b at table + b * table_stride, table_cols >= 1
+ *              entries (all may be read; those that lens[b] does not reach may
+ *              hold anything). Sequences may share pages.
  *   lens       device int32 [n_seqs]
  *   scale      finite
  *   lse        device f32 [n_seqs][q_heads] or NULL: ln sum_t exp(scale * q . k_t)
@@ -147,8 +150,10 @@ size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uin
  *   dev_status device int32 or NULL; KVC_DEV_BAD_PAGE, KVC_DEV_BAD_LENGTH: the
  *              sequence's output is then unspecified (lengths are clamped, a
  *              page that is none is taken as page 0)
- * q_heads * n_seqs < 2^29; table_cols * page_tokens < 2^31, and n_seqs times
- * (table_cols * page_tokens / 128 + 1) < 2^31.
+ * n_seqs * q_heads < 2^23; table_cols * page_tokens < 2^31, and n_seqs times
+ * (table_cols * page_tokens / 128 + 1) < 2^31. Long sequences are cut up among
+ * workgroups and their parts joined by a second launch, in an order that the
+ * arguments alone decide: the same call gives the same bits.
  * The 8-bit formats' weights p_t * step are rounded to binary16 after division
  * by a power of two (about the largest step) for the matrix cores, bf16's are
  * split into two bf16 terms; products and sums are binary32.
@@ -187,7 +192,8 @@ size_t kvpool_attend_workspace_bytes(const kvc_shape* shape, uint32_t n_agents, 
  *   tail       NULL: the pool alone
  *   dev_status device int32 or NULL; KVC_DEV_BAD_HEADER (nothing is written),
  *              KVC_DEV_BAD_PAGE, KVC_DEV_BAD_LENGTH
- * The other arguments, roundings and errors are those of kvpage_attend. */
+ * The other arguments, roundings and errors are those of kvpage_attend
+ * (n_agents * q_heads < 2^23). */
 int kvpool_attend(const kvc_shape* shape, const void* pool, size_t pool_bytes, uint32_t layer, uint32_t n_agents,
                   uint32_t q_heads, const kvc_rows* q, float scale, const kvc_tail* tail, const kvc_rows* out,
                   float* lse, void* ws, size_t ws_bytes, int32_t* dev_status, hipStream_t stream);

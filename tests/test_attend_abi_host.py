@@ -169,7 +169,7 @@ def test_page_attend_refusals():
                 {"ws": None}):
         assert _attend(**bad) == kv.KVC_E_NULL, bad
     for bad in ({"spec": ka.kvc_pages(6, HK, 16, 96, 1)}, {"hq": 7}, {"hq": 0}, {"cols": 0}, {"cols": 1 << 27},
-                {"n": 1 << 27}, {"q": rows(2 * A, ts=1 << 62)}):
+                {"n": 1 << 20}, {"q": rows(2 * A, ts=1 << 62)}):
         assert _attend(**bad) == kv.KVC_E_SHAPE, bad
     for bad in ({"scale": float("inf")}, {"scale": float("nan")}, {"stride": 3}, {"stride": 1 << 31}):
         assert _attend(**bad) == kv.KVC_E_RANGE, bad
