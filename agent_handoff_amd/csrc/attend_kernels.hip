@@ -23,7 +23,7 @@
 // holds 178 bytes for a token's key and value of 128 channels instead of 264, and
 // many rows share them: there the vector instructions of widening and softmax
 // and the matrix instructions, which a SIMD issues one at a time, bound it
-// (131071 tokens, 8 kv heads of 128, 60 rows: 80 us, 2.3 TB/s; VALU busy 79 % of
+// (131071 tokens, 8 kv heads of 128, 60 rows: 82 us, 2.3 TB/s; VALU busy 79 % of
 // the CUs' time, matrix cores 20 %). Short calls are bound by latency: three
 // dependent reads, a tile, the join of four waves: 6 us.
 //
@@ -43,7 +43,11 @@
 // one alone (2^-9) would show next to the output's own rounding.
 //
 // m is moved only when a tile's maximum passes it by kSlack (exponents of 2):
-// most tiles then need no exchange between lanes and no rescaling.
+// most tiles then need no exchange between lanes and no rescaling. It is kept as
+// the product K q, before the row's factor: (product - m) * factor is 0 at the
+// maximum however large the logits are, where a fused product * factor - m (a
+// pool of 131071 tokens: 1 us less of 82) leaves the rounding of m, which
+// passes binary16's range at logits of 2^25.
 #include "attend.h"
 #include "codebook.h"
 #include "kernels_common.h"
@@ -578,15 +582,17 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         }
 
         // running state
+        // m: the running maximum before the row's factor (0 while there is none);
+        // past: the maximum that moves it (-inf while there is none)
         f32x4 o[RT][NC];
-        float m[RT], mu[RT], l[RT];
+        float m[RT], past[RT], l[RT];
         int E = kMinExp;  // exponent taken out of the weights (HALF)
         float elimit = __builtin_amdgcn_ldexpf(1.0f, kMinExp);  // 2^E, which no step so far has reached
         float wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - kMinExp);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            m[rt] = kNegInf;
-            mu[rt] = 0.0f;
+            m[rt] = 0.0f;
+            past[rt] = kNegInf;
             l[rt] = 0.0f;
 #pragma unroll
             for (int n = 0; n < NC; ++n) o[rt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -725,8 +731,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                 top[rt] = y[rt][0];
 #pragma unroll
                 for (int j = 1; j < 8; ++j) top[rt] = fmaxf(top[rt], y[rt][j]);
-                top[rt] *= qscale[rt];
-                move |= top[rt] > m[rt] + kSlack;
+                move |= top[rt] > past[rt];
             }
             float big = 0.0f;
             if (HALF) {
@@ -752,10 +757,11 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                 for (int rt = 0; rt < RT; ++rt) {
                     float x2 = fmaxf(top[rt], __shfl_xor(top[rt], 16));
                     x2 = fmaxf(x2, __shfl_xor(x2, 32));
-                    const float nm = fmaxf(m[rt], x2);
-                    const float a = nm == kNegInf ? 1.0f : exp2_fast(m[rt] - nm);
-                    m[rt] = nm;
-                    mu[rt] = nm == kNegInf ? 0.0f : nm;
+                    const bool none = past[rt] == kNegInf;
+                    const float nm = none ? x2 : fmaxf(m[rt], x2);
+                    const float a = none ? 1.0f : exp2_fast((m[rt] - nm) * qscale[rt]);
+                    m[rt] = nm == kNegInf ? 0.0f : nm;
+                    past[rt] = nm == kNegInf ? kNegInf : nm + kSlack * __builtin_amdgcn_rcpf(qscale[rt]);
                     l[rt] *= a;
 #pragma unroll
                     for (int n = 0; n < NC; ++n) o[rt][n] *= a;
@@ -770,7 +776,8 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                 float w[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    float e = exp2_fast(fmaf(y[rt][j], qscale[rt], -mu[rt]));
+                    // difference first: exact near the maximum, however large the logits
+                    float e = exp2_fast((y[rt][j] - m[rt]) * qscale[rt]);
                     // by the token, not by its logit: -inf * 0 has no sign
                     if (PART) e = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? e : 0.0f;
                     l[rt] += e;
@@ -815,7 +822,10 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             return;
         }
 
-        // ---- join the waves: m and l first, then the sums
+        // ---- join the waves: m (as a logit) and l first, then the sums
+        float top[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) top[rt] = past[rt] == kNegInf ? kNegInf : m[rt] * qscale[rt];
         const bool whole = take == nb;
         const uint32_t slot = whole ? (src.whole ? 0 : 2 * src.W) + b * per_seq + hr : off ? 2 * w : 2 * w + 1;
         if (off == 0 && threadIdx.x == 0 && !(src.whole && p.direct)) {
@@ -839,7 +849,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
             if (g == 0) {
-                sh.ml[wave][rt * 16 + c][0] = m[rt];
+                sh.ml[wave][rt * 16 + c][0] = top[rt];
                 sh.ml[wave][rt * 16 + c][1] = s;
             }
         }
@@ -849,7 +859,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             float M = sh.ml[0][rt * 16 + c][0];
 #pragma unroll
             for (int v = 1; v < kWaves; ++v) M = fmaxf(M, sh.ml[v][rt * 16 + c][0]);
-            float a = exp2_fast(m[rt] - (M == kNegInf ? 0.0f : M));
+            float a = exp2_fast(top[rt] - (M == kNegInf ? 0.0f : M));
             if (HALF) a *= __builtin_amdgcn_ldexpf(1.0f, E - kWeightExp);
 #pragma unroll
             for (int r = 0; r < 4; ++r)

@@ -136,6 +136,9 @@ int check_tail(const kvc_pages* spec, const void* pages, size_t pages_bytes, uin
     return KVC_OK;
 }
 
+// finite, and so in powers of two
+bool scale_ok(float scale) { return isfinite(scale * 1.4426950408889634f); }
+
 struct Span {
     const void* p;
     uint64_t n;
@@ -230,7 +233,7 @@ int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, 
                   int32_t* dev_status, hipStream_t stream) {
     if (!spec) return KVC_E_NULL;
     if (!spec_ok(spec) || !heads_ok(n_seqs, spec->num_kv_heads, q_heads)) return KVC_E_SHAPE;
-    if (!isfinite(scale)) return KVC_E_RANGE;
+    if (!scale_ok(scale)) return KVC_E_RANGE;
     if (n_seqs == 0) return KVC_OK;
     if (!q || !out || !q->data || !out->data || !ws) return KVC_E_NULL;
     const int rc = check_tail(spec, pages, pages_bytes, n_seqs, table, table_cols, table_stride, lens);
@@ -302,7 +305,7 @@ int kvpool_attend(const kvc_shape* shape, const void* pool, size_t pool_bytes, u
     if (!kvc::pool_shape_ok(shape->num_layers, shape->num_kv_heads, shape->num_tokens, shape->head_dim) ||
         !heads_ok(n_agents, shape->num_kv_heads, q_heads))
         return KVC_E_SHAPE;
-    if (layer >= shape->num_layers || !isfinite(scale)) return KVC_E_RANGE;
+    if (layer >= shape->num_layers || !scale_ok(scale)) return KVC_E_RANGE;
     if (n_agents == 0) return KVC_OK;
     if (!pool || !q || !out || !q->data || !out->data || !ws) return KVC_E_NULL;
     const uint32_t H = shape->num_kv_heads, d = shape->head_dim;

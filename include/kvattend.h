@@ -143,7 +143,7 @@ size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uin
  *              entries (all may be read; those that lens[b] does not reach may
  *              hold anything). Sequences may share pages.
  *   lens       device int32 [n_seqs]
- *   scale      finite
+ *   scale      finite, and so times log2(e)
  *   lse        device f32 [n_seqs][q_heads] or NULL: ln sum_t exp(scale * q . k_t)
  *   ws         device workspace, 256-byte aligned, >=
  *              kvpage_attend_workspace_bytes(spec, n_seqs, q_heads, table_cols * page_tokens)
@@ -156,7 +156,12 @@ size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uin
  * arguments alone decide: the same call gives the same bits.
  * The 8-bit formats' weights p_t * step are rounded to binary16 after division
  * by a power of two (about the largest step) for the matrix cores, bf16's are
- * split into two bf16 terms; products and sums are binary32.
+ * split into two bf16 terms; products and sums are binary32. So logits, and the
+ * weighted sums before they are divided by the weights' (at most 8 times the
+ * tokens times the largest value), have to stay in binary32's range, and keys
+ * of the 8-bit formats below 2^105. Where all logits of a row are -inf, the row
+ * is as that of an empty sequence; a NaN in a query or in a key or value that
+ * its length reaches gives NaN.
  * Errors: KVC_E_NULL, KVC_E_SHAPE, KVC_E_RANGE, KVC_E_SIZE, KVC_E_ALIGN,
  * KVC_E_ALIAS, KVC_E_HIP. */
 int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs, uint32_t q_heads,

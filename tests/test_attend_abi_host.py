@@ -260,3 +260,8 @@ def test_binding_refuses_wrong_tensors():
         ka.kvpool_attend((1, 2, 8, 128), pages, 0, q, q.clone(), ws)
     with pytest.raises(ValueError):
         ka.PagedKV(4, 2, 24, 64, device="cpu")
+
+
+def test_scales_that_powers_of_two_cannot_hold():
+    assert _attend(scale=3e38) == kv.KVC_E_RANGE
+    assert _pool(scale=-3e38) == kv.KVC_E_RANGE

@@ -529,3 +529,79 @@ def test_pool_many_rows(shape, agents, group):
     tails = [(*sequence(store, table, a, lens[a]), _steps(store)) for a in pick]
     _pool_check(host_f64(out)[pick], host_f64(lse)[pick], oa.f64(q)[pick], pool, shape, 0, 1 / math.sqrt(shape[3]), tails,
                 (shape, agents, "tails"))
+
+
+def _hot(rng, n, heads, group, seqs, d, at):
+    """Queries of 2^11..2^12 a channel and keys [n, heads, d] of about 2^10, one of which (token at) has the
+    queries' signs at 2^14: logits up to 10^9, that token's far above the rest."""
+    sign = np.where(rng.random(d) < 0.5, -1.0, 1.0)
+    k = rng.standard_normal((n, heads, d)) * 2.0 ** 10
+    if at is not None:
+        k[at] = sign * 2.0 ** 14 * (1 + rng.random((heads, d)) / 8)
+    q = sign * 2.0 ** 11 * (1 + rng.random((seqs, heads * group, d)))
+    return synth.f32_to_bf16_bits(q.astype(np.float32)), synth.f32_to_bf16_bits(k.astype(np.float32))
+
+
+def _far(q, keys, scale, at):
+    """Every row's logit at `at` passes all others by far more than what logits may be off."""
+    group = q.shape[0] // keys.shape[0]
+    for h in range(q.shape[0]):
+        x = keys[h // group] @ q[h] * scale
+        rest = np.delete(x, at)
+        assert x[at] - np.max(rest, initial=-np.inf) > 100 + 2 * np.max(logit_bound(q, keys, scale))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n, at", [(1, 0), (200, 3), (700, 699), (5000, 2500)])
+def test_logits_of_a_thousand_million(fmt, n, at):
+    """One token takes all the weight (its difference to the maximum is 0 whatever the maximum's rounding):
+    the output is its value, each rounding as for a single token."""
+    rng = np.random.default_rng(n)
+    d, heads, group, page = 128, 2, 4, 16
+    spec = (-(-n // page) + 1, heads, page, d, fmt)
+    store, table = random_sequences(rng, spec, [n])
+    q, k = _hot(rng, n, heads, group, 1, d, at)
+    t = np.arange(n)
+    store.put(k, bits(rng, (n, heads, d)), table[0, t // page] * page + t % page)
+    out, lse = _pages_attend(spec, store.dev(), q, table, [n])
+    keys, values = sequence(store, table, 0, n)
+    q64, scale = oa.f64(q)[0], 1 / math.sqrt(d)
+    _far(q64, keys, scale, at)
+    want = np.repeat(values[:, at], group, axis=0)
+    tol = U_BF16 if fmt == 0 else U_BF16 + 1.01 * 2.0 ** -11
+    assert np.all(np.abs(host_f64(out)[0] - want) <= np.abs(want) * tol + 1e-30)
+    wl = oa.attend(q64, keys, values, scale)[1]
+    assert np.all(np.abs(host_f64(lse)[0] - wl) <= lse_bound(wl, logit_bound(q64, keys, scale), n))
+
+
+@pytest.mark.parametrize("d, T, group", [(128, 300, 4), (64, 9000, 2)])
+def test_pool_logits_of_a_thousand_million(d, T, group):
+    """The same with a pool, where the first agent's token lies in the pool and the second one's in its tail."""
+    rng = np.random.default_rng(d)
+    heads, page, lens = 2, 16, [5, 40]
+    shape, spec = (1, heads, T, d), (6, heads, page, d, 1)
+    q, k = _hot(rng, T, heads, group, 2, d, T // 2)
+    v = bits(rng, (heads, T, d))
+    pool = oracle.pool_encode(k.transpose(1, 0, 2)[None].copy(), v[None])
+    store, table = random_sequences(rng, spec, lens)
+    q[1] ^= 0x8000  # the second agent turns away from the pool's token ...
+    tk = rng.standard_normal((lens[1], heads, d)).astype(np.float32)
+    tk[7] = -oa.f64(k[T // 2])  # ... towards one of its own
+    t = np.arange(lens[1])
+    store.put(synth.f32_to_bf16_bits(tk), bits(rng, (lens[1], heads, d)), table[1, t // page] * page + t % page)
+    out, lse = _pool_attend(shape, torch.from_numpy(pool).to(DEV), 0, q, (spec, store.dev(), _i32(table), _i32(lens)))
+    keys, rot = oa.pool_rotated(pool, shape, 0)
+    vals, scale = rot @ oa.hadamard(d) / math.sqrt(d), 1 / math.sqrt(d)
+    for a, at in ((0, T // 2), (1, T + 7)):
+        k2, v2 = sequence(store, table, a, lens[a])
+        kk, vv, q64 = np.concatenate([keys, k2], 1), np.concatenate([vals, v2], 1), oa.f64(q)[a]
+        _far(q64, kk, scale, at)
+        want = np.repeat(vv[:, at], group, axis=0)
+        if a == 0:  # weight and level rounded to binary16 in rotated space, binary32 sums of d
+            b = np.repeat(np.sum(np.abs(rot[:, at]), -1), group)[:, None] / math.sqrt(d) * (2.01 * 2.0 ** -11 + 2.0 ** -20)
+        else:
+            b = np.abs(want) * 1.01 * 2.0 ** -11
+        b = b + U_BF16 * (np.abs(want) + b) + 1e-30
+        assert np.all(np.abs(host_f64(out)[a] - want) <= b)
+        wl = oa.attend(q64, kk, vv, scale)[1]
+        assert np.all(np.abs(host_f64(lse)[a] - wl) <= lse_bound(wl, logit_bound(q64, kk, scale), T + lens[a]))
