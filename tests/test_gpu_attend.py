@@ -605,3 +605,21 @@ def test_pool_logits_of_a_thousand_million(d, T, group):
         assert np.all(np.abs(host_f64(out)[a] - want) <= b)
         wl = oa.attend(q64, kk, vv, scale)[1]
         assert np.all(np.abs(host_f64(lse)[a] - wl) <= lse_bound(wl, logit_bound(q64, kk, scale), T + lens[a]))
+
+
+def test_pool_offsets_past_32_bits():
+    """The second layer of a pool of 6 GB gives the bits of the same layer in a pool of its own."""
+    H, T, d, n = 4, (1 << 22) - 3, 128, 2
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    k, v = (torch.empty(2, H, T, d, dtype=torch.bfloat16, device=DEV).normal_(generator=gen) for _ in range(2))
+    q = torch.empty(n, 2 * H, d, dtype=torch.bfloat16, device=DEV).normal_(0, 2, generator=gen)
+    got = []
+    for shape, kk, vv, layer in (((2, H, T, d), k, v, 1), ((1, H, T, d), k[1:], v[1:], 0)):
+        pool = torch.empty(kv.kvpool_bytes(shape), dtype=torch.uint8, device=DEV)
+        ws = torch.empty(kv.kvpool_workspace_bytes(shape), dtype=torch.uint8, device=DEV)
+        kv.kvpool_encode(shape, kk, vv, pool, ws, _status())
+        out, lse = _pool_attend(shape, pool, layer, to_host(q))
+        got.append((out, lse))
+    assert pool.numel() * 2 > 1 << 32
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert bool(torch.isfinite(got[0][0]).all())
