@@ -23,13 +23,13 @@
 // holds 178 bytes for a token's key and value of 128 channels instead of 264, and
 // many rows share them: there the vector instructions of widening and softmax
 // and the matrix instructions, which a SIMD issues one at a time, bound it
-// (131071 tokens, 8 kv heads of 128, 60 rows: 82 us, 2.3 TB/s; VALU busy 79 % of
-// the CUs' time, matrix cores 20 %). Short calls are bound by latency: three
+// (131071 tokens, 8 kv heads of 128, 60 rows: 79 us, 2.4 TB/s; of a SIMD's
+// cycles the VALU takes 70 %, the matrix core 17 %). Short calls are bound by latency: three
 // dependent reads, a tile, the join of four waves: 6 us.
 //
 // Tried and left out: keeping two tiles of loads in registers (spills, or the same
 // time); sharing widened tokens among the waves through LDS (a quarter fewer
-// vector instructions, the same 77 us); joining parts in the workgroup that ends a
+// vector instructions, the same time); joining parts in the workgroup that ends a
 // unit (the agent-scope fences write back and drop L2: 20 -> 78 us).
 //
 // Number formats: int8 and e4m3 codes, and the pool's levels, are widened to
@@ -43,11 +43,11 @@
 // one alone (2^-9) would show next to the output's own rounding.
 //
 // m is moved only when a tile's maximum passes it by kSlack (exponents of 2):
-// most tiles then need no exchange between lanes and no rescaling. It is kept as
-// the product K q, before the row's factor: (product - m) * factor is 0 at the
-// maximum however large the logits are, where a fused product * factor - m (a
-// pool of 131071 tokens: 1 us less of 82) leaves the rounding of m, which
-// passes binary16's range at logits of 2^25.
+// most tiles then need no exchange between lanes and no rescaling. Logits are
+// rounded products of K q with the row's factor, so the maximum's difference to m
+// is exact however large they are: a fused product * factor - m leaves the rounding
+// of m, which passes binary16's range at logits of 2^25 (and costs the same: the
+// compiler makes matrix results canonical before it compares them).
 #include "attend.h"
 #include "codebook.h"
 #include "kernels_common.h"
@@ -174,6 +174,14 @@ struct Raw<kFmtPool, D> {
     uint32_t v[2][3];  // one word of each plane of one token per run of 16 (see gather_bytes)
     uint2 vs[2];       // four binary16 sizes per run
 };
+
+// a where the mask has ones, b elsewhere; one instruction, which the compiler
+// would take apart again for the bits that are used in the end.
+__device__ __forceinline__ uint32_t merge(uint32_t mask, uint32_t a, uint32_t b) {
+    uint32_t r = (a & mask) | (b & ~mask);
+    asm("" : "+v"(r));
+    return r;
+}
 
 // Bytes of four tokens, from four lanes that each hold a word of one: lane
 // 4 b + w of 16 gets byte b of word w of tokens 0..3, whose words are in
@@ -582,17 +590,15 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         }
 
         // running state
-        // m: the running maximum before the row's factor (0 while there is none);
-        // past: the maximum that moves it (-inf while there is none)
         f32x4 o[RT][NC];
-        float m[RT], past[RT], l[RT];
+        float m[RT], mu[RT], l[RT];
         int E = kMinExp;  // exponent taken out of the weights (HALF)
         float elimit = __builtin_amdgcn_ldexpf(1.0f, kMinExp);  // 2^E, which no step so far has reached
         float wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - kMinExp);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            m[rt] = 0.0f;
-            past[rt] = kNegInf;
+            m[rt] = kNegInf;
+            mu[rt] = 0.0f;
             l[rt] = 0.0f;
 #pragma unroll
             for (int n = 0; n < NC; ++n) o[rt][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -650,14 +656,16 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
 #pragma unroll
                     for (int q = 0; q < 3; ++q) {
                         pl[q] = gather_bytes(x.v[i][q], sel_a, sel_b);
-                        if (D == 64) pl[q] = pl[q] >> ((c >> 1 & 1) * 4) & 0x0F0F0F0Fu;
+                        if (D == 64) pl[q] >>= (c >> 1 & 1) * 4;  // its nibble: what comes in above is not used
                     }
+                    // bits of two planes next to one another, for even and odd channels
+                    const uint32_t even = merge(0x55555555u, pl[0], pl[1] << 1), odd = merge(0x55555555u, pl[0] >> 1, pl[1]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        // the codes of channels k and k + 4, a nibble each
-                        uint32_t code = pl[0] >> k & 0x11111111u;
-                        code |= (k >= 1 ? pl[1] >> (k >= 1 ? k - 1 : 0) : pl[1] << 1) & 0x22222222u;
-                        code |= (k >= 2 ? pl[2] >> (k >= 2 ? k - 2 : 0) : pl[2] << (k >= 2 ? 0 : 2 - k)) & 0x44444444u;
+                        // the codes of channels k and k + 4: the low three bits of each nibble
+                        const uint32_t two = k % 2 ? odd : even;
+                        const uint32_t code = merge(0x33333333u, k < 2 ? two : two >> 2,
+                                                    k < 2 ? pl[2] << (k < 2 ? 2 - k : 0) : pl[2] >> (k < 2 ? 0 : k - 2));
 #pragma unroll
                         for (int n = k; n < NC; n += 4) {
                             const uint32_t sel = (n == k ? code : code >> 4) & 0x07070707u;
@@ -717,21 +725,21 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             }
             if (t_next < end) load(t_next, it + 1, x);
 
-            // logits (before the row's factor), their maxima, and the steps' largest
+            // logits (in powers of two), their maxima, and the steps' largest
             float y[RT][8], top[RT];
             bool move = false;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    y[rt][j] = s[rt][j >> 2][j & 3];
+                    y[rt][j] = s[rt][j >> 2][j & 3] * qscale[rt];
                     if constexpr (FMT == kFmtInt8 || FMT == kFmtFp8) y[rt][j] *= ks[j];
                     if (PART) y[rt][j] = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? y[rt][j] : kNegInf;
                 }
                 top[rt] = y[rt][0];
 #pragma unroll
                 for (int j = 1; j < 8; ++j) top[rt] = fmaxf(top[rt], y[rt][j]);
-                move |= top[rt] > past[rt];
+                move |= top[rt] > m[rt] + kSlack;
             }
             float big = 0.0f;
             if (HALF) {
@@ -740,31 +748,27 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                 move |= big >= elimit;
             }
             if (__ballot(move) != 0) {
+                float shrink = 1.0f;
                 if (HALF) {
                     big = fmaxf(big, __shfl_xor(big, 16));
                     big = fmaxf(big, __shfl_xor(big, 32));
                     const int e = __builtin_amdgcn_frexp_expf(big), ne = big >= elimit ? e : E;
-                    const float a = __builtin_amdgcn_ldexpf(1.0f, E - ne);
+                    shrink = __builtin_amdgcn_ldexpf(1.0f, E - ne);
                     E = ne;
                     elimit = __builtin_amdgcn_ldexpf(1.0f, E);
                     wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - E);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                        for (int n = 0; n < NC; ++n) o[rt][n] *= a;
                 }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     float x2 = fmaxf(top[rt], __shfl_xor(top[rt], 16));
                     x2 = fmaxf(x2, __shfl_xor(x2, 32));
-                    const bool none = past[rt] == kNegInf;
-                    const float nm = none ? x2 : fmaxf(m[rt], x2);
-                    const float a = none ? 1.0f : exp2_fast((m[rt] - nm) * qscale[rt]);
-                    m[rt] = nm == kNegInf ? 0.0f : nm;
-                    past[rt] = nm == kNegInf ? kNegInf : nm + kSlack * __builtin_amdgcn_rcpf(qscale[rt]);
+                    const float nm = fmaxf(m[rt], x2);
+                    const float a = nm == kNegInf ? 1.0f : exp2_fast(m[rt] - nm);
+                    m[rt] = nm;
+                    mu[rt] = nm == kNegInf ? 0.0f : nm;
                     l[rt] *= a;
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) o[rt][n] *= a;
+                    for (int n = 0; n < NC; ++n) o[rt][n] *= a * shrink;
                 }
             }
             if (HALF) {
@@ -776,8 +780,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                 float w[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    // difference first: exact near the maximum, however large the logits
-                    float e = exp2_fast((y[rt][j] - m[rt]) * qscale[rt]);
+                    float e = exp2_fast(y[rt][j] - mu[rt]);
                     // by the token, not by its logit: -inf * 0 has no sign
                     if (PART) e = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? e : 0.0f;
                     l[rt] += e;
@@ -822,10 +825,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             return;
         }
 
-        // ---- join the waves: m (as a logit) and l first, then the sums
-        float top[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) top[rt] = past[rt] == kNegInf ? kNegInf : m[rt] * qscale[rt];
+        // ---- join the waves: m and l first, then the sums
         const bool whole = take == nb;
         const uint32_t slot = whole ? (src.whole ? 0 : 2 * src.W) + b * per_seq + hr : off ? 2 * w : 2 * w + 1;
         if (off == 0 && threadIdx.x == 0 && !(src.whole && p.direct)) {
@@ -849,7 +849,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
             if (g == 0) {
-                sh.ml[wave][rt * 16 + c][0] = top[rt];
+                sh.ml[wave][rt * 16 + c][0] = m[rt];
                 sh.ml[wave][rt * 16 + c][1] = s;
             }
         }
@@ -859,7 +859,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             float M = sh.ml[0][rt * 16 + c][0];
 #pragma unroll
             for (int v = 1; v < kWaves; ++v) M = fmaxf(M, sh.ml[v][rt * 16 + c][0]);
-            float a = exp2_fast(top[rt] - (M == kNegInf ? 0.0f : M));
+            float a = exp2_fast(m[rt] - (M == kNegInf ? 0.0f : M));
             if (HALF) a *= __builtin_amdgcn_ldexpf(1.0f, E - kWeightExp);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -1081,7 +1081,7 @@ AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens,
     a.rows = rows;
     // Two row tiles of a wave share the widening of the tokens, but start and
     // join later: taken where every workgroup has a block to do. Pool, 60 rows,
-    // heads of 128: 131071 tokens 80 us, with one tile 112; 1024 tokens 11.7 and
+    // heads of 128: 131071 tokens 79 us, with one tile 112; 1024 tokens 11.7 and
     // 8.8. Pages, 8 sequences of 8192, int8: heads of 64, 32 rows 12.2 and 13.8;
     // heads of 128, 32 rows 18.2 and 16.4 (registers), 48 rows 22.0 and 23.9.
     const uint64_t most_blocks = (max_tokens + kBlock - 1) / kBlock;

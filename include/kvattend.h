@@ -158,10 +158,9 @@ size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uin
  * by a power of two (about the largest step) for the matrix cores, bf16's are
  * split into two bf16 terms; products and sums are binary32. So logits, and the
  * weighted sums before they are divided by the weights' (at most 8 times the
- * tokens times the largest value), have to stay in binary32's range, and keys
- * of the 8-bit formats below 2^105. Where all logits of a row are -inf, the row
- * is as that of an empty sequence; a NaN in a query or in a key or value that
- * its length reaches gives NaN.
+ * tokens times the largest value), have to stay in binary32's range. Where all
+ * logits of a row are -inf, the row is as that of an empty sequence; a NaN in a
+ * query or in a key or value that its length reaches gives NaN.
  * Errors: KVC_E_NULL, KVC_E_SHAPE, KVC_E_RANGE, KVC_E_SIZE, KVC_E_ALIGN,
  * KVC_E_ALIAS, KVC_E_HIP. */
 int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs, uint32_t q_heads,

@@ -623,3 +623,19 @@ def test_pool_offsets_past_32_bits():
     assert pool.numel() * 2 > 1 << 32
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     assert bool(torch.isfinite(got[0][0]).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("e", [-90, 110])
+def test_keys_far_from_their_queries_in_size(fmt, e):
+    """Keys of about 2^e and queries of about 2^-e: ordinary logits."""
+    rng = np.random.default_rng(e + 100)
+    d, n, page, heads = 128, 150, 32, 2
+    spec = (6, heads, page, d, fmt)
+    store, table = random_sequences(rng, spec, [n])
+    t = np.arange(n)
+    store.put(bits(rng, (n, heads, d), 2.0 ** e), bits(rng, (n, heads, d)), table[0, t // page] * page + t % page)
+    q = bits(rng, (1, 3 * heads, d), 2.0 ** -e)
+    out, lse = _pages_attend(spec, store.dev(), q, table, [n])
+    k, v = sequence(store, table, 0, n)
+    check_attend(host_f64(out)[0], host_f64(lse)[0], oa.f64(q)[0], k, v, 1 / math.sqrt(d), fmt != 0, _steps(store), e)
