@@ -73,6 +73,7 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
 
 struct Common {
     RowsDev q, out;
@@ -542,45 +543,40 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         float qscale[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            uint32_t(&z)[KS][4] = qw[rt];
-            const uint32_t r = (rb * RT + rt) * 16 + c;
+            const uint32_t(&z)[KS][4] = qw[rt];
             // a row that is none is a zero; the factor of a row's logits is kept
             // >= 0, so that the largest product is the largest logit: a negative
             // scale turns the queries' signs
-            const uint32_t turn = p.scale_log2 < 0.0f ? 0x80008000u : 0;
+            const bool live = (rb * RT + rt) * 16 + c < src.rows;
             qscale[rt] = fabsf(p.scale_log2);
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[s][i] = r < src.rows ? z[s][i] ^ turn : 0;
             if (HALF) {
-                uint32_t big = 0;
-#pragma unroll
-                for (int s = 0; s < KS; ++s)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t lo = z[s][i] & 0x7FFFu, hi = (z[s][i] >> 16) & 0x7FFFu;
-                        big = lo > big ? lo : big;
-                        big = hi > big ? hi : big;
-                    }
-                uint32_t other = __shfl_xor(big, 16);
-                big = other > big ? other : big;
-                other = __shfl_xor(big, 32);
-                big = other > big ? other : big;
-                // largest magnitude to [2^14, 2^15); Inf and NaN stay what they are
-                const int e = (big == 0 || big >= 0x7F80u) ? 0 : 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(big << 16));
+                ushort2_t top = 0;
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        qf[rt][s][i] = pack_half2(__builtin_amdgcn_ldexpf(bf16_lo(z[s][i]), e),
-                                                  __builtin_amdgcn_ldexpf(bf16_hi(z[s][i]), e));
-                qscale[rt] = __builtin_amdgcn_ldexpf(qscale[rt], -e);
-            } else {
+                        top = __builtin_elementwise_max(top, __builtin_bit_cast(ushort2_t, z[s][i] & 0x7FFF7FFFu));
+                uint32_t big = top.x > top.y ? top.x : top.y;
+                uint32_t other = __shfl_xor(big, 16);
+                big = other > big ? other : big;
+                other = __shfl_xor(big, 32);
+                big = other > big ? other : big;
+                // largest magnitude to [2^14, 2^15), by 2^112 at most, which brings the smallest
+                // bf16 into range; Inf and NaN stay what they are
+                int e = (big == 0 || big >= 0x7F80u) ? 0 : 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(big << 16));
+                e = e < 112 ? e : 112;
+                const float f = live ? copysignf(__builtin_amdgcn_ldexpf(1.0f, e), p.scale_log2) : 0.0f;
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) qf[rt][s][i] = z[s][i];
+                    for (int i = 0; i < 4; ++i) qf[rt][s][i] = pack_half2(bf16_lo(z[s][i]) * f, bf16_hi(z[s][i]) * f);
+                qscale[rt] = __builtin_amdgcn_ldexpf(qscale[rt], -e);
+            } else {
+                const uint32_t turn = p.scale_log2 < 0.0f ? 0x80008000u : 0;
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qf[rt][s][i] = live ? z[s][i] ^ turn : 0;
             }
         }
         if (FMT == kFmtPool) {
