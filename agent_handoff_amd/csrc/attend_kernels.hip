@@ -99,6 +99,8 @@ struct Source {
     const uint8_t* pool;
     PoolLayout lay;
     uint32_t L, T, layer;
+    uint32_t more;  // shares of `each` blocks, the first `more` of them one larger
+    uint64_t each;
     // pages
     const uint8_t* pages;
     const int32_t* table;
@@ -346,14 +348,17 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
     // shares of `each` blocks, the first `more` of them one larger; this one begins at x0
     uint64_t each = 0, x0 = 0, left;
     uint32_t more = 0;
+    const auto begin_share = [&]() {
+        x0 = each * w + (w < more ? w : more);
+        left = each + (w < more);
+    };
     const auto share = [&](uint64_t total) {
         // no empty shares
         if (w >= total) return false;
         const uint32_t W = total < src.W ? (uint32_t)total : src.W;
         if (w >= W) return false;
         divmod_u64(total, W, each, more);
-        x0 = each * w + (w < more ? w : more);
-        left = each + (w < more);
+        begin_share();
         return true;
     };
     bool header = true;
@@ -365,7 +370,9 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             hr = w;
             left = nb;
         } else {
-            if (!share((uint64_t)per_seq * nb)) return;
+            each = src.each;
+            more = src.more;
+            begin_share();
             uint64_t q;
             divmod_u64(x0, nb, q, off);
             hr = (uint32_t)q;
@@ -978,6 +985,7 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
         if ((uint32_t)s >= p.sources) break;
         const Source& x = p.src[s];
         const uint32_t tile = 16 * p.rt[s], r = x.pool ? seq * p.c.group + i : i;
+        // (a long pool's numbers could be worked out here: 0.6 us more than the load)
         const uint2 info = x.info[(x.pool ? 0 : (uint64_t)seq * p.c.H * x.row_blocks) + h * x.row_blocks + r / tile];
         slot[s] = wave_uniform(info.x);
         parts[s] = wave_uniform(info.y);
@@ -1077,8 +1085,8 @@ AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens,
     a.rows = rows;
     // Two row tiles of a wave share the widening of the tokens, but start and
     // join later: taken where every workgroup has a block to do. Pool, 60 rows,
-    // heads of 128: 131071 tokens 79 us, with one tile 112; 1024 tokens 11.7 and
-    // 8.8. Pages, 8 sequences of 8192, int8: heads of 64, 32 rows 12.2 and 13.8;
+    // heads of 128: 131071 tokens 79 us, with one tile 112; 4096 13.2 and
+    // 16.2; 1024 11.7 and 8.8. Pages, 8 sequences of 8192, int8: heads of 64, 32 rows 12.2 and 13.8;
     // heads of 128, 32 rows 18.2 and 16.4 (registers), 48 rows 22.0 and 23.9.
     const uint64_t most_blocks = (max_tokens + kBlock - 1) / kBlock;
     const bool enough = units_of_rows * ((rows + 31) / 32) * most_blocks >= 256ull * waves_per_simd(d, 2);
@@ -1157,6 +1165,9 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
         pool.L = a.L;
         pool.T = a.T;
         pool.layer = a.layer;
+        const uint64_t total = pool_plan.units * ((a.T + kBlock - 1) / kBlock);
+        pool.each = total / pool_plan.W;
+        pool.more = (uint32_t)(total % pool_plan.W);
     }
     if (has_pages) {
         const PageLayout& lay = a.tail.lay;
