@@ -296,11 +296,11 @@ __device__ __forceinline__ void fwht_row(float (&y)[C], uint32_t lane) {
 // workgroups a CU holds.
 constexpr int waves_per_simd(int d, int rt) { return d == 64 ? (rt == 1 ? 3 : 2) : 2; }
 
-// LDS of a workgroup.
+// LDS of a workgroup. (Without its alignment, accesses of four floats come out in pairs.)
 template <int D, int RT>
 struct Shared {
-    float ml[kWaves][RT * 16][2];
-    float os[RT][kWaves][16][D + 4];
+    alignas(16) float ml[kWaves][RT * 16][2];
+    alignas(16) float os[RT][kWaves][16][D + 4];
     uint32_t sums[kWaves];
     uint32_t found[3];  // sequence, blocks before it, its blocks
 };
