@@ -35,13 +35,13 @@ PROBE_SRC = os.path.join(PKG, "probe", "stream_probe.hip")
 PROBE_LIB = os.path.join(PKG, "libkvprobe.so")
 
 
-def _hipcc(srcs, out, verbose, extra=()):
+def _hipcc(srcs, out, verbose, extra=(), cwd=None):
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     tmp = out + ".tmp"
     cmd = [hipcc] + HIPCC_FLAGS + ([] if "-c" in extra else ["-shared"]) + list(extra) + list(srcs) + ["-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    res = subprocess.run(cmd, capture_output=True, text=True, cwd=cwd)
     errs = "\n".join(l for l in res.stderr.splitlines()
                      if "packed-fp32-ops" not in l and l.strip())
     if res.returncode != 0:
@@ -49,7 +49,7 @@ def _hipcc(srcs, out, verbose, extra=()):
         raise RuntimeError(f"hipcc failed ({res.returncode})")
     if verbose and errs:
         print(errs)
-    os.replace(tmp, out)
+    os.replace(os.path.join(cwd or "", tmp), os.path.join(cwd or "", out))
     return out
 
 
@@ -70,15 +70,16 @@ def build(verbose=False, extra=()):
     """libkvcodec.so (the codec), libkvprobe.so (the benchmark's probes) and _kvattend.so (a binding),
     every source compiled anew, a few at a time."""
     with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(6) as pool:
-        compiled = [os.path.join(tmp, os.path.basename(s) + ".o") for s in sources()]
+        # named without the folder, whose path would get into the library: the same sources give the same bytes
+        compiled = [os.path.basename(s) + ".o" for s in sources()]
         # the slowest first
         order = sorted(zip(sources(), compiled), key=lambda x: -os.path.getsize(x[0]))
         jobs = [pool.submit(_binding, verbose)]
-        jobs += [pool.submit(_hipcc, [s], o, verbose, ["-c"] + list(extra)) for s, o in order]
+        jobs += [pool.submit(_hipcc, [s], o, verbose, ["-c"] + list(extra), tmp) for s, o in order]
         jobs.append(pool.submit(_hipcc, [PROBE_SRC], PROBE_LIB, verbose))
         for j in jobs:
             j.result()
-        _hipcc(compiled, LIB_PATH, verbose, extra)
+        _hipcc(compiled, LIB_PATH, verbose, extra, tmp)
     return LIB_PATH
 
 
