@@ -27,7 +27,7 @@ struct RotateParams {
     float f[kMaxPairs];
 };
 
-__device__ __forceinline__ void unpack8(const uint4& x, float (&y)[8]) {
+__device__ __forceinline__ void unpack8(const kvc_u32x4& x, float (&y)[8]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -36,10 +36,23 @@ __device__ __forceinline__ void unpack8(const uint4& x, float (&y)[8]) {
     }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
-    return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                      pack_bf16x2(y[6], y[7]));
+__device__ __forceinline__ kvc_u32x4 pack8(const float (&y)[8]) {
+    return kvc_u32x4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
 }
+
+// Rows of queries and keys, of which each lane chooses. Kept in scalar registers:
+// the compiler would turn the choice of a value into that of its address among the
+// kernel's arguments, and read it from there for every vector (8191 tokens: 32.9 us,
+// so 30.1).
+struct Rows {
+    uint64_t q, k, qts, kts, qhs, khs;  // addresses; strides in elements
+};
+__device__ __forceinline__ Rows rows_of(const RowsDev& q, const RowsDev& k) {
+    Rows x{(uint64_t)q.data, (uint64_t)k.data, q.ts, k.ts, q.hs, k.hs};
+    asm("" : "+s"(x.q), "+s"(x.k), "+s"(x.qts), "+s"(x.kts), "+s"(x.qhs), "+s"(x.khs));
+    return x;
+}
+typedef __attribute__((address_space(1))) kvc_u32x4 global_u32x4;
 
 // sum over the LPV (4 or 8) lanes of a vector
 template <int LPV>
@@ -51,8 +64,8 @@ __device__ __forceinline__ float sum_lanes(float v) {
     return v;
 }
 
-// TW tokens of one workgroup. Five waves a SIMD: what a wave has on its way
-// bounds a prompt (four: 36.5 us, five: 33.6; more would spill).
+// TW tokens of one workgroup. Five waves a SIMD (a prompt of 8191 tokens: 30.1 us,
+// with four 30.2; six spill: 39).
 template <int D, int TW>
 __global__ __launch_bounds__(kBlockThreads, 5) void norm_rotate_kernel(RotateParams p) {
     constexpr uint32_t LPV = D / 16;
@@ -66,14 +79,14 @@ __global__ __launch_bounds__(kBlockThreads, 5) void norm_rotate_kernel(RotatePar
     const uint32_t oa = turned && p.pairing == 0 ? 8 * i : 16 * i;
     const uint32_t ob = turned && p.pairing == 0 ? p.n_pairs + 8 * i : 16 * i + 8;
     // weights stay packed: registers bound how many vectors are on their way
-    uint4 wq[2] = {}, wk[2] = {};
+    kvc_u32x4 wq[2] = {}, wk[2] = {};
     if (p.q_weight) {
-        wq[0] = *reinterpret_cast<const uint4*>(p.q_weight + oa);
-        wq[1] = *reinterpret_cast<const uint4*>(p.q_weight + ob);
+        wq[0] = *reinterpret_cast<const kvc_u32x4*>(p.q_weight + oa);
+        wq[1] = *reinterpret_cast<const kvc_u32x4*>(p.q_weight + ob);
     }
     if (p.k_weight) {
-        wk[0] = *reinterpret_cast<const uint4*>(p.k_weight + oa);
-        wk[1] = *reinterpret_cast<const uint4*>(p.k_weight + ob);
+        wk[0] = *reinterpret_cast<const kvc_u32x4*>(p.k_weight + oa);
+        wk[1] = *reinterpret_cast<const kvc_u32x4*>(p.k_weight + ob);
     }
     // the first vector's loads go out before the angles are taken, the next
     // one's before each is turned
@@ -84,14 +97,19 @@ __global__ __launch_bounds__(kBlockThreads, 5) void norm_rotate_kernel(RotatePar
             ++t;
         }
     };
-    uint4 xa, xb;
+    // the vector's row, from fields in registers
+    const Rows in = rows_of(p.q_in, p.k_in), out = rows_of(p.q_out, p.k_out);
+    const auto row_at = [&](const Rows& x) {
+        const bool is_q = h < p.Hq;
+        const uint64_t at = (tok0 + t) * (is_q ? x.qts : x.kts) + (is_q ? h : h - p.Hq) * (is_q ? x.qhs : x.khs);
+        return (is_q ? x.q : x.k) + 2 * at;
+    };
+    kvc_u32x4 xa, xb;
     const auto load = [&]() {
         if (t >= ntok) return;
-        const bool is_q = h < p.Hq;
-        const RowsDev& in = is_q ? p.q_in : p.k_in;
-        const uint16_t* x = in.data + (uint64_t)(tok0 + t) * in.ts + (uint64_t)(is_q ? h : h - p.Hq) * in.hs;
-        xa = *reinterpret_cast<const uint4*>(x + oa);
-        xb = *reinterpret_cast<const uint4*>(x + ob);
+        const uint64_t x = row_at(in);
+        xa = *(const global_u32x4*)(x + 2 * oa);
+        xb = *(const global_u32x4*)(x + 2 * ob);
     };
     settle();
     load();
@@ -109,8 +127,8 @@ __global__ __launch_bounds__(kBlockThreads, 5) void norm_rotate_kernel(RotatePar
     __syncthreads();
     while (t < ntok) {
         const bool is_q = h < p.Hq;
-        const RowsDev& to = is_q ? p.q_out : p.k_out;
-        uint16_t* y = to.data + (uint64_t)(tok0 + t) * to.ts + (uint64_t)(is_q ? h : h - p.Hq) * to.hs;
+        const uint64_t y = row_at(out);
+        global_u32x4 *const ya = (global_u32x4*)(y + 2 * oa), *const yb = (global_u32x4*)(y + 2 * ob);
         float a[8], b[8];
         unpack8(xa, a);
         unpack8(xb, b);
@@ -160,12 +178,12 @@ __global__ __launch_bounds__(kBlockThreads, 5) void norm_rotate_kernel(RotatePar
                 }
             }
         }
-        if (TW > 1) {  // a prompt's rows: 33.6 us with the hint, 37 without
-            st_stream(reinterpret_cast<uint4*>(y + oa), pack8(a));
-            st_stream(reinterpret_cast<uint4*>(y + ob), pack8(b));
+        if (TW > 1) {  // a prompt's rows: 30.1 us with the hint, 35.3 without
+            __builtin_nontemporal_store(pack8(a), ya);
+            __builtin_nontemporal_store(pack8(b), yb);
         } else {
-            *reinterpret_cast<uint4*>(y + oa) = pack8(a);
-            *reinterpret_cast<uint4*>(y + ob) = pack8(b);
+            *ya = pack8(a);
+            *yb = pack8(b);
         }
     }
 }
@@ -189,8 +207,8 @@ hipError_t launch_norm_rotate(const RotateArgs& a, hipStream_t stream) {
     p.eps = a.eps;
     for (uint32_t j = 0; j < a.n_pairs; ++j) p.f[j] = a.inv_freq[j];
     // four tokens a workgroup (every thread takes an angle) once that still
-    // leaves four workgroups to a CU; 8191 tokens of 40 heads of 128: 33.6 us
-    // (5.0 TB/s), with two 44, with eight 35
+    // leaves four workgroups to a CU; 8191 tokens of 40 heads of 128: 30.1 us
+    // (5.6 TB/s), with two 29.6, with eight 30.7
     if (a.n >= 4096)
         return launch_kernel(a.d == 64 ? norm_rotate_kernel<64, 4> : norm_rotate_kernel<128, 4>, dim3((a.n + 3) / 4),
                              dim3(kBlockThreads), stream, p);
