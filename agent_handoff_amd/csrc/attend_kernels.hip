@@ -72,6 +72,7 @@ typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t ushort2_t __attribute__((ext_vector_type(2)));
 
@@ -228,11 +229,19 @@ __device__ __forceinline__ void load_words(const uint8_t* a, uint32_t (&w)[W]) {
     }
 }
 
+// What no workgroup of a launch writes, at an address that is the same in all
+// lanes: read through the scalar cache, without a wait until it is used.
+template <class T>
+__device__ __forceinline__ T scalar_load(const void* a) {
+    return *(const __attribute__((address_space(4))) T*)(uint64_t)a;
+}
+
+// (all words at once: compared one after another, each would wait for its load)
 __device__ __forceinline__ bool pool_header_ok(const Source& p, uint32_t H, uint32_t D) {
-    const uint32_t* hd = reinterpret_cast<const uint32_t*>(p.pool);
-    const uint64_t t = (uint64_t)hd[14] | ((uint64_t)hd[15] << 32);
-    return hd[0] == kPoolMagic && hd[1] == (1u | (1u << 16)) && hd[2] == p.L && hd[3] == H && hd[4] == p.T &&
-           hd[5] == D && t == p.lay.total;
+    const u32x4 a = scalar_load<u32x4>(p.pool), b = scalar_load<u32x4>(p.pool + 16), c = scalar_load<u32x4>(p.pool + 48);
+    const uint64_t t = (uint64_t)c.z | ((uint64_t)c.w << 32);
+    return (a.x == kPoolMagic) & (a.y == (1u | (1u << 16))) & (a.z == p.L) & (a.w == H) & (b.x == p.T) & (b.y == D) &
+           (t == p.lay.total);
 }
 
 // A sequence's length, within what its table's row holds.
@@ -361,10 +370,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         begin_share();
         return true;
     };
-    bool header = true;
     if (FMT == kFmtPool) {
-        // (looked at before anything is written: the loads do not depend on it)
-        header = pool_header_ok(src, p.H, D);
         const uint32_t nb = blocks_of(src.T);
         if (src.whole) {
             hr = w;
@@ -545,6 +551,8 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         };
         R x;
         if (begin + wave * kTile < end) load(begin + wave * kTile, 0, x);
+        // looked at before anything is written: the loads do not depend on it
+        const bool header = FMT != kFmtPool || pool_header_ok(src, p.H, D);
 
         u32x4 qf[RT][KS];
         float qscale[RT];
@@ -972,64 +980,68 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
     typedef float vec __attribute__((ext_vector_type(C)));
     const uint32_t lane = lane_id();
     const uint32_t wave = wave_uniform(threadIdx.x / kWave), w = wave % V;
-    const uint64_t row = (uint64_t)blockIdx.x * RPB + wave / V;
-    if (row >= (uint64_t)p.c.n * p.c.Hq) return;
-    const uint32_t seq = (uint32_t)(row / p.c.Hq), qh = (uint32_t)(row % p.c.Hq);
+    const uint32_t row = blockIdx.x * RPB + wave / V;
+    if (row >= p.c.n * p.c.Hq) return;
+    const uint32_t seq = row / p.c.Hq, qh = row % p.c.Hq;
     const uint32_t h = qh / p.c.group, i = qh % p.c.group;
-    // this row's place in each source: its part k at from[s] + stride[s] * slot
-    const float *from[2], *ml[2];
-    uint64_t stride[2];
-    uint32_t slot[2], parts[2] = {0, 0};
+    // this row's place in each source: its part k at from[s] + stride[s] * slot,
+    // and the part's maximum and sum `ml` floats behind it
+    const float* from[2] = {};
+    uint32_t stride[2] = {}, ml[2] = {};
+    u32x2 info[2] = {};  // first slot, number of parts
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         if ((uint32_t)s >= p.sources) break;
         const Source& x = p.src[s];
-        const uint32_t tile = 16 * p.rt[s], r = x.pool ? seq * p.c.group + i : i;
+        const uint32_t tile = 16 * p.rt[s], r = x.pool ? seq * p.c.group + i : i, at = r % tile;
         // (a long pool's numbers could be worked out here: 0.6 us more than the load)
-        const uint2 info = x.info[(x.pool ? 0 : (uint64_t)seq * p.c.H * x.row_blocks) + h * x.row_blocks + r / tile];
-        slot[s] = wave_uniform(info.x);
-        parts[s] = wave_uniform(info.y);
-        stride[s] = (uint64_t)tile * (D + 2);
-        from[s] = x.part + r % tile * D;
-        ml[s] = x.part + tile * D + r % tile * 2;
+        info[s] = scalar_load<u32x2>(x.info + (x.pool ? 0 : seq * p.c.H * x.row_blocks) + h * x.row_blocks + r / tile);
+        stride[s] = tile * (D + 2);
+        from[s] = x.part + at * D;
+        ml[s] = (tile - at) * D + at * 2;
     }
     const bool header = !p.src[0].pool || pool_header_ok(p.src[0], p.c.H, D);
-    const uint32_t n0 = parts[0], n = n0 + parts[1];
+    const uint32_t n0 = info[0].y, n = n0 + info[1].y;
     if (n == 0 || !header) return;  // written already, or never to be
-    const auto at = [&](const float* const (&base)[2], uint32_t k) {
-        const int s = k >= n0;
-        const uint32_t j = s ? k - n0 : k;
-        return base[s] + stride[s] * (j ? slot[s] - 1 + 2 * j : slot[s]);
-    };
-    // this wave's parts w, w + V, ...: a lane has the maximum and sum of one of
-    // each 64, and the first U parts' sums are on their way before the maxima
-    // are needed (parts behind the last are read as the wave's first, or the row's)
+    // this wave's parts w, w + V, ...: a lane has the place, maximum and sum of one of
+    // each 64, and the first U parts' sums are on their way before the maxima are
+    // needed (parts behind the last are read as the wave's first, or the row's)
     const uint32_t safe = w < n ? w : 0;
-    const auto ml_of = [&](uint32_t k) { return *reinterpret_cast<const float2*>(at(ml, k < n ? k : safe)); };
+    const float* place;
+    const auto ml_of = [&](uint32_t k) {
+        k = k < n ? k : safe;
+        const bool second = k >= n0;
+        const uint32_t j = second ? k - n0 : k, slot = second ? info[1].x : info[0].x;
+        place = (second ? from[1] : from[0]) + (uint64_t)(second ? stride[1] : stride[0]) * (j ? slot - 1 + 2 * j : slot);
+        return *reinterpret_cast<const float2*>(place + (second ? ml[1] : ml[0]));
+    };
     vec x[U];
-    const auto load = [&](uint32_t base, uint32_t j) {
+    const auto load = [&](uint32_t j) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t k = base + V * (j + u);
-            x[u] = *reinterpret_cast<const vec*>(at(from, k < n ? k : safe) + C * lane);
+            const uint64_t a = (uint64_t)place;
+            const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((uint32_t)a, (j + u) & 63),
+                           hi = (uint32_t)__builtin_amdgcn_readlane((uint32_t)(a >> 32), (j + u) & 63);
+            x[u] = *((const __attribute__((address_space(1))) vec*)(lo | hi << 32) + lane);
         }
     };
     float2 v = ml_of(w + V * lane);
-    load(w, 0);
+    load(0);
     float M = w + V * lane < n ? v.x : kNegInf, total = 0.0f;
-    for (uint32_t k = w + V * (lane + kWave); k < n; k += V * kWave) M = fmaxf(M, at(ml, k)[0]);
+    const bool many = n > w + V * kWave;  // more than one part a lane: `place` moves on
+    for (uint32_t k = w + V * (lane + kWave); k < n; k += V * kWave) M = fmaxf(M, ml_of(k).x);
 #pragma unroll
     for (int i = 1; i < 64; i *= 2) M = fmaxf(M, __shfl_xor(M, i));
     const float Mu = M == kNegInf ? 0.0f : M;
     vec y = 0.0f;
     for (uint32_t base = w; base < n; base += V * kWave) {
         const uint32_t k = base + V * lane;
-        if (base != w) v = ml_of(k);
+        if (many) v = ml_of(k);
         const float a = exp2_fast(v.x - Mu);
         total = k < n ? fmaf(v.y, a, total) : total;
         const uint32_t rest = (n - base + V - 1) / V, count = rest < kWave ? rest : kWave;
         for (uint32_t j = 0; j < count; j += U) {
-            if (j || base != w) load(base, j);
+            if (j || many) load(j);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, a), (j + u) & 63));
