@@ -314,15 +314,29 @@ struct Shared {
     uint32_t found[3];  // sequence, blocks before it, its blocks
 };
 
-// Sum over the wave's lanes up to this one.
-__device__ __forceinline__ uint32_t scan_lanes(uint32_t v) {
-    const uint32_t lane = lane_id();
-#pragma unroll
-    for (int i = 1; i < 64; i *= 2) {
-        const uint32_t o = __shfl_up(v, i);
-        if (lane >= (uint32_t)i) v += o;
-    }
+// Over the wave's lanes up to this one, by moves inside rows of 16 and the last
+// lanes of rows to the rows behind them (with LDS permutes: some 100 cycles a step).
+template <class T, class F>
+__device__ __forceinline__ T scan_wave(T v, T none, F join) {
+    const auto step = [&](auto ctrl, auto rows) {
+        const int o = __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v),
+                                                  decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+        v = join(v, __builtin_bit_cast(T, o));
+    };
+    using All = std::integral_constant<int, 0xF>;
+    step(std::integral_constant<int, 0x111>{}, All{});  // from 1, 2, 4, 8 lanes before, in the row
+    step(std::integral_constant<int, 0x112>{}, All{});
+    step(std::integral_constant<int, 0x114>{}, All{});
+    step(std::integral_constant<int, 0x118>{}, All{});
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // rows 0, 2 to 1, 3
+    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});  // half 0 to 1
     return v;
+}
+__device__ __forceinline__ uint32_t scan_lanes(uint32_t v) {
+    return scan_wave(v, 0u, [](uint32_t a, uint32_t b) { return a + b; });
+}
+__device__ __forceinline__ float last_lane(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 // Sum over the workgroup's threads before this one, and the sum of all.
@@ -1030,8 +1044,7 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
     float M = w + V * lane < n ? v.x : kNegInf, total = 0.0f;
     const bool many = n > w + V * kWave;  // more than one part a lane: `place` moves on
     for (uint32_t k = w + V * (lane + kWave); k < n; k += V * kWave) M = fmaxf(M, ml_of(k).x);
-#pragma unroll
-    for (int i = 1; i < 64; i *= 2) M = fmaxf(M, __shfl_xor(M, i));
+    M = last_lane(scan_wave(M, kNegInf, [](float a, float b) { return fmaxf(a, b); }));
     const float Mu = M == kNegInf ? 0.0f : M;
     vec y = 0.0f;
     for (uint32_t base = w; base < n; base += V * kWave) {
@@ -1049,8 +1062,7 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
             }
         }
     }
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) total += __shfl_xor(total, x);
+    total = last_lane(scan_wave(total, 0.0f, [](float a, float b) { return a + b; }));
     if constexpr (V > 1) {
         __shared__ float mt[V][2];
         __shared__ vec ys[V][kWave];
