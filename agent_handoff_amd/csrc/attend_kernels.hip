@@ -314,6 +314,17 @@ struct Shared {
     uint32_t found[3];  // sequence, blocks before it, its blocks
 };
 
+// Over the four lanes that hold a query row (lane % 16), in all of them: rows of 16
+// lanes change places, then halves.
+template <class T, class F>
+__device__ __forceinline__ T over_groups(T v, F join) {
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    const uint32_t b = __builtin_bit_cast(uint32_t, join(__builtin_bit_cast(T, (uint32_t)r[0]), __builtin_bit_cast(T, (uint32_t)r[1])));
+    const auto h = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return join(__builtin_bit_cast(T, (uint32_t)h[0]), __builtin_bit_cast(T, (uint32_t)h[1]));
+}
+
 // Over the wave's lanes up to this one, by moves inside rows of 16 and the last
 // lanes of rows to the rows behind them (with LDS permutes: some 100 cycles a step).
 template <class T, class F>
@@ -586,10 +597,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                     for (int i = 0; i < 4; ++i)
                         top = __builtin_elementwise_max(top, __builtin_bit_cast(ushort2_t, z[s][i] & 0x7FFF7FFFu));
                 uint32_t big = top.x > top.y ? top.x : top.y;
-                uint32_t other = __shfl_xor(big, 16);
-                big = other > big ? other : big;
-                other = __shfl_xor(big, 32);
-                big = other > big ? other : big;
+                big = over_groups(big, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
                 // largest magnitude to [2^14, 2^15), by 2^112 at most, which brings the smallest
                 // bf16 into range; Inf and NaN stay what they are
                 int e = (big == 0 || big >= 0x7F80u) ? 0 : 15 - __builtin_amdgcn_frexp_expf(__uint_as_float(big << 16));
@@ -773,10 +781,10 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                 move |= big >= elimit;
             }
             if (__ballot(move) != 0) {
+                const auto larger = [](float a, float b) { return fmaxf(a, b); };
                 float shrink = 1.0f;
                 if (HALF) {
-                    big = fmaxf(big, __shfl_xor(big, 16));
-                    big = fmaxf(big, __shfl_xor(big, 32));
+                    big = over_groups(big, larger);
                     const int e = __builtin_amdgcn_frexp_expf(big), ne = big >= elimit ? e : E;
                     shrink = __builtin_amdgcn_ldexpf(1.0f, E - ne);
                     E = ne;
@@ -785,9 +793,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                 }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    float x2 = fmaxf(top[rt], __shfl_xor(top[rt], 16));
-                    x2 = fmaxf(x2, __shfl_xor(x2, 32));
-                    const float nm = fmaxf(m[rt], x2);
+                    const float nm = fmaxf(m[rt], over_groups(top[rt], larger));
                     const float a = nm == kNegInf ? 1.0f : exp2_fast(m[rt] - nm);
                     m[rt] = nm;
                     mu[rt] = nm == kNegInf ? 0.0f : nm;
@@ -870,9 +876,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            float s = l[rt];
-            s += __shfl_xor(s, 16);
-            s += __shfl_xor(s, 32);
+            const float s = over_groups(l[rt], [](float a, float b) { return a + b; });
             if (g == 0) {
                 sh.ml[wave][rt * 16 + c][0] = m[rt];
                 sh.ml[wave][rt * 16 + c][1] = s;
