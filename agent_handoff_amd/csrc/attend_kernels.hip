@@ -23,7 +23,7 @@
 // holds 178 bytes for a token's key and value of 128 channels instead of 264, and
 // many rows share them: there the vector instructions of widening and softmax
 // and the matrix instructions, which a SIMD issues one at a time, bound it
-// (131071 tokens, 8 kv heads of 128, 60 rows: 77 us, 2.4 TB/s; of a SIMD's
+// (131071 tokens, 8 kv heads of 128, 60 rows: 76 us, 2.5 TB/s; of a SIMD's
 // cycles the VALU takes 71 %, the matrix core 17 %). Short calls are bound by latency: three
 // dependent reads, a tile, the join of four waves: 5.5 us.
 //
@@ -1113,7 +1113,7 @@ AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens,
     a.rows = rows;
     // Two row tiles of a wave share the widening of the tokens, but start and
     // join later: taken where every workgroup has a block to do. Two and one, us:
-    // pool, 60 rows, heads of 128: 131071 tokens 77 and 112, 4096 13.2 and 16.2,
+    // pool, 60 rows, heads of 128: 131071 tokens 76 and 112, 4096 13.2 and 16.2,
     // 1024 11.7 and 8.8. Pages, 8 sequences of 8192, 2 kv heads: heads of 64, 17 rows
     // int8 13.6 and 14.3, bf16 12.9 and 16.8; heads of 128, int8 32 rows 18.2 and
     // 17.8 (registers), 48 rows 23.7 and 26.8, bf16 28.6 and 38.4.
