@@ -1101,9 +1101,9 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
 }
 
 // A workgroup gets at least kMinBlocks blocks: half a launch's latency goes
-// into starting a share and joining it (a 4096-token pool for 15 agents with
-// tails: 20 us with 1, 14.4 with 2, 15.8 with 4). Up to kWholeTokens tokens a
-// unit stays whole and its outputs need no second launch.
+// into starting a share and joining it (a 4096-token pool for 15 agents, alone and with
+// tails: 17.3 and 20.8 us with 1, 13.7 and 15.2 with 2, 14.7 and 15.4 with 4). Up to
+// kWholeTokens tokens a unit stays whole and its outputs need no second launch.
 constexpr uint64_t kMinBlocks = 2, kWholeTokens = 512;
 
 // one_tile: up to so many rows are taken one row tile a wave.
@@ -1112,11 +1112,11 @@ AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens,
     AttendPlan a;
     a.rows = rows;
     // Two row tiles of a wave share the widening of the tokens, but start and
-    // join later: taken where every workgroup has a block to do. Two and one, us:
-    // pool, 60 rows, heads of 128: 131071 tokens 76 and 112, 4096 13.2 and 16.2,
-    // 1024 11.7 and 8.8. Pages, 8 sequences of 8192, 2 kv heads: heads of 64, 17 rows
-    // int8 13.6 and 14.3, bf16 12.9 and 16.8; heads of 128, int8 32 rows 18.2 and
-    // 17.8 (registers), 48 rows 23.7 and 26.8, bf16 28.6 and 38.4.
+    // join later: taken where every workgroup has a block to do. A call with two and
+    // with one, us: pool of 15 agents, 60 rows, heads of 128: 131071 tokens 68.5 and 103,
+    // 4096 with tails 15.2 and 18.0, 1024 11.5 and 9.7. Pages, 8 sequences of 8192, 2 kv
+    // heads: heads of 64, 17 rows int8 12.4 and 13.0, bf16 12.0 and 15.6; heads of 128,
+    // int8 32 rows 19.9 and 17.0 (registers), 48 rows 22.0 and 25.3, bf16 27.3 and 37.3.
     const uint64_t most_blocks = (max_tokens + kBlock - 1) / kBlock;
     const bool enough = units_of_rows * ((rows + 31) / 32) * most_blocks >= 256ull * waves_per_simd(d, 2);
     a.rt = rows > one_tile && enough ? 2 : 1;
