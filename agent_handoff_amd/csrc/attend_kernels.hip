@@ -616,10 +616,20 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                     for (int i = 0; i < 4; ++i) qf[rt][s][i] = live ? z[s][i] ^ turn : 0;
             }
         }
-        if (FMT == kFmtPool) {
-            const float step = reinterpret_cast<const float*>(src.pool + src.lay.k_scale)[src.layer];
+        // A logit is a sum of codes (below 2^31) times its row's factor and its key's step, either of which
+        // may lie near an end of binary32's range. A factor up to 1 comes first: that sum cannot
+        // overflow. One above 1 (queries from 2^18 on) comes last, so that nothing overflows before the logit does.
+        bool above = false;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) qscale[rt] *= step;
+        for (int rt = 0; rt < RT; ++rt) above |= qscale[rt] > 1.0f;
+        const bool late = HALF && __ballot(above) != 0;
+        float step = 0.0f;
+        if (FMT == kFmtPool) {
+            step = reinterpret_cast<const float*>(src.pool + src.lay.k_scale)[src.layer];
+            if (!late) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) qscale[rt] *= step;
+            }
         }
 
         // running state
@@ -761,12 +771,28 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             // logits (in powers of two), their maxima, and the steps' largest
             float y[RT][8], top[RT];
             bool move = false;
+            if (__builtin_expect(late, 0)) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float k = FMT == kFmtPool ? step : ks[j];
+                        const bool last = qscale[rt] > 1.0f;
+                        y[rt][j] = s[rt][j >> 2][j & 3] * (last ? k : qscale[rt]) * (last ? qscale[rt] : k);
+                    }
+            } else {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        y[rt][j] = s[rt][j >> 2][j & 3] * qscale[rt];
+                        if constexpr (FMT == kFmtInt8 || FMT == kFmtFp8) y[rt][j] *= ks[j];
+                    }
+            }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    y[rt][j] = s[rt][j >> 2][j & 3] * qscale[rt];
-                    if constexpr (FMT == kFmtInt8 || FMT == kFmtFp8) y[rt][j] *= ks[j];
                     if (PART) y[rt][j] = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? y[rt][j] : kNegInf;
                 }
                 top[rt] = y[rt][0];

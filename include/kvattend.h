@@ -156,9 +156,10 @@ size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uin
  * arguments alone decide: the same call gives the same bits.
  * The 8-bit formats' weights p_t * step are rounded to binary16 after division
  * by a power of two (about the largest step) for the matrix cores, bf16's are
- * split into two bf16 terms; products and sums are binary32. So logits, and the
- * weighted sums before they are divided by the weights' (at most 8 times the
- * tokens times the largest value), have to stay in binary32's range. Where all
+ * split into two bf16 terms; products and sums are binary32. So q . k (before
+ * and after the scale), and the weighted sums before they are divided by the
+ * weights' (at most 8 times the tokens times the largest value), have to stay in
+ * binary32's range; queries and keys may lie anywhere in bf16's. Where all
  * logits of a row are -inf, the row is as that of an empty sequence; a NaN in a
  * query or in a key or value that its length reaches gives NaN.
  * Errors: KVC_E_NULL, KVC_E_SHAPE, KVC_E_RANGE, KVC_E_SIZE, KVC_E_ALIGN,
