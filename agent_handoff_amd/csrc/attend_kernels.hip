@@ -33,7 +33,7 @@
 // unit (the agent-scope fences write back and drop L2: 20 -> 78 us).
 //
 // Number formats: int8 and e4m3 codes, and the pool's levels, are widened to
-// binary16, where codes are exact (levels: rounded, 2^-12). Queries go to
+// binary16, where codes are exact (levels: within 2^-17.5, see kLevelFactor). Queries go to
 // binary16 after division by a power of two per row (the row's largest
 // becomes 2^14..2^15, so what is lost is below 2^-39 of it). Weights p * step
 // go to binary16 (2^-12) after division by 2^E, E the wave's largest step
@@ -150,10 +150,13 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
 }
 
 // Level i of the value codes as binary16, and one byte (from bit `shift`) of
-// levels first .. first + 3.
+// levels first .. first + 3. As they are the levels would lose up to 0.83 of 2^-12,
+// every token alike, so no sum over tokens averages it out; times this factor, which the
+// transform takes out again, each lies within 0.0212 of 2^-12 of a binary16 number.
+constexpr double kLevelFactor = 1.8587914;
 constexpr uint32_t level_half(int i) {
     const float pos[4] = {kLv0, kLv1, kLv2, kLv3};
-    return __builtin_bit_cast(uint16_t, (_Float16)(i < 4 ? -pos[3 - i] : pos[i - 4]));
+    return __builtin_bit_cast(uint16_t, (_Float16)(float)((i < 4 ? -pos[3 - i] : pos[i - 4]) * kLevelFactor));
 }
 constexpr uint32_t level_bytes(int first, int shift) {
     uint32_t w = 0;
@@ -949,7 +952,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             }
             if (FMT == kFmtPool) {
                 fwht_row<NC>(y, lane);
-                const float k = D == 128 ? 0.08838834764831845f : 0.125f;  // 1 / sqrt(d)
+                const float k = (float)((D == 128 ? 0.08838834764831845 : 0.125) / kLevelFactor);  // 1 / sqrt(d)
 #pragma unroll
                 for (int n = 0; n < NC; ++n) y[n] *= k;
             }

@@ -191,7 +191,8 @@ size_t kvpool_attend_workspace_bytes(const kvc_shape* shape, uint32_t n_agents, 
  * The pool's keys are code * step; its values are the inverse transform of
  * the levels times the vector's scale, as real numbers. (kvpool_decode gives
  * these rounded to bf16.) The transform is linear, so it is applied to the
- * weighted sums of levels, once for each query head and part of the tokens.
+ * weighted sums of levels, once for each query head and part of the tokens;
+ * each level is taken within 2^-17 of itself.
  *   pool       as written by kvpool_encode, read only
  *   q, out     rows of n_agents x q_heads; q_heads a multiple of num_kv_heads
  *   tail       NULL: the pool alone
