@@ -69,8 +69,13 @@ struct AttendPlan {
     uint64_t units, W;    // W: workgroups
     uint64_t blocks;      // blocks of tokens of all units, at most
     uint64_t slots;       // places for partial results: 16 rt rows of d sums, a maximum and a sum
+    // Bytes that serve this plan and that of every call with fewer sequences, rows or
+    // tokens: never less for more of them, where `bytes` falls (a call whose units are
+    // whole needs no places at all).
+    uint64_t room;
     uint64_t part_bytes(uint32_t d) const { return slots * 16 * rt * (d + 2) * 4; }
-    uint64_t bytes(uint32_t d) const { return align_up(part_bytes(d) + units * 8, 256); }
+    uint64_t bytes_of(uint64_t places, uint32_t d) const { return align_up(places * 16 * rt * (d + 2) * 4 + units * 8, 256); }
+    uint64_t bytes(uint32_t d) const { return bytes_of(slots, d); }
 };
 // tail: pages behind a pool (all parts are joined, none is written as output).
 AttendPlan page_attend_plan(uint32_t n_seqs, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens, bool tail);

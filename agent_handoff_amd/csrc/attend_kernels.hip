@@ -1135,11 +1135,34 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
 // kWholeTokens tokens a unit stays whole and its outputs need no second launch.
 constexpr uint64_t kMinBlocks = 2, kWholeTokens = 512;
 
+// The plan with rt row tiles a wave.
+AttendPlan plan_of(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens, uint32_t d, uint32_t rt, bool direct) {
+    AttendPlan a;
+    a.rows = rows;
+    a.rt = rt;
+    a.row_blocks = (rows + 16 * rt - 1) / (16 * rt);
+    a.units = units_of_rows * a.row_blocks;
+    const uint64_t slots = 256ull * waves_per_simd(d, rt);
+    a.blocks = a.units * ((max_tokens + kBlock - 1) / kBlock);
+    a.whole = max_tokens <= kWholeTokens || a.units >= 8 * slots;
+    uint64_t w = a.blocks / kMinBlocks < slots ? a.blocks / kMinBlocks : slots;
+    if (w < 1) w = 1;
+    a.W = a.whole ? a.units : w;
+    a.slots = a.whole ? (direct ? 0 : a.units) : 2 * w + (direct ? 0 : a.units);
+    // what the workspace has room for: that of a plan that is cut up, unless no sequence is long enough for one,
+    // and of one row tile a wave, which fewer rows or tokens would take
+    const uint64_t room = max_tokens <= kWholeTokens ? a.slots : 2 * w + (direct ? 0 : a.units);
+    a.room = a.bytes_of(room, d);
+    if (rt > 1) {
+        const uint64_t one = plan_of(units_of_rows, rows, max_tokens, d, 1, direct).room;
+        if (one > a.room) a.room = one;
+    }
+    return a;
+}
+
 // one_tile: up to so many rows are taken one row tile a wave.
 AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens, uint32_t d, uint32_t one_tile,
                      bool direct) {
-    AttendPlan a;
-    a.rows = rows;
     // Two row tiles of a wave share the widening of the tokens, but start and
     // join later: taken where every workgroup has a block to do. A call with two and
     // with one, us: pool of 15 agents, 60 rows, heads of 128: 131071 tokens 68.5 and 103,
@@ -1148,18 +1171,7 @@ AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens,
     // int8 32 rows 19.9 and 17.0 (registers), 48 rows 22.0 and 25.3, bf16 27.3 and 37.3.
     const uint64_t most_blocks = (max_tokens + kBlock - 1) / kBlock;
     const bool enough = units_of_rows * ((rows + 31) / 32) * most_blocks >= 256ull * waves_per_simd(d, 2);
-    a.rt = rows > one_tile && enough ? 2 : 1;
-    a.row_blocks = (rows + 16 * a.rt - 1) / (16 * a.rt);
-    a.units = units_of_rows * a.row_blocks;
-    const uint64_t slots = 256ull * waves_per_simd(d, a.rt);
-    const uint64_t blocks = a.units * most_blocks;
-    a.blocks = blocks;
-    a.whole = max_tokens <= kWholeTokens || a.units >= 8 * slots;
-    uint64_t w = blocks / kMinBlocks < slots ? blocks / kMinBlocks : slots;
-    if (w < 1) w = 1;
-    a.W = a.whole ? a.units : w;
-    a.slots = a.whole ? (direct ? 0 : a.units) : 2 * w + (direct ? 0 : a.units);
-    return a;
+    return plan_of(units_of_rows, rows, max_tokens, d, rows > one_tile && enough ? 2 : 1, direct);
 }
 
 template <int D>

@@ -144,6 +144,44 @@ struct Span {
     uint64_t n;
 };
 
+// Workspace bytes of a call: `need`, what it uses, and `room`, which serves every smaller call too; false
+// if an argument is invalid.
+struct Workspace {
+    uint64_t need, room;
+    bool add(const kvc::AttendPlan& p, uint32_t d) {
+        need += p.bytes(d);
+        room += p.room;
+        return plan_ok(p);
+    }
+};
+bool page_workspace(const kvc_pages* spec, uint32_t n, uint32_t q_heads, uint32_t max_tokens, Workspace& w) {
+    w = Workspace{0, 0};
+    if (!spec_ok(spec) || !heads_ok(n, spec->num_kv_heads, q_heads) || !tokens_ok(n, max_tokens)) return false;
+    if (n == 0) w = Workspace{256, 256};
+    const uint32_t d = spec->head_dim;
+    return n == 0 || w.add(kvc::page_attend_plan(n, spec->num_kv_heads, q_heads, d, max_tokens, false), d);
+}
+bool pool_workspace(const kvc_shape* s, uint32_t n, uint32_t q_heads, const kvc_pages* tail, uint32_t max_tokens,
+                    Workspace& w) {
+    w = Workspace{0, 0};
+    if (!s || !kvc::pool_shape_ok(s->num_layers, s->num_kv_heads, s->num_tokens, s->head_dim) ||
+        !heads_ok(n, s->num_kv_heads, q_heads))
+        return false;
+    if (tail && (!spec_ok(tail) || tail->num_kv_heads != s->num_kv_heads || tail->head_dim != s->head_dim ||
+                 !tokens_ok(n, max_tokens)))
+        return false;
+    if (n == 0) {
+        w = Workspace{256, 256};
+        return true;
+    }
+    const uint32_t H = s->num_kv_heads, d = s->head_dim;
+    const kvc::AttendPlan p = kvc::pool_attend_plan(H, n, q_heads, d, s->num_tokens, tail != nullptr);
+    if (!w.add(p, d)) return false;
+    if (!tail) return true;
+    const kvc::AttendPlan t = kvc::page_attend_plan(n, H, q_heads, d, max_tokens, true);
+    return w.add(t, d) && t.W + p.W < (1ull << 31);
+}
+
 }  // namespace
 
 extern "C" {
@@ -220,11 +258,8 @@ int kvpage_read(const kvc_pages* spec, const void* pages, size_t pages_bytes, ui
 }
 
 size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uint32_t q_heads, uint32_t max_tokens) {
-    if (!spec_ok(spec) || !heads_ok(n_seqs, spec->num_kv_heads, q_heads) || !tokens_ok(n_seqs, max_tokens)) return 0;
-    if (n_seqs == 0) return 256;
-    const kvc::AttendPlan p =
-        kvc::page_attend_plan(n_seqs, spec->num_kv_heads, q_heads, spec->head_dim, max_tokens, false);
-    return plan_ok(p) ? (size_t)p.bytes(spec->head_dim) : 0;
+    Workspace w;
+    return page_workspace(spec, n_seqs, q_heads, max_tokens, w) ? (size_t)w.room : 0;
 }
 
 int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs, uint32_t q_heads,
@@ -238,8 +273,9 @@ int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, 
     if (!q || !out || !q->data || !out->data || !ws) return KVC_E_NULL;
     const int rc = check_tail(spec, pages, pages_bytes, n_seqs, table, table_cols, table_stride, lens);
     if (rc != KVC_OK) return rc;
-    const uint64_t need = kvpage_attend_workspace_bytes(spec, n_seqs, q_heads, table_cols * spec->page_tokens);
-    if (need == 0) return KVC_E_SHAPE;
+    Workspace w;
+    if (!page_workspace(spec, n_seqs, q_heads, table_cols * spec->page_tokens, w)) return KVC_E_SHAPE;
+    const uint64_t need = w.need;
     if (ws_bytes < need) return KVC_E_SIZE;
     View qv, ov;
     if (!view_of(q, n_seqs, q_heads, spec->head_dim, qv) || !view_of(out, n_seqs, q_heads, spec->head_dim, ov))
@@ -278,24 +314,8 @@ int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, 
 
 size_t kvpool_attend_workspace_bytes(const kvc_shape* shape, uint32_t n_agents, uint32_t q_heads,
                                      const kvc_pages* tail_spec, uint32_t max_tail_tokens) {
-    if (!shape || !kvc::pool_shape_ok(shape->num_layers, shape->num_kv_heads, shape->num_tokens, shape->head_dim) ||
-        !heads_ok(n_agents, shape->num_kv_heads, q_heads))
-        return 0;
-    if (tail_spec && (!spec_ok(tail_spec) || tail_spec->num_kv_heads != shape->num_kv_heads ||
-                      tail_spec->head_dim != shape->head_dim || !tokens_ok(n_agents, max_tail_tokens)))
-        return 0;
-    if (n_agents == 0) return 256;
-    const uint32_t H = shape->num_kv_heads;
-    const uint32_t d = shape->head_dim;
-    const kvc::AttendPlan p = kvc::pool_attend_plan(H, n_agents, q_heads, d, shape->num_tokens, tail_spec != nullptr);
-    if (!plan_ok(p)) return 0;
-    uint64_t bytes = p.bytes(d);
-    if (tail_spec) {
-        const kvc::AttendPlan t = kvc::page_attend_plan(n_agents, H, q_heads, d, max_tail_tokens, true);
-        if (!plan_ok(t) || t.W + p.W >= (1ull << 31)) return 0;
-        bytes += t.bytes(d);
-    }
-    return (size_t)bytes;
+    Workspace w;
+    return pool_workspace(shape, n_agents, q_heads, tail_spec, max_tail_tokens, w) ? (size_t)w.room : 0;
 }
 
 int kvpool_attend(const kvc_shape* shape, const void* pool, size_t pool_bytes, uint32_t layer, uint32_t n_agents,
@@ -316,9 +336,11 @@ int kvpool_attend(const kvc_shape* shape, const void* pool, size_t pool_bytes, u
         if (tail->spec->num_kv_heads != H || tail->spec->head_dim != d) return KVC_E_SHAPE;
     }
     const uint64_t pool_need = kvpool_bytes(shape);
-    const uint64_t need = kvpool_attend_workspace_bytes(shape, n_agents, q_heads, tail ? tail->spec : nullptr,
-                                                        tail ? tail->table_cols * tail->spec->page_tokens : 0);
-    if (need == 0) return KVC_E_SHAPE;
+    Workspace w;
+    if (!pool_workspace(shape, n_agents, q_heads, tail ? tail->spec : nullptr,
+                        tail ? tail->table_cols * tail->spec->page_tokens : 0, w))
+        return KVC_E_SHAPE;
+    const uint64_t need = w.need;
     if (pool_bytes < pool_need || ws_bytes < need) return KVC_E_SIZE;
     View qv, ov;
     if (!view_of(q, n_agents, q_heads, d, qv) || !view_of(out, n_agents, q_heads, d, ov)) return KVC_E_SHAPE;

@@ -126,8 +126,10 @@ int kvpage_read(const kvc_pages* spec, const void* pages, size_t pages_bytes, ui
 
 /* --------------------------------------------------------------- attention */
 
-/* Workspace bytes of kvpage_attend for sequences of at most max_tokens
- * tokens (table_cols * page_tokens of the call); 0 if an argument is invalid. */
+/* Workspace bytes of kvpage_attend for at most n_seqs sequences of at most
+ * max_tokens tokens (table_cols * page_tokens of the call): never less for more of
+ * either, so one workspace of a program's largest call serves all of its calls. 0 if
+ * an argument is invalid. */
 size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uint32_t q_heads, uint32_t max_tokens);
 
 /* Attention of one new token for each of n_seqs sequences over its pages:
@@ -145,8 +147,9 @@ size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uin
  *   lens       device int32 [n_seqs]
  *   scale      finite, and so times log2(e)
  *   lse        device f32 [n_seqs][q_heads] or NULL: ln sum_t exp(scale * q . k_t)
- *   ws         device workspace, 256-byte aligned, >=
+ *   ws         device workspace, 256-byte aligned, of
  *              kvpage_attend_workspace_bytes(spec, n_seqs, q_heads, table_cols * page_tokens)
+ *              bytes or more
  *   dev_status device int32 or NULL; KVC_DEV_BAD_PAGE, KVC_DEV_BAD_LENGTH: the
  *              sequence's output is then unspecified (lengths are clamped, a
  *              page that is none is taken as page 0)
@@ -180,8 +183,9 @@ typedef struct kvc_tail {
     const int32_t* lens; /* [n_agents] */
 } kvc_tail;
 
-/* Workspace bytes of kvpool_attend; tail_spec NULL: without tails, else for
- * tails of at most max_tail_tokens tokens. 0 if an argument is invalid. */
+/* Workspace bytes of kvpool_attend for at most n_agents agents; tail_spec NULL:
+ * without tails, else for tails of at most max_tail_tokens tokens. Never less for more
+ * agents, pool or tail tokens, or for tails than for none. 0 if an argument is invalid. */
 size_t kvpool_attend_workspace_bytes(const kvc_shape* shape, uint32_t n_agents, uint32_t q_heads,
                                      const kvc_pages* tail_spec, uint32_t max_tail_tokens);
 
