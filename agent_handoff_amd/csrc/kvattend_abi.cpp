@@ -190,8 +190,9 @@ int kvc_norm_rotate(uint32_t n_tokens, uint32_t q_heads, uint32_t kv_heads, uint
                     const kvc_rows* k_in, const void* q_weight, const void* k_weight, float eps,
                     const int64_t* positions, const float* inv_freq, uint32_t n_pairs, uint32_t pairing,
                     const kvc_rows* q_out, const kvc_rows* k_out, hipStream_t stream) {
+    // four tokens a workgroup of 256 threads, fewer than 2^32 threads a launch
     if ((head_dim != 64 && head_dim != 128) || q_heads > (1u << 16) || kv_heads > (1u << 16) ||
-        n_tokens >= (1u << 26))
+        n_tokens > (1u << 26) - 4)
         return KVC_E_SHAPE;
     if (pairing > 1 || n_pairs % 8 != 0 || n_pairs > head_dim / 2 || !(eps >= 0.0f) || isinf(eps)) return KVC_E_RANGE;
     if (n_tokens == 0 || q_heads + kv_heads == 0) return KVC_OK;

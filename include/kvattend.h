@@ -76,7 +76,7 @@ enum {
  * 2 * n_pairs on are not turned. The angle is the binary64 product, reduced
  * to a turn in binary64; everything else is binary32, rounded once to bf16.
  *   q_in, k_in     rows of n_tokens x q_heads and n_tokens x kv_heads;
- *                  n_tokens < 2^26
+ *                  n_tokens <= 2^26 - 4
  *   q_weight, k_weight  device bf16 [head_dim], 16-byte aligned, or NULL: no norm
  *   eps            >= 0 and finite
  *   positions      device int64 [n_tokens], 8-byte aligned (not used, may be
