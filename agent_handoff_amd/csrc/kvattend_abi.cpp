@@ -6,6 +6,9 @@
 
 #include <math.h>
 
+#include <initializer_list>
+#include <numeric>
+
 #include "attend.h"
 #include "layout.h"
 
@@ -50,18 +53,34 @@ bool view_apart(const View& v) {
     return heads_inside || tokens_inside;
 }
 
-// Whether two sets of vectors may share an element: their ranges meet, and
-// they are not interleaved rows of one buffer (equal token strides, each
-// token's heads within the stride, in places of their own).
+// Whether two sets of vectors may share an element: their ranges meet, and no stride S tells them apart, that
+// is, modulo S all of the one lies in places of its own. S is tried as the token stride of both (each token's
+// heads together, as the rows of one buffer), the head stride of both (each head's tokens together), and the
+// greatest common divisor of all strides (single vectors, as of [tokens][heads][3][d]).
 bool views_meet(const View& a, const View& b) {
     if (!overlap(a.data, a.bytes, b.data, b.bytes)) return false;
     const View& x = (uintptr_t)a.data <= (uintptr_t)b.data ? a : b;
     const View& y = (uintptr_t)a.data <= (uintptr_t)b.data ? b : a;
-    const unsigned __int128 rx = (unsigned __int128)(x.heads - 1) * x.hs + x.d;
-    const unsigned __int128 ry = (unsigned __int128)(y.heads - 1) * y.hs + y.d;
-    if (x.ts != y.ts || x.n == 1 || rx > x.ts || ry > y.ts) return true;
-    const uint64_t stride = 2 * x.ts, off = ((uintptr_t)y.data - (uintptr_t)x.data) % stride;
-    return off < 2 * rx || stride - off < 2 * ry;
+    const uint64_t apart = (uintptr_t)y.data - (uintptr_t)x.data;
+    // elements that x and y take from their place on, of every S
+    const auto told_apart = [&](uint64_t S, unsigned __int128 ex, unsigned __int128 ey) {
+        if (ex > S || ey > S) return false;
+        const uint64_t off = apart % (2 * S);
+        return off >= 2 * ex && 2 * S - off >= 2 * ey;
+    };
+    const auto together = [](uint64_t count, uint64_t stride, uint64_t d) {
+        return (unsigned __int128)(count - 1) * stride + d;
+    };
+    if (x.n > 1 && y.n > 1 && x.ts == y.ts && told_apart(x.ts, together(x.heads, x.hs, x.d), together(y.heads, y.hs, y.d)))
+        return false;
+    if (x.heads > 1 && y.heads > 1 && x.hs == y.hs && told_apart(x.hs, together(x.n, x.ts, x.d), together(y.n, y.ts, y.d)))
+        return false;
+    uint64_t g = 0;
+    for (const View* v : {&x, &y}) {
+        if (v->n > 1) g = std::gcd(g, v->ts);
+        if (v->heads > 1) g = std::gcd(g, v->hs);
+    }
+    return !told_apart(g, x.d, y.d);
 }
 
 bool view_meets(const View& a, const void* p, uint64_t n) { return overlap(a.data, a.bytes, p, n); }

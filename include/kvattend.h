@@ -20,9 +20,12 @@
  *    aligned, head_dim is 64 or 128. A stride whose count is 1 is not used.
  *    Rows that are read may repeat (stride 0) and may lie in one buffer (the
  *    rows of a fused projection). Rows that are written must be apart from
- *    one another and from everything that is read; heads of several outputs
- *    may lie in the rows of one buffer. What lies between rows is neither
- *    read nor written.
+ *    one another and from everything that is read. Two sets of rows may lie
+ *    in one buffer, between one another: the heads of a token (or the tokens of
+ *    a head) of each together at places of their own within an equal stride, or
+ *    single vectors at places of their own within the greatest common divisor of
+ *    the strides, as of [tokens][heads][3][head_dim]. What lies between rows is
+ *    neither read nor written.
  *  - Sizes of 0 (tokens, sequences, agents) enqueue nothing and return KVC_OK.
  *  - Sums, maxima and sums of the softmax, and norms are binary32.
  *  - A workspace needs no clearing and holds nothing between calls. Calls
