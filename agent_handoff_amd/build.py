@@ -59,7 +59,11 @@ BINDING_LIB = os.path.join(PKG, "_kvattend.so")
 
 
 def _binding(verbose):
-    import torch
+    try:
+        import torch
+    except ImportError as e:
+        print(f"{os.path.basename(BINDING_LIB)} left out, it needs torch: {e}", flush=True)
+        return
     base = os.path.dirname(torch.__file__)
     _hipcc([BINDING_SRC], BINDING_LIB, verbose,
            ["-isystem", os.path.join(base, "include"), "-I", sysconfig.get_paths()["include"],
@@ -67,19 +71,22 @@ def _binding(verbose):
 
 
 def build(verbose=False, extra=()):
-    """libkvcodec.so (the codec), libkvprobe.so (the benchmark's probes) and _kvattend.so (a binding),
-    every source compiled anew, a few at a time."""
+    """libkvcodec.so (the codec), libkvprobe.so (the benchmark's probes) and _kvattend.so (a binding, which
+    alone needs torch), every source compiled anew, a few at a time. The library is linked whatever becomes of the
+    other two."""
     with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(6) as pool:
         # named without the folder, whose path would get into the library: the same sources give the same bytes
         compiled = [os.path.basename(s) + ".o" for s in sources()]
         # the slowest first
         order = sorted(zip(sources(), compiled), key=lambda x: -os.path.getsize(x[0]))
-        jobs = [pool.submit(_binding, verbose)]
-        jobs += [pool.submit(_hipcc, [s], o, verbose, ["-c"] + list(extra), tmp) for s, o in order]
-        jobs.append(pool.submit(_hipcc, [PROBE_SRC], PROBE_LIB, verbose))
-        for j in jobs:
+        others = [pool.submit(_binding, verbose)]
+        objects = [pool.submit(_hipcc, [s], o, verbose, ["-c"] + list(extra), tmp) for s, o in order]
+        others.append(pool.submit(_hipcc, [PROBE_SRC], PROBE_LIB, verbose))
+        for j in objects:
             j.result()
         _hipcc(compiled, LIB_PATH, verbose, extra, tmp)
+        for j in others:
+            j.result()
     return LIB_PATH
 
 
