@@ -16,6 +16,23 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: long-running")
 
 
+# Tests that hand made-up device addresses to the C entry points without a mark of their own.
+FAKE_ADDRESSES = {("test_attend_abi_host.py", "test_scales_that_powers_of_two_cannot_hold")}
+
+
+def _gpus():
+    import torch
+    return torch.cuda.device_count()
+
+
+def pytest_collection_modifyitems(items):
+    """They run on hosts without a GPU alone: a check that goes missing must not launch a kernel on such addresses."""
+    found = [i for i in items if (i.path.name, getattr(i, "originalname", None)) in FAKE_ADDRESSES]
+    if found and _gpus():
+        for i in found:
+            i.add_marker(pytest.mark.skip(reason="fake device addresses: CPU-only host"))
+
+
 def read_golden(name):
     """key value pairs from tests/golden/<name>; repeated keys become lists."""
     out = {}
