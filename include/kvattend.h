@@ -77,7 +77,9 @@ enum {
  *     pair j of y turned by positions[n] * inv_freq[j]   (first 2 * n_pairs channels)
  * Pair j is (j, j + n_pairs) or (2j, 2j + 1) (KVC_ROPE_*); channels from
  * 2 * n_pairs on are not turned. The angle is the binary64 product, reduced
- * to a turn in binary64; everything else is binary32, rounded once to bf16.
+ * to a turn in binary64; everything else is binary32, rounded once to bf16. So
+ * mean(x^2) + eps has to be a normal binary32 number: values up to 2^60, and with
+ * eps = 0 vectors whose largest value is 2^-59 or more (a zero vector gives NaN).
  *   q_in, k_in     rows of n_tokens x q_heads and n_tokens x kv_heads;
  *                  n_tokens <= 2^26 - 4
  *   q_weight, k_weight  device bf16 [head_dim], 16-byte aligned, or NULL: no norm
@@ -162,7 +164,8 @@ size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uin
  * arguments alone decide: the same call gives the same bits.
  * The 8-bit formats' weights p_t * step are rounded to binary16 after division
  * by a power of two (about the largest step) for the matrix cores, bf16's are
- * split into two bf16 terms; products and sums are binary32. So q . k (before
+ * split into two bf16 terms; products and sums are binary32. Of a weight times its
+ * step, what lies below 2^-36 of the largest step (or of 2^-100) is lost. So q . k (before
  * and after the scale), and the weighted sums before they are divided by the
  * weights' (at most 8 times the tokens times the largest value), have to stay in
  * binary32's range; queries and keys may lie anywhere in bf16's. Where all
