@@ -1129,10 +1129,13 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
     if (p.c.lse && lane == 0) p.c.lse[row] = (M + log2f(total)) * 0.69314718055994531f;
 }
 
-// A workgroup gets at least kMinBlocks blocks: half a launch's latency goes
-// into starting a share and joining it (a 4096-token pool for 15 agents, alone and with
-// tails: 17.3 and 20.8 us with 1, 13.7 and 15.2 with 2, 14.7 and 15.4 with 4). Up to
-// kWholeTokens tokens a unit stays whole and its outputs need no second launch.
+// A workgroup gets at least kMinBlocks blocks of sequences as long as their table is wide: half a launch's latency
+// goes into starting a share and joining it (a 4096-token pool for 15 agents, alone and with tails: 17.3 and 20.8
+// us with 1, 13.7 and 15.2 with 2, 14.7 and 15.4 with 4). The host knows no lengths: far shorter sequences are
+// shared out a block each (one of 100 tokens 5.0 us, with a table eight times as wide as it needs 7.3).
+// Up to kWholeTokens tokens a unit stays whole and its outputs need no second launch: 1, 15 and 64 sequences of 512
+// tokens (8 kv heads of 128, int8) 8.5, 8.8 and 14.9 us, cut up 9.7, 10.2 and 17.5; of 1024 12.3, 13.7 and 24.2,
+// cut up 9.8, 12.7 and 26.9.
 constexpr uint64_t kMinBlocks = 2, kWholeTokens = 512;
 
 // The plan with rt row tiles a wave.
@@ -1144,6 +1147,9 @@ AttendPlan plan_of(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens, u
     a.units = units_of_rows * a.row_blocks;
     const uint64_t slots = 256ull * waves_per_simd(d, rt);
     a.blocks = a.units * ((max_tokens + kBlock - 1) / kBlock);
+    // Eight units for each place of a workgroup balance one another, whatever their lengths, but for a single
+    // long one: 512 sequences (8 kv heads of 128, int8) of 1024 tokens 182 us, cut up 202; of 1 to 2048 197 and
+    // 245; one of 32768 among 511 of 100 tokens 250 and 62.
     a.whole = max_tokens <= kWholeTokens || a.units >= 8 * slots;
     uint64_t w = a.blocks / kMinBlocks < slots ? a.blocks / kMinBlocks : slots;
     if (w < 1) w = 1;
@@ -1165,10 +1171,12 @@ AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens,
                      bool direct) {
     // Two row tiles of a wave share the widening of the tokens, but start and
     // join later: taken where every workgroup has a block to do. A call with two and
-    // with one, us: pool of 15 agents, 60 rows, heads of 128: 131071 tokens 68.5 and 103,
-    // 4096 with tails 15.2 and 18.0, 1024 11.5 and 9.7. Pages, 8 sequences of 8192, 2 kv
-    // heads: heads of 64, 17 rows int8 12.4 and 13.0, bf16 12.0 and 15.6; heads of 128,
-    // int8 32 rows 19.9 and 17.0 (registers), 48 rows 22.0 and 25.3, bf16 27.3 and 37.3.
+    // with one, over the same inputs again and again (which the 256 MB cache then holds; a
+    // pool of 131071 tokens that it does not hold takes 78), us: pool of 15 agents, 60 rows, heads of 128:
+    // 131071 tokens 70 and 103, 4096 with tails 15.2 and 18.0, 1024 11.5 and 9.7. Pages, 8
+    // sequences of 8192, 2 kv heads: heads of 64, 17 rows int8 12.4 and 13.0, bf16 12.0 and
+    // 15.6; heads of 128, int8 32 rows 19.9 and 17.0, 48 rows 21.6 and 25.3, bf16 27.3
+    // and 37.3 (where 44 vector registers are spilled).
     const uint64_t most_blocks = (max_tokens + kBlock - 1) / kBlock;
     const bool enough = units_of_rows * ((rows + 31) / 32) * most_blocks >= 256ull * waves_per_simd(d, 2);
     return plan_of(units_of_rows, rows, max_tokens, d, rows > one_tile && enough ? 2 : 1, direct);
@@ -1276,6 +1284,10 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     j.rt[1] = has_pages ? page_plan.rt : 1;
     j.sources = p.direct ? 1 : 2;
     const uint64_t rows = (uint64_t)a.n * a.Hq;
+    // One wave joins a row of few parts, four one of many. A call with one and with four, us: pages of 1, 4, 8, 15
+    // and 32 sequences of 4096 tokens (W / units 64, 16, 8, 4, 2) 10.4 and 10.0, 13.4 and 13.1, 18.3 and 18.6, 28.8
+    // and 29.2, 48.0 and 48.7; a pool of 8192 tokens for 4 agents (32) 12.2 and 10.7, of 131071 over 2 kv heads (256) 32.9
+    // and 19.9. It goes by the mean: of 100 sequences (5) one of 40000 tokens among 99 of 100 takes 31.2, with four 16.4.
     const bool few = first.whole || first.W <= 6 * first.units;
     if (few)
         return launch_kernel(a.d == 64 ? attend_join_kernel<64, 1> : attend_join_kernel<128, 1>,

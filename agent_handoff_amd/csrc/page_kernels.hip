@@ -262,7 +262,10 @@ PageParams page_params(const PageLayout& l, const void* pages, uint32_t n, const
     return p;
 }
 
-// Four vectors for each group of lanes where that still fills the GPU.
+// Four vectors for each group of lanes where that still fills the GPU: 8 heads of 128, us with one and with four,
+// 2048 tokens bf16 written 3.8 and 4.0, read 3.2 and 3.4, e4m3 4.3 and 5.0, 3.4 and 3.7; 4096 (from where it is
+// taken) 5.7 and 5.4, 4.5 and 4.3, e4m3 6.5 and 7.0, 4.5 and 4.6; 8192 11.8 and 11.0, 8.8 and 9.2, e4m3 11.6 and
+// 11.3, 7.6 and 7.2.
 template <int FMT, int D>
 hipError_t launch_page(bool write, const PageParams& p, hipStream_t stream) {
     constexpr uint32_t VPB = kBlockThreads / (D / 8);

@@ -178,7 +178,7 @@ __global__ __launch_bounds__(kBlockThreads, 5) void norm_rotate_kernel(RotatePar
                 }
             }
         }
-        if (TW > 1) {  // a prompt's rows: 30.1 us with the hint, 35.3 without
+        if (TW > 1) {  // a prompt's rows: 33.7 us with the hint, 35.1 without
             __builtin_nontemporal_store(pack8(a), ya);
             __builtin_nontemporal_store(pack8(b), yb);
         } else {
@@ -206,9 +206,11 @@ hipError_t launch_norm_rotate(const RotateArgs& a, hipStream_t stream) {
     p.pairing = a.pairing;
     p.eps = a.eps;
     for (uint32_t j = 0; j < a.n_pairs; ++j) p.f[j] = a.inv_freq[j];
-    // four tokens a workgroup (every thread takes an angle) once that still
-    // leaves four workgroups to a CU; 8191 tokens of 40 heads of 128: 30.1 us
-    // (5.6 TB/s), with two 29.6, with eight 30.7
+    // From 4096 tokens on a workgroup takes four (every thread an angle) and stores past the caches, below one,
+    // with plain stores. Calls over rows that no cache holds, 40 heads of 128, us, for one token a workgroup, one
+    // with the hint, and two and four with it: 256 tokens 4.6, 4.2, 5.0, 6.6; 1024 7.3, 6.9, 7.7, 8.3; 2048 11.9,
+    // 10.6, 10.3, 11.3; 4095 20.0, 19.3, 19.0, 18.8; 8191 33.4, 31.7, 32.3, 33.7 (5.0 TB/s). Not taken yet:
+    // the hint with fewer tokens, 5 % from 256 tokens on.
     if (a.n >= 4096)
         return launch_kernel(a.d == 64 ? norm_rotate_kernel<64, 4> : norm_rotate_kernel<128, 4>, dim3((a.n + 3) / 4),
                              dim3(kBlockThreads), stream, p);
