@@ -19,12 +19,12 @@
 //
 // Bound: pages, memory; the codes are read once, and a tile costs d / 4 matrix
 // instructions per 16 rows, far below their rate (32 sequences of up to 16384
-// tokens, 8 kv heads of 128, e4m3: 99 us, 5.6 TB/s of codes and steps). A pool
+// tokens, 8 kv heads of 128, e4m3: 98 us, 5.6 TB/s of codes and steps). A pool
 // holds 178 bytes for a token's key and value of 128 channels instead of 264, and
 // many rows share them: there the vector instructions of widening and softmax
 // and the matrix instructions, which a SIMD issues one at a time, bound it
-// (131071 tokens, 8 kv heads of 128, 60 rows: 76 us, 2.4 TB/s; of a SIMD's
-// cycles the VALU takes 71 %, the matrix core 18 %). Short calls are bound by latency: three
+// (131071 tokens, 8 kv heads of 128, 60 rows: 77 us, 2.4 TB/s; of a SIMD's
+// cycles the VALU takes 72 %, the matrix core 18 %). Short calls are bound by latency: three
 // dependent reads, a tile, the join of four waves: 5.5 us.
 //
 // Tried and left out: keeping two tiles of loads in registers (spills, or the same
