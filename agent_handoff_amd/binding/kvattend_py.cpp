@@ -23,6 +23,9 @@ decltype(&kvpage_write) f_page_write = nullptr;
 decltype(&kvpage_read) f_page_read = nullptr;
 decltype(&kvpage_attend) f_page_attend = nullptr;
 decltype(&kvpool_attend) f_pool_attend = nullptr;
+decltype(&kvpage_append) f_page_append = nullptr;
+decltype(&kvpage_attend_window) f_page_attend_window = nullptr;
+decltype(&kvpage_attend_prompt) f_page_attend_prompt = nullptr;
 
 PyObject* g_kvc_error = nullptr;   // kvcodec.KvcError
 PyObject* g_raw_stream = nullptr;  // device -> handle of its current stream
@@ -375,7 +378,60 @@ PyObject* page_copy(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject
     });
 }
 
-// What the two attention calls have in common.
+const char kAppendDoc[] =
+    "kvpage_append(spec, pages, q, k, v, positions, inv_freq, slots, q_out, q_weight=None, k_weight=None, eps=1e-6,\n"
+    "              pairing=0, dev_status=None, stream=None)\n\n"
+    "q, q_out: rows [n, q_heads, head_dim] (both may be None; the same tensor for in place); k, v: rows\n"
+    "[n, num_kv_heads, head_dim]; positions, inv_freq and weights as for kvc_norm_rotate, slots as for kvpage_write.";
+PyObject* page_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+    return guarded([&]() -> PyObject* {
+        static const char* const names[15] = {"spec", "pages", "q", "k", "v", "positions", "inv_freq", "slots", "q_out",
+                                              "q_weight", "k_weight", "eps", "pairing", "dev_status", "stream"};
+        Args<15> a("kvpage_append", names, 15, 9, args, nargs, kwnames);
+        PyObject** g = a.given;
+        if (!g[0]) refuse("spec: description required");
+        if ((!g[2]) != (!g[8])) refuse("q needs q_out");
+        const kvc_pages spec = spec_of(g[0]);
+        const at::Tensor& pages = a.need(g[1], "pages");
+        void* at = bytes_of(pages, "pages");
+        const at::Tensor& slots = a.need(g[7], "slots");
+        const int64_t n = slots.numel(), d = spec.head_dim;
+        const int64_t shape[3] = {n, spec.num_kv_heads, d};
+        const kvc_rows k = rows_of(a.need(g[3], "k"), shape, "k"), v = rows_of(a.need(g[4], "v"), shape, "v");
+        const auto* sl = static_cast<const int64_t*>(plain(slots, at::kLong, {n}, "slots"));
+        kvc_rows q{}, out{};
+        int64_t heads = 0;
+        if (g[2]) {
+            const at::Tensor& x = a.need(g[2], "q");
+            if (x.dim() != 3) refuse("q: expected rows [tokens, heads, head_dim]");
+            heads = x.size(1);
+            q = rows_of(x, {n, heads, d}, "q");
+            out = rows_of(a.need(g[8], "q_out"), {n, heads, d}, "q_out");
+        }
+        const void* weight[2] = {};
+        static const char* const what[2] = {"q_weight", "k_weight"};
+        for (int i = 0; i < 2; ++i)
+            if (g[9 + i]) weight[i] = plain(a.need(g[9 + i], what[i]), at::kBFloat16, {d}, what[i]);
+        if (!g[6]) refuse("inv_freq: floats required");
+        const Floats f(g[6]);
+        const void* pos = nullptr;
+        if (g[5])
+            pos = plain(a.need(g[5], "positions"), at::kLong, {n}, "positions");
+        else if (f.size())
+            refuse("positions: tensor required");
+        const float eps = number(g[11], 1e-6f);
+        const uint32_t pairing = g[12] ? whole(g[12], "pairing") : 0, nt = count32(n, "slots"), hq = count32(heads, "q_heads");
+        int32_t* st = g[13] ? static_cast<int32_t*>(plain(a.need(g[13], "dev_status"), at::kInt, {1}, "dev_status")) : nullptr;
+        const size_t size = (size_t)pages.numel();
+        return launch("kvpage_append", a, g[14], [&](hipStream_t s) {
+            return f_page_append(&spec, at, size, nt, hq, g[2] ? &q : nullptr, &k, &v, weight[0], weight[1], eps,
+                                 static_cast<const int64_t*>(pos), f.size() ? f.data() : nullptr, f.size(), pairing, sl,
+                                 g[2] ? &out : nullptr, st, s);
+        });
+    });
+}
+
+// What the attention calls have in common.
 struct Attend {
     uint32_t n, hq;
     int64_t d;
@@ -408,7 +464,7 @@ struct Table {
     uint32_t cols;
     uint64_t stride;
     template <class A>
-    Table(A& a, PyObject* to, PyObject* lo, uint32_t n) {
+    Table(A& a, PyObject* to, PyObject* lo, int64_t n) {
         const at::Tensor& t = a.need(to, "table");
         if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != n || (n && t.size(1) > 1 && t.stride(1) != 1))
             refuse("table: expected int32 [" + std::to_string(n) + ", columns] with contiguous rows");
@@ -440,6 +496,64 @@ PyObject* page_attend(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
         return launch("kvpage_attend", a, g[10], [&](hipStream_t s) {
             return f_page_attend(&spec, at, size, x.n, x.hq, &x.q, t.table, t.cols, t.stride, t.lens, x.scale, &x.out, x.lse,
                                  x.ws, x.ws_bytes, x.status, s);
+        });
+    });
+}
+
+const char kWindowDoc[] =
+    "kvpage_attend_window(spec, pages, q, table, lens, window, sinks, out, ws, lse=None, scale=None, dev_status=None,\n"
+    "                     stream=None)\n\n"
+    "kvpage_attend of the last `window` tokens (0: all) and the first `sinks`; ws: uint8 workspace\n"
+    "(kvpage_attend_window_workspace_bytes).";
+PyObject* page_attend_window(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+    return guarded([&]() -> PyObject* {
+        static const char* const names[13] = {"spec", "pages", "q", "table", "lens", "window", "sinks", "out", "ws", "lse",
+                                              "scale", "dev_status", "stream"};
+        Args<13> a("kvpage_attend_window", names, 13, 9, args, nargs, kwnames);
+        PyObject** g = a.given;
+        if (!g[0] || !g[5] || !g[6]) refuse("spec, window and sinks are required");
+        const kvc_pages spec = spec_of(g[0]);
+        const at::Tensor& pages = a.need(g[1], "pages");
+        void* at = bytes_of(pages, "pages");
+        const uint32_t window = whole(g[5], "window"), sinks = whole(g[6], "sinks");
+        const Attend x(a, spec.head_dim, g[2], g[7], g[8], g[9], g[10], g[11]);
+        const Table t(a, g[3], g[4], x.n);
+        const size_t size = (size_t)pages.numel();
+        return launch("kvpage_attend_window", a, g[12], [&](hipStream_t s) {
+            return f_page_attend_window(&spec, at, size, x.n, x.hq, &x.q, t.table, t.cols, t.stride, t.lens, window, sinks,
+                                        x.scale, &x.out, x.lse, x.ws, x.ws_bytes, x.status, s);
+        });
+    });
+}
+
+const char kPromptDoc[] =
+    "kvpage_attend_prompt(spec, pages, q, starts, table, lens, out, ws, window=0, sinks=0, lse=None, scale=None,\n"
+    "                     dev_status=None, stream=None)\n\n"
+    "q, out: rows [n, q_heads, head_dim] of the new tokens of all sequences; starts: int32 [sequences + 1], first row\n"
+    "of each and the end of the last; table: int32 [sequences, columns]; lens: int32 [sequences], the new tokens\n"
+    "among them; ws: uint8 workspace (kvpage_attend_prompt_workspace_bytes); lse: float32 [n, q_heads] or None.";
+PyObject* page_attend_prompt(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kwnames) {
+    return guarded([&]() -> PyObject* {
+        static const char* const names[14] = {"spec", "pages", "q", "starts", "table", "lens", "out", "ws", "window", "sinks",
+                                              "lse", "scale", "dev_status", "stream"};
+        Args<14> a("kvpage_attend_prompt", names, 14, 8, args, nargs, kwnames);
+        PyObject** g = a.given;
+        if (!g[0]) refuse("spec: description required");
+        const kvc_pages spec = spec_of(g[0]);
+        const at::Tensor& pages = a.need(g[1], "pages");
+        void* at = bytes_of(pages, "pages");
+        const uint32_t window = g[8] ? whole(g[8], "window") : 0, sinks = g[9] ? whole(g[9], "sinks") : 0;
+        const Attend x(a, spec.head_dim, g[2], g[6], g[7], g[10], g[11], g[12]);
+        const at::Tensor& starts = a.need(g[3], "starts");
+        if (starts.dim() != 1 || starts.size(0) < 1) refuse("starts: expected int32 [sequences + 1]");
+        const int64_t n = starts.size(0) - 1;
+        const auto* st = static_cast<const int32_t*>(plain(starts, at::kInt, {n + 1}, "starts"));
+        const Table t(a, g[4], g[5], n);
+        const uint32_t seqs = count32(n, "starts");
+        const size_t size = (size_t)pages.numel();
+        return launch("kvpage_attend_prompt", a, g[13], [&](hipStream_t s) {
+            return f_page_attend_prompt(&spec, at, size, seqs, x.n, x.hq, &x.q, st, t.table, t.cols, t.stride, t.lens, window,
+                                        sinks, x.scale, &x.out, x.lse, x.ws, x.ws_bytes, x.status, s);
         });
     });
 }
@@ -488,12 +602,13 @@ bool take_address(F& f, PyObject* o) {
 // setup(KvcError, raw_stream, device, device_guard, as_floats, the entry points' addresses...)
 PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     PyObject** to[5] = {&g_kvc_error, &g_raw_stream, &g_device, &g_device_guard, &g_as_floats};
-    if (nargs != 10) {
-        PyErr_SetString(PyExc_TypeError, "setup takes 10 arguments");
+    if (nargs != 13) {
+        PyErr_SetString(PyExc_TypeError, "setup takes 13 arguments");
         return nullptr;
     }
     if (!take_address(f_norm_rotate, args[5]) || !take_address(f_page_write, args[6]) || !take_address(f_page_read, args[7]) ||
-        !take_address(f_page_attend, args[8]) || !take_address(f_pool_attend, args[9]))
+        !take_address(f_page_attend, args[8]) || !take_address(f_pool_attend, args[9]) || !take_address(f_page_append, args[10]) ||
+        !take_address(f_page_attend_window, args[11]) || !take_address(f_page_attend_prompt, args[12]))
         return nullptr;
     for (int i = 0; i < 5; ++i) {
         Py_INCREF(args[i]);
@@ -509,6 +624,9 @@ PyMethodDef methods[] = {
     {"kvpage_read", FAST(page_copy<false>), kReadDoc},
     {"kvpage_attend", FAST(page_attend), kPageDoc},
     {"kvpool_attend", FAST(pool_attend), kPoolDoc},
+    {"kvpage_append", FAST(page_append), kAppendDoc},
+    {"kvpage_attend_window", FAST(page_attend_window), kWindowDoc},
+    {"kvpage_attend_prompt", FAST(page_attend_prompt), kPromptDoc},
     {"setup", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(setup)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvattend", "Calls of include/kvattend.h on torch tensors.", -1, methods};

@@ -15,17 +15,29 @@ struct RowsDev {
     uint64_t ts, hs;
 };
 
-// Byte layout of one page (see kvattend.h): codes, then (8-bit formats) steps.
+// KVC_PAGE_*
+constexpr int kPageBf16 = 0, kPageInt8 = 1, kPageFp8 = 2, kPageFp4 = 4;
+constexpr uint32_t kFp4Block = 32;  // channels that share a power of two
+
+// Byte layout of one page (see kvattend.h): codes, then (but for bf16) steps.
 struct PageLayout {
     uint32_t num_pages, H, P, d, format;
-    uint32_t esize;        // bytes of one code
     uint64_t steps;        // offset of the steps in a page
     uint64_t page_bytes;
 };
 
+// Bytes of a vector's codes, and of its step or steps.
+KVC_HD constexpr uint32_t page_code_bytes(int format, uint32_t d) {
+    return format == kPageBf16 ? 2 * d : format == kPageFp4 ? d / 2 : d;
+}
+KVC_HD constexpr uint32_t page_step_bytes(int format, uint32_t d) {
+    return format == kPageBf16 ? 0 : format == kPageFp4 ? d / kFp4Block : 4;
+}
+
 inline bool page_spec_ok(uint32_t num_pages, uint32_t H, uint32_t P, uint32_t d, uint32_t format) {
     return num_pages >= 1 && num_pages <= 0x7FFFFFFFu && H >= 1 && H <= (1u << 16) &&
-           (P == 16 || P == 32 || P == 64 || P == 128 || P == 256) && (d == 64 || d == 128) && format <= 2;
+           (P == 16 || P == 32 || P == 64 || P == 128 || P == 256) && (d == 64 || d == 128) &&
+           (format <= 2 || format == kPageFp4);
 }
 
 inline PageLayout page_layout(uint32_t num_pages, uint32_t H, uint32_t P, uint32_t d, uint32_t format) {
@@ -35,9 +47,8 @@ inline PageLayout page_layout(uint32_t num_pages, uint32_t H, uint32_t P, uint32
     l.P = P;
     l.d = d;
     l.format = format;
-    l.esize = format == 0 ? 2 : 1;
-    l.steps = 2ull * H * P * d * l.esize;
-    l.page_bytes = align_up(l.steps + (format == 0 ? 0 : 2ull * H * P * 4), 256);
+    l.steps = 2ull * H * P * page_code_bytes(format, d);
+    l.page_bytes = align_up(l.steps + 2ull * H * P * page_step_bytes(format, d), 256);
     return l;
 }
 
@@ -57,6 +68,22 @@ hipError_t launch_page_write(const PageLayout& l, void* pages, uint32_t n, const
                              const int64_t* slots, int32_t* dev_status, hipStream_t stream);
 hipError_t launch_page_read(const PageLayout& l, const void* pages, uint32_t n, const int64_t* slots,
                             const RowsDev& k_out, const RowsDev& v_out, int32_t* dev_status, hipStream_t stream);
+
+// Norms, rotation and the write (kvpage_append).
+struct AppendArgs {
+    uint32_t n, Hq;
+    PageLayout lay;
+    uint8_t* pages;
+    RowsDev q_in, k_in, v_in, q_out;
+    const void *q_weight, *k_weight;
+    float eps;
+    const int64_t* positions;
+    const float* inv_freq;  // host
+    uint32_t n_pairs, pairing;
+    const int64_t* slots;
+    int32_t* status;
+};
+hipError_t launch_append(const AppendArgs& a, hipStream_t stream);
 
 // How the tokens of one source (a pool's layer, or pages) are shared out among
 // workgroups. A unit is the work of one kv head of one sequence (of all
@@ -81,6 +108,14 @@ struct AttendPlan {
 AttendPlan page_attend_plan(uint32_t n_seqs, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens, bool tail);
 AttendPlan pool_attend_plan(uint32_t H, uint32_t n_agents, uint32_t Hq, uint32_t d, uint32_t T, bool tail);
 
+// Tokens that a call over at most max_tokens counts for a sequence, at most: with a
+// window, its tokens and the sinks, each up to the next run of 16.
+inline uint64_t seen_tokens(uint64_t max_tokens, uint64_t window, uint64_t sinks) {
+    if (!window) return max_tokens;
+    const uint64_t most = window + align_up(sinks, 16) + 15;
+    return most < max_tokens ? most : max_tokens;
+}
+
 struct TailArgs {
     PageLayout lay;
     const uint8_t* pages;
@@ -88,6 +123,7 @@ struct TailArgs {
     uint32_t table_cols;
     uint64_t table_stride;
     const int32_t* lens;
+    uint32_t window, sinks;  // window 0: every token
 };
 struct AttendArgs {
     uint32_t n, H, Hq, d;  // sequences (agents), kv heads, query heads, channels
@@ -103,6 +139,31 @@ struct AttendArgs {
     TailArgs tail;
 };
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
+
+// Attention of many new tokens. The query rows of a sequence and kv head (tokens x
+// the heads that share it) are taken in blocks, one a workgroup and share of the
+// tokens; `blocks` bounds how many a kv head has, which the host does not know.
+constexpr uint32_t kPromptRows = 64;  // of the smallest block
+struct PromptPlan {
+    uint32_t rows;    // of a block
+    uint32_t splits;  // shares of the tokens
+    uint64_t blocks;
+    uint64_t bytes;   // of the workspace: what the call uses,
+    uint64_t room;    // and what serves every smaller call too
+};
+PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens,
+                       uint32_t window, uint32_t sinks);
+struct PromptArgs {
+    uint32_t n, rows, H, Hq, d;  // sequences, query rows (tokens), kv heads, query heads, channels
+    RowsDev q, out;
+    float scale;
+    float* lse;
+    void* ws;
+    int32_t* status;
+    const int32_t* starts;
+    TailArgs tail;
+};
+hipError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& plan, hipStream_t stream);
 
 #ifdef __HIPCC__
 // Asks for every 64-byte line of the kernel's arguments (BYTES of them) at

@@ -51,6 +51,7 @@
 #include "attend.h"
 #include "codebook.h"
 #include "kernels_common.h"
+#include "page_codes.h"
 
 #include <type_traits>
 
@@ -58,7 +59,9 @@ namespace kvc {
 namespace {
 
 constexpr int kDevBadHeader = 1, kDevBadPage = 32, kDevBadLength = 64;  // KVC_DEV_*
-constexpr int kFmtBf16 = 0, kFmtInt8 = 1, kFmtFp8 = 2, kFmtPool = 3;
+constexpr int kFmtBf16 = kPageBf16, kFmtInt8 = kPageInt8, kFmtFp8 = kPageFp8, kFmtFp4 = kPageFp4, kFmtPool = 3;
+// Products in binary16 (codes of 8 bits, levels) or in bf16 (which holds a 4-bit code times its power of two exactly).
+constexpr bool half_products(int fmt) { return fmt != kFmtBf16 && fmt != kFmtFp4; }
 constexpr int kWaves = 4;
 constexpr uint32_t kTile = 32;
 constexpr uint32_t kBlock = kWaves * kTile;  // tokens of one step of a workgroup
@@ -68,7 +71,6 @@ constexpr int kWeightExp = 12;
 constexpr int kMinExp = -100;  // steps below 2^-100 are taken with this exponent
 constexpr float kNegInf = -__builtin_inff();
 
-typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -99,7 +101,15 @@ struct Source {
     // pool
     const uint8_t* pool;
     PoolLayout lay;
-    uint32_t L, T, layer;
+    union {
+        uint32_t L;
+        uint32_t window;  // pages with a window
+    };
+    union {
+        uint32_t T;
+        uint32_t sinks;
+    };
+    uint32_t layer;
     uint32_t more;  // shares of `each` blocks, the first `more` of them one larger
     uint64_t each;
     // pages
@@ -122,28 +132,9 @@ __device__ __forceinline__ f32x4 mfma_bf16(const u32x4& a, const u32x4& b, const
 }
 template <int FMT>
 __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
-    return FMT == kFmtBf16 ? mfma_bf16(a, b, c) : mfma_half(a, b, c);
+    return half_products(FMT) ? mfma_half(a, b, c) : mfma_bf16(a, b, c);
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    half2_t r;
-    r.x = (_Float16)lo;
-    r.y = (_Float16)hi;
-    return __builtin_bit_cast(uint32_t, r);
-}
-
-// Bytes b0, b1 (or b2, b3) of w, int8 codes with their sign bit flipped, to
-// two binary16 codes: 0x64bb is 1024 + b, exact, and so is the difference.
-template <bool HI>
-__device__ __forceinline__ uint32_t widen_int8(uint32_t w) {
-    const uint32_t u = __builtin_amdgcn_perm(0x64646464u, w, HI ? 0x04030402u : 0x04010400u);
-    const half2_t bias = {(_Float16)1152.0f, (_Float16)1152.0f};
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, u) - bias);
-}
-template <bool HI>
-__device__ __forceinline__ uint32_t widen_fp8(uint32_t w) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.0f, HI));
-}
 template <int FMT, bool HI>
 __device__ __forceinline__ uint32_t widen(uint32_t w) {
     return FMT == kFmtFp8 ? widen_fp8<HI>(w) : widen_int8<HI>(w);
@@ -180,6 +171,14 @@ struct Raw<kFmtPool, D> {
     uint4 k[2][D / 64];
     uint32_t v[2][3];  // one word of each plane of one token per run of 16 (see gather_bytes)
     uint2 vs[2];       // four binary16 sizes per run
+};
+
+template <int D>
+struct Raw<kFmtFp4, D> {
+    uint32_t k[2][D / 32];   // the lane's quarter of a key's codes
+    uint32_t kp[2];          // its power of two
+    uint32_t v[8];           // D / 16 codes of a value
+    uint32_t vp[2][D / 32];  // powers of the four tokens of a run, D / 32 bytes each
 };
 
 // a where the mask has ones, b elsewhere; one instruction, which the compiler
@@ -254,6 +253,26 @@ __device__ __forceinline__ uint32_t clamp_length(const Source& p, int32_t len) {
 }
 __device__ __forceinline__ bool bad_length(const Source& p, int32_t len) {
     return len < 0 || (uint32_t)len > p.table_cols << p.page_shift;
+}
+// What a new token sees of `len` tokens with a window and sinks: tokens below
+// min(sinks, lo) and from lo = len - window on. The gap between them is cut out
+// in whole runs of 16, so that runs stay inside pages: tokens are counted without it
+// (`len` of them), and those from hid0 to hid1, less than two runs, do not count.
+struct Seen {
+    uint32_t len, hid0, hid1;
+    uint32_t cut, gap;  // token t stands for t + gap from `cut` on
+};
+template <bool WIN>
+__device__ __forceinline__ Seen seen_of(const Source& p, uint32_t len) {
+    Seen s{len, 0, 0, 0, 0};
+    if (!WIN) return s;
+    const uint32_t lo = len > p.window ? len - p.window : 0;
+    s.hid0 = p.sinks < lo ? p.sinks : lo;
+    s.cut = (s.hid0 + 15) & ~15u;
+    s.gap = (lo & ~15u) > s.cut ? (lo & ~15u) - s.cut : 0;
+    s.len = len - s.gap;
+    s.hid1 = lo - s.gap;
+    return s;
 }
 // Blocks of a length; an empty sequence has one, without tokens.
 __device__ __forceinline__ uint32_t blocks_of(uint32_t len) { return len <= kBlock ? 1 : (len + kBlock - 1) / kBlock; }
@@ -370,11 +389,11 @@ __device__ __forceinline__ uint32_t scan_threads(uint32_t v, uint32_t* sums, uin
 }
 
 // The share of workgroup w.
-template <int FMT, int D, int RT>
+template <int FMT, int D, int RT, bool WIN>
 __device__ __forceinline__ void attend_share(const Common& p, const Source& src, uint32_t w, Shared<D, RT>& sh) {
     constexpr int KS = D / 32;   // key product steps
     constexpr int NC = D / 16;   // channels of a lane, value products
-    constexpr bool HALF = FMT != kFmtBf16;
+    constexpr bool HALF = half_products(FMT);
     using R = Raw<FMT, D>;
     const uint32_t lane = lane_id(), c = lane & 15, g = lane >> 4;
     const uint32_t wave = wave_uniform(threadIdx.x / kWave);
@@ -422,7 +441,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         uint32_t part;
         if (p.n <= kWave) {
             // a sequence a lane, in every wave for itself
-            const uint32_t v = lane < p.n ? blocks_of(clamp_length(src, src.lens[lane])) : 0;
+            const uint32_t v = lane < p.n ? blocks_of(seen_of<WIN>(src, clamp_length(src, src.lens[lane])).len) : 0;
             const uint32_t up = scan_lanes(v);
             if (!share((uint64_t)__builtin_amdgcn_readlane(up, 63) * per_seq)) return;
             divmod_u64(x0, per_seq, q64, part);
@@ -434,7 +453,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             const uint32_t run = (p.n + kWaves * kWave - 1) / (kWaves * kWave);
             const uint32_t s0 = threadIdx.x * run, s1 = s0 + run < p.n ? s0 + run : p.n;
             uint32_t v = 0, all;
-            for (uint32_t s = s0; s < s1; ++s) v += blocks_of(clamp_length(src, src.lens[s]));
+            for (uint32_t s = s0; s < s1; ++s) v += blocks_of(seen_of<WIN>(src, clamp_length(src, src.lens[s])).len);
             const uint32_t at0 = scan_threads(v, sh.sums, all);
             if (!share((uint64_t)wave_uniform(all) * per_seq)) return;
             divmod_u64(x0, per_seq, q64, part);
@@ -442,7 +461,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             if (q >= at0 && q - at0 < v) {
                 uint32_t at = at0, s = s0, nb = 0;
                 for (; s < s1; ++s) {
-                    nb = blocks_of(clamp_length(src, src.lens[s]));
+                    nb = blocks_of(seen_of<WIN>(src, clamp_length(src, src.lens[s])).len);
                     if (q - at < nb) break;
                     at += nb;
                 }
@@ -479,23 +498,29 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             const uint8_t* qp = reinterpret_cast<const uint8_t*>(p.q.data + (uint64_t)seq * p.q.ts + (uint64_t)qh * p.q.hs);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const uint32_t ch = HALF ? (s / 2) * 64 + g * 16 + (s % 2) * 8 : s * 32 + g * 8;
+                const uint32_t ch = FMT == kFmtFp4 ? g * (D / 4) + s * 8
+                                    : HALF         ? (s / 2) * 64 + g * 16 + (s % 2) * 8
+                                                   : s * 32 + g * 8;
                 load_words(qp + 2 * ch, qw[rt][s]);
             }
         }
         // page numbers of this wave's 16-token runs: run i of tile t in lane 2t + i
         // (whole rows of the table can be read, whatever the length)
         const uint32_t run0 = ((lane >> 1) * kWaves + wave) * kTile + (lane & 1) * 16;
+        Seen seen{};
+        const auto real = [&](uint32_t t) { return WIN && t >= seen.cut ? t + seen.gap : t; };
         const auto load_pages = [&](uint32_t base) {
-            const uint32_t t = (base + run0) >> src.page_shift;
+            const uint32_t t = real(base + run0) >> src.page_shift;
             return src.table[b * src.table_stride + (t < src.table_cols ? t : 0)];
         };
         int32_t given = 0, page = 0;
         if (FMT != kFmtPool) {
             given = src.lens[b];
-            page = load_pages(off * kBlock);
+            if (!WIN) page = load_pages(off * kBlock);
         }
-        const uint32_t len = FMT == kFmtPool ? src.T : wave_uniform(clamp_length(src, given));
+        seen = seen_of<WIN>(src, FMT == kFmtPool ? src.T : wave_uniform(clamp_length(src, given)));
+        if (WIN) page = load_pages(off * kBlock);
+        const uint32_t len = seen.len;
         if (FMT != kFmtPool && hr == 0 && off == 0 && threadIdx.x == 0 && bad_length(src, given) && p.status)
             atomicOr(p.status, kDevBadLength);
         nb = blocks_of(len);
@@ -547,32 +572,45 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                     }
                 }
             } else {
-                constexpr uint32_t ROW = FMT == kFmtBf16 ? 2 * D : D;
+                constexpr uint32_t ROW = page_code_bytes(FMT, D);
                 const uint32_t P = 1u << src.page_shift;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t pg = __builtin_amdgcn_readlane(my_page, (2 * it + i) & 63);
                     const uint8_t* pb = src.pages + (uint64_t)pg * src.page_bytes;
-                    const uint32_t at = (t0 + 16 * i) & (P - 1);
+                    const uint32_t at = real(t0 + 16 * i) & (P - 1);
                     const uint32_t kl = h * P + at, vl = (p.H + h) * P + at;  // rows inside the page
                     const uint8_t* kb = pb + (uint64_t)kl * ROW;
                     const uint8_t* vb = pb + (uint64_t)vl * ROW;
+                    if constexpr (FMT == kFmtFp4) {
+                        constexpr uint32_t PB = D / kFp4Block;  // powers of a vector
+                        const uint8_t* sb = pb + src.steps;
+                        load_words(kb + c * ROW + g * (ROW / 4), x.k[i]);
+                        x.kp[i] = sb[(uint64_t)(kl + c) * PB + g / (4 / PB)];
 #pragma unroll
-                    for (int s = 0; s < R::KL; ++s)
-                        x.k[i][s] = *reinterpret_cast<const uint4*>(kb + c * ROW + 64 * s + 16 * g);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint8_t* va = vb + (4 * g + j) * ROW + c * (ROW / 16);
+                            x.v[4 * i + j] = D == 128 ? *reinterpret_cast<const uint32_t*>(va) : *reinterpret_cast<const uint16_t*>(va);
+                        }
+                        load_words(sb + (uint64_t)(vl + 4 * g) * PB, x.vp[i]);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) load_words(vb + (4 * g + j) * ROW + c * (ROW / 16), x.v[4 * i + j]);
-                    if (FMT != kFmtBf16) {
-                        const float4 a = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(kl + 4 * g) * 4);
-                        const float4 w = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(vl + 4 * g) * 4);
-                        x.ks[4 * i] = a.x;
-                        x.ks[4 * i + 1] = a.y;
-                        x.ks[4 * i + 2] = a.z;
-                        x.ks[4 * i + 3] = a.w;
-                        x.vs[4 * i] = w.x;
-                        x.vs[4 * i + 1] = w.y;
-                        x.vs[4 * i + 2] = w.z;
-                        x.vs[4 * i + 3] = w.w;
+                        for (int s = 0; s < R::KL; ++s)
+                            x.k[i][s] = *reinterpret_cast<const uint4*>(kb + c * ROW + 64 * s + 16 * g);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) load_words(vb + (4 * g + j) * ROW + c * (ROW / 16), x.v[4 * i + j]);
+                        if (FMT != kFmtBf16) {
+                            const float4 a = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(kl + 4 * g) * 4);
+                            const float4 w = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(vl + 4 * g) * 4);
+                            x.ks[4 * i] = a.x;
+                            x.ks[4 * i + 1] = a.y;
+                            x.ks[4 * i + 2] = a.z;
+                            x.ks[4 * i + 3] = a.w;
+                            x.vs[4 * i] = w.x;
+                            x.vs[4 * i + 1] = w.y;
+                            x.vs[4 * i + 2] = w.z;
+                            x.vs[4 * i + 3] = w.w;
+                        }
                     }
                 }
             }
@@ -653,12 +691,16 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         uint32_t sel_a = 0, sel_b = 0;
         if (FMT == kFmtPool) gather_selectors(c >> 2, sel_a, sel_b);
 
+        // whether the lane's token j of a tile at t0 counts
+        const auto counts = [&](uint32_t t0, int j) {
+            const uint32_t t = t0 + (j < 4 ? 0 : 16) + 4 * g + (j & 3);
+            return WIN ? t < end && (t < seen.hid0 || t >= seen.hid1) : t < end;
+        };
         // One tile: its loads are in x; those of the next one (at t_next, if
-        // below end) go out as soon as x has been widened. PART: the tile ends
-        // behind `end`.
+        // below end) go out as soon as x has been widened. PART: some of its tokens
+        // do not count.
         const auto tile = [&](auto part, uint32_t t0, uint32_t t_next, uint32_t it, R& x) {
-            constexpr bool PART = decltype(part)::value;
-            const uint32_t live = end - t0;
+            const bool PART = part;  // known when this is compiled, but for a window
             f32x4 s[RT][2];
             {
                 u32x4 kf[2][KS];
@@ -666,7 +708,10 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                 for (int i = 0; i < 2; ++i) {
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
-                        if (HALF) {
+                        if constexpr (FMT == kFmtFp4) {
+                            const uint32_t y = x.k[i][k], p2 = x.kp[i] << 23;
+                            kf[i][k] = u32x4{widen_fp4<0>(y, p2), widen_fp4<1>(y, p2), widen_fp4<2>(y, p2), widen_fp4<3>(y, p2)};
+                        } else if constexpr (HALF) {
                             const uint4& y = x.k[i][k / 2];
                             uint32_t a = k % 2 ? y.z : y.x, d = k % 2 ? y.w : y.y;
                             if (FMT != kFmtFp8) {
@@ -728,12 +773,49 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                         vs[4 * i + 2 * j + 1] = (float)s2.y;
                     }
                 }
+            } else if constexpr (FMT == kFmtFp4) {
+                constexpr int PB = D / kFp4Block;
+                if (PART) {  // as below; a power that no token wrote may be NaN, times a code of 0 too
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const bool ok = counts(t0, j);
+                        x.v[j] = ok ? x.v[j] : 0;
+                        uint32_t& w = x.vp[j >> 2][(j & 3) * PB / 4];
+                        const uint32_t none = w & ~((PB == 4 ? ~0u : 0xFFFFu) << ((j & 3) * PB % 4 * 8));
+                        w = ok ? w : none;
+                    }
+                }
+                const uint32_t block = c / (16 / PB);  // of the lane's channels
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // token pair (2j, 2j + 1)
+                    uint32_t y[2], p2[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int t = 2 * j + u, r = t & 3;  // token r of its run
+                        y[u] = x.v[t];
+                        // the power's byte, from bit `at`, to bits 23 to 30
+                        const uint32_t at = 8 * ((r * PB & 3) + block), w = x.vp[t >> 2][r * PB / 4];
+                        p2[u] = __builtin_amdgcn_alignbit(w, w, at + 9 & 31);
+                    }
+                    const auto pair = [&](auto which) {
+                        constexpr int B = decltype(which)::value;
+                        const uint32_t a = widen_fp4<B>(y[0], p2[0]), d = widen_fp4<B>(y[1], p2[1]);
+                        vf[2 * B][j] = __builtin_amdgcn_perm(d, a, 0x05040100u);
+                        vf[2 * B + 1][j] = __builtin_amdgcn_perm(d, a, 0x07060302u);
+                    };
+                    pair(std::integral_constant<int, 0>{});
+                    pair(std::integral_constant<int, 1>{});
+                    if constexpr (NC == 8) {
+                        pair(std::integral_constant<int, 2>{});
+                        pair(std::integral_constant<int, 3>{});
+                    }
+                }
             } else {
                 if (PART) {
                     // rows behind the end may hold anything: NaN times a weight of 0 would stay
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const bool ok = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live;
+                        const bool ok = counts(t0, j);
 #pragma unroll
                         for (int w = 0; w < R::VW; ++w) x.v[j][w] = ok ? x.v[j][w] : 0;
                         if (FMT != kFmtBf16) x.vs[j] = ok ? x.vs[j] : 0.0f;
@@ -794,9 +876,9 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
+                if (PART) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (PART) y[rt][j] = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? y[rt][j] : kNegInf;
+                    for (int j = 0; j < 8; ++j) y[rt][j] = counts(t0, j) ? y[rt][j] : kNegInf;
                 }
                 top[rt] = y[rt][0];
 #pragma unroll
@@ -842,7 +924,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                 for (int j = 0; j < 8; ++j) {
                     float e = exp2_fast(y[rt][j] - mu[rt]);
                     // by the token, not by its logit: -inf * 0 has no sign
-                    if (PART) e = (j < 4 ? 0 : 16) + 4 * g + (j & 3) < live ? e : 0.0f;
+                    if (PART && !WIN) e = counts(t0, j) ? e : 0.0f;
                     l[rt] += e;
                     w[j] = HALF ? e * vs[j] : e;
                 }
@@ -875,9 +957,16 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             }
             const uint32_t stop = FMT == kFmtPool || end - base <= kPageRun ? end : base + kPageRun;
             uint32_t it = 0, t0 = base + wave * kTile;
-            for (; t0 + kTile <= stop; t0 += kBlock, ++it)
-                tile(std::false_type{}, t0, t0 + kBlock < stop ? t0 + kBlock : end, it, x);
-            if (t0 < stop) tile(std::true_type{}, t0, end, it, x);
+            if (WIN) {
+                for (; t0 < stop; t0 += kBlock, ++it) {
+                    const bool all = t0 + kTile <= stop && (t0 + kTile <= seen.hid0 || t0 >= seen.hid1);
+                    tile(!all, t0, t0 + kBlock < stop ? t0 + kBlock : end, it, x);
+                }
+            } else {
+                for (; t0 + kTile <= stop; t0 += kBlock, ++it)
+                    tile(std::false_type{}, t0, t0 + kBlock < stop ? t0 + kBlock : end, it, x);
+                if (t0 < stop) tile(std::true_type{}, t0, end, it, x);
+            }
             if (FMT == kFmtPool) break;
         }
         if (FMT == kFmtPool && !header) {
@@ -987,11 +1076,11 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
     }
 }
 
-template <int FMT, int D, int RT>
+template <int FMT, int D, int RT, bool WIN>
 __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_kernel(Common p, Source src) {
     fetch_arguments<sizeof(Common) + sizeof(Source)>();
     __shared__ Shared<D, RT> sh;
-    attend_share<FMT, D, RT>(p, src, blockIdx.x, sh);
+    attend_share<FMT, D, RT, WIN>(p, src, blockIdx.x, sh);
 }
 
 // A pool's workgroups and those of the tails behind it, in one launch.
@@ -1004,9 +1093,9 @@ __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_b
         Shared<D, 1> b;
     } sh;
     if (blockIdx.x < pool.W)
-        attend_share<kFmtPool, D, RT>(p, pool, blockIdx.x, sh.a);
+        attend_share<kFmtPool, D, RT, false>(p, pool, blockIdx.x, sh.a);
     else
-        attend_share<FMT, D, 1>(p, tail, blockIdx.x - pool.W, sh.b);
+        attend_share<FMT, D, 1, false>(p, tail, blockIdx.x - pool.W, sh.b);
 }
 
 // Joins the parts of a row: V waves a row, which take its parts in turn, d / 64
@@ -1182,20 +1271,37 @@ AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens,
     return plan_of(units_of_rows, rows, max_tokens, d, rows > one_tile && enough ? 2 : 1, direct);
 }
 
-template <int D>
-hipError_t launch_pages(uint32_t format, uint32_t rt, uint32_t grid, const Common& p, const Source& s, hipStream_t stream) {
-    const auto f = format == 0   ? (rt == 1 ? attend_kernel<kFmtBf16, D, 1> : attend_kernel<kFmtBf16, D, 2>)
-                   : format == 1 ? (rt == 1 ? attend_kernel<kFmtInt8, D, 1> : attend_kernel<kFmtInt8, D, 2>)
-                                 : (rt == 1 ? attend_kernel<kFmtFp8, D, 1> : attend_kernel<kFmtFp8, D, 2>);
+template <int FMT, int D>
+hipError_t launch_pages(uint32_t rt, bool window, uint32_t grid, const Common& p, const Source& s, hipStream_t stream) {
+    auto f = rt == 1 ? attend_kernel<FMT, D, 1, false> : attend_kernel<FMT, D, 2, false>;
+    if constexpr (FMT != kFmtPool)
+        if (window) f = rt == 1 ? attend_kernel<FMT, D, 1, true> : attend_kernel<FMT, D, 2, true>;
     return launch_kernel(f, dim3(grid), dim3(kWaves * kWave), stream, p, s);
 }
 template <int D>
-hipError_t launch_both(uint32_t format, uint32_t rt, uint32_t grid, const Common& p, const Source& a, const Source& b,
-                       hipStream_t stream) {
-    const auto f = format == 0   ? (rt == 1 ? attend_both_kernel<kFmtBf16, D, 1> : attend_both_kernel<kFmtBf16, D, 2>)
-                   : format == 1 ? (rt == 1 ? attend_both_kernel<kFmtInt8, D, 1> : attend_both_kernel<kFmtInt8, D, 2>)
-                                 : (rt == 1 ? attend_both_kernel<kFmtFp8, D, 1> : attend_both_kernel<kFmtFp8, D, 2>);
-    return launch_kernel(f, dim3(grid), dim3(kWaves * kWave), stream, p, a, b);
+hipError_t launch_pages_of(uint32_t format, uint32_t rt, bool window, uint32_t grid, const Common& p, const Source& s,
+                           hipStream_t stream) {
+    switch (format) {
+        case kPageBf16: return launch_pages<kFmtBf16, D>(rt, window, grid, p, s, stream);
+        case kPageInt8: return launch_pages<kFmtInt8, D>(rt, window, grid, p, s, stream);
+        case kPageFp8: return launch_pages<kFmtFp8, D>(rt, window, grid, p, s, stream);
+        default: return launch_pages<kFmtFp4, D>(rt, window, grid, p, s, stream);
+    }
+}
+template <int FMT, int D>
+hipError_t launch_both(uint32_t rt, uint32_t grid, const Common& p, const Source& a, const Source& b, hipStream_t stream) {
+    return launch_kernel(rt == 1 ? attend_both_kernel<FMT, D, 1> : attend_both_kernel<FMT, D, 2>, dim3(grid),
+                         dim3(kWaves * kWave), stream, p, a, b);
+}
+template <int D>
+hipError_t launch_both_of(uint32_t format, uint32_t rt, uint32_t grid, const Common& p, const Source& a, const Source& b,
+                          hipStream_t stream) {
+    switch (format) {
+        case kPageBf16: return launch_both<kFmtBf16, D>(rt, grid, p, a, b, stream);
+        case kPageInt8: return launch_both<kFmtInt8, D>(rt, grid, p, a, b, stream);
+        case kPageFp8: return launch_both<kFmtFp8, D>(rt, grid, p, a, b, stream);
+        default: return launch_both<kFmtFp4, D>(rt, grid, p, a, b, stream);
+    }
 }
 
 // The source's share of the workspace, and the bytes it takes.
@@ -1249,12 +1355,15 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     }
     if (has_pages) {
         const PageLayout& lay = a.tail.lay;
-        page_plan = page_attend_plan(a.n, a.H, a.Hq, a.d, (uint64_t)a.tail.table_cols * lay.P, has_pool);
+        page_plan = page_attend_plan(a.n, a.H, a.Hq, a.d,
+                                     seen_tokens((uint64_t)a.tail.table_cols * lay.P, a.tail.window, a.tail.sinks), has_pool);
         ws += place_source(pages, page_plan, a.d, ws);
         pages.pages = a.tail.pages;
         pages.table = a.tail.table;
         pages.table_stride = a.tail.table_stride;
         pages.lens = a.tail.lens;
+        pages.window = a.tail.window;
+        pages.sinks = a.tail.sinks;
         pages.table_cols = a.tail.table_cols;
         pages.num_pages = lay.num_pages;
         pages.page_shift = 31 - __builtin_clz(lay.P);
@@ -1264,15 +1373,15 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     hipError_t e;
     if (has_pool && has_pages) {
         const uint32_t grid = pool.W + pages.W;
-        e = a.d == 64 ? launch_both<64>(a.tail.lay.format, pool_plan.rt, grid, p, pool, pages, stream)
-                      : launch_both<128>(a.tail.lay.format, pool_plan.rt, grid, p, pool, pages, stream);
+        e = a.d == 64 ? launch_both_of<64>(a.tail.lay.format, pool_plan.rt, grid, p, pool, pages, stream)
+                      : launch_both_of<128>(a.tail.lay.format, pool_plan.rt, grid, p, pool, pages, stream);
     } else if (has_pool) {
-        const auto f = a.d == 64 ? (pool_plan.rt == 1 ? attend_kernel<kFmtPool, 64, 1> : attend_kernel<kFmtPool, 64, 2>)
-                                 : (pool_plan.rt == 1 ? attend_kernel<kFmtPool, 128, 1> : attend_kernel<kFmtPool, 128, 2>);
-        e = launch_kernel(f, dim3(pool.W), dim3(kWaves * kWave), stream, p, pool);
+        e = a.d == 64 ? launch_pages<kFmtPool, 64>(pool_plan.rt, false, pool.W, p, pool, stream)
+                      : launch_pages<kFmtPool, 128>(pool_plan.rt, false, pool.W, p, pool, stream);
     } else {
-        e = a.d == 64 ? launch_pages<64>(a.tail.lay.format, page_plan.rt, pages.W, p, pages, stream)
-                      : launch_pages<128>(a.tail.lay.format, page_plan.rt, pages.W, p, pages, stream);
+        const uint32_t format = a.tail.lay.format;
+        e = a.d == 64 ? launch_pages_of<64>(format, page_plan.rt, a.tail.window != 0, pages.W, p, pages, stream)
+                      : launch_pages_of<128>(format, page_plan.rt, a.tail.window != 0, pages.W, p, pages, stream);
     }
     const AttendPlan& first = has_pool ? pool_plan : page_plan;
     if (e != hipSuccess || (p.direct && first.whole)) return e;

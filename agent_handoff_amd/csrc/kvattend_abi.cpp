@@ -163,6 +163,21 @@ struct Span {
     uint64_t n;
 };
 
+// Whether rows or spans that are written meet what else a call reads or writes.
+template <int I, int O>
+bool spans_meet(const View& q, const View& out, const Span (&ins)[I], const Span (&outs)[O]) {
+    for (const Span& x : ins)
+        if (view_meets(out, x.p, x.n)) return true;
+    for (int i = 0; i < O; ++i) {
+        if (view_meets(out, outs[i].p, outs[i].n) || view_meets(q, outs[i].p, outs[i].n)) return true;
+        for (const Span& x : ins)
+            if (overlap(outs[i].p, outs[i].n, x.p, x.n)) return true;
+        for (int j = i + 1; j < O; ++j)
+            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
+    }
+    return false;
+}
+
 // Workspace bytes of a call: `need`, what it uses, and `room`, which serves every smaller call too; false
 // if an argument is invalid.
 struct Workspace {
@@ -173,12 +188,14 @@ struct Workspace {
         return plan_ok(p);
     }
 };
-bool page_workspace(const kvc_pages* spec, uint32_t n, uint32_t q_heads, uint32_t max_tokens, Workspace& w) {
+bool page_workspace(const kvc_pages* spec, uint32_t n, uint32_t q_heads, uint32_t max_tokens, uint32_t window,
+                    uint32_t sinks, Workspace& w) {
     w = Workspace{0, 0};
     if (!spec_ok(spec) || !heads_ok(n, spec->num_kv_heads, q_heads) || !tokens_ok(n, max_tokens)) return false;
     if (n == 0) w = Workspace{256, 256};
     const uint32_t d = spec->head_dim;
-    return n == 0 || w.add(kvc::page_attend_plan(n, spec->num_kv_heads, q_heads, d, max_tokens, false), d);
+    const uint64_t most = kvc::seen_tokens(max_tokens, window, sinks);
+    return n == 0 || w.add(kvc::page_attend_plan(n, spec->num_kv_heads, q_heads, d, most, false), d);
 }
 bool pool_workspace(const kvc_shape* s, uint32_t n, uint32_t q_heads, const kvc_pages* tail, uint32_t max_tokens,
                     Workspace& w) {
@@ -201,6 +218,69 @@ bool pool_workspace(const kvc_shape* s, uint32_t n, uint32_t q_heads, const kvc_
     return w.add(t, d) && t.W + p.W < (1ull << 31);
 }
 
+bool rotation_ok(uint32_t head_dim, float eps, uint32_t n_pairs, uint32_t pairing) {
+    return pairing <= 1 && n_pairs % 8 == 0 && n_pairs <= head_dim / 2 && eps >= 0.0f && !isinf(eps);
+}
+
+// The window and the sinks of a call: no window where it holds every token that a table's row can; sinks up to those.
+void take_window(kvc::TailArgs& t, uint32_t window, uint32_t sinks) {
+    const uint32_t most = t.table_cols * t.lay.P;
+    t.window = window < most ? window : 0;
+    t.sinks = sinks < most ? sinks : most;
+}
+
+// kvpage_attend, with a window (0: none) and sinks
+int attend_pages(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs, uint32_t q_heads,
+                 const kvc_rows* q, const int32_t* table, uint32_t table_cols, uint64_t table_stride,
+                 const int32_t* lens, uint32_t window, uint32_t sinks, float scale, const kvc_rows* out, float* lse,
+                 void* ws, size_t ws_bytes, int32_t* dev_status, hipStream_t stream) {
+    if (!spec) return KVC_E_NULL;
+    if (!spec_ok(spec) || !heads_ok(n_seqs, spec->num_kv_heads, q_heads)) return KVC_E_SHAPE;
+    if (!scale_ok(scale)) return KVC_E_RANGE;
+    if (n_seqs == 0) return KVC_OK;
+    if (!q || !out || !q->data || !out->data || !ws) return KVC_E_NULL;
+    const int rc = check_tail(spec, pages, pages_bytes, n_seqs, table, table_cols, table_stride, lens);
+    if (rc != KVC_OK) return rc;
+    Workspace w;
+    if (!page_workspace(spec, n_seqs, q_heads, table_cols * spec->page_tokens, window, sinks, w)) return KVC_E_SHAPE;
+    const uint64_t need = w.need;
+    if (ws_bytes < need) return KVC_E_SIZE;
+    View qv, ov;
+    if (!view_of(q, n_seqs, q_heads, spec->head_dim, qv) || !view_of(out, n_seqs, q_heads, spec->head_dim, ov))
+        return KVC_E_SHAPE;
+    if (!view_aligned(qv) || !view_aligned(ov) || !aligned(ws, 256) || (lse && !aligned(lse, 4)) ||
+        (dev_status && !aligned(dev_status, 4)))
+        return KVC_E_ALIGN;
+    const Span ins[3] = {{pages, kvpage_bytes(spec)},
+                         {table, ((uint64_t)(n_seqs - 1) * table_stride + table_cols) * 4},
+                         {lens, (uint64_t)n_seqs * 4}};
+    const Span outs[3] = {{lse, lse ? (uint64_t)n_seqs * q_heads * 4 : 0}, {ws, need}, {dev_status, dev_status ? 4u : 0u}};
+    if (!view_apart(ov) || views_meet(ov, qv) || spans_meet(qv, ov, ins, outs)) return KVC_E_ALIAS;
+    kvc::AttendArgs a{};
+    a.n = n_seqs;
+    a.H = spec->num_kv_heads;
+    a.Hq = q_heads;
+    a.d = spec->head_dim;
+    a.q = rows_dev(qv);
+    a.out = rows_dev(ov);
+    a.scale = scale;
+    a.lse = lse;
+    a.ws = ws;
+    a.status = dev_status;
+    a.tail = kvc::TailArgs{layout_of(spec), static_cast<const uint8_t*>(pages), table, table_cols, table_stride, lens,
+                           0, 0};
+    take_window(a.tail, window, sinks);
+    return kvc::launch_attend(a, stream) == hipSuccess ? KVC_OK : KVC_E_HIP;
+}
+
+// What kvpage_attend_prompt takes, before its pages are looked at.
+bool prompt_ok(const kvc_pages* s, uint64_t n_seqs, uint64_t n_tokens, uint32_t q_heads) {
+    if (!spec_ok(s)) return false;
+    const uint64_t H = s->num_kv_heads;
+    return q_heads >= 1 && q_heads % H == 0 && q_heads <= (1u << 16) && n_tokens * q_heads < (1ull << 30) &&
+           n_seqs < (1u << 20) && H * (n_tokens * (q_heads / H) / kvc::kPromptRows + n_seqs) < (1ull << 23);
+}
+
 }  // namespace
 
 extern "C" {
@@ -213,7 +293,7 @@ int kvc_norm_rotate(uint32_t n_tokens, uint32_t q_heads, uint32_t kv_heads, uint
     if ((head_dim != 64 && head_dim != 128) || q_heads > (1u << 16) || kv_heads > (1u << 16) ||
         n_tokens > (1u << 26) - 4)
         return KVC_E_SHAPE;
-    if (pairing > 1 || n_pairs % 8 != 0 || n_pairs > head_dim / 2 || !(eps >= 0.0f) || isinf(eps)) return KVC_E_RANGE;
+    if (!rotation_ok(head_dim, eps, n_pairs, pairing)) return KVC_E_RANGE;
     if (n_tokens == 0 || q_heads + kv_heads == 0) return KVC_OK;
     if (n_pairs && (!positions || !inv_freq)) return KVC_E_NULL;
     const kvc_rows* ins[2] = {q_in, k_in};
@@ -277,59 +357,145 @@ int kvpage_read(const kvc_pages* spec, const void* pages, size_t pages_bytes, ui
     return page_copy(false, spec, pages, pages_bytes, n_tokens, k_out, v_out, slots, dev_status, stream);
 }
 
+int kvpage_append(const kvc_pages* spec, void* pages, size_t pages_bytes, uint32_t n_tokens, uint32_t q_heads,
+                  const kvc_rows* q_in, const kvc_rows* k_in, const kvc_rows* v_in, const void* q_weight,
+                  const void* k_weight, float eps, const int64_t* positions, const float* inv_freq, uint32_t n_pairs,
+                  uint32_t pairing, const int64_t* slots, const kvc_rows* q_out, int32_t* dev_status,
+                  hipStream_t stream) {
+    if (!spec) return KVC_E_NULL;
+    // four tokens a workgroup of 256 threads, fewer than 2^32 threads a launch
+    if (!spec_ok(spec) || q_heads > (1u << 16) || n_tokens > (1u << 26) - 4) return KVC_E_SHAPE;
+    const uint32_t d = spec->head_dim, H = spec->num_kv_heads;
+    if (!rotation_ok(d, eps, n_pairs, pairing)) return KVC_E_RANGE;
+    if (n_tokens == 0) return KVC_OK;
+    if (!pages || !k_in || !v_in || !k_in->data || !v_in->data || !slots || (n_pairs && (!positions || !inv_freq)))
+        return KVC_E_NULL;
+    if (q_heads && (!q_in || !q_out || !q_in->data || !q_out->data)) return KVC_E_NULL;
+    const kvc::PageLayout lay = layout_of(spec);
+    const uint64_t need = lay.page_bytes * lay.num_pages;
+    if (pages_bytes < need) return KVC_E_SIZE;
+    View in[3]{}, out{};  // queries, keys, values
+    if (!view_of(k_in, n_tokens, H, d, in[1]) || !view_of(v_in, n_tokens, H, d, in[2]) ||
+        (q_heads && (!view_of(q_in, n_tokens, q_heads, d, in[0]) || !view_of(q_out, n_tokens, q_heads, d, out))))
+        return KVC_E_SHAPE;
+    if (!aligned(pages, 256) || !view_aligned(in[1]) || !view_aligned(in[2]) || !aligned(slots, 8) ||
+        (n_pairs && !aligned(positions, 8)) || (q_heads && (!view_aligned(in[0]) || !view_aligned(out))) ||
+        (q_heads && q_weight && !aligned(q_weight, 16)) || (k_weight && !aligned(k_weight, 16)) ||
+        (dev_status && !aligned(dev_status, 4)))
+        return KVC_E_ALIGN;
+    const Span ins[4] = {{positions, n_pairs ? (uint64_t)n_tokens * 8 : 0},
+                         {slots, (uint64_t)n_tokens * 8},
+                         {q_weight, q_heads && q_weight ? d * 2u : 0u},
+                         {k_weight, k_weight ? d * 2u : 0u}};
+    const Span outs[2] = {{pages, need}, {dev_status, dev_status ? 4u : 0u}};
+    for (int i = q_heads ? 0 : 1; i < 3; ++i) {
+        if (view_meets(in[i], outs[0].p, outs[0].n) || view_meets(in[i], outs[1].p, outs[1].n)) return KVC_E_ALIAS;
+        if (q_heads && !(i == 0 && same_view(out, in[0])) && views_meet(out, in[i])) return KVC_E_ALIAS;
+    }
+    // (without queries `out` is empty and meets nothing)
+    if ((q_heads && !view_apart(out)) || spans_meet(in[1], out, ins, outs)) return KVC_E_ALIAS;
+    kvc::AppendArgs a{};
+    a.n = n_tokens;
+    a.Hq = q_heads;
+    a.lay = lay;
+    a.pages = static_cast<uint8_t*>(pages);
+    a.q_in = rows_dev(in[0]);
+    a.k_in = rows_dev(in[1]);
+    a.v_in = rows_dev(in[2]);
+    a.q_out = rows_dev(out);
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.eps = eps;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.n_pairs = n_pairs;
+    a.pairing = pairing;
+    a.slots = slots;
+    a.status = dev_status;
+    return kvc::launch_append(a, stream) == hipSuccess ? KVC_OK : KVC_E_HIP;
+}
+
 size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uint32_t q_heads, uint32_t max_tokens) {
     Workspace w;
-    return page_workspace(spec, n_seqs, q_heads, max_tokens, w) ? (size_t)w.room : 0;
+    return page_workspace(spec, n_seqs, q_heads, max_tokens, 0, 0, w) ? (size_t)w.room : 0;
 }
 
 int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs, uint32_t q_heads,
                   const kvc_rows* q, const int32_t* table, uint32_t table_cols, uint64_t table_stride,
                   const int32_t* lens, float scale, const kvc_rows* out, float* lse, void* ws, size_t ws_bytes,
                   int32_t* dev_status, hipStream_t stream) {
+    return attend_pages(spec, pages, pages_bytes, n_seqs, q_heads, q, table, table_cols, table_stride, lens, 0, 0, scale,
+                        out, lse, ws, ws_bytes, dev_status, stream);
+}
+
+size_t kvpage_attend_window_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uint32_t q_heads,
+                                            uint32_t max_tokens, uint32_t window, uint32_t sinks) {
+    Workspace w;
+    return page_workspace(spec, n_seqs, q_heads, max_tokens, window, sinks, w) ? (size_t)w.room : 0;
+}
+
+int kvpage_attend_window(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs,
+                         uint32_t q_heads, const kvc_rows* q, const int32_t* table, uint32_t table_cols,
+                         uint64_t table_stride, const int32_t* lens, uint32_t window, uint32_t sinks, float scale,
+                         const kvc_rows* out, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                         hipStream_t stream) {
+    return attend_pages(spec, pages, pages_bytes, n_seqs, q_heads, q, table, table_cols, table_stride, lens, window, sinks,
+                        scale, out, lse, ws, ws_bytes, dev_status, stream);
+}
+
+size_t kvpage_attend_prompt_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uint32_t n_tokens,
+                                            uint32_t q_heads, uint32_t max_tokens, uint32_t window, uint32_t sinks) {
+    if (!prompt_ok(spec, n_seqs, n_tokens, q_heads) || max_tokens >= (1u << 31)) return 0;
+    return (size_t)kvc::prompt_plan(n_seqs, n_tokens, spec->num_kv_heads, q_heads, spec->head_dim, max_tokens, window,
+                                    sinks).room;
+}
+
+int kvpage_attend_prompt(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs,
+                         uint32_t n_tokens, uint32_t q_heads, const kvc_rows* q, const int32_t* starts,
+                         const int32_t* table, uint32_t table_cols, uint64_t table_stride, const int32_t* lens,
+                         uint32_t window, uint32_t sinks, float scale, const kvc_rows* out, float* lse, void* ws,
+                         size_t ws_bytes, int32_t* dev_status, hipStream_t stream) {
     if (!spec) return KVC_E_NULL;
-    if (!spec_ok(spec) || !heads_ok(n_seqs, spec->num_kv_heads, q_heads)) return KVC_E_SHAPE;
+    if (!prompt_ok(spec, n_seqs, n_tokens, q_heads)) return KVC_E_SHAPE;
     if (!scale_ok(scale)) return KVC_E_RANGE;
-    if (n_seqs == 0) return KVC_OK;
-    if (!q || !out || !q->data || !out->data || !ws) return KVC_E_NULL;
+    if (n_seqs == 0 || n_tokens == 0) return KVC_OK;
+    if (!q || !out || !q->data || !out->data || !starts || !ws) return KVC_E_NULL;
     const int rc = check_tail(spec, pages, pages_bytes, n_seqs, table, table_cols, table_stride, lens);
     if (rc != KVC_OK) return rc;
-    Workspace w;
-    if (!page_workspace(spec, n_seqs, q_heads, table_cols * spec->page_tokens, w)) return KVC_E_SHAPE;
-    const uint64_t need = w.need;
-    if (ws_bytes < need) return KVC_E_SIZE;
+    const uint32_t d = spec->head_dim;
+    const kvc::PromptPlan plan = kvc::prompt_plan(n_seqs, n_tokens, spec->num_kv_heads, q_heads, d,
+                                                  table_cols * spec->page_tokens, window, sinks);
+    if (ws_bytes < plan.bytes) return KVC_E_SIZE;
     View qv, ov;
-    if (!view_of(q, n_seqs, q_heads, spec->head_dim, qv) || !view_of(out, n_seqs, q_heads, spec->head_dim, ov))
-        return KVC_E_SHAPE;
-    if (!view_aligned(qv) || !view_aligned(ov) || !aligned(ws, 256) || (lse && !aligned(lse, 4)) ||
+    if (!view_of(q, n_tokens, q_heads, d, qv) || !view_of(out, n_tokens, q_heads, d, ov)) return KVC_E_SHAPE;
+    if (!view_aligned(qv) || !view_aligned(ov) || !aligned(starts, 4) || !aligned(ws, 256) || (lse && !aligned(lse, 4)) ||
         (dev_status && !aligned(dev_status, 4)))
         return KVC_E_ALIGN;
-    const Span ins[3] = {{pages, kvpage_bytes(spec)},
+    const Span ins[4] = {{pages, kvpage_bytes(spec)},
                          {table, ((uint64_t)(n_seqs - 1) * table_stride + table_cols) * 4},
-                         {lens, (uint64_t)n_seqs * 4}};
-    const Span outs[3] = {{lse, lse ? (uint64_t)n_seqs * q_heads * 4 : 0}, {ws, need}, {dev_status, dev_status ? 4u : 0u}};
-    if (!view_apart(ov) || views_meet(ov, qv)) return KVC_E_ALIAS;
-    for (int i = 0; i < 3; ++i) {
-        if (view_meets(ov, ins[i].p, ins[i].n) || view_meets(ov, outs[i].p, outs[i].n) ||
-            view_meets(qv, outs[i].p, outs[i].n))
-            return KVC_E_ALIAS;
-        for (int j = 0; j < 3; ++j)
-            if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n) ||
-                (j > i && overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)))
-                return KVC_E_ALIAS;
-    }
-    kvc::AttendArgs a{};
+                         {lens, (uint64_t)n_seqs * 4},
+                         {starts, (uint64_t)n_seqs * 4 + 4}};
+    const Span outs[3] = {{lse, lse ? (uint64_t)n_tokens * q_heads * 4 : 0},
+                          {ws, plan.bytes},
+                          {dev_status, dev_status ? 4u : 0u}};
+    if (!view_apart(ov) || views_meet(ov, qv) || spans_meet(qv, ov, ins, outs)) return KVC_E_ALIAS;
+    kvc::PromptArgs a{};
     a.n = n_seqs;
+    a.rows = n_tokens;
     a.H = spec->num_kv_heads;
     a.Hq = q_heads;
-    a.d = spec->head_dim;
+    a.d = d;
     a.q = rows_dev(qv);
     a.out = rows_dev(ov);
     a.scale = scale;
     a.lse = lse;
     a.ws = ws;
     a.status = dev_status;
-    a.tail = kvc::TailArgs{layout_of(spec), static_cast<const uint8_t*>(pages), table, table_cols, table_stride, lens};
-    return kvc::launch_attend(a, stream) == hipSuccess ? KVC_OK : KVC_E_HIP;
+    a.starts = starts;
+    a.tail = kvc::TailArgs{layout_of(spec), static_cast<const uint8_t*>(pages), table, table_cols, table_stride, lens,
+                           0, 0};
+    take_window(a.tail, window, sinks);
+    return kvc::launch_attend_prompt(a, plan, stream) == hipSuccess ? KVC_OK : KVC_E_HIP;
 }
 
 size_t kvpool_attend_workspace_bytes(const kvc_shape* shape, uint32_t n_agents, uint32_t q_heads,
@@ -373,16 +539,7 @@ int kvpool_attend(const kvc_shape* shape, const void* pool, size_t pool_bytes, u
         {tail ? tail->table : nullptr, tail ? ((uint64_t)(n_agents - 1) * tail->table_stride + tail->table_cols) * 4 : 0},
         {tail ? tail->lens : nullptr, tail ? (uint64_t)n_agents * 4 : 0}};
     const Span outs[3] = {{lse, lse ? (uint64_t)n_agents * q_heads * 4 : 0}, {ws, need}, {dev_status, dev_status ? 4u : 0u}};
-    if (!view_apart(ov) || views_meet(ov, qv)) return KVC_E_ALIAS;
-    for (int j = 0; j < 4; ++j)
-        if (view_meets(ov, ins[j].p, ins[j].n)) return KVC_E_ALIAS;
-    for (int i = 0; i < 3; ++i) {
-        if (view_meets(ov, outs[i].p, outs[i].n) || view_meets(qv, outs[i].p, outs[i].n)) return KVC_E_ALIAS;
-        for (int j = 0; j < 4; ++j)
-            if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return KVC_E_ALIAS;
-        for (int j = i + 1; j < 3; ++j)
-            if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return KVC_E_ALIAS;
-    }
+    if (!view_apart(ov) || views_meet(ov, qv) || spans_meet(qv, ov, ins, outs)) return KVC_E_ALIAS;
     kvc::AttendArgs a{};
     a.n = n_agents;
     a.H = H;
@@ -400,7 +557,7 @@ int kvpool_attend(const kvc_shape* shape, const void* pool, size_t pool_bytes, u
     a.layer = layer;
     if (tail)
         a.tail = kvc::TailArgs{layout_of(tail->spec), static_cast<const uint8_t*>(tail->pages), tail->table,
-                               tail->table_cols, tail->table_stride, tail->lens};
+                               tail->table_cols, tail->table_stride, tail->lens, 0, 0};
     return kvc::launch_attend(a, stream) == hipSuccess ? KVC_OK : KVC_E_HIP;
 }
 

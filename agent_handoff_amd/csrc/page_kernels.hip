@@ -2,13 +2,13 @@
 // and reading them back, for gfx950.
 //
 // d / 8 lanes take one head vector, 8 channels (one 16-byte chunk) each, so
-// every access of bf16 rows and of codes is one contiguous run per vector.
+// every access of bf16 rows and of codes is one contiguous run per vector. (Four
+// lanes share the power of two of 4-bit codes.)
 // Both directions are bound by memory alone: 2 d bytes on one side, d + 4
-// (bf16: 2 d) on the other. 32768 tokens of 8 heads of 128 read back from int8
+// (bf16: 2 d, 4 bits: d / 2 + d / 32) on the other. 32768 tokens of 8 heads of 128 read back from int8
 // pages: 34.3 us, 5.9 TB/s; 8191 tokens written to e4m3 slots in random order:
 // 11.9 us, 4.3 TB/s (the 4-byte steps of scattered slots each move a line).
-#include "attend.h"
-#include "kernels_common.h"
+#include "page_codes.h"
 
 namespace kvc {
 namespace {
@@ -25,17 +25,6 @@ struct PageParams {
     uint32_t heads_inner;  // tokens hold their heads next to one another
     uint32_t vecs;         // of one row of the grid: n * H, or n of one head
 };
-
-// Maximum over the LPV (8 or 16) lanes of a vector.
-template <int LPV>
-__device__ __forceinline__ uint32_t max_lanes(uint32_t v) {
-    const auto step = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
-    v = step(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));   // quad_perm xor 1
-    v = step(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));   // quad_perm xor 2
-    v = step(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));  // row_half_mirror
-    if (LPV == 16) v = step(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));  // row_mirror
-    return v;
-}
 
 // One vector: whether there is one, its token's slot (as given), the element
 // offset of its row and the line it takes in a page but for the slot's.
@@ -61,120 +50,23 @@ __device__ __forceinline__ Vector vector_of(const PageParams& p, uint32_t at) {
     return x;
 }
 
-// Its byte offsets in the cache: of its codes and its step. A vector whose slot
+// Its byte offsets in the cache: of its codes and its step (or steps). A vector whose slot
 // is outside the cache, or negative, is not live, and has those of slot 0.
 struct Place {
     uint64_t code, step;
 };
-template <int D, int ES>
+template <int FMT, int D>
 __device__ __forceinline__ Place place_of(const PageParams& p, Vector& x) {
     const bool inside = x.slot >= 0 && (uint64_t)x.slot < (uint64_t)p.num_pages * p.P;
     x.live = x.live && inside;
     const uint64_t s = inside ? (uint64_t)x.slot : 0;
     const uint32_t shift = 31 - __clz(p.P);
     const uint64_t page = s >> shift, line = x.line + (s & (p.P - 1));
-    return Place{page * p.page_bytes + line * (D * ES), page * p.page_bytes + p.steps + line * 4};
+    return Place{page * p.page_bytes + line * page_code_bytes(FMT, D),
+                 page * p.page_bytes + p.steps + line * page_step_bytes(FMT, D)};
 }
 __device__ __forceinline__ void report(const PageParams& p, int64_t slot) {
     if (slot >= 0 && (uint64_t)slot >= (uint64_t)p.num_pages * p.P && p.status) atomicOr(p.status, kDevBadSlot);
-}
-
-__device__ __forceinline__ void unpack8(const uint4& x, float (&y)[8]) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[2 * i] = bf16_lo(w[i]);
-        y[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
-
-// 8 channels of a vector -> codes (8 bytes) and the vector's step.
-//
-// code = round(x * M / m), m the vector's maximum. With m brought to A in
-// [1/2, 1) by a power of two, x * (M * that power) is exact in binary32 (8 + 7
-// bits), and q = x * M / m by a reciprocal is corrected by its exact remainder: a
-// quotient that is a tie (representable) comes out exact; any other is at
-// least 2^-13 of its size away from a tie, since it is a ratio of integers of few
-// bits. So the codes are those of exact arithmetic. The step m / M is made the
-// same way, correctly rounded (so for each of the 128 significands of m).
-// Maxima below 2^-100 take the slow way: their factors leave binary32's range.
-template <int FMT, int LPV>
-__device__ __forceinline__ uint2 quantise8(const uint4& x, float& step) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t m = 0;  // magnitudes as integers: NaN above Inf above the rest
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-        const uint32_t y = lo > hi ? lo : hi;
-        m = y > m ? y : m;
-    }
-    m = max_lanes<LPV>(m);
-    const float most = FMT == 1 ? 127.0f : 448.0f, inv_most = 1.0f / most;
-    const float big = __uint_as_float(m << 16);
-    float y[8], q[8];
-    unpack8(x, y);
-    const int e = __builtin_amdgcn_frexp_expf(big);
-    const float A = __builtin_amdgcn_ldexpf(big, -e);
-    const float rA = __builtin_amdgcn_rcpf(A);
-    const auto corrected = [](float r, float divisor, float reciprocal) {
-        const float q0 = r * reciprocal;
-        return fmaf(fmaf(-q0, divisor, r), reciprocal, q0);
-    };
-    if (m >= 0x0D80u) {  // 2^-100
-        step = m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __builtin_amdgcn_ldexpf(corrected(A, most, inv_most), e);
-        if (m >= 0x7F80u) return make_uint2(0, 0);
-        const float up = __builtin_amdgcn_ldexpf(most, -e);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = corrected(y[i] * up, A, rA);
-    } else {
-        step = big / most;
-        if (m == 0) return make_uint2(0, 0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = corrected(__builtin_amdgcn_ldexpf(y[i], -e) * most, A, rA);
-    }
-    if (FMT == 2) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = copysignf(q[i], y[i]);  // the remainder of -0 is +0: e4m3 keeps the sign
-    }
-    uint32_t o[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (FMT == 1) {
-            // adding 1.5 * 2^23 rounds to an integer (ties to even) held in the low bits
-            uint32_t b[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) b[u] = __float_as_uint(q[4 * i + u] + 12582912.0f);
-            const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u);
-            const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
-            o[i] = lo | hi;
-        } else {
-            int v = 0;
-            v = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], v, false);
-            v = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], v, true);
-            o[i] = (uint32_t)v;
-        }
-    }
-    return make_uint2(o[0], o[1]);
-}
-
-template <int FMT>
-__device__ __forceinline__ uint4 dequantise8(const uint2& c, float step) {
-    float y[8];
-    const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (FMT == 1) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) y[4 * i + u] = (float)(int32_t)(int8_t)(w[i] >> (8 * u) & 0xFF) * step;
-        } else {
-            y[4 * i] = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 0) * step;
-            y[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 1) * step;
-            y[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 2) * step;
-            y[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8((int)w[i], 3) * step;
-        }
-    }
-    return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                      pack_bf16x2(y[6], y[7]));
 }
 
 // U vectors of each group of lanes at a time: their slots and rows are asked for
@@ -182,7 +74,7 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& c, float step) {
 // one after another, 13.5).
 template <int FMT, int D, int U>
 __global__ __launch_bounds__(kBlockThreads) void page_write_kernel(PageParams p) {
-    constexpr int LPV = D / 8, ES = FMT == 0 ? 2 : 1;
+    constexpr int LPV = D / 8;
     constexpr uint32_t VPB = kBlockThreads / LPV;
     const uint32_t i = threadIdx.x % LPV;
     const uint32_t v0 = blockIdx.x * (VPB * U) + threadIdx.x / LPV;
@@ -195,12 +87,20 @@ __global__ __launch_bounds__(kBlockThreads) void page_write_kernel(PageParams p)
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const Place at = place_of<D, ES>(p, vec[u]);
-        if (FMT == 0) {
+        const Place at = place_of<FMT, D>(p, vec[u]);
+        const uint4 y = make_uint4(x[u].x, x[u].y, x[u].z, x[u].w);
+        if (FMT == kPageBf16) {
             if (vec[u].live) *reinterpret_cast<kvc_u32x4*>(p.pages + at.code + 16 * i) = x[u];
+        } else if (FMT == kPageFp4) {
+            uint32_t power;
+            const uint32_t c = quantise8_fp4(y, max_lanes<kFp4Block / 8>(magnitude8(y)), power);
+            if (vec[u].live) {
+                *reinterpret_cast<uint32_t*>(p.pages + at.code + 4 * i) = c;
+                if (i % 4 == 0) p.pages[at.step + i / 4] = (uint8_t)power;
+            }
         } else {
             float step;
-            const uint2 c = quantise8<FMT, LPV>(make_uint4(x[u].x, x[u].y, x[u].z, x[u].w), step);
+            const uint2 c = quantise8<FMT>(y, max_lanes<LPV>(magnitude8(y)), step);
             if (vec[u].live) {
                 *reinterpret_cast<uint2*>(p.pages + at.code + 8 * i) = c;
                 if (i == 0) *reinterpret_cast<float*>(p.pages + at.step) = step;
@@ -213,7 +113,7 @@ __global__ __launch_bounds__(kBlockThreads) void page_write_kernel(PageParams p)
 
 template <int FMT, int D, int U>
 __global__ __launch_bounds__(kBlockThreads) void page_read_kernel(PageParams p) {
-    constexpr int LPV = D / 8, ES = FMT == 0 ? 2 : 1;
+    constexpr int LPV = D / 8;
     constexpr uint32_t VPB = kBlockThreads / LPV;
     const uint32_t i = threadIdx.x % LPV;
     const uint32_t v0 = blockIdx.x * (VPB * U) + threadIdx.x / LPV;
@@ -225,9 +125,12 @@ __global__ __launch_bounds__(kBlockThreads) void page_read_kernel(PageParams p) 
     for (int u = 0; u < U; ++u) vec[u] = vector_of(p, v0 + u * VPB);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const Place at = place_of<D, ES>(p, vec[u]);
-        if (FMT == 0) {
+        const Place at = place_of<FMT, D>(p, vec[u]);
+        if (FMT == kPageBf16) {
             x[u] = *reinterpret_cast<const uint4*>(p.pages + at.code + 16 * i);
+        } else if (FMT == kPageFp4) {
+            c[u].x = *reinterpret_cast<const uint32_t*>(p.pages + at.code + 4 * i);
+            c[u].y = p.pages[at.step + i / 4];
         } else {
             c[u] = *reinterpret_cast<const uint2*>(p.pages + at.code + 8 * i);
             step[u] = *reinterpret_cast<const float*>(p.pages + at.step);
@@ -235,7 +138,10 @@ __global__ __launch_bounds__(kBlockThreads) void page_read_kernel(PageParams p) 
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (FMT != 0) x[u] = dequantise8<FMT>(c[u], step[u]);
+        if (FMT == kPageFp4)
+            x[u] = dequantise8_fp4(c[u].x, c[u].y);
+        else if (FMT != kPageBf16)
+            x[u] = dequantise8<FMT>(c[u], step[u]);
         if (vec[u].live) st_stream(reinterpret_cast<uint4*>(p.rows[blockIdx.z].data + vec[u].row + 8 * i), x[u]);
     }
 #pragma unroll
@@ -277,14 +183,17 @@ hipError_t launch_page(bool write, const PageParams& p, hipStream_t stream) {
     return launch_kernel(many ? page_read_kernel<FMT, D, 4> : page_read_kernel<FMT, D, 1>, grid, block, stream, p);
 }
 
+template <int D>
+hipError_t launch_page_of(bool write, uint32_t format, const PageParams& p, hipStream_t stream) {
+    switch (format) {
+        case kPageBf16: return launch_page<kPageBf16, D>(write, p, stream);
+        case kPageInt8: return launch_page<kPageInt8, D>(write, p, stream);
+        case kPageFp8: return launch_page<kPageFp8, D>(write, p, stream);
+        default: return launch_page<kPageFp4, D>(write, p, stream);
+    }
+}
 hipError_t launch_page_any(bool write, const PageLayout& l, const PageParams& p, hipStream_t stream) {
-    if (l.d == 64)
-        return l.format == 0   ? launch_page<0, 64>(write, p, stream)
-               : l.format == 1 ? launch_page<1, 64>(write, p, stream)
-                               : launch_page<2, 64>(write, p, stream);
-    return l.format == 0   ? launch_page<0, 128>(write, p, stream)
-           : l.format == 1 ? launch_page<1, 128>(write, p, stream)
-                           : launch_page<2, 128>(write, p, stream);
+    return l.d == 64 ? launch_page_of<64>(write, l.format, p, stream) : launch_page_of<128>(write, l.format, p, stream);
 }
 
 }  // namespace

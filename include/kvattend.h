@@ -7,7 +7,10 @@
  *    rotation, in one pass over the projection's rows;
  *  - kvpage_write, kvpage_read: a paged cache of one layer, quantised as it is
  *    written, and read back;
+ *  - kvpage_append: norms, rotation and the write of the new keys and values in one;
  *  - kvpage_attend: attention of one new token per sequence over its pages;
+ *  - kvpage_attend_window: the same with a sliding window and sinks;
+ *  - kvpage_attend_prompt: attention of many new tokens of each sequence;
  *  - kvpool_attend: attention of one new token of each of n agents over one
  *    layer of the shared pool (PolyKV section 2.A: every agent reads the same
  *    compressed document), without decompressing it, together with the pages
@@ -61,12 +64,14 @@ typedef struct kvc_pages {
 #define KVC_PAGE_BF16 0u /* the values as they are */
 #define KVC_PAGE_INT8 1u /* int8 codes, one binary32 step for each head vector */
 #define KVC_PAGE_FP8 2u  /* e4m3 codes (OCP, no infinities), one binary32 step for each head vector */
+#define KVC_PAGE_FP4 4u  /* e2m1 codes, one power of two for each 32 channels (OCP microscaling) */
 
 /* Further bits of *dev_status. */
 enum {
     KVC_DEV_BAD_SLOT = 16,  /* a slot is not below num_pages * page_tokens */
     KVC_DEV_BAD_PAGE = 32,  /* a page number of a table is not a page */
-    KVC_DEV_BAD_LENGTH = 64 /* a length is negative or longer than its table's row */
+    KVC_DEV_BAD_LENGTH = 64, /* a length is negative or longer than its table's row */
+    KVC_DEV_BAD_START = 128  /* first rows of sequences fall, or leave the rows given */
 };
 
 /* ------------------------------------------------------ norm and rotation */
@@ -101,8 +106,10 @@ int kvc_norm_rotate(uint32_t n_tokens, uint32_t q_heads, uint32_t kv_heads, uint
 /* Bytes of a paged cache; 0 if the description is invalid. Layout: pages one
  * after another, each on a 256-byte boundary:
  *   codes  [2][num_kv_heads][page_tokens][head_dim]  keys, then values (bf16,
- *          int8 or e4m3)
- *   steps  f32 [2][num_kv_heads][page_tokens]        (8-bit formats) */
+ *          int8, e4m3, or e2m1: two to a byte, the even channel in its low half)
+ *   steps  f32 [2][num_kv_heads][page_tokens]        (8-bit formats), or bytes
+ *          [2][num_kv_heads][page_tokens][head_dim / 32] (e2m1): byte s stands for
+ *          2^(s - 127), 255 for NaN */
 size_t kvpage_bytes(const kvc_pages* spec);
 
 /* Write keys and values of n_tokens tokens into their slots.
@@ -116,18 +123,39 @@ size_t kvpage_bytes(const kvc_pages* spec);
  * and correctly rounded quotients, so a code is the nearest one). m = 0 gives
  * step 0 and codes 0. A vector that holds an Inf or NaN gets a NaN step and
  * codes 0: it reads back as NaN.
+ * KVC_PAGE_FP4, for each 32 channels: with m = max |x| and 2^a <= m < 2^(a+1), the
+ * power is 2^(a-2), or 2^(a-1) if m > 1.75 * 2^a, held to 2^-125 .. 2^125; code =
+ * x / power rounded to nearest, ties to even, and cut off at 6. m = 0 gives codes 0;
+ * channels that hold an Inf or NaN get the power 255 and codes 0: all 32 read
+ * back as NaN.
  *   dev_status  device int32 or NULL; KVC_DEV_BAD_SLOT (that token is not written)
  * Errors: KVC_E_NULL, KVC_E_SHAPE, KVC_E_SIZE, KVC_E_ALIGN, KVC_E_ALIAS,
  * KVC_E_HIP. */
 int kvpage_write(const kvc_pages* spec, void* pages, size_t pages_bytes, uint32_t n_tokens, const kvc_rows* k,
                  const kvc_rows* v, const int64_t* slots, int32_t* dev_status, hipStream_t stream);
 
-/* Read tokens back: bf16(code * step), one rounding. Rows of negative slots,
+/* Read tokens back: bf16(code * step), one rounding (none for KVC_PAGE_FP4). Rows of negative slots,
  * and of slots outside the cache (KVC_DEV_BAD_SLOT), are left as they were.
  * Errors as kvpage_write. */
 int kvpage_read(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_tokens,
                 const int64_t* slots, const kvc_rows* k_out, const kvc_rows* v_out, int32_t* dev_status,
                 hipStream_t stream);
+
+/* Norms, rotation and the write in one pass over the projection's rows:
+ * kvc_norm_rotate of q and k, and kvpage_write of the keys it gives (rounded to
+ * bf16, but not kept) and of v. The bytes of q_out and of the pages are those of the
+ * two calls.
+ *   q_in, k_in, v_in  rows of n_tokens x q_heads and twice n_tokens x num_kv_heads;
+ *                  n_tokens <= 2^26 - 4. q_heads may be 0 (q_in, q_out are not used)
+ *   q_out          rows; the same as q_in turns in place
+ *   slots          as for kvpage_write; a token with a negative slot (padding) or one
+ *                  outside the cache has its queries turned all the same
+ * The other arguments, roundings and errors are those of the two calls. */
+int kvpage_append(const kvc_pages* spec, void* pages, size_t pages_bytes, uint32_t n_tokens, uint32_t q_heads,
+                  const kvc_rows* q_in, const kvc_rows* k_in, const kvc_rows* v_in, const void* q_weight,
+                  const void* k_weight, float eps, const int64_t* positions, const float* inv_freq, uint32_t n_pairs,
+                  uint32_t pairing, const int64_t* slots, const kvc_rows* q_out, int32_t* dev_status,
+                  hipStream_t stream);
 
 /* --------------------------------------------------------------- attention */
 
@@ -163,8 +191,8 @@ size_t kvpage_attend_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uin
  * workgroups and their parts joined by a second launch, in an order that the
  * arguments alone decide: the same call gives the same bits.
  * The 8-bit formats' weights p_t * step are rounded to binary16 after division
- * by a power of two (about the largest step) for the matrix cores, bf16's are
- * split into two bf16 terms; products and sums are binary32. Of a weight times its
+ * by a power of two (about the largest step) for the matrix cores, bf16's and
+ * KVC_PAGE_FP4's are split into two bf16 terms; products and sums are binary32. Of a weight times its
  * step, what lies below 2^-36 of the largest step (or of 2^-100) is lost. So q . k (before
  * and after the scale), and the weighted sums before they are divided by the
  * weights' (at most 8 times the tokens times the largest value), have to stay in
@@ -177,6 +205,64 @@ int kvpage_attend(const kvc_pages* spec, const void* pages, size_t pages_bytes, 
                   const kvc_rows* q, const int32_t* table, uint32_t table_cols, uint64_t table_stride,
                   const int32_t* lens, float scale, const kvc_rows* out, float* lse, void* ws, size_t ws_bytes,
                   int32_t* dev_status, hipStream_t stream);
+
+/* Workspace bytes of kvpage_attend_window; never less for more sequences, tokens,
+ * window or sinks. 0 if an argument is invalid. */
+size_t kvpage_attend_window_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uint32_t q_heads,
+                                            uint32_t max_tokens, uint32_t window, uint32_t sinks);
+
+/* kvpage_attend of a new token that sees the last `window` tokens of its sequence
+ * (itself among them) and the first `sinks`: token t counts if t < sinks or
+ * t >= lens[b] - window. window 0: every token counts, whatever sinks is.
+ * Tokens in between are not used, whatever their pages hold, and table entries of
+ * pages without a token that counts may hold anything.
+ *   ws         kvpage_attend_window_workspace_bytes(spec, n_seqs, q_heads,
+ *              table_cols * page_tokens, window, sinks) bytes or more
+ * The other arguments, roundings and errors are those of kvpage_attend. */
+int kvpage_attend_window(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs,
+                         uint32_t q_heads, const kvc_rows* q, const int32_t* table, uint32_t table_cols,
+                         uint64_t table_stride, const int32_t* lens, uint32_t window, uint32_t sinks, float scale,
+                         const kvc_rows* out, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status,
+                         hipStream_t stream);
+
+/* Workspace bytes of kvpage_attend_prompt for at most n_seqs sequences with at most
+ * n_tokens new tokens together, of at most max_tokens tokens each; never less for
+ * more of any. 0 if an argument is invalid. */
+size_t kvpage_attend_prompt_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uint32_t n_tokens,
+                                            uint32_t q_heads, uint32_t max_tokens, uint32_t window, uint32_t sinks);
+
+/* Attention of the new tokens of each of n_seqs sequences over its pages, which
+ * hold the new tokens' keys and values already (kvpage_append): a prompt, a part of one
+ * behind a context, or drafted tokens. Sequence b has the rows starts[b] to
+ * starts[b + 1] - 1, which are the last of its lens[b] tokens; row i of m stands at
+ * position p = lens[b] - m + i and sees the tokens t <= p, with a window those
+ * with t < sinks or t > p - window. window 0: all of them. A row that sees no token (m >
+ * lens[b]) gives zeros and lse = -inf. Rows before starts[0] and from
+ * starts[n_seqs] on are left as they were. Table entries of pages without a token that
+ * a row sees may hold anything.
+ *   q, out     rows of n_tokens x q_heads (out elsewhere than q)
+ *   starts     device int32 [n_seqs + 1], rising, from 0 to n_tokens at most
+ *   lse        device f32 [n_tokens][q_heads] or NULL
+ *   ws         kvpage_attend_prompt_workspace_bytes(spec, n_seqs, n_tokens, q_heads,
+ *              table_cols * page_tokens, window, sinks) bytes or more
+ *   dev_status besides those of kvpage_attend KVC_DEV_BAD_START (outputs are then
+ *              unspecified)
+ * n_tokens * q_heads < 2^30 and, with g = q_heads / num_kv_heads, num_kv_heads *
+ * (n_tokens * g / 64 + n_seqs) < 2^23; n_seqs < 2^20; table_cols * page_tokens < 2^31.
+ * The same call gives the same bits. Weights are rounded once, to bf16 (2^-8; bf16 and
+ * KVC_PAGE_FP4 pages) or, times the step, to binary16 (2^-11; 8-bit formats): a row sums
+ * over many tokens, and the rounding errors do not add up as the weights do. The
+ * softmax's sums are those of the weights before that. Products and sums are
+ * binary32. Logits in powers of two (scale * q . k * log2 e) have to stay below 2^24 in
+ * size, 8-bit key steps that are not 0 between 2^-90 and 2^90. A NaN in a key or value,
+ * or an Inf in a value, makes rows that see its token NaN or Inf (of a value: in its
+ * channel; in its whole vector or 32 channels where they share a step), and no others.
+ * The other arguments and errors are those of kvpage_attend. */
+int kvpage_attend_prompt(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs,
+                         uint32_t n_tokens, uint32_t q_heads, const kvc_rows* q, const int32_t* starts,
+                         const int32_t* table, uint32_t table_cols, uint64_t table_stride, const int32_t* lens,
+                         uint32_t window, uint32_t sinks, float scale, const kvc_rows* out, float* lse, void* ws,
+                         size_t ws_bytes, int32_t* dev_status, hipStream_t stream);
 
 /* The pages of the agents behind a shared pool (see kvpage_attend). */
 typedef struct kvc_tail {

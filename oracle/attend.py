@@ -10,7 +10,8 @@ import numpy as np
 from . import codebook, pool_layout
 
 HALVES, ADJACENT = 0, 1
-BF16, INT8, FP8 = 0, 1, 2
+BF16, INT8, FP8, FP4 = 0, 1, 2, 4
+BLOCK4 = 32  # channels that share a power of two (FP4)
 
 
 def f64(bits):
@@ -49,12 +50,21 @@ def _e4m3_values():
 E4M3 = _e4m3_values()
 
 
+#: The value of each e2m1 code.
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6])
+
+
 def page_layout(spec):
     """(bytes of a code, offset of the steps in a page, bytes of a page)."""
     _, heads, page, d, fmt = spec
-    size = 2 if fmt == BF16 else 1
-    steps = 2 * heads * page * d * size
-    return size, steps, -(-(steps + (0 if fmt == BF16 else 8 * heads * page)) // 256) * 256
+    size = {BF16: 2, FP4: 0.5}.get(fmt, 1)
+    steps = int(2 * heads * page * d * size)
+    return size, steps, -(-(steps + 2 * heads * page * step_bytes(fmt, d)) // 256) * 256
+
+
+def step_bytes(fmt, d):
+    """Bytes of a vector's step or steps."""
+    return {BF16: 0, FP4: d // BLOCK4}.get(fmt, 4)
 
 
 def page_bytes(spec):
@@ -86,6 +96,32 @@ def quantise(bits, fmt):
     return code | sign, step
 
 
+def quantise4(bits):
+    """Codes (uint8, two to a byte) and powers (uint8) of bf16 vectors [..., d], by exact arithmetic."""
+    x = f64(bits).reshape(*np.shape(bits)[:-1], np.shape(bits)[-1] // BLOCK4, BLOCK4)
+    m = np.max(np.abs(x), -1)
+    bad = ~np.isfinite(x).all(-1)
+    m = np.where(bad | (m == 0), 2.0 ** -133, m)
+    fraction, exponent = np.frexp(m)                       # fraction in [1/2, 1)
+    e = np.clip(exponent - 3 + (fraction > 0.875), -125, 125)
+    y = np.where(bad[..., None], 0.0, x) * np.exp2(-e.astype(np.float64))[..., None]
+    a = np.minimum(np.abs(y), 6.0)
+    hi = np.clip(np.searchsorted(E2M1[:8], a), 1, 7)
+    lo = hi - 1
+    dl, dh = a - E2M1[lo], E2M1[hi] - a
+    code = np.where((dl < dh) | ((dl == dh) & (lo % 2 == 0)), lo, hi)
+    none = (bad | (np.max(np.abs(np.where(bad[..., None], 0, x)), -1) == 0))[..., None]
+    code = np.where(none, 0, code | np.where(np.signbit(y), 8, 0)).astype(np.uint8).reshape(np.shape(bits))
+    return code[..., 0::2] | code[..., 1::2] << 4, np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def values4(codes, powers):
+    """binary64 values [..., d] of codes [..., d / 2] and powers [..., d / 32]."""
+    c = np.stack([codes & 15, codes >> 4], -1).reshape(*powers.shape, BLOCK4)
+    s = np.where(powers == 255, np.nan, np.exp2(powers.astype(np.float64) - 127))
+    return (E2M1[c] * s[..., None]).reshape(*codes.shape[:-1], 2 * codes.shape[-1])
+
+
 def page_write(pages, spec, k, v, slots):
     """Writes k, v (bits [n, heads, d]) into the uint8 array `pages`."""
     num, heads, page, d, fmt = spec
@@ -97,8 +133,13 @@ def page_write(pages, spec, k, v, slots):
         for j, x in enumerate((k[i], v[i])):
             for h in range(heads):
                 line = (j * heads + h) * page + slot % page
-                at = base + line * d * size
-                if fmt == BF16:
+                at = int(base + line * d * size)
+                if fmt == FP4:
+                    code, power = quantise4(x[h])
+                    pages[at:at + d // 2] = code
+                    st = base + steps + line * (d // BLOCK4)
+                    pages[st:st + d // BLOCK4] = power
+                elif fmt == BF16:
                     pages[at:at + 2 * d] = np.ascontiguousarray(x[h], np.uint16).view(np.uint8)
                 else:
                     code, step = quantise(x[h], fmt)
@@ -113,9 +154,13 @@ def page_values(pages, spec, slots):
     size, steps, each = page_layout(spec)
     slots = np.asarray(slots, np.int64)
     store = pages.reshape(num, each)
-    rows = store[:, :2 * heads * page * d * size].reshape(num, 2, heads, page, d * size)
+    rows = store[:, :steps].reshape(num, 2, heads, page, int(d * size))
     x = rows[slots // page, :, :, slots % page]
-    if fmt == BF16:
+    if fmt == FP4:
+        n = d // BLOCK4
+        s = store[:, steps:steps + 2 * heads * page * n].reshape(num, 2, heads, page, n)
+        x = values4(x, s[slots // page, :, :, slots % page])
+    elif fmt == BF16:
         x = f64(np.ascontiguousarray(x).view(np.uint16))
     else:
         s = np.ascontiguousarray(store[:, steps:steps + 8 * heads * page]).view(np.float32).reshape(num, 2, heads, page)
@@ -147,6 +192,13 @@ def pool_rotated(pool, shape, layer):
     levels = np.asarray(codebook.codec_table()[0], np.float64)
     y = levels[bits[:, 0] + 2 * bits[:, 1] + 4 * bits[:, 2]] * size[:, None]
     return k.reshape(H, T, d), y.reshape(H, T, d)
+
+
+def seen(length, position, window=0, sinks=0):
+    """Which of `length` tokens the one at `position` sees."""
+    t = np.arange(length)
+    s = t <= position
+    return s & ((t < sinks) | (t > position - window)) if window else s
 
 
 def attend(q, keys, values, scale):
