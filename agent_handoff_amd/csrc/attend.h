@@ -146,7 +146,7 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
 constexpr uint32_t kPromptRows = 64;  // of the smallest block
 struct PromptPlan {
     uint32_t rows;    // of a block
-    uint32_t splits;  // shares of the tokens
+    uint32_t more;    // shares that a kv head's blocks may have beyond one each
     uint64_t blocks;
     uint64_t bytes;   // of the workspace: what the call uses,
     uint64_t room;    // and what serves every smaller call too

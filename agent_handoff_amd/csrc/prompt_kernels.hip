@@ -2,7 +2,7 @@
 // pages (a prompt, a part of one, drafted tokens), for gfx950.
 //
 // The query rows of a sequence and kv head are its new tokens times the query heads
-// that share the kv head, token by token. A workgroup takes 128 of them, 32 a wave, and
+// that share the kv head, token by token. A workgroup takes a block of them, 32 a wave, and
 // walks the tokens that they see in tiles of 64, with one pass over the data
 // (running maximum m and sum l):
 //     S^T = K Q^T           32x32x16 matrix instructions, tokens x rows
@@ -22,12 +22,11 @@ namespace kvc {
 namespace {
 
 constexpr int kDevBadPage = 32, kDevBadLength = 64, kDevBadStart = 128;  // KVC_DEV_*
-constexpr uint32_t kRows = 128;    // of a workgroup
 constexpr uint32_t kTokens = 64;   // of a tile
 constexpr uint32_t kRun = 16;      // tokens that lie in one page: a wave fetches one run of each tile
-constexpr int kWavesOf = 4;
 constexpr float kSlack = 3.0f;     // m moves when a tile's maximum passes it by this (powers of two)
 constexpr int kWeightExp = 12;     // binary16 weights: the largest stays below 2^(12 + 3 + 1)
+constexpr uint32_t kMinShare = 8;  // tiles of a share, at least
 constexpr float kNegInf = -__builtin_inff();
 constexpr bool half_products(int fmt) { return fmt == kPageInt8 || fmt == kPageFp8; }
 
@@ -50,9 +49,9 @@ struct PromptParams {
     uint32_t n, rows, H, Hq, group;
     uint32_t table_cols, num_pages, page_shift;
     uint32_t window, sinks;
-    uint32_t splits;
+    uint32_t more;  // workgroups that a kv head has for shares beyond one of each block (0: no block is cut up)
     float scale_log2;
-    float* part;  // of each split and row: sums [splits][rows * Hq][d], then {m, l} [splits][rows * Hq][2]
+    float* part;  // of each share of a block that is cut up: sums [rows of a block][d], then {m, l} of each row
 };
 
 template <int FMT>
@@ -98,92 +97,310 @@ __device__ __forceinline__ uint32_t place_v(uint32_t token, uint32_t chunk) {
     return token * (2 * D) + ((chunk ^ (D == 128 ? (token & 3) << 2 : (token >> 1 & 1) << 2)) << 4);
 }
 
-// 16 bytes of each lane from memory to LDS, at lds + 16 * lane.
-__device__ __forceinline__ void fetch16(const uint8_t* from, uint8_t* lds) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(uint64_t)from, (KVC_LDS void*)lds, 16, 0, 0);
+// 16 bytes of each lane from memory (base + off, base the same in all lanes) to LDS, at lds + 16 * lane. Written out:
+// behind the builtin the compiler waits for it before the next read of LDS, of whichever buffer. Here it knows of
+// nothing; arrive() waits. (No register is written but M0, which nothing else here uses; what reads it comes a wait
+// state behind its write.)
+__device__ __forceinline__ void fetch16(const uint8_t* base, uint32_t off, uint8_t* lds) {
+    const uint64_t from = (uint64_t)base;
+    const uint64_t at = (uint64_t)wave_uniform((uint32_t)(from >> 32)) << 32 | wave_uniform((uint32_t)from);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(wave_uniform((uint32_t)(uint64_t)(KVC_LDS uint8_t*)lds)), "v"(off), "s"(at)
+                 : "memory");
 }
 
 template <int FMT, int D>
-struct Tile {
-    static constexpr uint32_t kBytes = kTokens * D * 2;  // of keys, and of values
-    alignas(16) uint8_t kv[2][2][kBytes];                // [buffer][keys, values]
+struct Tiles {
+    static constexpr uint32_t kBytes = kTokens * D * 2;
+    alignas(16) uint8_t kv[2][2][kBytes];  // [keys, values][buffer]
     float steps[half_products(FMT) ? 2 : 1][2][half_products(FMT) ? kTokens : 1];
+    float big[2][4];  // largest step of the values of each run (8 bits)
+    uint32_t odd[2];  // a buffer's values or their steps are not all finite: 1 + the tile they are of
 };
 
-template <int FMT, int D>
-__global__ __launch_bounds__(kWavesOf* kWave, 2) void prompt_kernel(PromptParams p) {
+// Tiles of what a block's rows see, from its first row's position to its last's: tokens below `sunk` and from `lo` to `end`.
+struct Range {
+    uint32_t sunk, lo, end;
+    uint32_t tiles0, from, tiles;  // tiles of the sinks; the first behind them; all
+};
+__device__ __forceinline__ Range range_of(const PromptParams& p, int32_t pos_lo, int32_t pos_hi) {
+    Range r;
+    r.end = pos_hi < 0 ? 0 : pos_hi + 1;
+    r.lo = p.window && pos_lo >= 0 && (uint32_t)pos_lo >= p.window ? pos_lo - p.window + 1 : 0;
+    r.sunk = p.sinks < r.lo ? p.sinks : r.lo;
+    r.tiles0 = (r.sunk + kTokens - 1) / kTokens;
+    r.from = r.lo / kTokens > r.tiles0 ? r.lo / kTokens : r.tiles0;
+    const uint32_t last = (r.end + kTokens - 1) / kTokens;
+    r.tiles = r.tiles0 + (last > r.from ? last - r.from : 0);
+    return r;
+}
+
+// A sequence's new tokens and length, and the positions of the first and last row of one of its blocks.
+struct Sequence {
+    uint32_t b, first, m;  // first: its first row
+    int32_t len;
+    uint32_t blocks, shares;
+    __device__ __forceinline__ int32_t pos_of(uint32_t row, uint32_t group) const { return len - (int32_t)m + (int32_t)(row / group); }
+};
+
+// Which item of work (`at`, of one kv head) this is: sequence, block, share, and the place of its partial results if
+// the sequence's blocks are cut up. Every workgroup finds that for itself, a lane a sequence. Sequences and their blocks
+// are taken from the last to the first, so that the longest of a prompt come first. Blocks of a sequence are cut into
+// so many shares that none has more than `each` tiles, where all of them together have at most `more` shares
+// beyond one of each block.
+struct Item {
+    bool found;
+    Sequence s;
+    uint32_t block, share;
+    uint32_t slot;  // of the block's first share
+};
+template <uint32_t ROWS, bool JOIN>
+__device__ __forceinline__ Item item_of(const PromptParams& p, uint32_t at) {
+    const uint32_t lane = lane_id();
+    Item x{};
+    const auto sequence = [&](uint32_t base, uint32_t& tiles) {
+        Sequence s{};
+        tiles = 0;
+        if (base + lane >= p.n) return s;
+        s.b = p.n - 1 - base - lane;
+        const int32_t a = p.starts[s.b], e = p.starts[s.b + 1], given = p.lens[s.b];
+        const bool bad = a < 0 || e < a || (uint32_t)e > p.rows;
+        const uint32_t most = p.table_cols << p.page_shift;
+        s.len = given < 0 ? 0 : (uint32_t)given > most ? (int32_t)most : given;
+        if (!JOIN && p.status && (bad || s.len != given))
+            atomicOr(p.status, (bad ? kDevBadStart : 0) | (s.len != given ? kDevBadLength : 0));
+        s.first = a;
+        s.m = bad ? 0 : e - a;
+        s.blocks = (s.m * p.group + ROWS - 1) / ROWS;
+        s.shares = 1;
+        if (p.more && s.blocks) tiles = range_of(p, s.pos_of((s.blocks - 1) * ROWS, p.group), s.len - 1).tiles;
+        return s;
+    };
+    uint32_t tiles, each = 0;
+    Sequence s = sequence(0, tiles);
+    if (p.more) {
+        uint64_t all = 0;
+        for (uint32_t base = 0;;) {
+            // (below 2^36: fewer than 2^11 blocks, of 2^25 tiles)
+            const uint64_t t = (uint64_t)s.blocks * tiles;
+            const uint32_t low = scan_lanes((uint32_t)t & 4095), high = scan_lanes((uint32_t)(t >> 12));
+            all += (uint32_t)__builtin_amdgcn_readlane(low, 63) + ((uint64_t)(uint32_t)__builtin_amdgcn_readlane(high, 63) << 12);
+            base += kWave;
+            if (base >= p.n) break;
+            s = sequence(base, tiles);
+        }
+        all = (all + p.more - 1) / p.more;
+        each = all < kMinShare ? kMinShare : all > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)all;
+        if (p.n > kWave) s = sequence(0, tiles);
+    }
+    uint32_t before = 0, slots = 0;
+    for (uint32_t base = 0;;) {
+        if (p.more && tiles) s.shares = (tiles - 1) / each + 1;
+        const uint32_t items = s.blocks * s.shares, mine = JOIN ? s.blocks : items;
+        const uint32_t up = scan_lanes(mine), up_slots = scan_lanes(s.shares > 1 ? items : 0);
+        const uint32_t all = __builtin_amdgcn_readlane(up, 63);
+        if (at < before + all) {
+            const int l = __builtin_popcountll(__ballot(before + up <= at));
+            const auto of = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane(v, l); };
+            x.found = true;
+            x.s = Sequence{of(s.b), of(s.first), of(s.m), (int32_t)of(s.len), of(s.blocks), of(s.shares)};
+            const uint32_t back = before + of(up) - 1 - at;  // from the sequence's last item
+            x.block = JOIN ? back : back / x.s.shares;
+            x.share = JOIN ? 0 : back % x.s.shares;
+            x.slot = slots + of(up_slots) - x.s.blocks * x.s.shares + x.block * x.s.shares;
+            return x;
+        }
+        before += all;
+        slots += __builtin_amdgcn_readlane(up_slots, 63);
+        base += kWave;
+        if (base >= p.n) return x;
+        s = sequence(base, tiles);
+    }
+}
+
+template <int FMT, int D, int WAVES>
+__global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p) {
     fetch_arguments<sizeof(PromptParams)>();
     constexpr bool HALF = half_products(FMT);
     constexpr int KS = D / 16, CB = D / 32;
-    __shared__ Tile<FMT, D> sh;
+    constexpr uint32_t ROWS = 32 * WAVES;
+    // waves that fetch keys; with 8 of them the others fetch the values
+    constexpr bool APART = WAVES == 8;
+    static_assert(WAVES == 4 || WAVES == 8);
+    __shared__ Tiles<FMT, D> sh;
     const uint32_t lane = lane_id(), wave = wave_uniform(threadIdx.x / kWave);
     const uint32_t col = lane & 31, hi = lane >> 5;
+    const uint32_t run = wave % 4;  // of a tile: tokens 16 run .. 16 run + 15
 
-    // ---- the block of rows: sequences and their blocks from the last to the first, so that the longest come first
-    const uint32_t h = blockIdx.x % p.H, rest = blockIdx.x / p.H;
-    const uint32_t split = rest % p.splits, block = rest / p.splits;
-    uint32_t b = 0, row0 = 0, first = 0, m_rows = 0;  // sequence, first row of the block, first token's row, new tokens
-    {
-        uint32_t before = 0;
-        bool found = false;
-        for (uint32_t base = 0; base < p.n; base += kWave) {
-            const bool live = base + lane < p.n;
-            const uint32_t s = live ? p.n - 1 - base - lane : 0;
-            const int32_t a = p.starts[s], e = p.starts[s + 1];
-            const bool bad = a < 0 || e < a || (uint32_t)e > p.rows;
-            if (live && bad && p.status) atomicOr(p.status, kDevBadStart);
-            const uint32_t m = live && !bad ? e - a : 0;
-            const uint32_t nb = (m * p.group + kRows - 1) / kRows;
-            const uint32_t up = scan_lanes(nb);
-            const uint32_t all = __builtin_amdgcn_readlane(up, 63);
-            if (block < before + all) {
-                const int at = __builtin_popcountll(__ballot(before + up <= block));
-                b = __builtin_amdgcn_readlane(s, at);
-                first = __builtin_amdgcn_readlane(a, at);
-                m_rows = __builtin_amdgcn_readlane(m, at);
-                row0 = (before + __builtin_amdgcn_readlane(up, at) - 1 - block) * kRows;
-                found = true;
-                break;
-            }
-            before += all;
-        }
-        if (!found) return;
-    }
-    const uint32_t unit_rows = m_rows * p.group;
-    const uint32_t nrows = unit_rows - row0 < kRows ? unit_rows - row0 : kRows;
-    const int32_t given = p.lens[b];
-    const uint32_t most = p.table_cols << p.page_shift;
-    const int32_t len = given < 0 ? 0 : (uint32_t)given > most ? (int32_t)most : given;
-    if (len != given && p.status && threadIdx.x == 0) atomicOr(p.status, kDevBadLength);
-
-    // ---- what its rows see: tokens below `sunk` and from lo to end, in tiles; tile i starts at start_of(i)
-    const int32_t base_pos = len - (int32_t)m_rows;
-    const int32_t pos_lo = base_pos + (int32_t)(row0 / p.group), pos_hi = base_pos + (int32_t)((row0 + nrows - 1) / p.group);
-    const uint32_t end = pos_hi < 0 ? 0 : pos_hi + 1;
-    const uint32_t lo = p.window && pos_lo >= 0 && (uint32_t)pos_lo >= p.window ? pos_lo - p.window + 1 : 0;
-    const uint32_t sunk = p.sinks < lo ? p.sinks : lo;
-    const uint32_t tiles0 = (sunk + kTokens - 1) / kTokens;
-    const uint32_t from = lo / kTokens > tiles0 ? lo / kTokens : tiles0;
-    const uint32_t tiles = tiles0 + ((end + kTokens - 1) / kTokens > from ? (end + kTokens - 1) / kTokens - from : 0);
-    const auto start_of = [&](uint32_t i) { return (i < tiles0 ? i : i - tiles0 + from) * kTokens; };
-    const uint32_t i0 = (uint32_t)((uint64_t)tiles * split / p.splits), i1 = (uint32_t)((uint64_t)tiles * (split + 1) / p.splits);
+    const uint32_t h = blockIdx.x % p.H;
+    const Item item = item_of<ROWS, false>(p, blockIdx.x / p.H);
+    if (!item.found) return;
+    const Sequence& sq = item.s;
+    const uint32_t row0 = item.block * ROWS;
+    const uint32_t nrows = sq.m * p.group - row0 < ROWS ? sq.m * p.group - row0 : ROWS;
+    const Range see = range_of(p, sq.pos_of(row0, p.group), sq.pos_of(row0 + nrows - 1, p.group));
+    const auto start_of = [&](uint32_t i) { return (i < see.tiles0 ? i : i - see.tiles0 + see.from) * kTokens; };
+    const uint32_t i0 = (uint32_t)((uint64_t)see.tiles * item.share / sq.shares),
+                   i1 = (uint32_t)((uint64_t)see.tiles * (item.share + 1) / sq.shares);
 
     // ---- this lane's row; a lane without one takes the block's last, which is not written
     const uint32_t my_row = wave * 32 + col;
     const bool has_row = my_row < nrows;
     const uint32_t R = row0 + (has_row ? my_row : nrows - 1);
     const uint32_t tok = R / p.group, qh = h * p.group + R % p.group;
-    const int32_t pos = base_pos + (int32_t)tok;
+    const int32_t pos = sq.pos_of(R, p.group);
     const bool works = wave * 32 < nrows;  // uniform
-    // positions of the wave's rows
+    // positions of the wave's rows, and of the block's
     const int32_t wave_lo = __builtin_amdgcn_readlane(pos, 0), wave_hi = __builtin_amdgcn_readlane(pos, 31);
+
+    // ---- tiles from memory: a wave fetches one run of 16 tokens, from one page. Tokens that no row sees may hold
+    // anything, NaN too, which times a weight of 0 would stay: a token that is seen takes their place, of the run
+    // if it has one, else the last of all.
+    const auto run_of = [&](uint32_t i) {
+        const uint32_t t = start_of(i) + kRun * run;
+        const bool needed = (t < see.end) & ((t < see.sunk) | (t + kRun > see.lo));
+        return needed ? t : (see.end - 1) & ~(kRun - 1);
+    };
+    const auto page_of = [&](uint32_t i) -> const uint8_t* {
+        uint32_t page = 0;
+        if (i < i1) {
+            // (through the scalar cache: a vector load's wait would be for every tile on its way too)
+            page = *(const __attribute__((address_space(4))) uint32_t*)(uint64_t)(p.table + sq.b * p.table_stride +
+                                                                                 (run_of(i) >> p.page_shift));
+            if (page >= p.num_pages) {
+                if (p.status && lane == 0) atomicOr(p.status, kDevBadPage);
+                page = 0;
+            }
+        }
+        return p.pages + (uint64_t)page * p.page_bytes;
+    };
+    const uint32_t P = 1u << p.page_shift;
+    constexpr uint32_t CODE = page_code_bytes(FMT, D), STEP = page_step_bytes(FMT, D);
+    // registers of tiles on their way (formats that are widened)
+    constexpr int NR = FMT == kPageBf16 ? 1 : (kRun * CODE + 1023) / 1024;  // 16-byte loads of a lane
+    u32x4 raw[2][NR];
+    uint32_t raw_step[2];
+    const auto ask = [&](int kv, uint32_t i, const uint8_t* page) {
+        if (i >= i1 || (APART && wave / 4 != (uint32_t)kv)) return;
+        const uint32_t buf = i & 1;
+        const uint32_t t = run_of(i), at = t & (P - 1);
+        const bool same = t == start_of(i) + kRun * run;
+        const bool whole = same & (t + kRun <= see.end) & ((t + kRun <= see.sunk) | (t >= see.lo));
+        // the row that stands for row r of a run that is not whole
+        const uint32_t last = see.end - 1 - t, near = t < see.sunk ? see.sunk - 1 - t : see.lo - t;
+        const auto other = [&](uint32_t r) {
+            const uint32_t token = t + r;
+            const bool hidden = (token >= see.sunk) & (token < see.lo), none = (token >= see.end) | !same;
+            return none ? last : hidden ? near : r;
+        };
+        const uint32_t line = ((kv ? p.H : 0) + h) * P + at;
+        const uint8_t* rows = page + (uint64_t)line * CODE;
+        const uint8_t* steps = page + p.steps + (uint64_t)line * STEP;
+        if constexpr (FMT == kPageBf16) {
+            constexpr uint32_t RPI = 1024 / CODE;  // rows of one load
+            uint8_t* to = sh.kv[kv][buf] + kRun * run * CODE;
+            // of row r the chunk whose place is at16: places change by exclusive or, so the same change leads back
+            const auto off = [&](uint32_t u) {
+                const uint32_t r = u * RPI + lane / (CODE / 16), at16 = lane % (CODE / 16);
+                return kv ? place_v<D>(r, at16) : place_k<D>(r, at16);
+            };
+            if (whole) {
+#pragma unroll
+                for (uint32_t u = 0; u < kRun / RPI; ++u) fetch16(rows, off(u), to + u * 1024);
+            } else {
+#pragma unroll
+                for (uint32_t u = 0; u < kRun / RPI; ++u)
+                    fetch16(rows, off(u) % CODE + other(off(u) / CODE) * CODE, to + u * 1024);
+            }
+        } else if constexpr (FMT == kPageFp4) {
+            const uint32_t r = whole ? lane / 4 : other(lane / 4);
+            if constexpr (D == 128) {
+                raw[kv][0] = *reinterpret_cast<const u32x4*>(rows + r * CODE + lane % 4 * 16);
+            } else {
+                const u32x2 y = *reinterpret_cast<const u32x2*>(rows + r * CODE + lane % 4 * 8);
+                raw[kv][0] = u32x4{y.x, y.y, 0, 0};
+            }
+            raw_step[kv] = steps[r * STEP + lane % 4 * STEP / 4];
+        } else {
+#pragma unroll
+            for (int u = 0; u < NR; ++u)
+                raw[kv][u] = *reinterpret_cast<const u32x4*>(
+                    rows + (whole ? u * 1024 + lane * 16 : other((u * 1024 + lane * 16) / CODE) * CODE + lane * 16 % CODE));
+            raw_step[kv] = *reinterpret_cast<const uint32_t*>(steps + (whole ? lane % kRun : other(lane % kRun)) * STEP);
+        }
+    };
+    // whether some row of the block does not see some token of the tile
+    const auto mixed = [&](uint32_t i) {
+        const uint32_t t0 = start_of(i);
+        return t0 + kTokens > (uint32_t)(sq.pos_of(row0, p.group) + 1) || sq.pos_of(row0, p.group) < 0 ||
+               (p.window && t0 + kTokens > see.sunk && (int32_t)t0 <= (int32_t)see.end - 1 - (int32_t)p.window);
+    };
+    // ... widened into its buffer
+    const auto put = [&](int kv, uint32_t i) {
+        if (i >= i1 || (APART && wave / 4 != (uint32_t)kv)) return;
+        const uint32_t buf = i & 1;
+        uint8_t* to = sh.kv[kv][buf];
+        if constexpr (FMT == kPageFp4) {
+            const uint32_t r = kRun * run + lane / 4, s = raw_step[kv] << 23;
+            if (kv && raw_step[kv] == 255) sh.odd[buf] = i + 1;
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u) {
+                const uint32_t y = raw[kv][0][u], chunk = lane % 4 * (D / 32) + u;
+                *reinterpret_cast<u32x4*>(to + (kv ? place_v<D>(r, chunk) : place_k<D>(r, chunk))) =
+                    u32x4{widen_fp4<0>(y, s), widen_fp4<1>(y, s), widen_fp4<2>(y, s), widen_fp4<3>(y, s)};
+            }
+        } else if constexpr (HALF) {
+#pragma unroll
+            for (int u = 0; u < NR; ++u) {
+                const uint32_t r = kRun * run + (u * 1024 + lane * 16) / D, chunk = lane * 16 % D / 8;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t a = raw[kv][u][2 * j], c = raw[kv][u][2 * j + 1];
+                    u32x4 y;
+                    if constexpr (FMT == kPageInt8) {
+                        a ^= 0x80808080u;
+                        c ^= 0x80808080u;
+                        y = u32x4{widen_int8<false>(a), widen_int8<true>(a), widen_int8<false>(c), widen_int8<true>(c)};
+                    } else {
+                        y = u32x4{widen_fp8<false>(a), widen_fp8<true>(a), widen_fp8<false>(c), widen_fp8<true>(c)};
+                    }
+                    *reinterpret_cast<u32x4*>(to + (kv ? place_v<D>(r, chunk + j) : place_k<D>(r, chunk + j))) = y;
+                }
+            }
+            if (lane < kRun) sh.steps[kv][buf][kRun * run + lane] = __uint_as_float(raw_step[kv]);
+            if (kv) {
+                const bool nan = raw_step[kv] > 0x7F800000u;
+                if (nan) sh.odd[buf] = i + 1;
+                sh.big[buf][run] = __uint_as_float(max_lanes<16>(nan ? 0 : raw_step[kv]));
+            }
+        } else if (kv && mixed(i)) {
+            // (its loads have arrived) values that are not finite are looked for where some row does not see them
+            uint32_t bad = 0;
+#pragma unroll
+            for (uint32_t u = 0; u < kRun * CODE / 1024; ++u) {
+                const u32x4 y = *reinterpret_cast<const u32x4*>(to + kRun * run * CODE + u * 1024 + lane * 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bad |= ((y[j] & 0x7F80u) == 0x7F80u) | ((y[j] & 0x7F800000u) == 0x7F800000u);
+            }
+            if (bad) sh.odd[buf] = i + 1;
+        }
+    };
+    const auto arrive = [&]() {
+        // LDS that other waves' loads fill is whole once each has waited for its own
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    };
+
+    // the first tile's keys are on their way before the queries are waited for
+    const uint8_t* page = page_of(i0);
+    if (i0 < i1) ask(0, i0, page);
+    if (threadIdx.x < 2) sh.odd[threadIdx.x] = 0;
 
     // ---- queries
     u32x4 qf[KS];
     float f = fabsf(p.scale_log2);
-    f = fmaxf(f, 1e-45f);  // of a scale of 0: all logits alike, and -inf stays what it is
     {
-        const uint16_t* qp = p.q.data + (uint64_t)(first + tok) * p.q.ts + (uint64_t)qh * p.q.hs + 8 * hi;
+        const uint16_t* qp = p.q.data + (uint64_t)(sq.first + tok) * p.q.ts + (uint64_t)qh * p.q.hs + 8 * hi;
 #pragma unroll
         for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qp + 16 * s);
         if constexpr (HALF) {
@@ -202,433 +419,395 @@ __global__ __launch_bounds__(kWavesOf* kWave, 2) void prompt_kernel(PromptParams
             for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) qf[s][i] = pack_half2(bf16_lo(qf[s][i]) * up, bf16_hi(qf[s][i]) * up);
-            f = fmaxf(__builtin_amdgcn_ldexpf(f, -e), 1e-45f);
+            f = __builtin_amdgcn_ldexpf(f, -e);
         } else {
             const uint32_t turn = p.scale_log2 < 0.0f ? 0x80008000u : 0;
 #pragma unroll
             for (int s = 0; s < KS; ++s) qf[s] ^= turn;
         }
+        f = fmaxf(f, 1e-45f);  // of a scale of 0: all logits alike, and -inf stays what it is
     }
 
-    // ---- tiles from memory: wave w fetches tokens 16 w .. 16 w + 15 of keys and values, one run, from one page. Tokens
-    // that no row sees may hold anything, NaN too, which times a weight of 0 would stay: a token that is seen takes
-    // their place, of the run if it has one, else the last of all.
-    const auto needed = [&](uint32_t t) { return (t < end) & ((t < sunk) | (t + kRun > lo)); };
-    const auto run_of = [&](uint32_t i) {
-        const uint32_t t = start_of(i) + kRun * wave;
-        return needed(t) ? t : (end - 1) & ~(kRun - 1);
-    };
-    const auto page_of = [&](uint32_t i) -> const uint8_t* {
-        uint32_t page = 0;
-        if (i < i1) {
-            page = (uint32_t)p.table[b * p.table_stride + (run_of(i) >> p.page_shift)];
-            if (page >= p.num_pages) {
-                if (p.status && lane == 0) atomicOr(p.status, kDevBadPage);
-                page = 0;
-            }
-        }
-        return p.pages + (uint64_t)wave_uniform(page) * p.page_bytes;
-    };
-    const uint32_t P = 1u << p.page_shift;
-    constexpr uint32_t CODE = page_code_bytes(FMT, D), STEP = page_step_bytes(FMT, D);
-    // registers of a tile on its way (formats that are widened)
-    constexpr int NR = FMT == kPageBf16 ? 1 : (kRun * CODE + 1023) / 1024;  // 16-byte loads of a lane
-    u32x4 raw[2][NR];
-    uint32_t raw_step[2];
-    const auto ask = [&](uint32_t i, uint32_t buf, const uint8_t* page) {
-        const uint32_t t = run_of(i), at = t & (P - 1);
-        const bool whole = (t == start_of(i) + kRun * wave) & (t + kRun <= end) & ((t + kRun <= sunk) | (t >= lo));
-        // the row that stands for row r of the run
-        const auto row = [&](uint32_t r) {
-            if (whole) return r;
-            const uint32_t tok = t + r;
-            if (tok >= end || t != start_of(i) + kRun * wave) return end - 1 - t;
-            return tok < sunk || tok >= lo ? r : t < sunk ? sunk - 1 - t : lo - t;
-        };
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t line = ((kv ? p.H : 0) + h) * P + at;
-            const uint8_t* rows = page + (uint64_t)line * CODE;
-            const uint8_t* steps = page + p.steps + (uint64_t)line * STEP;
-            if constexpr (FMT == kPageBf16) {
-                constexpr uint32_t RPI = 1024 / CODE;  // rows of one load
-                uint8_t* to = sh.kv[buf][kv] + kRun * wave * CODE;
-#pragma unroll
-                for (uint32_t u = 0; u < kRun / RPI; ++u) {
-                    const uint32_t r = u * RPI + lane / (CODE / 16), at16 = lane % (CODE / 16);
-                    // the chunk whose place is at16: places change by exclusive or, so the same change leads back
-                    const uint32_t off = kv ? place_v<D>(r, at16) : place_k<D>(r, at16);
-                    fetch16(rows + (off % CODE + row(r) * CODE), to + u * 1024);
-                }
-            } else if constexpr (FMT == kPageFp4) {
-                const uint32_t r = row(lane / 4);
-                if constexpr (D == 128) {
-                    raw[kv][0] = *reinterpret_cast<const u32x4*>(rows + r * CODE + lane % 4 * 16);
-                } else {
-                    const u32x2 y = *reinterpret_cast<const u32x2*>(rows + r * CODE + lane % 4 * 8);
-                    raw[kv][0] = u32x4{y.x, y.y, 0, 0};
-                }
-                raw_step[kv] = steps[r * STEP + lane % 4 * STEP / 4];
-            } else {
-#pragma unroll
-                for (int u = 0; u < NR; ++u)
-                    raw[kv][u] = *reinterpret_cast<const u32x4*>(rows + row((u * 1024 + lane * 16) / CODE) * CODE + lane * 16 % CODE);
-                raw_step[kv] = *reinterpret_cast<const uint32_t*>(steps + row(lane % kRun) * STEP);
-            }
-        }
-    };
-    const auto put = [&](uint32_t buf) {
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            uint8_t* to = sh.kv[buf][kv];
-            if constexpr (FMT == kPageFp4) {
-                const uint32_t r = kRun * wave + lane / 4, s = raw_step[kv] << 23;
-#pragma unroll
-                for (int u = 0; u < D / 32; ++u) {
-                    const uint32_t y = raw[kv][0][u], chunk = lane % 4 * (D / 32) + u;
-                    *reinterpret_cast<u32x4*>(to + (kv ? place_v<D>(r, chunk) : place_k<D>(r, chunk))) =
-                        u32x4{widen_fp4<0>(y, s), widen_fp4<1>(y, s), widen_fp4<2>(y, s), widen_fp4<3>(y, s)};
-                }
-            } else if constexpr (HALF) {
-#pragma unroll
-                for (int u = 0; u < NR; ++u) {
-                    const uint32_t r = kRun * wave + (u * 1024 + lane * 16) / D, chunk = lane * 16 % D / 8;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t a = raw[kv][u][2 * j], c = raw[kv][u][2 * j + 1];
-                        u32x4 y;
-                        if constexpr (FMT == kPageInt8) {
-                            a ^= 0x80808080u;
-                            c ^= 0x80808080u;
-                            y = u32x4{widen_int8<false>(a), widen_int8<true>(a), widen_int8<false>(c), widen_int8<true>(c)};
-                        } else {
-                            y = u32x4{widen_fp8<false>(a), widen_fp8<true>(a), widen_fp8<false>(c), widen_fp8<true>(c)};
-                        }
-                        *reinterpret_cast<u32x4*>(to + (kv ? place_v<D>(r, chunk + j) : place_k<D>(r, chunk + j))) = y;
-                    }
-                }
-                if (lane < kRun) sh.steps[buf][kv][kRun * wave + lane] = __uint_as_float(raw_step[kv]);
-            }
-        }
-    };
-
     // ---- running state
-    f32x16 o[CB];
+    f32x16 o[CB], s[2];
 #pragma unroll
     for (int n = 0; n < CB; ++n)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[n][i] = 0.0f;
-    float m = kNegInf, mu = 0.0f, l = 0.0f;
+    float m = kNegInf, mu = 0.0f, l = 0.0f, top = kNegInf;
     int E = -100;  // exponent taken out of the weights (HALF), which no step so far has reached
     float wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp + 100);
 
-    const auto tile = [&](uint32_t t0, uint32_t buf) {
-        const uint8_t* kt = sh.kv[buf][0];
-        const uint8_t* vt = sh.kv[buf][1];
-        // whether this wave's rows see none, some or all of the tile
-        if (!works || wave_hi < (int32_t)t0) return;
-        const bool seen_by_window =  // all of it
-            !p.window || t0 + kTokens <= p.sinks || (int32_t)t0 > wave_hi - (int32_t)p.window;
-        const bool all = (int32_t)(t0 + kTokens - 1) <= wave_lo && seen_by_window;
-        // whether the row sees token t0 + 4 hi + c
-        const int32_t past = pos - (int32_t)t0 - 4 * (int32_t)hi;
-        const int32_t left = p.window ? past - (int32_t)p.window : -0x7FFFFFFF;
-        const int32_t sunk_to = p.window ? (int32_t)p.sinks - (int32_t)t0 - 4 * (int32_t)hi : 0;
-        const auto counts = [&](int32_t c) { return (c <= past) & ((c > left) | (c < sunk_to)); };
-
-        f32x16 s[2];
+    // whether the row sees token t0 + 4 hi + c
+    struct Sight {
+        int32_t past, left, sunk_to;
+        __device__ __forceinline__ bool operator()(int32_t c) const { return (c <= past) & ((c > left) | (c < sunk_to)); }
+    };
+    const auto sight_of = [&](uint32_t t0) {
+        Sight x;
+        x.past = pos - (int32_t)t0 - 4 * (int32_t)hi;
+        x.left = p.window ? x.past - (int32_t)p.window : -0x7FFFFFFF;
+        x.sunk_to = p.window ? (int32_t)p.sinks - (int32_t)t0 - 4 * (int32_t)hi : 0;
+        return x;
+    };
+    // whether every row of the wave sees the whole tile
+    const auto all_seen = [&](uint32_t t0) {
+        return (int32_t)(t0 + kTokens - 1) <= wave_lo &&
+               (!p.window || t0 + kTokens <= p.sinks || (int32_t)t0 > wave_hi - (int32_t)p.window);
+    };
+    const auto zero = [](f32x16 (&x)[2]) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[u][i] = 0.0f;
+            for (int i = 0; i < 16; ++i) x[u][i] = 0.0f;
+    };
+    // a product step's keys: 32 tokens each, 16 channels
+    const auto keys = [&](const uint8_t* kt, int k, u32x4 (&a)[2]) {
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const u32x4 a = *reinterpret_cast<const u32x4*>(kt + place_k<D>(32 * u + col, 2 * k + hi));
-                s[u] = mfma<FMT>(a, qf[k], s[u]);
-            }
-        }
+        for (int u = 0; u < 2; ++u) a[u] = *reinterpret_cast<const u32x4*>(kt + place_k<D>(32 * u + col, 2 * k + hi));
+    };
+    // its steps and its mask, and the largest logit
+    const auto finish = [&](uint32_t i, f32x16 (&x)[2]) {
         if constexpr (HALF) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const f32x4 ks = *reinterpret_cast<const f32x4*>(&sh.steps[buf][0][32 * u + 8 * j + 4 * hi]);
+                    const f32x4 ks = *reinterpret_cast<const f32x4*>(&sh.steps[0][i & 1][32 * u + 8 * j + 4 * hi]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[u][4 * j + i] *= ks[i];
+                    for (int c = 0; c < 4; ++c) x[u][4 * j + c] *= ks[c];
                 }
         }
-        if (!all) {
+        const uint32_t t0 = start_of(i);
+        if (!all_seen(t0)) {
+            const Sight sees = sight_of(t0);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[u][i] = counts(32 * u + 8 * (i / 4) + i % 4) ? s[u][i] : kNegInf;
+                for (int c = 0; c < 16; ++c) x[u][c] = sees(32 * u + 8 * (c / 4) + c % 4) ? x[u][c] : kNegInf;
         }
-        float top = s[0][0];
+        float y = x[0][0];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-        top *= f;
-        // steps of the values, brought into binary16's range by 2^-E
-        float vs[HALF ? 32 : 1];
-        bool move = top > m + kSlack;
-        float big = 0.0f;
-        if constexpr (HALF) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x4 y = *reinterpret_cast<const f32x4*>(&sh.steps[buf][1][32 * u + 8 * j + 4 * hi]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        vs[16 * u + 4 * j + i] = y[i];
-                        big = fmaxf(big, (all | counts(32 * u + 8 * j + i)) ? y[i] : 0.0f);
-                    }
-                }
-            move |= big >= __builtin_amdgcn_ldexpf(1.0f, E);
-        }
-        if (__ballot(move) != 0) {
-            const auto larger = [](float a, float c) { return fmaxf(a, c); };
-            const float nm = fmaxf(m, over_pair(top, larger));
-            float a = nm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - nm);
-            m = nm;
-            mu = nm == kNegInf ? 0.0f : nm;
-            l *= a;
-            if constexpr (HALF) {
-                big = over_pair(big, larger);
-                const int ne = big >= __builtin_amdgcn_ldexpf(1.0f, E) ? __builtin_amdgcn_frexp_expf(big) : E;
-                a *= __builtin_amdgcn_ldexpf(1.0f, E - ne);
-                E = ne;
-                wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - E);
-            }
-#pragma unroll
-            for (int n = 0; n < CB; ++n) o[n] *= a;
-        }
-        u32x4 pf[4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float e[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    e[i] = __builtin_amdgcn_exp2f(fmaf(s[u][2 * j + i], f, -mu));
-                    l += e[i];
-                    if constexpr (HALF) {
-                        e[i] *= vs[16 * u + 2 * j + i] * wmul;
-                    }
-                }
-                if constexpr (HALF) {
-                    if (!all) {  // a step that does not count may be NaN
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) e[i] = s[u][2 * j + i] == kNegInf ? 0.0f : e[i];
-                    }
-                    pf[2 * u + j / 4][j % 4] = pack_half2(e[0], e[1]);
-                } else {
-                    pf[2 * u + j / 4][j % 4] = pack_bf16x2(e[0], e[1]);
-                }
-            }
-        // four tokens of one channel a read: token 4 g + (lane % 16) / 4 of the tile, channels of 64 bytes
-        const uint32_t i16 = lane & 15;
-        const auto values = [&](int k, int n) {
-            const uint32_t chunk = 4 * n + (lane >> 4 & 1) * 2 + (i16 & 3) / 2;
-            const uint32_t t = 16 * k + 4 * hi + i16 / 4;
-            const auto part = [&](uint32_t token) {
-                return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                     (KVC_LDS s16x4*)(vt + place_v<D>(token, chunk) + (i16 & 1) * 8)));
-            };
-            const u32x2 a = part(t), c = part(t + 8);
-            return u32x4{a.x, a.y, c.x, c.y};
+            for (int c = 0; c < 16; ++c) y = fmaxf(y, x[u][c]);
+        top = y * f;
+    };
+    // four tokens of one channel a read: token 4 hi + (lane % 16) / 4 of each 8, channels of 64 bytes
+    const uint32_t i16 = lane & 15;
+    const auto values = [&](const uint8_t* vt, int k, int n) {
+        const uint32_t chunk = 4 * n + (lane >> 4 & 1) * 2 + (i16 & 3) / 2;
+        const uint32_t t = 16 * k + 4 * hi + i16 / 4;
+        const auto part = [&](uint32_t token) {
+            return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                 (KVC_LDS s16x4*)(vt + place_v<D>(token, chunk) + (i16 & 1) * 8)));
         };
-        bool clean = true;
-        if constexpr (!HALF) {
-            if (!all) {
-                // a value that is not finite, times a weight of 0, would reach rows that do not see its token
-                uint32_t bad = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int n = 0; n < CB; ++n) {
-                        const u32x4 y = values(k, n);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            bad |= ((y[i] & 0x7F80u) == 0x7F80u) | ((y[i] & 0x7F800000u) == 0x7F800000u);
-                    }
-                clean = __ballot(bad != 0) == 0;
-            }
-        }
-        if (__builtin_expect(!clean, 0)) {
-            // rows that see such a value become NaN in its channel here; below it is left out
+        const u32x2 a = part(t), c = part(t + 8);
+        return u32x4{a.x, a.y, c.x, c.y};
+    };
+    // Values of a buffer (8 bits: their steps) that are not finite, in a tile that some row sees only part of: rows that
+    // see one become NaN in its channel here, and it becomes 0. (Every wave comes by.)
+    const auto take_out = [&](uint32_t t0, uint32_t buf) __attribute__((always_inline)) {
+        uint8_t* vt = sh.kv[1][buf];
+        const Sight sees = sight_of(t0);
+        const float nan = __builtin_nanf("");
 #pragma unroll 1
-            for (int t = 0; t < (int)kTokens; ++t) {
-                const bool sees = counts(t - 4 * (int32_t)hi);
+        for (int t = 0; t < (int)kTokens; ++t) {
+            const bool sees_it = sees(t - 4 * (int32_t)hi);
 #pragma unroll
-                for (int n = 0; n < CB; ++n)
+            for (int n = 0; n < CB; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const u32x2 y = *reinterpret_cast<const u32x2*>(vt + place_v<D>(t, 4 * n + j) + 8 * hi);
+                for (int j = 0; j < 4; ++j) {
+                    u32x2 y{};
+                    if (!HALF) y = *reinterpret_cast<const u32x2*>(vt + place_v<D>(t, 4 * n + j) + 8 * hi);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t bits = y[i / 2] >> (16 * (i % 2)) & 0x7F80u;
-                            o[n][4 * j + i] = (sees & (bits == 0x7F80u)) ? __builtin_nanf("") : o[n][4 * j + i];
-                        }
-                    }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int n = 0; n < CB; ++n) {
-                u32x4 y = values(k, n);
-                if (__builtin_expect(!clean, 0)) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[i] = (y[i] & 0x7F80u) == 0x7F80u ? y[i] & 0xFFFF0000u : y[i];
-                        y[i] = (y[i] & 0x7F800000u) == 0x7F800000u ? y[i] & 0xFFFFu : y[i];
+                    for (int c = 0; c < 4; ++c) {
+                        const bool bad = HALF ? __builtin_isnan(sh.steps[1][buf][HALF ? t : 0])
+                                              : (y[c / 2] >> (16 * (c % 2)) & 0x7F80u) == 0x7F80u;
+                        o[n][4 * j + c] = (sees_it & bad) ? nan : o[n][4 * j + c];
                     }
                 }
-                o[n] = mfma<FMT>(y, pf[k], o[n]);
+        }
+        __syncthreads();
+        if constexpr (HALF) {
+            if (threadIdx.x < kTokens) {
+                float& x = sh.steps[1][buf][threadIdx.x];
+                x = __builtin_isnan(x) ? 0.0f : x;
             }
+        } else {
+            for (uint32_t at = threadIdx.x * 16; at < Tiles<FMT, D>::kBytes; at += WAVES * kWave * 16) {
+                u32x4 y = *reinterpret_cast<u32x4*>(vt + at);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    y[c] = (y[c] & 0x7F80u) == 0x7F80u ? y[c] & 0xFFFF0000u : y[c];
+                    y[c] = (y[c] & 0x7F800000u) == 0x7F800000u ? y[c] & 0xFFFFu : y[c];
+                }
+                *reinterpret_cast<u32x4*>(vt + at) = y;
+            }
+        }
+        __syncthreads();
     };
 
+    // ---- the tiles: while a tile's weights are formed and its values added, the next one's logits are on their way,
+    // and the keys behind those and the next values come from memory
     if (i0 < i1) {
-        const auto arrive = [&]() {
-            // LDS that other waves' loads fill is whole once each has waited for its own
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            __syncthreads();
-        };
-        const uint8_t* page = page_of(i0);
-        ask(i0, 0, page);
-        page = page_of(i0 + 1);
-        if (FMT != kPageBf16) put(0);
         arrive();
-        for (uint32_t i = i0; i < i1; ++i) {
-            const uint32_t buf = (i - i0) & 1;
-            if (i + 1 < i1) {
-                ask(i + 1, buf ^ 1, page);
-                page = page_of(i + 2);
+        put(0, i0);
+        __syncthreads();
+        ask(1, i0, page);
+        page = page_of(i0 + 1);
+        ask(0, i0 + 1, page);
+        const uint8_t* page2 = page_of(i0 + 2);
+        if (works) {
+            zero(s);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                u32x4 a[2];
+                keys(sh.kv[0][i0 & 1], k, a);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) s[u] = mfma<FMT>(a[u], qf[k], s[u]);
             }
-            tile(start_of(i), buf);
-            if (FMT != kPageBf16 && i + 1 < i1) put(buf ^ 1);
+            finish(i0, s);
+        }
+        const auto step = [&](uint32_t i, f32x16 (&s)[2], f32x16 (&next)[2]) __attribute__((always_inline)) {
+            const uint32_t buf = i & 1;
             arrive();
+            put(1, i);
+            put(0, i + 1);
+            __syncthreads();  // values i and keys i + 1 are there; keys i and values i - 1 are done with
+            ask(1, i + 1, page);
+            page = page2;
+            ask(0, i + 2, page);
+            page2 = page_of(i + 3);
+            if (__builtin_expect(sh.odd[buf] == i + 1, 0)) {
+                if (mixed(i)) take_out(start_of(i), buf);
+            }
+            if (!works) return;
+            bool move = top > m + kSlack;
+            // steps of the values are brought into binary16's range by 2^-E; those that the row sees count for E
+            float big = 0.0f;
+            if constexpr (HALF) {
+                const uint32_t t0 = start_of(i);
+                if (all_seen(t0)) {
+                    const f32x4 y = *reinterpret_cast<const f32x4*>(sh.big[buf]);
+                    big = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+                } else {
+                    const Sight sees = sight_of(t0);
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) {
+                        const int t = 8 * w;
+                        const f32x4 y = *reinterpret_cast<const f32x4*>(&sh.steps[1][buf][t + 4 * hi]);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) big = fmaxf(big, sees(t + c) ? y[c] : 0.0f);
+                    }
+                }
+                move |= big >= __builtin_amdgcn_ldexpf(1.0f, E);
+            }
+            if (__ballot(move) != 0) {
+                const auto larger = [](float a, float c) { return fmaxf(a, c); };
+                const float nm = fmaxf(m, over_pair(top, larger));
+                float a = nm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - nm);
+                m = nm;
+                mu = nm == kNegInf ? 0.0f : nm;
+                l *= a;
+                if constexpr (HALF) {
+                    big = over_pair(big, larger);
+                    const int ne = big >= __builtin_amdgcn_ldexpf(1.0f, E) ? __builtin_amdgcn_frexp_expf(big) : E;
+                    a *= __builtin_amdgcn_ldexpf(1.0f, E - ne);
+                    E = ne;
+                    wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - E);
+                }
+#pragma unroll
+                for (int n = 0; n < CB; ++n) o[n] *= a;
+            }
+            // The next tile's logits (behind the last tile: of whatever the buffer holds, not used), a step of them beside
+            // some of this one's weights; then the values. What a step reads from LDS was asked for one step before.
+            // The barriers keep the compiler from asking for everything at once, which spills 100 registers.
+            zero(next);
+            const uint8_t* kt = sh.kv[0][buf ^ 1];
+            const uint8_t* vt = sh.kv[1][buf];
+            constexpr int PAIRS = 16 / KS;  // of weights in a step
+            u32x4 pf[4], a[2][2], y[2][2];
+            f32x4 vs[2][HALF ? PAIRS / 2 : 1];
+            const auto steps_of = [&](int k, f32x4 (&x)[HALF ? PAIRS / 2 : 1]) {
+                if constexpr (HALF) {
+#pragma unroll
+                    for (int w = 0; w < PAIRS / 2; ++w)
+                        x[w] = *reinterpret_cast<const f32x4*>(&sh.steps[1][buf][8 * (PAIRS / 2 * k + w) + 4 * hi]);
+                }
+            };
+            keys(kt, 0, a[0]);
+            steps_of(0, vs[0]);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                if (k + 1 < KS) {
+                    keys(kt, k + 1, a[(k + 1) & 1]);
+                    steps_of(k + 1, vs[(k + 1) & 1]);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) y[0][x] = values(vt, 0, x);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) next[u] = mfma<FMT>(a[k & 1][u], qf[k], next[u]);
+#pragma unroll
+                for (int x = 0; x < PAIRS; ++x) {
+                    const int w = PAIRS * k + x;  // tokens of elements 2 w, 2 w + 1 of 32
+                    float e[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        e[c] = __builtin_amdgcn_exp2f(fmaf(s[w / 8][2 * (w % 8) + c], f, -mu));
+                        l += e[c];
+                        if constexpr (HALF) e[c] = e[c] * vs[k & 1][x / 2][2 * (x % 2) + c] * wmul;
+                    }
+                    pf[w / 4][w % 4] = HALF ? pack_half2(e[0], e[1]) : pack_bf16x2(e[0], e[1]);
+                }
+                asm volatile("" : "+v"(l));  // added up here, not at the end, where all weights would have to be kept
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            constexpr int VS = 4 * CB / 2;  // steps of two products
+#pragma unroll
+            for (int v = 0; v < VS; ++v) {
+                if (v + 1 < VS) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) y[(v + 1) & 1][x] = values(vt, (2 * v + 2 + x) / CB, (2 * v + 2 + x) % CB);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int k = (2 * v + x) / CB, n = (2 * v + x) % CB;
+                    o[n] = mfma<FMT>(y[v & 1][x], pf[k], o[n]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (i + 1 < i1) finish(i + 1, next);
+        };
+        // two tiles a turn, so that the logits need no moving
+        f32x16 other[2];
+        for (uint32_t i = i0;;) {
+            step(i, s, other);
+            if (++i == i1) break;
+            step(i, other, s);
+            if (++i == i1) break;
         }
     }
 
     // ---- output
     l = over_pair(l, [](float a, float c) { return a + c; });
-    const uint64_t out_row = (uint64_t)(first + tok) * p.Hq + qh;
     if (HALF) {
         const float down = __builtin_amdgcn_ldexpf(1.0f, E - kWeightExp);
 #pragma unroll
         for (int n = 0; n < CB; ++n) o[n] *= down;
     }
-    if (p.splits > 1) {
+    if (sq.shares > 1) {
         if (!has_row) return;
-        const uint64_t all_rows = (uint64_t)p.rows * p.Hq;
-        float* to = p.part + (split * all_rows + out_row) * D;
+        float* to = p.part + ((uint64_t)(item.slot + item.share) * p.H + h) * (ROWS * (D + 2));
 #pragma unroll
         for (int n = 0; n < CB; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<f32x4*>(to + 32 * n + 8 * j + 4 * hi) =
+                *reinterpret_cast<f32x4*>(to + my_row * D + 32 * n + 8 * j + 4 * hi) =
                     f32x4{o[n][4 * j], o[n][4 * j + 1], o[n][4 * j + 2], o[n][4 * j + 3]};
-        if (hi == 0)
-            *reinterpret_cast<float2*>(p.part + p.splits * all_rows * D + (split * all_rows + out_row) * 2) = make_float2(m, l);
+        if (hi == 0) *reinterpret_cast<float2*>(to + ROWS * D + 2 * my_row) = make_float2(m, l);
         return;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    if (p.lse && has_row && hi == 0) p.lse[out_row] = (m + log2f(l)) * 0.69314718055994531f;
-    // rows go through LDS, so that they are written in one piece
-    constexpr uint32_t LINE = 2 * D + 16;
-    static_assert(kWavesOf * 32 * LINE <= sizeof(sh.kv));
-    uint8_t* mine = &sh.kv[0][0][0] + wave * 32 * LINE;
+    if (p.lse && has_row && hi == 0) p.lse[(uint64_t)(sq.first + tok) * p.Hq + qh] = (m + log2f(l)) * 0.69314718055994531f;
+    // rows go through LDS, 16 of a wave at a time, so that they are written in one piece
+    constexpr uint32_t LINE = 2 * D + 16, LPR = 2 * D / 16;  // bytes of a row there; lanes that write one
+    static_assert(WAVES * 16 * LINE <= sizeof(sh.kv));
+    uint8_t* mine = &sh.kv[0][0][0] + wave * 16 * LINE;
+    __syncthreads();
 #pragma unroll
-    for (int n = 0; n < CB; ++n)
+    for (uint32_t part = 0; part < 2; ++part) {
+        if (col / 16 == part) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<u32x2*>(mine + col * LINE + 2 * (32 * n + 8 * j + 4 * hi)) =
-                u32x2{pack_bf16x2(o[n][4 * j] * inv, o[n][4 * j + 1] * inv), pack_bf16x2(o[n][4 * j + 2] * inv, o[n][4 * j + 3] * inv)};
-    __builtin_amdgcn_wave_barrier();
-    constexpr uint32_t LPR = 2 * D / 16;  // lanes of a row
+            for (int n = 0; n < CB; ++n)
 #pragma unroll
-    for (uint32_t u = 0; u < 32 * LPR / kWave; ++u) {
-        const uint32_t r = u * (kWave / LPR) + lane / LPR, piece = lane % LPR;
-        const uint32_t at = wave * 32 + r;
-        if (at >= nrows) continue;
-        const uint32_t to_tok = (row0 + at) / p.group, to_head = h * p.group + (row0 + at) % p.group;
-        *reinterpret_cast<u32x4*>(p.out.data + (uint64_t)(first + to_tok) * p.out.ts + (uint64_t)to_head * p.out.hs + 8 * piece) =
-            *reinterpret_cast<const u32x4*>(mine + r * LINE + 16 * piece);
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<u32x2*>(mine + col % 16 * LINE + 2 * (32 * n + 8 * j + 4 * hi)) =
+                        u32x2{pack_bf16x2(o[n][4 * j] * inv, o[n][4 * j + 1] * inv),
+                              pack_bf16x2(o[n][4 * j + 2] * inv, o[n][4 * j + 3] * inv)};
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (uint32_t u = 0; u < 16 * LPR / kWave; ++u) {
+            const uint32_t r = u * (kWave / LPR) + lane / LPR, piece = lane % LPR, at = wave * 32 + part * 16 + r;
+            const uint32_t to_tok = (row0 + at) / p.group, to_head = h * p.group + (row0 + at) % p.group;
+            if (at < nrows)
+                *reinterpret_cast<u32x4*>(p.out.data + (uint64_t)(sq.first + to_tok) * p.out.ts + (uint64_t)to_head * p.out.hs +
+                                          8 * piece) = *reinterpret_cast<const u32x4*>(mine + r * LINE + 16 * piece);
+        }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
-// Joins the shares of a row's tokens, a wave a row.
-template <int D>
+// Joins the shares of a block's rows: a workgroup a block, four channels a lane.
+template <int D, uint32_t ROWS>
 __global__ __launch_bounds__(kBlockThreads) void prompt_join_kernel(PromptParams p) {
-    constexpr int C = D / kWave;
-    const uint32_t lane = lane_id(), wave = wave_uniform(threadIdx.x / kWave);
-    const uint64_t all_rows = (uint64_t)p.rows * p.Hq, row = (uint64_t)blockIdx.x * (kBlockThreads / kWave) + wave;
-    if (row >= all_rows) return;
-    const int32_t n = (int32_t)(row / p.Hq);
-    if (n < p.starts[0] || n >= p.starts[p.n]) return;
-    const float* ml = p.part + p.splits * all_rows * D;
-    float M = kNegInf;
-    for (uint32_t s = 0; s < p.splits; ++s) M = fmaxf(M, ml[(s * all_rows + row) * 2]);
-    const float mu = M == kNegInf ? 0.0f : M;
-    float total = 0.0f, y[C] = {};
-    for (uint32_t s = 0; s < p.splits; ++s) {
-        const float2 x = *reinterpret_cast<const float2*>(ml + (s * all_rows + row) * 2);
-        const float a = __builtin_amdgcn_exp2f(x.x - mu);
-        total = fmaf(x.y, a, total);
-#pragma unroll
-        for (int c = 0; c < C; ++c) y[c] += p.part[(s * all_rows + row) * D + C * lane + c] * a;
+    fetch_arguments<sizeof(PromptParams)>();
+    constexpr uint32_t LPR = D / 4, RPB = kBlockThreads / LPR;
+    const uint32_t h = blockIdx.x % p.H;
+    const Item item = item_of<ROWS, true>(p, blockIdx.x / p.H);
+    if (!item.found || item.s.shares == 1) return;
+    const uint32_t row0 = item.block * ROWS, all = item.s.m * p.group;
+    const uint32_t nrows = all - row0 < ROWS ? all - row0 : ROWS, shares = item.s.shares;
+    const uint64_t each = (uint64_t)p.H * (ROWS * (D + 2));
+    const float* from = p.part + ((uint64_t)item.slot * p.H + h) * (ROWS * (D + 2));
+    const uint32_t c = threadIdx.x % LPR * 4;
+    for (uint32_t r = threadIdx.x / LPR; r < nrows; r += RPB) {
+        float M = kNegInf;
+        for (uint32_t s = 0; s < shares; ++s) M = fmaxf(M, from[s * each + ROWS * D + 2 * r]);
+        const float Mu = M == kNegInf ? 0.0f : M;
+        float total = 0.0f;
+        f32x4 y = 0.0f;
+        for (uint32_t s = 0; s < shares; ++s) {
+            const float2 ml = *reinterpret_cast<const float2*>(from + s * each + ROWS * D + 2 * r);
+            const float a = __builtin_amdgcn_exp2f(ml.x - Mu);
+            total = fmaf(ml.y, a, total);
+            y += *reinterpret_cast<const f32x4*>(from + s * each + r * D + c) * a;
+        }
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        const uint32_t tok = item.s.first + (row0 + r) / p.group, qh = h * p.group + (row0 + r) % p.group;
+        *reinterpret_cast<u32x2*>(p.out.data + (uint64_t)tok * p.out.ts + (uint64_t)qh * p.out.hs + c) =
+            u32x2{pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv)};
+        if (p.lse && c == 0) p.lse[(uint64_t)tok * p.Hq + qh] = (M + log2f(total)) * 0.69314718055994531f;
     }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    uint16_t* to = p.out.data + (uint64_t)n * p.out.ts + (row % p.Hq) * p.out.hs + C * lane;
-    if constexpr (C == 2)
-        *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(y[0] * inv, y[1] * inv);
-    else
-        *to = (uint16_t)pack_bf16x2(y[0] * inv, 0.0f);
-    if (p.lse && lane == 0) p.lse[row] = (M + log2f(total)) * 0.69314718055994531f;
 }
 
 template <int FMT, int D>
-hipError_t launch(const PromptParams& p, uint32_t grid, hipStream_t stream) {
-    return launch_kernel(prompt_kernel<FMT, D>, dim3(grid), dim3(kWavesOf * kWave), stream, p);
+hipError_t launch(const PromptParams& p, uint32_t waves, uint32_t grid, hipStream_t stream) {
+    return launch_kernel(waves == 8 ? prompt_kernel<FMT, D, 8> : prompt_kernel<FMT, D, 4>, dim3(grid), dim3(waves * kWave),
+                         stream, p);
 }
 template <int D>
-hipError_t launch_of(uint32_t format, const PromptParams& p, uint32_t grid, hipStream_t stream) {
+hipError_t launch_of(uint32_t format, const PromptParams& p, uint32_t waves, uint32_t grid, hipStream_t stream) {
     switch (format) {
-        case kPageBf16: return launch<kPageBf16, D>(p, grid, stream);
-        case kPageInt8: return launch<kPageInt8, D>(p, grid, stream);
-        case kPageFp8: return launch<kPageFp8, D>(p, grid, stream);
-        default: return launch<kPageFp4, D>(p, grid, stream);
+        case kPageBf16: return launch<kPageBf16, D>(p, waves, grid, stream);
+        case kPageInt8: return launch<kPageInt8, D>(p, waves, grid, stream);
+        case kPageFp8: return launch<kPageFp8, D>(p, waves, grid, stream);
+        default: return launch<kPageFp4, D>(p, waves, grid, stream);
     }
 }
 
-// Workgroups that the GPU holds at once, and the fewest tokens of a share.
-constexpr uint64_t kPlaces = 512, kMinShare = 256;
+// Workgroups of 4 waves that the GPU holds at once.
+constexpr uint64_t kPlaces = 512;
 
 }  // namespace
 
 PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens,
                        uint32_t window, uint32_t sinks) {
-    PromptPlan a{kRows, 1, 0, 256, 256};
     const uint64_t group = Hq / H;
-    a.blocks = n_tokens * group / kRows + n_seqs;
+    PromptPlan a{};
+    a.rows = 128;
+    a.blocks = n_tokens * group / a.rows + n_seqs;
+    a.bytes = a.room = 256;
     // with a window, a block's rows see the tokens of one row and as many more as the block has tokens
-    const uint64_t seen = window ? seen_tokens(max_tokens, (uint64_t)window + kRows / group, sinks) : max_tokens;
-    const uint64_t most = (seen + kMinShare - 1) / kMinShare;
-    const uint64_t shares = a.blocks ? kPlaces / (H * a.blocks) : 1;
-    a.splits = (uint32_t)(shares < 1 || most < 1 ? 1 : shares < most ? shares : most);
-    const uint64_t rows = (uint64_t)n_tokens * Hq, each = (uint64_t)(d + 2) * 4;
-    if (a.splits > 1) a.bytes = align_up(a.splits * rows * each, 256);
-    if (most > 1) {
-        // at most kPlaces shares of kRows rows
-        const uint64_t bound = rows * most < kPlaces * kRows ? rows * most : kPlaces * kRows;
-        a.room = align_up(bound * each, 256);
-        if (a.room < 256) a.room = 256;
-    }
+    const uint64_t seen = window ? seen_tokens(max_tokens, (uint64_t)window + a.rows / group, sinks) : max_tokens;
+    const bool can = seen > kMinShare * kTokens;
+    if (can && H * a.blocks < 4 * kPlaces) a.more = (uint32_t)((kPlaces + H - 1) / H);
+    // a block that is cut up has two shares at least: no more than 2 more of them
+    const uint64_t each = (uint64_t)a.rows * (d + 2) * 4;
+    if (a.more) a.bytes = align_up(2 * a.more * H * each, 256);
+    if (can) a.room = align_up(2 * ((kPlaces + H - 1) / H) * H * each, 256);
     return a;
 }
 
@@ -656,15 +835,16 @@ hipError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& plan, hip
     p.page_shift = 31 - __builtin_clz(lay.P);
     p.window = a.tail.window;
     p.sinks = a.tail.sinks;
-    p.splits = plan.splits;
+    p.more = plan.more;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.part = static_cast<float*>(a.ws);
-    const uint32_t grid = (uint32_t)(plan.blocks * a.H * plan.splits);
-    const hipError_t e = a.d == 64 ? launch_of<64>(lay.format, p, grid, stream) : launch_of<128>(lay.format, p, grid, stream);
-    if (e != hipSuccess || plan.splits == 1) return e;
-    const uint64_t rows = (uint64_t)a.rows * a.Hq;
-    return launch_kernel(a.d == 64 ? prompt_join_kernel<64> : prompt_join_kernel<128>,
-                         dim3((uint32_t)((rows + 3) / 4)), dim3(kBlockThreads), stream, p);
+    const uint32_t waves = plan.rows / 32;
+    const uint32_t grid = (uint32_t)((plan.blocks + plan.more) * a.H);
+    const hipError_t e = a.d == 64 ? launch_of<64>(lay.format, p, waves, grid, stream) : launch_of<128>(lay.format, p, waves, grid, stream);
+    if (e != hipSuccess || !plan.more) return e;
+    const auto join = a.d == 64 ? (waves == 8 ? prompt_join_kernel<64, 256> : prompt_join_kernel<64, 128>)
+                                : (waves == 8 ? prompt_join_kernel<128, 256> : prompt_join_kernel<128, 128>);
+    return launch_kernel(join, dim3((uint32_t)(plan.blocks * a.H)), dim3(kBlockThreads), stream, p);
 }
 
 }  // namespace kvc
