@@ -145,7 +145,6 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
 // tokens; `blocks` bounds how many a kv head has, which the host does not know.
 constexpr uint32_t kPromptRows = 64;  // of the smallest block
 struct PromptPlan {
-    uint32_t rows;    // of a block
     uint32_t more;    // shares that a kv head's blocks may have beyond one each
     uint64_t blocks;
     uint64_t bytes;   // of the workspace: what the call uses,

@@ -22,11 +22,13 @@ namespace kvc {
 namespace {
 
 constexpr int kDevBadPage = 32, kDevBadLength = 64, kDevBadStart = 128;  // KVC_DEV_*
-constexpr uint32_t kTokens = 64;   // of a tile
-constexpr uint32_t kRun = 16;      // tokens that lie in one page: a wave fetches one run of each tile
+constexpr uint32_t kTokens = 32;   // of a tile
+constexpr uint32_t kRows = 128;    // of a block, 32 a wave
+constexpr int kWaves = 4;
+constexpr uint32_t kRun = 16;      // tokens that lie in one page: a wave fetches a run of each two tiles
 constexpr float kSlack = 3.0f;     // m moves when a tile's maximum passes it by this (powers of two)
 constexpr int kWeightExp = 12;     // binary16 weights: the largest stays below 2^(12 + 3 + 1)
-constexpr uint32_t kMinShare = 8;  // tiles of a share, at least
+constexpr uint32_t kMinShare = 16;  // tiles of a share, at least
 constexpr float kNegInf = -__builtin_inff();
 constexpr bool half_products(int fmt) { return fmt == kPageInt8 || fmt == kPageFp8; }
 
@@ -97,26 +99,43 @@ __device__ __forceinline__ uint32_t place_v(uint32_t token, uint32_t chunk) {
     return token * (2 * D) + ((chunk ^ (D == 128 ? (token & 3) << 2 : (token >> 1 & 1) << 2)) << 4);
 }
 
-// 16 bytes of each lane from memory (base + off, base the same in all lanes) to LDS, at lds + 16 * lane. Written out:
-// behind the builtin the compiler waits for it before the next read of LDS, of whichever buffer. Here it knows of
-// nothing; arrive() waits. (No register is written but M0, which nothing else here uses; what reads it comes a wait
-// state behind its write.)
-__device__ __forceinline__ void fetch16(const uint8_t* base, uint32_t off, uint8_t* lds) {
+// N times 16 bytes of each lane from memory to LDS: from base (the same in all lanes) + off[u] + 1024 u to lds + 1024 u
+// + 16 * lane. Written out: behind the builtin the compiler waits for it before the next read of LDS, of whichever
+// buffer. Here it knows of nothing; arrive() waits. (No register is written but M0, which nothing else here uses; what
+// reads it comes a wait state behind its write.)
+template <int N>
+__device__ __forceinline__ void fetch16(const uint8_t* base, const uint32_t (&off)[N], uint8_t* lds) {
     const uint64_t from = (uint64_t)base;
     const uint64_t at = (uint64_t)wave_uniform((uint32_t)(from >> 32)) << 32 | wave_uniform((uint32_t)from);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(wave_uniform((uint32_t)(uint64_t)(KVC_LDS uint8_t*)lds)), "v"(off), "s"(at)
-                 : "memory");
+    const uint32_t to = wave_uniform((uint32_t)(uint64_t)(KVC_LDS uint8_t*)lds);
+    static_assert(N == 2 || N == 4);
+    if constexpr (N == 4)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+                     "global_load_lds_dwordx4 %2, %1\n\t"
+                     "global_load_lds_dwordx4 %3, %1 offset:1024\n\t"
+                     "global_load_lds_dwordx4 %4, %1 offset:2048\n\t"
+                     "global_load_lds_dwordx4 %5, %1 offset:3072"
+                     :
+                     : "s"(to), "s"(at), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3])
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+                     "global_load_lds_dwordx4 %2, %1\n\t"
+                     "global_load_lds_dwordx4 %3, %1 offset:1024"
+                     :
+                     : "s"(to), "s"(at), "v"(off[0]), "v"(off[1])
+                     : "memory");
 }
 
+// LDS: tile j of keys, and of values, is in buffer j % 4. The steps of both (8 bits) come with the keys and are read
+// for as long as the values, so they have eight places.
 template <int FMT, int D>
 struct Tiles {
     static constexpr uint32_t kBytes = kTokens * D * 2;
-    alignas(16) uint8_t kv[2][2][kBytes];  // [keys, values][buffer]
-    float steps[half_products(FMT) ? 2 : 1][2][half_products(FMT) ? kTokens : 1];
-    float big[2][4];  // largest step of the values of each run (8 bits)
-    uint32_t odd[2];  // a buffer's values or their steps are not all finite: 1 + the tile they are of
+    alignas(16) uint8_t kv[2][4][kBytes];  // [keys, values][buffer]
+    float steps[half_products(FMT) ? 2 : 1][8][half_products(FMT) ? kTokens : 1];
+    float big[8][2];  // largest step of the values of each run (8 bits)
+    uint32_t odd[8];  // a tile's values or their steps are not all finite: 1 + the tile
 };
 
 // Tiles of what a block's rows see, from its first row's position to its last's: tokens below `sunk` and from `lo` to `end`.
@@ -155,7 +174,7 @@ struct Item {
     uint32_t block, share;
     uint32_t slot;  // of the block's first share
 };
-template <uint32_t ROWS, bool JOIN>
+template <bool JOIN>
 __device__ __forceinline__ Item item_of(const PromptParams& p, uint32_t at) {
     const uint32_t lane = lane_id();
     Item x{};
@@ -172,9 +191,9 @@ __device__ __forceinline__ Item item_of(const PromptParams& p, uint32_t at) {
             atomicOr(p.status, (bad ? kDevBadStart : 0) | (s.len != given ? kDevBadLength : 0));
         s.first = a;
         s.m = bad ? 0 : e - a;
-        s.blocks = (s.m * p.group + ROWS - 1) / ROWS;
+        s.blocks = (s.m * p.group + kRows - 1) / kRows;
         s.shares = 1;
-        if (p.more && s.blocks) tiles = range_of(p, s.pos_of((s.blocks - 1) * ROWS, p.group), s.len - 1).tiles;
+        if (p.more && s.blocks) tiles = range_of(p, s.pos_of((s.blocks - 1) * kRows, p.group), s.len - 1).tiles;
         return s;
     };
     uint32_t tiles, each = 0;
@@ -219,30 +238,26 @@ __device__ __forceinline__ Item item_of(const PromptParams& p, uint32_t at) {
     }
 }
 
-template <int FMT, int D, int WAVES>
-__global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p) {
+template <int FMT, int D>
+__global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p) {
     fetch_arguments<sizeof(PromptParams)>();
     constexpr bool HALF = half_products(FMT);
-    constexpr int KS = D / 16, CB = D / 32;
-    constexpr uint32_t ROWS = 32 * WAVES;
-    // waves that fetch keys; with 8 of them the others fetch the values
-    constexpr bool APART = WAVES == 8;
-    static_assert(WAVES == 4 || WAVES == 8);
+    constexpr int KS = D / 16, CB = D / 32;  // steps of a key product, blocks of channels
     __shared__ Tiles<FMT, D> sh;
     const uint32_t lane = lane_id(), wave = wave_uniform(threadIdx.x / kWave);
     const uint32_t col = lane & 31, hi = lane >> 5;
-    const uint32_t run = wave % 4;  // of a tile: tokens 16 run .. 16 run + 15
 
     const uint32_t h = blockIdx.x % p.H;
-    const Item item = item_of<ROWS, false>(p, blockIdx.x / p.H);
+    const Item item = item_of<false>(p, blockIdx.x / p.H);
     if (!item.found) return;
     const Sequence& sq = item.s;
-    const uint32_t row0 = item.block * ROWS;
-    const uint32_t nrows = sq.m * p.group - row0 < ROWS ? sq.m * p.group - row0 : ROWS;
-    const Range see = range_of(p, sq.pos_of(row0, p.group), sq.pos_of(row0 + nrows - 1, p.group));
+    const uint32_t row0 = item.block * kRows;
+    const uint32_t nrows = sq.m * p.group - row0 < kRows ? sq.m * p.group - row0 : kRows;
+    const int32_t block_lo = sq.pos_of(row0, p.group);
+    const Range see = range_of(p, block_lo, sq.pos_of(row0 + nrows - 1, p.group));
     const auto start_of = [&](uint32_t i) { return (i < see.tiles0 ? i : i - see.tiles0 + see.from) * kTokens; };
-    const uint32_t i0 = (uint32_t)((uint64_t)see.tiles * item.share / sq.shares),
-                   i1 = (uint32_t)((uint64_t)see.tiles * (item.share + 1) / sq.shares);
+    const uint32_t j0 = (uint32_t)((uint64_t)see.tiles * item.share / sq.shares),
+                   j1 = (uint32_t)((uint64_t)see.tiles * (item.share + 1) / sq.shares);
 
     // ---- this lane's row; a lane without one takes the block's last, which is not written
     const uint32_t my_row = wave * 32 + col;
@@ -250,71 +265,77 @@ __global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p)
     const uint32_t R = row0 + (has_row ? my_row : nrows - 1);
     const uint32_t tok = R / p.group, qh = h * p.group + R % p.group;
     const int32_t pos = sq.pos_of(R, p.group);
-    const bool works = wave * 32 < nrows;  // uniform
-    // positions of the wave's rows, and of the block's
+    // positions of the wave's rows
     const int32_t wave_lo = __builtin_amdgcn_readlane(pos, 0), wave_hi = __builtin_amdgcn_readlane(pos, 31);
 
-    // ---- tiles from memory: a wave fetches one run of 16 tokens, from one page. Tokens that no row sees may hold
-    // anything, NaN too, which times a weight of 0 would stay: a token that is seen takes their place, of the run
-    // if it has one, else the last of all.
-    const auto run_of = [&](uint32_t i) {
-        const uint32_t t = start_of(i) + kRun * run;
-        const bool needed = (t < see.end) & ((t < see.sunk) | (t + kRun > see.lo));
-        return needed ? t : (see.end - 1) & ~(kRun - 1);
-    };
-    const auto page_of = [&](uint32_t i) -> const uint8_t* {
-        uint32_t page = 0;
-        if (i < i1) {
-            // (through the scalar cache: a vector load's wait would be for every tile on its way too)
-            page = *(const __attribute__((address_space(4))) uint32_t*)(uint64_t)(p.table + sq.b * p.table_stride +
-                                                                                 (run_of(i) >> p.page_shift));
-            if (page >= p.num_pages) {
-                if (p.status && lane == 0) atomicOr(p.status, kDevBadPage);
-                page = 0;
-            }
-        }
-        return p.pages + (uint64_t)page * p.page_bytes;
+    // ---- tiles from memory: two at a time, of which a wave fetches one run of 16 tokens, from one page. Tokens that
+    // no row sees may hold anything, NaN too, which times a weight of 0 would stay: a token that is seen takes their
+    // place, of the run if it has one, else the last of all.
+    struct Run {
+        uint32_t tile, t;     // its tile, and first token
+        bool any, own, whole; // there is one; it is the tile's own; all of it is seen
+        const uint8_t* page;
     };
     const uint32_t P = 1u << p.page_shift;
     constexpr uint32_t CODE = page_code_bytes(FMT, D), STEP = page_step_bytes(FMT, D);
+    const int32_t* row_of_table = p.table + sq.b * p.table_stride;
+    // this wave's run of tiles j and j + 1
+    const auto run_of = [&](uint32_t j) {
+        Run r{};
+        r.tile = j + wave / 2;
+        r.any = (int32_t)r.tile >= (int32_t)j0 && r.tile < j1;
+        if (!r.any) return r;
+        const uint32_t t = start_of(r.tile) + kRun * (wave % 2);
+        r.own = (t < see.end) & ((t < see.sunk) | (t + kRun > see.lo));
+        r.t = r.own ? t : (see.end - 1) & ~(kRun - 1);
+        r.whole = r.own & (t + kRun <= see.end) & ((t + kRun <= see.sunk) | (t >= see.lo));
+        // (through the scalar cache: a vector load's wait would be for every tile on its way too)
+        uint32_t page = *(const __attribute__((address_space(4))) uint32_t*)(uint64_t)(row_of_table + (r.t >> p.page_shift));
+        if (page >= p.num_pages) {
+            if (p.status && lane == 0) atomicOr(p.status, kDevBadPage);
+            page = 0;
+        }
+        r.page = p.pages + (uint64_t)page * p.page_bytes;
+        return r;
+    };
     // registers of tiles on their way (formats that are widened)
     constexpr int NR = FMT == kPageBf16 ? 1 : (kRun * CODE + 1023) / 1024;  // 16-byte loads of a lane
     u32x4 raw[2][NR];
     uint32_t raw_step[2];
-    const auto ask = [&](int kv, uint32_t i, const uint8_t* page) {
-        if (i >= i1 || (APART && wave / 4 != (uint32_t)kv)) return;
-        const uint32_t buf = i & 1;
-        const uint32_t t = run_of(i), at = t & (P - 1);
-        const bool same = t == start_of(i) + kRun * run;
-        const bool whole = same & (t + kRun <= see.end) & ((t + kRun <= see.sunk) | (t >= see.lo));
+    const uint32_t head_line[2] = {h * P, (p.H + h) * P};
+    const auto ask = [&](int kv, const Run& x) __attribute__((always_inline)) {
+        if (!x.any) return;
+        const uint32_t t = x.t;
         // the row that stands for row r of a run that is not whole
         const uint32_t last = see.end - 1 - t, near = t < see.sunk ? see.sunk - 1 - t : see.lo - t;
         const auto other = [&](uint32_t r) {
             const uint32_t token = t + r;
-            const bool hidden = (token >= see.sunk) & (token < see.lo), none = (token >= see.end) | !same;
+            const bool hidden = (token >= see.sunk) & (token < see.lo), none = (token >= see.end) | !x.own;
             return none ? last : hidden ? near : r;
         };
-        const uint32_t line = ((kv ? p.H : 0) + h) * P + at;
-        const uint8_t* rows = page + (uint64_t)line * CODE;
-        const uint8_t* steps = page + p.steps + (uint64_t)line * STEP;
+        const uint32_t line = head_line[kv] + (t & (P - 1));
+        const uint8_t* rows = x.page + (uint64_t)line * CODE;
+        const uint8_t* steps = x.page + p.steps + (uint64_t)line * STEP;
         if constexpr (FMT == kPageBf16) {
-            constexpr uint32_t RPI = 1024 / CODE;  // rows of one load
-            uint8_t* to = sh.kv[kv][buf] + kRun * run * CODE;
-            // of row r the chunk whose place is at16: places change by exclusive or, so the same change leads back
-            const auto off = [&](uint32_t u) {
+            constexpr int N = kRun * CODE / 1024, RPI = 1024 / CODE;  // loads, and rows of one
+            uint8_t* to = sh.kv[kv][x.tile & 3] + kRun * (wave % 2) * CODE;
+            uint32_t off[N];
+#pragma unroll
+            for (uint32_t u = 0; u < (uint32_t)N; ++u) {
+                // of row r the chunk whose place is at16: places change by exclusive or, so the same change leads back
                 const uint32_t r = u * RPI + lane / (CODE / 16), at16 = lane % (CODE / 16);
-                return kv ? place_v<D>(r, at16) : place_k<D>(r, at16);
-            };
-            if (whole) {
-#pragma unroll
-                for (uint32_t u = 0; u < kRun / RPI; ++u) fetch16(rows, off(u), to + u * 1024);
-            } else {
-#pragma unroll
-                for (uint32_t u = 0; u < kRun / RPI; ++u)
-                    fetch16(rows, off(u) % CODE + other(off(u) / CODE) * CODE, to + u * 1024);
+                off[u] = kv ? place_v<D>(r, at16) : place_k<D>(r, at16);
             }
+            if (!x.whole) {
+#pragma unroll
+                for (int u = 0; u < N; ++u) off[u] = off[u] % CODE + other(off[u] / CODE) * CODE;
+            }
+            // (offsets are unsigned: the base is as far below as the instructions add at most)
+#pragma unroll
+            for (int u = 0; u < N; ++u) off[u] += (N - 1 - u) * 1024;
+            fetch16(rows - (N - 1) * 1024, off, to);
         } else if constexpr (FMT == kPageFp4) {
-            const uint32_t r = whole ? lane / 4 : other(lane / 4);
+            const uint32_t r = x.whole ? lane / 4 : other(lane / 4);
             if constexpr (D == 128) {
                 raw[kv][0] = *reinterpret_cast<const u32x4*>(rows + r * CODE + lane % 4 * 16);
             } else {
@@ -326,24 +347,28 @@ __global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p)
 #pragma unroll
             for (int u = 0; u < NR; ++u)
                 raw[kv][u] = *reinterpret_cast<const u32x4*>(
-                    rows + (whole ? u * 1024 + lane * 16 : other((u * 1024 + lane * 16) / CODE) * CODE + lane * 16 % CODE));
-            raw_step[kv] = *reinterpret_cast<const uint32_t*>(steps + (whole ? lane % kRun : other(lane % kRun)) * STEP);
+                    rows + (x.whole ? u * 1024 + lane * 16 : other((u * 1024 + lane * 16) / CODE) * CODE + lane * 16 % CODE));
+            if (kv == 0) {
+                const uint32_t at = (x.whole ? lane % kRun : other(lane % kRun)) * STEP;
+                raw_step[0] = *reinterpret_cast<const uint32_t*>(steps + at);
+                raw_step[1] = *reinterpret_cast<const uint32_t*>(steps + (uint64_t)(head_line[1] - head_line[0]) * STEP + at);
+            }
         }
     };
     // whether some row of the block does not see some token of the tile
-    const auto mixed = [&](uint32_t i) {
-        const uint32_t t0 = start_of(i);
-        return t0 + kTokens > (uint32_t)(sq.pos_of(row0, p.group) + 1) || sq.pos_of(row0, p.group) < 0 ||
+    const auto mixed = [&](uint32_t j) {
+        const uint32_t t0 = start_of(j);
+        return (int32_t)(t0 + kTokens - 1) > block_lo ||
                (p.window && t0 + kTokens > see.sunk && (int32_t)t0 <= (int32_t)see.end - 1 - (int32_t)p.window);
     };
     // ... widened into its buffer
-    const auto put = [&](int kv, uint32_t i) {
-        if (i >= i1 || (APART && wave / 4 != (uint32_t)kv)) return;
-        const uint32_t buf = i & 1;
+    const auto put = [&](int kv, const Run& x) __attribute__((always_inline)) {
+        if (!x.any) return;
+        const uint32_t buf = x.tile & 3, first = kRun * (wave % 2);
         uint8_t* to = sh.kv[kv][buf];
         if constexpr (FMT == kPageFp4) {
-            const uint32_t r = kRun * run + lane / 4, s = raw_step[kv] << 23;
-            if (kv && raw_step[kv] == 255) sh.odd[buf] = i + 1;
+            const uint32_t r = first + lane / 4, s = raw_step[kv] << 23;
+            if (kv && raw_step[kv] == 255) sh.odd[x.tile & 7] = x.tile + 1;
 #pragma unroll
             for (int u = 0; u < D / 32; ++u) {
                 const uint32_t y = raw[kv][0][u], chunk = lane % 4 * (D / 32) + u;
@@ -353,7 +378,7 @@ __global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p)
         } else if constexpr (HALF) {
 #pragma unroll
             for (int u = 0; u < NR; ++u) {
-                const uint32_t r = kRun * run + (u * 1024 + lane * 16) / D, chunk = lane * 16 % D / 8;
+                const uint32_t r = first + (u * 1024 + lane * 16) / D, chunk = lane * 16 % D / 8;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     uint32_t a = raw[kv][u][2 * j], c = raw[kv][u][2 * j + 1];
@@ -368,22 +393,26 @@ __global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p)
                     *reinterpret_cast<u32x4*>(to + (kv ? place_v<D>(r, chunk + j) : place_k<D>(r, chunk + j))) = y;
                 }
             }
-            if (lane < kRun) sh.steps[kv][buf][kRun * run + lane] = __uint_as_float(raw_step[kv]);
-            if (kv) {
-                const bool nan = raw_step[kv] > 0x7F800000u;
-                if (nan) sh.odd[buf] = i + 1;
-                sh.big[buf][run] = __uint_as_float(max_lanes<16>(nan ? 0 : raw_step[kv]));
+            if (kv == 0) {
+                if (lane < kRun) {
+                    sh.steps[0][x.tile & 7][first + lane] = __uint_as_float(raw_step[0]);
+                    sh.steps[1][x.tile & 7][first + lane] = __uint_as_float(raw_step[1]);
+                }
+                const bool nan = raw_step[1] > 0x7F800000u;
+                if (nan) sh.odd[x.tile & 7] = x.tile + 1;
+                const float big = __uint_as_float(max_lanes<16>(nan ? 0 : raw_step[1]));
+                if (lane == 0) sh.big[x.tile & 7][wave % 2] = big;
             }
-        } else if (kv && mixed(i)) {
+        } else if (kv && mixed(x.tile)) {
             // (its loads have arrived) values that are not finite are looked for where some row does not see them
             uint32_t bad = 0;
 #pragma unroll
             for (uint32_t u = 0; u < kRun * CODE / 1024; ++u) {
-                const u32x4 y = *reinterpret_cast<const u32x4*>(to + kRun * run * CODE + u * 1024 + lane * 16);
+                const u32x4 y = *reinterpret_cast<const u32x4*>(to + first * CODE + u * 1024 + lane * 16);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) bad |= ((y[j] & 0x7F80u) == 0x7F80u) | ((y[j] & 0x7F800000u) == 0x7F800000u);
             }
-            if (bad) sh.odd[buf] = i + 1;
+            if (bad) sh.odd[x.tile & 7] = x.tile + 1;
         }
     };
     const auto arrive = [&]() {
@@ -391,10 +420,14 @@ __global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p)
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     };
 
-    // the first tile's keys are on their way before the queries are waited for
-    const uint8_t* page = page_of(i0);
-    if (i0 < i1) ask(0, i0, page);
-    if (threadIdx.x < 2) sh.odd[threadIdx.x] = 0;
+    // the first keys and values are on their way before the queries are waited for: tile j0 in the place of two, its second
+    const Run first = run_of(j0 - 1);
+    ask(0, first);
+    ask(1, first);
+    if (threadIdx.x < 8) sh.odd[threadIdx.x] = 0;
+    // the first turn adds the values of a tile before the first, with weights of 0
+    for (uint32_t at = threadIdx.x * 16; at < Tiles<FMT, D>::kBytes; at += kWaves * kWave * 16)
+        *reinterpret_cast<u32x4*>(sh.kv[1][(j0 - 1) & 3] + at) = u32x4{0, 0, 0, 0};
 
     // ---- queries
     u32x4 qf[KS];
@@ -429,7 +462,7 @@ __global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p)
     }
 
     // ---- running state
-    f32x16 o[CB], s[2];
+    f32x16 o[CB], s0, s1;
 #pragma unroll
     for (int n = 0; n < CB; ++n)
 #pragma unroll
@@ -437,6 +470,10 @@ __global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p)
     float m = kNegInf, mu = 0.0f, l = 0.0f, top = kNegInf;
     int E = -100;  // exponent taken out of the weights (HALF), which no step so far has reached
     float wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp + 100);
+    typedef u32x4 Weights[2];  // of a tile: 16 tokens each
+    Weights w0, w1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) w0[k] = w1[k] = 0;
 
     // whether the row sees token t0 + 4 hi + c
     struct Sight {
@@ -455,87 +492,77 @@ __global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p)
         return (int32_t)(t0 + kTokens - 1) <= wave_lo &&
                (!p.window || t0 + kTokens <= p.sinks || (int32_t)t0 > wave_hi - (int32_t)p.window);
     };
-    const auto zero = [](f32x16 (&x)[2]) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[u][i] = 0.0f;
+    // keys of a product step: 32 tokens, 16 channels
+    const auto keys = [&](uint32_t buf, int k) {
+        return *reinterpret_cast<const u32x4*>(sh.kv[0][buf] + place_k<D>(col, 2 * k + hi));
     };
-    // a product step's keys: 32 tokens each, 16 channels
-    const auto keys = [&](const uint8_t* kt, int k, u32x4 (&a)[2]) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) a[u] = *reinterpret_cast<const u32x4*>(kt + place_k<D>(32 * u + col, 2 * k + hi));
-    };
-    // its steps and its mask, and the largest logit
-    const auto finish = [&](uint32_t i, f32x16 (&x)[2]) {
-        if constexpr (HALF) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x4 ks = *reinterpret_cast<const f32x4*>(&sh.steps[0][i & 1][32 * u + 8 * j + 4 * hi]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) x[u][4 * j + c] *= ks[c];
-                }
-        }
-        const uint32_t t0 = start_of(i);
-        if (!all_seen(t0)) {
-            const Sight sees = sight_of(t0);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int c = 0; c < 16; ++c) x[u][c] = sees(32 * u + 8 * (c / 4) + c % 4) ? x[u][c] : kNegInf;
-        }
-        float y = x[0][0];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int c = 0; c < 16; ++c) y = fmaxf(y, x[u][c]);
-        top = y * f;
-    };
-    // four tokens of one channel a read: token 4 hi + (lane % 16) / 4 of each 8, channels of 64 bytes
+    // values of a product: 32 channels (block n), 16 tokens. A read gives four tokens of one channel to a lane: token
+    // 4 hi + (lane % 16) / 4 of each 8, channels of 64 bytes
     const uint32_t i16 = lane & 15;
-    const auto values = [&](const uint8_t* vt, int k, int n) {
+    const auto values = [&](uint32_t buf, int k, int n) {
         const uint32_t chunk = 4 * n + (lane >> 4 & 1) * 2 + (i16 & 3) / 2;
         const uint32_t t = 16 * k + 4 * hi + i16 / 4;
         const auto part = [&](uint32_t token) {
             return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                 (KVC_LDS s16x4*)(vt + place_v<D>(token, chunk) + (i16 & 1) * 8)));
+                                                 (KVC_LDS s16x4*)(sh.kv[1][buf] + place_v<D>(token, chunk) + (i16 & 1) * 8)));
         };
         const u32x2 a = part(t), c = part(t + 8);
         return u32x4{a.x, a.y, c.x, c.y};
     };
-    // Values of a buffer (8 bits: their steps) that are not finite, in a tile that some row sees only part of: rows that
-    // see one become NaN in its channel here, and it becomes 0. (Every wave comes by.)
-    const auto take_out = [&](uint32_t t0, uint32_t buf) __attribute__((always_inline)) {
+    // a tile's logits from its products: their keys' steps, the mask (behind the last tile, of all of them, whatever the
+    // buffer holds), and the largest of them
+    const auto logits = [&](uint32_t j, f32x16& x) __attribute__((always_inline)) {
+        if constexpr (HALF) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const f32x4 ks = *reinterpret_cast<const f32x4*>(&sh.steps[0][j & 7][8 * w + 4 * hi]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[4 * w + c] *= ks[c];
+            }
+        }
+        const uint32_t t0 = start_of(j);
+        if (j >= j1 || !all_seen(t0)) {
+            Sight sees = sight_of(t0);
+            if (j >= j1) sees.past = -1;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) x[c] = sees(8 * (c / 4) + c % 4) ? x[c] : kNegInf;
+        }
+        float y = x[0];
+#pragma unroll
+        for (int c = 1; c < 16; ++c) y = fmaxf(y, x[c]);
+        top = y * f;
+    };
+    // Values of a buffer (8 bits: their steps) that are not finite, in a tile that some row sees only part of: a row that
+    // sees one is NaN in its channel, which is noted here (bit 16 n + 4 j + c of the lane's channels), and it becomes 0.
+    // (Every wave comes by.)
+    uint64_t lost = 0;
+    const auto take_out = [&](uint32_t j) __attribute__((always_inline)) {
+        const uint32_t buf = j & 3;
         uint8_t* vt = sh.kv[1][buf];
-        const Sight sees = sight_of(t0);
-        const float nan = __builtin_nanf("");
+        const Sight sees = sight_of(start_of(j));
 #pragma unroll 1
         for (int t = 0; t < (int)kTokens; ++t) {
-            const bool sees_it = sees(t - 4 * (int32_t)hi);
+            if (!sees(t - 4 * (int32_t)hi)) continue;
+            if constexpr (HALF) {
+                if (__builtin_isnan(sh.steps[HALF][j & 7][t])) lost = ~0ull;
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < 4 * CB; ++i) {
+                    const u32x2 y = *reinterpret_cast<const u32x2*>(vt + place_v<D>(t, i) + 8 * hi);
 #pragma unroll
-            for (int n = 0; n < CB; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    u32x2 y{};
-                    if (!HALF) y = *reinterpret_cast<const u32x2*>(vt + place_v<D>(t, 4 * n + j) + 8 * hi);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const bool bad = HALF ? __builtin_isnan(sh.steps[1][buf][HALF ? t : 0])
-                                              : (y[c / 2] >> (16 * (c % 2)) & 0x7F80u) == 0x7F80u;
-                        o[n][4 * j + c] = (sees_it & bad) ? nan : o[n][4 * j + c];
-                    }
+                    for (int c = 0; c < 4; ++c)
+                        if ((y[c / 2] >> (16 * (c % 2)) & 0x7F80u) == 0x7F80u) lost |= 1ull << (4 * i + c);
                 }
+            }
         }
         __syncthreads();
         if constexpr (HALF) {
             if (threadIdx.x < kTokens) {
-                float& x = sh.steps[1][buf][threadIdx.x];
+                float& x = sh.steps[1][j & 7][threadIdx.x];
                 x = __builtin_isnan(x) ? 0.0f : x;
             }
         } else {
-            for (uint32_t at = threadIdx.x * 16; at < Tiles<FMT, D>::kBytes; at += WAVES * kWave * 16) {
+            for (uint32_t at = threadIdx.x * 16; at < Tiles<FMT, D>::kBytes; at += kWaves * kWave * 16) {
                 u32x4 y = *reinterpret_cast<u32x4*>(vt + at);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -547,150 +574,157 @@ __global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p)
         }
         __syncthreads();
     };
+    // adds a tile's weighted values
+    const auto add_values = [&](uint32_t buf, const Weights& w) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int n = 0; n < CB; ++n) o[n] = mfma<FMT>(values(buf, k, n), w[k], o[n]);
+    };
 
-    // ---- the tiles: while a tile's weights are formed and its values added, the next one's logits are on their way,
-    // and the keys behind those and the next values come from memory
-    if (i0 < i1) {
-        arrive();
-        put(0, i0);
-        __syncthreads();
-        ask(1, i0, page);
-        page = page_of(i0 + 1);
-        ask(0, i0 + 1, page);
-        const uint8_t* page2 = page_of(i0 + 2);
-        if (works) {
-            zero(s);
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                u32x4 a[2];
-                keys(sh.kv[0][i0 & 1], k, a);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) s[u] = mfma<FMT>(a[u], qf[k], s[u]);
-            }
-            finish(i0, s);
+    // ---- One tile's part of the pipeline: the products of the next tile's keys (into `next`), this one's weights (from
+    // `now`, into `w`) and the values of the one before (weighted by `before`) are independent, and go side by side: a
+    // product of each kind beside two weights (four with 64 channels). What a step reads from LDS was asked for one
+    // step before. (The barriers keep the compiler from asking for everything at once, which spills 100 registers.)
+    const auto turn = [&](uint32_t j, f32x16& now, f32x16& next, Weights& before, Weights& w) __attribute__((always_inline)) {
+        // (steps count for their tile's weights, values when they are added)
+        if (__builtin_expect(HALF ? sh.odd[j & 7] == j + 1 : sh.odd[(j - 1) & 7] == j && j > j0, 0)) {
+            if (mixed(HALF ? j : j - 1)) take_out(HALF ? j : j - 1);
         }
-        const auto step = [&](uint32_t i, f32x16 (&s)[2], f32x16 (&next)[2]) __attribute__((always_inline)) {
-            const uint32_t buf = i & 1;
-            arrive();
-            put(1, i);
-            put(0, i + 1);
-            __syncthreads();  // values i and keys i + 1 are there; keys i and values i - 1 are done with
-            ask(1, i + 1, page);
-            page = page2;
-            ask(0, i + 2, page);
-            page2 = page_of(i + 3);
-            if (__builtin_expect(sh.odd[buf] == i + 1, 0)) {
-                if (mixed(i)) take_out(start_of(i), buf);
+        bool move = top > m + kSlack;
+        // steps of the values are brought into binary16's range by 2^-E; those that the row sees count for E
+        float big = 0.0f;
+        if constexpr (HALF) {
+            const uint32_t t0 = start_of(j);
+            if (j >= j1) {
+            } else if (all_seen(t0)) {
+                const float2 y = *reinterpret_cast<const float2*>(sh.big[j & 7]);
+                big = fmaxf(y.x, y.y);
+            } else {
+                const Sight sees = sight_of(t0);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const f32x4 y = *reinterpret_cast<const f32x4*>(&sh.steps[1][j & 7][8 * v + 4 * hi]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) big = fmaxf(big, sees(8 * v + c) ? y[c] : 0.0f);
+                }
             }
-            if (!works) return;
-            bool move = top > m + kSlack;
-            // steps of the values are brought into binary16's range by 2^-E; those that the row sees count for E
-            float big = 0.0f;
+            move |= big >= __builtin_amdgcn_ldexpf(1.0f, E);
+        }
+        if (__ballot(move) != 0) {
+            // (the weights before are relative to m as it was)
+            add_values((j - 1) & 3, before);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) before[k] = 0;
+            const auto larger = [](float a, float c) { return fmaxf(a, c); };
+            const float nm = fmaxf(m, over_pair(top, larger));
+            float a = nm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - nm);
+            m = nm;
+            mu = nm == kNegInf ? 0.0f : nm;
+            l *= a;
             if constexpr (HALF) {
-                const uint32_t t0 = start_of(i);
-                if (all_seen(t0)) {
-                    const f32x4 y = *reinterpret_cast<const f32x4*>(sh.big[buf]);
-                    big = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
-                } else {
-                    const Sight sees = sight_of(t0);
-#pragma unroll
-                    for (int w = 0; w < 8; ++w) {
-                        const int t = 8 * w;
-                        const f32x4 y = *reinterpret_cast<const f32x4*>(&sh.steps[1][buf][t + 4 * hi]);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) big = fmaxf(big, sees(t + c) ? y[c] : 0.0f);
-                    }
-                }
-                move |= big >= __builtin_amdgcn_ldexpf(1.0f, E);
+                big = over_pair(big, larger);
+                const int ne = big >= __builtin_amdgcn_ldexpf(1.0f, E) ? __builtin_amdgcn_frexp_expf(big) : E;
+                a *= __builtin_amdgcn_ldexpf(1.0f, E - ne);
+                E = ne;
+                wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - E);
             }
-            if (__ballot(move) != 0) {
-                const auto larger = [](float a, float c) { return fmaxf(a, c); };
-                const float nm = fmaxf(m, over_pair(top, larger));
-                float a = nm == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - nm);
-                m = nm;
-                mu = nm == kNegInf ? 0.0f : nm;
-                l *= a;
-                if constexpr (HALF) {
-                    big = over_pair(big, larger);
-                    const int ne = big >= __builtin_amdgcn_ldexpf(1.0f, E) ? __builtin_amdgcn_frexp_expf(big) : E;
-                    a *= __builtin_amdgcn_ldexpf(1.0f, E - ne);
-                    E = ne;
-                    wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - E);
-                }
 #pragma unroll
-                for (int n = 0; n < CB; ++n) o[n] *= a;
+            for (int n = 0; n < CB; ++n) o[n] *= a;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) next[i] = 0.0f;
+        constexpr int PAIRS = 8 / KS;  // of weights in a step
+        const uint32_t kb = (j + 1) & 3, vb = (j - 1) & 3, sb = j & 7;
+        u32x4 a[2], y[2];
+        u32x2 vs[2][HALF ? PAIRS : 1];
+        const auto steps_of = [&](int k, u32x2 (&x)[HALF ? PAIRS : 1]) {
+            if constexpr (HALF) {
+#pragma unroll
+                for (int c = 0; c < PAIRS; ++c) {
+                    const int v = PAIRS * k + c;  // tokens of elements 2 v, 2 v + 1 of 16
+                    x[c] = *reinterpret_cast<const u32x2*>(&sh.steps[1][sb][8 * (v / 2) + 4 * hi + 2 * (v % 2)]);
+                }
             }
-            // The next tile's logits (behind the last tile: of whatever the buffer holds, not used), a step of them beside
-            // some of this one's weights; then the values. What a step reads from LDS was asked for one step before.
-            // The barriers keep the compiler from asking for everything at once, which spills 100 registers.
-            zero(next);
-            const uint8_t* kt = sh.kv[0][buf ^ 1];
-            const uint8_t* vt = sh.kv[1][buf];
-            constexpr int PAIRS = 16 / KS;  // of weights in a step
-            u32x4 pf[4], a[2][2], y[2][2];
-            f32x4 vs[2][HALF ? PAIRS / 2 : 1];
-            const auto steps_of = [&](int k, f32x4 (&x)[HALF ? PAIRS / 2 : 1]) {
-                if constexpr (HALF) {
-#pragma unroll
-                    for (int w = 0; w < PAIRS / 2; ++w)
-                        x[w] = *reinterpret_cast<const f32x4*>(&sh.steps[1][buf][8 * (PAIRS / 2 * k + w) + 4 * hi]);
-                }
-            };
-            keys(kt, 0, a[0]);
-            steps_of(0, vs[0]);
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                if (k + 1 < KS) {
-                    keys(kt, k + 1, a[(k + 1) & 1]);
-                    steps_of(k + 1, vs[(k + 1) & 1]);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) y[0][x] = values(vt, 0, x);
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) next[u] = mfma<FMT>(a[k & 1][u], qf[k], next[u]);
-#pragma unroll
-                for (int x = 0; x < PAIRS; ++x) {
-                    const int w = PAIRS * k + x;  // tokens of elements 2 w, 2 w + 1 of 32
-                    float e[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        e[c] = __builtin_amdgcn_exp2f(fmaf(s[w / 8][2 * (w % 8) + c], f, -mu));
-                        l += e[c];
-                        if constexpr (HALF) e[c] = e[c] * vs[k & 1][x / 2][2 * (x % 2) + c] * wmul;
-                    }
-                    pf[w / 4][w % 4] = HALF ? pack_half2(e[0], e[1]) : pack_bf16x2(e[0], e[1]);
-                }
-                asm volatile("" : "+v"(l));  // added up here, not at the end, where all weights would have to be kept
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            constexpr int VS = 4 * CB / 2;  // steps of two products
-#pragma unroll
-            for (int v = 0; v < VS; ++v) {
-                if (v + 1 < VS) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) y[(v + 1) & 1][x] = values(vt, (2 * v + 2 + x) / CB, (2 * v + 2 + x) % CB);
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int k = (2 * v + x) / CB, n = (2 * v + x) % CB;
-                    o[n] = mfma<FMT>(y[v & 1][x], pf[k], o[n]);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            if (i + 1 < i1) finish(i + 1, next);
         };
-        // two tiles a turn, so that the logits need no moving
-        f32x16 other[2];
-        for (uint32_t i = i0;;) {
-            step(i, s, other);
-            if (++i == i1) break;
-            step(i, other, s);
-            if (++i == i1) break;
+        a[0] = keys(kb, 0);
+        y[0] = values(vb, 0, 0);
+        steps_of(0, vs[0]);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            if (k + 1 < KS) {
+                a[(k + 1) & 1] = keys(kb, k + 1);
+                y[(k + 1) & 1] = values(vb, (k + 1) / CB, (k + 1) % CB);
+                steps_of(k + 1, vs[(k + 1) & 1]);
+            }
+            next = mfma<FMT>(a[k & 1], qf[k], next);
+            o[k % CB] = mfma<FMT>(y[k & 1], before[k / CB], o[k % CB]);
+#pragma unroll
+            for (int x = 0; x < PAIRS; ++x) {
+                const int v = PAIRS * k + x;
+                float e[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    e[c] = __builtin_amdgcn_exp2f(fmaf(now[2 * v + c], f, -mu));
+                    l += e[c];
+                    if constexpr (HALF) e[c] = e[c] * __uint_as_float(vs[k & 1][x][c]) * wmul;
+                }
+                w[v / 4][v % 4] = HALF ? pack_half2(e[0], e[1]) : pack_bf16x2(e[0], e[1]);
+            }
+            // added up and packed here, not at the end, where all weights would have to be kept
+            asm volatile("" : "+v"(l));
+#pragma unroll
+            for (int x = 0; x < PAIRS; ++x) asm volatile("" : "+v"(w[(PAIRS * k + x) / 4][(PAIRS * k + x) % 4]));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        logits(j + 1, next);
+    };
+
+    // ---- Two tiles, j and j + 1, between barriers: keys j + 1, j + 2 and values j - 1, j are there, keys j + 3, j + 4 and
+    // values j + 1, j + 2 on their way
+    if (j0 < j1) {
+        Run ahead = run_of(j0 + 1);
+        if (FMT != kPageBf16) {  // (their registers are needed again)
+            put(0, first);
+            put(1, first);
+        }
+        ask(0, ahead);
+        arrive();
+        if (FMT == kPageBf16) put(1, first);
+        put(0, ahead);
+        Run then = run_of(j0 + 3);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s0[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) s0 = mfma<FMT>(keys(j0 & 3, k), qf[k], s0);
+        logits(j0, s0);
+        for (uint32_t j = j0; j < j1; j += 2) {
+            ask(1, ahead);
+            ask(0, then);
+            const Run behind = ahead;
+            ahead = then;
+            then = run_of(j + 5);
+            turn(j, s0, s1, w1, w0);
+            turn(j + 1, s1, s0, w0, w1);
+            arrive();
+            put(1, behind);
+            put(0, ahead);
+            __syncthreads();
+        }
+        if ((j1 - j0) % 2 == 0) {  // (else the last tile's values went beside a tile that is none)
+            if (!HALF && sh.odd[(j1 - 1) & 7] == j1 && mixed(j1 - 1)) take_out(j1 - 1);
+            add_values((j1 - 1) & 3, w1);
         }
     }
 
     // ---- output
+    if (__ballot(lost != 0) != 0) {
+#pragma unroll
+        for (int n = 0; n < CB; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[n][i] = lost >> (16 * n + i) & 1 ? __builtin_nanf("") : o[n][i];
+    }
     l = over_pair(l, [](float a, float c) { return a + c; });
     if (HALF) {
         const float down = __builtin_amdgcn_ldexpf(1.0f, E - kWeightExp);
@@ -699,68 +733,61 @@ __global__ __launch_bounds__(WAVES* kWave, 2) void prompt_kernel(PromptParams p)
     }
     if (sq.shares > 1) {
         if (!has_row) return;
-        float* to = p.part + ((uint64_t)(item.slot + item.share) * p.H + h) * (ROWS * (D + 2));
+        float* to = p.part + ((uint64_t)(item.slot + item.share) * p.H + h) * (kRows * (D + 2));
 #pragma unroll
         for (int n = 0; n < CB; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<f32x4*>(to + my_row * D + 32 * n + 8 * j + 4 * hi) =
                     f32x4{o[n][4 * j], o[n][4 * j + 1], o[n][4 * j + 2], o[n][4 * j + 3]};
-        if (hi == 0) *reinterpret_cast<float2*>(to + ROWS * D + 2 * my_row) = make_float2(m, l);
+        if (hi == 0) *reinterpret_cast<float2*>(to + kRows * D + 2 * my_row) = make_float2(m, l);
         return;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     if (p.lse && has_row && hi == 0) p.lse[(uint64_t)(sq.first + tok) * p.Hq + qh] = (m + log2f(l)) * 0.69314718055994531f;
-    // rows go through LDS, 16 of a wave at a time, so that they are written in one piece
+    // rows go through LDS, so that they are written in one piece
     constexpr uint32_t LINE = 2 * D + 16, LPR = 2 * D / 16;  // bytes of a row there; lanes that write one
-    static_assert(WAVES * 16 * LINE <= sizeof(sh.kv));
-    uint8_t* mine = &sh.kv[0][0][0] + wave * 16 * LINE;
+    static_assert(kRows * LINE <= sizeof(sh.kv));
+    uint8_t* mine = &sh.kv[0][0][0] + wave * 32 * LINE;
     __syncthreads();
 #pragma unroll
-    for (uint32_t part = 0; part < 2; ++part) {
-        if (col / 16 == part) {
+    for (int n = 0; n < CB; ++n)
 #pragma unroll
-            for (int n = 0; n < CB; ++n)
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<u32x2*>(mine + col * LINE + 2 * (32 * n + 8 * j + 4 * hi)) =
+                u32x2{pack_bf16x2(o[n][4 * j] * inv, o[n][4 * j + 1] * inv), pack_bf16x2(o[n][4 * j + 2] * inv, o[n][4 * j + 3] * inv)};
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<u32x2*>(mine + col % 16 * LINE + 2 * (32 * n + 8 * j + 4 * hi)) =
-                        u32x2{pack_bf16x2(o[n][4 * j] * inv, o[n][4 * j + 1] * inv),
-                              pack_bf16x2(o[n][4 * j + 2] * inv, o[n][4 * j + 3] * inv)};
-        }
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (uint32_t u = 0; u < 16 * LPR / kWave; ++u) {
-            const uint32_t r = u * (kWave / LPR) + lane / LPR, piece = lane % LPR, at = wave * 32 + part * 16 + r;
-            const uint32_t to_tok = (row0 + at) / p.group, to_head = h * p.group + (row0 + at) % p.group;
-            if (at < nrows)
-                *reinterpret_cast<u32x4*>(p.out.data + (uint64_t)(sq.first + to_tok) * p.out.ts + (uint64_t)to_head * p.out.hs +
-                                          8 * piece) = *reinterpret_cast<const u32x4*>(mine + r * LINE + 16 * piece);
-        }
-        __builtin_amdgcn_wave_barrier();
+    for (uint32_t u = 0; u < 32 * LPR / kWave; ++u) {
+        const uint32_t r = u * (kWave / LPR) + lane / LPR, piece = lane % LPR, at = wave * 32 + r;
+        const uint32_t to_tok = (row0 + at) / p.group, to_head = h * p.group + (row0 + at) % p.group;
+        if (at < nrows)
+            *reinterpret_cast<u32x4*>(p.out.data + (uint64_t)(sq.first + to_tok) * p.out.ts + (uint64_t)to_head * p.out.hs + 8 * piece) =
+                *reinterpret_cast<const u32x4*>(mine + r * LINE + 16 * piece);
     }
 }
 
 // Joins the shares of a block's rows: a workgroup a block, four channels a lane.
-template <int D, uint32_t ROWS>
+template <int D>
 __global__ __launch_bounds__(kBlockThreads) void prompt_join_kernel(PromptParams p) {
     fetch_arguments<sizeof(PromptParams)>();
     constexpr uint32_t LPR = D / 4, RPB = kBlockThreads / LPR;
     const uint32_t h = blockIdx.x % p.H;
-    const Item item = item_of<ROWS, true>(p, blockIdx.x / p.H);
+    const Item item = item_of<true>(p, blockIdx.x / p.H);
     if (!item.found || item.s.shares == 1) return;
-    const uint32_t row0 = item.block * ROWS, all = item.s.m * p.group;
-    const uint32_t nrows = all - row0 < ROWS ? all - row0 : ROWS, shares = item.s.shares;
-    const uint64_t each = (uint64_t)p.H * (ROWS * (D + 2));
-    const float* from = p.part + ((uint64_t)item.slot * p.H + h) * (ROWS * (D + 2));
+    const uint32_t row0 = item.block * kRows, all = item.s.m * p.group;
+    const uint32_t nrows = all - row0 < kRows ? all - row0 : kRows, shares = item.s.shares;
+    const uint64_t each = (uint64_t)p.H * (kRows * (D + 2));
+    const float* from = p.part + ((uint64_t)item.slot * p.H + h) * (kRows * (D + 2));
     const uint32_t c = threadIdx.x % LPR * 4;
     for (uint32_t r = threadIdx.x / LPR; r < nrows; r += RPB) {
         float M = kNegInf;
-        for (uint32_t s = 0; s < shares; ++s) M = fmaxf(M, from[s * each + ROWS * D + 2 * r]);
+        for (uint32_t s = 0; s < shares; ++s) M = fmaxf(M, from[s * each + kRows * D + 2 * r]);
         const float Mu = M == kNegInf ? 0.0f : M;
         float total = 0.0f;
         f32x4 y = 0.0f;
         for (uint32_t s = 0; s < shares; ++s) {
-            const float2 ml = *reinterpret_cast<const float2*>(from + s * each + ROWS * D + 2 * r);
+            const float2 ml = *reinterpret_cast<const float2*>(from + s * each + kRows * D + 2 * r);
             const float a = __builtin_amdgcn_exp2f(ml.x - Mu);
             total = fmaf(ml.y, a, total);
             y += *reinterpret_cast<const f32x4*>(from + s * each + r * D + c) * a;
@@ -773,19 +800,13 @@ __global__ __launch_bounds__(kBlockThreads) void prompt_join_kernel(PromptParams
     }
 }
 
-template <int FMT, int D>
-hipError_t launch(const PromptParams& p, uint32_t waves, uint32_t grid, hipStream_t stream) {
-    return launch_kernel(waves == 8 ? prompt_kernel<FMT, D, 8> : prompt_kernel<FMT, D, 4>, dim3(grid), dim3(waves * kWave),
-                         stream, p);
-}
 template <int D>
-hipError_t launch_of(uint32_t format, const PromptParams& p, uint32_t waves, uint32_t grid, hipStream_t stream) {
-    switch (format) {
-        case kPageBf16: return launch<kPageBf16, D>(p, waves, grid, stream);
-        case kPageInt8: return launch<kPageInt8, D>(p, waves, grid, stream);
-        case kPageFp8: return launch<kPageFp8, D>(p, waves, grid, stream);
-        default: return launch<kPageFp4, D>(p, waves, grid, stream);
-    }
+hipError_t launch_of(uint32_t format, const PromptParams& p, uint32_t grid, hipStream_t stream) {
+    const auto f = format == kPageBf16   ? prompt_kernel<kPageBf16, D>
+                   : format == kPageInt8 ? prompt_kernel<kPageInt8, D>
+                   : format == kPageFp8  ? prompt_kernel<kPageFp8, D>
+                                         : prompt_kernel<kPageFp4, D>;
+    return launch_kernel(f, dim3(grid), dim3(kWaves * kWave), stream, p);
 }
 
 // Workgroups of 4 waves that the GPU holds at once.
@@ -797,15 +818,14 @@ PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t 
                        uint32_t window, uint32_t sinks) {
     const uint64_t group = Hq / H;
     PromptPlan a{};
-    a.rows = 128;
-    a.blocks = n_tokens * group / a.rows + n_seqs;
+    a.blocks = n_tokens * group / kRows + n_seqs;
     a.bytes = a.room = 256;
     // with a window, a block's rows see the tokens of one row and as many more as the block has tokens
-    const uint64_t seen = window ? seen_tokens(max_tokens, (uint64_t)window + a.rows / group, sinks) : max_tokens;
+    const uint64_t seen = window ? seen_tokens(max_tokens, (uint64_t)window + kRows / group, sinks) : max_tokens;
     const bool can = seen > kMinShare * kTokens;
     if (can && H * a.blocks < 4 * kPlaces) a.more = (uint32_t)((kPlaces + H - 1) / H);
     // a block that is cut up has two shares at least: no more than 2 more of them
-    const uint64_t each = (uint64_t)a.rows * (d + 2) * 4;
+    const uint64_t each = (uint64_t)kRows * (d + 2) * 4;
     if (a.more) a.bytes = align_up(2 * a.more * H * each, 256);
     if (can) a.room = align_up(2 * ((kPlaces + H - 1) / H) * H * each, 256);
     return a;
@@ -838,12 +858,10 @@ hipError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& plan, hip
     p.more = plan.more;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.part = static_cast<float*>(a.ws);
-    const uint32_t waves = plan.rows / 32;
     const uint32_t grid = (uint32_t)((plan.blocks + plan.more) * a.H);
-    const hipError_t e = a.d == 64 ? launch_of<64>(lay.format, p, waves, grid, stream) : launch_of<128>(lay.format, p, waves, grid, stream);
+    const hipError_t e = a.d == 64 ? launch_of<64>(lay.format, p, grid, stream) : launch_of<128>(lay.format, p, grid, stream);
     if (e != hipSuccess || !plan.more) return e;
-    const auto join = a.d == 64 ? (waves == 8 ? prompt_join_kernel<64, 256> : prompt_join_kernel<64, 128>)
-                                : (waves == 8 ? prompt_join_kernel<128, 256> : prompt_join_kernel<128, 128>);
+    const auto join = a.d == 64 ? prompt_join_kernel<64> : prompt_join_kernel<128>;
     return launch_kernel(join, dim3((uint32_t)(plan.blocks * a.H)), dim3(kBlockThreads), stream, p);
 }
 
