@@ -127,7 +127,7 @@ __device__ __forceinline__ void fetch16(const uint8_t* base, const uint32_t (&of
                      : "memory");
 }
 
-// LDS: tile j of keys, and of values, is in buffer j % 4. The steps of both (8 bits) come with the keys and are read
+// LDS: tile j of keys, and of values, is in buffer (j - the share's first) % 4. The steps of both (8 bits) come with the keys and are read
 // for as long as the values, so they have eight places.
 template <int FMT, int D>
 struct Tiles {
@@ -274,51 +274,64 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
     struct Run {
         uint32_t tile, t;     // its tile, and first token
         bool any, own, whole; // there is one; it is the tile's own; all of it is seen
-        const uint8_t* page;
+        const uint8_t *rows, *steps;  // its keys
     };
     const uint32_t P = 1u << p.page_shift;
     constexpr uint32_t CODE = page_code_bytes(FMT, D), STEP = page_step_bytes(FMT, D);
+    const uint64_t to_values = (uint64_t)p.H * P * CODE, to_value_steps = (uint64_t)p.H * P * STEP;
     const int32_t* row_of_table = p.table + sq.b * p.table_stride;
+    // tiles from `plain0` to `plain1` - 1 lie behind the sinks' and are seen whole
+    const uint32_t plain0 = see.tiles0 > j0 ? see.tiles0 : j0;
+    const uint32_t seen0 = (see.lo + kTokens - 1) / kTokens;  // of the sequence's tiles
+    const uint32_t skip = see.from - see.tiles0;
+    const uint32_t from_lo = seen0 > skip ? seen0 - skip : 0, to_end = see.end / kTokens > skip ? see.end / kTokens - skip : 0;
+    const uint32_t first_plain = plain0 > from_lo ? plain0 : from_lo, end_plain = to_end < j1 ? to_end : j1;
     // this wave's run of tiles j and j + 1
     const auto run_of = [&](uint32_t j) {
         Run r{};
         r.tile = j + wave / 2;
-        r.any = (int32_t)r.tile >= (int32_t)j0 && r.tile < j1;
-        if (!r.any) return r;
-        const uint32_t t = start_of(r.tile) + kRun * (wave % 2);
-        r.own = (t < see.end) & ((t < see.sunk) | (t + kRun > see.lo));
-        r.t = r.own ? t : (see.end - 1) & ~(kRun - 1);
-        r.whole = r.own & (t + kRun <= see.end) & ((t + kRun <= see.sunk) | (t >= see.lo));
+        if (r.tile >= first_plain && r.tile < end_plain) {
+            r.any = r.own = r.whole = true;
+            r.t = (r.tile + skip) * kTokens + kRun * (wave % 2);
+        } else {
+            r.any = (int32_t)r.tile >= (int32_t)j0 && r.tile < j1;
+            if (!r.any) return r;
+            const uint32_t t = start_of(r.tile) + kRun * (wave % 2);
+            r.own = (t < see.end) & ((t < see.sunk) | (t + kRun > see.lo));
+            r.t = r.own ? t : (see.end - 1) & ~(kRun - 1);
+            r.whole = r.own & (t + kRun <= see.end) & ((t + kRun <= see.sunk) | (t >= see.lo));
+        }
         // (through the scalar cache: a vector load's wait would be for every tile on its way too)
         uint32_t page = *(const __attribute__((address_space(4))) uint32_t*)(uint64_t)(row_of_table + (r.t >> p.page_shift));
-        if (page >= p.num_pages) {
+        if (__builtin_expect(page >= p.num_pages, 0)) {
             if (p.status && lane == 0) atomicOr(p.status, kDevBadPage);
             page = 0;
         }
-        r.page = p.pages + (uint64_t)page * p.page_bytes;
+        const uint32_t line = h * P + (r.t & (P - 1));
+        const uint8_t* at = p.pages + (uint64_t)page * p.page_bytes;
+        r.rows = at + (uint64_t)line * CODE;
+        r.steps = at + p.steps + (uint64_t)line * STEP;
         return r;
     };
     // registers of tiles on their way (formats that are widened)
     constexpr int NR = FMT == kPageBf16 ? 1 : (kRun * CODE + 1023) / 1024;  // 16-byte loads of a lane
     u32x4 raw[2][NR];
     uint32_t raw_step[2];
-    const uint32_t head_line[2] = {h * P, (p.H + h) * P};
-    const auto ask = [&](int kv, const Run& x) __attribute__((always_inline)) {
+    // (buf: the tile's buffer is known when this is compiled, see below)
+    const auto ask = [&](int kv, const Run& x, uint32_t buf) __attribute__((always_inline)) {
         if (!x.any) return;
-        const uint32_t t = x.t;
         // the row that stands for row r of a run that is not whole
-        const uint32_t last = see.end - 1 - t, near = t < see.sunk ? see.sunk - 1 - t : see.lo - t;
         const auto other = [&](uint32_t r) {
-            const uint32_t token = t + r;
+            const uint32_t t = x.t, token = t + r;
+            const uint32_t last = see.end - 1 - t, near = t < see.sunk ? see.sunk - 1 - t : see.lo - t;
             const bool hidden = (token >= see.sunk) & (token < see.lo), none = (token >= see.end) | !x.own;
             return none ? last : hidden ? near : r;
         };
-        const uint32_t line = head_line[kv] + (t & (P - 1));
-        const uint8_t* rows = x.page + (uint64_t)line * CODE;
-        const uint8_t* steps = x.page + p.steps + (uint64_t)line * STEP;
+        const uint8_t* rows = kv ? x.rows + to_values : x.rows;
+        const uint8_t* steps = kv ? x.steps + to_value_steps : x.steps;
         if constexpr (FMT == kPageBf16) {
             constexpr int N = kRun * CODE / 1024, RPI = 1024 / CODE;  // loads, and rows of one
-            uint8_t* to = sh.kv[kv][x.tile & 3] + kRun * (wave % 2) * CODE;
+            uint8_t* to = sh.kv[kv][buf] + kRun * (wave % 2) * CODE;
             uint32_t off[N];
 #pragma unroll
             for (uint32_t u = 0; u < (uint32_t)N; ++u) {
@@ -351,20 +364,31 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
             if (kv == 0) {
                 const uint32_t at = (x.whole ? lane % kRun : other(lane % kRun)) * STEP;
                 raw_step[0] = *reinterpret_cast<const uint32_t*>(steps + at);
-                raw_step[1] = *reinterpret_cast<const uint32_t*>(steps + (uint64_t)(head_line[1] - head_line[0]) * STEP + at);
+                raw_step[1] = *reinterpret_cast<const uint32_t*>(steps + to_value_steps + at);
             }
         }
     };
-    // whether some row of the block does not see some token of the tile
-    const auto mixed = [&](uint32_t j) {
-        const uint32_t t0 = start_of(j);
-        return (int32_t)(t0 + kTokens - 1) > block_lo ||
-               (p.window && t0 + kTokens > see.sunk && (int32_t)t0 <= (int32_t)see.end - 1 - (int32_t)p.window);
+    // Tiles that all rows from position `lo` to `hi` see the whole of: from `first` on, `count` of them. (Without those
+    // among the sinks, where there is a window: they take the general way.)
+    struct Whole {
+        uint32_t first, count;
+        __device__ __forceinline__ bool operator()(uint32_t j) const { return j - first < count; }
     };
+    const auto whole_for = [&](int32_t lo, int32_t hi) {
+        Whole w;
+        const int32_t left = p.window ? hi - (int32_t)p.window + 1 : 0;  // the first token that row hi sees
+        const uint32_t a = left > 0 ? (left + kTokens - 1) / kTokens : 0, b = lo < 0 ? 0 : (lo + 1) / kTokens;
+        const uint32_t f = a > skip ? a - skip : 0, e = b > skip ? b - skip : 0;
+        w.first = f > see.tiles0 ? f : see.tiles0;
+        const uint32_t last = e < j1 ? e : j1;
+        w.count = last > w.first ? last - w.first : 0;
+        return w;
+    };
+    const Whole block_sees = whole_for(block_lo, (int32_t)see.end - 1), wave_sees = whole_for(wave_lo, wave_hi);
     // ... widened into its buffer
-    const auto put = [&](int kv, const Run& x) __attribute__((always_inline)) {
+    const auto put = [&](int kv, const Run& x, uint32_t buf) __attribute__((always_inline)) {
         if (!x.any) return;
-        const uint32_t buf = x.tile & 3, first = kRun * (wave % 2);
+        const uint32_t first = kRun * (wave % 2);
         uint8_t* to = sh.kv[kv][buf];
         if constexpr (FMT == kPageFp4) {
             const uint32_t r = first + lane / 4, s = raw_step[kv] << 23;
@@ -403,7 +427,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
                 const float big = __uint_as_float(max_lanes<16>(nan ? 0 : raw_step[1]));
                 if (lane == 0) sh.big[x.tile & 7][wave % 2] = big;
             }
-        } else if (kv && mixed(x.tile)) {
+        } else if (kv && !block_sees(x.tile)) {
             // (its loads have arrived) values that are not finite are looked for where some row does not see them
             uint32_t bad = 0;
 #pragma unroll
@@ -422,12 +446,13 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
 
     // the first keys and values are on their way before the queries are waited for: tile j0 in the place of two, its second
     const Run first = run_of(j0 - 1);
-    ask(0, first);
-    ask(1, first);
+    const uint32_t second = wave / 2;  // the wave's run is of the second of two tiles
+    ask(0, first, 0);
+    ask(1, first, 0);
     if (threadIdx.x < 8) sh.odd[threadIdx.x] = 0;
     // the first turn adds the values of a tile before the first, with weights of 0
     for (uint32_t at = threadIdx.x * 16; at < Tiles<FMT, D>::kBytes; at += kWaves * kWave * 16)
-        *reinterpret_cast<u32x4*>(sh.kv[1][(j0 - 1) & 3] + at) = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(sh.kv[1][3] + at) = u32x4{0, 0, 0, 0};
 
     // ---- queries
     u32x4 qf[KS];
@@ -487,11 +512,6 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
         x.sunk_to = p.window ? (int32_t)p.sinks - (int32_t)t0 - 4 * (int32_t)hi : 0;
         return x;
     };
-    // whether every row of the wave sees the whole tile
-    const auto all_seen = [&](uint32_t t0) {
-        return (int32_t)(t0 + kTokens - 1) <= wave_lo &&
-               (!p.window || t0 + kTokens <= p.sinks || (int32_t)t0 > wave_hi - (int32_t)p.window);
-    };
     // keys of a product step: 32 tokens, 16 channels
     const auto keys = [&](uint32_t buf, int k) {
         return *reinterpret_cast<const u32x4*>(sh.kv[0][buf] + place_k<D>(col, 2 * k + hi));
@@ -509,8 +529,8 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
         const u32x2 a = part(t), c = part(t + 8);
         return u32x4{a.x, a.y, c.x, c.y};
     };
-    // a tile's logits from its products: their keys' steps, the mask (behind the last tile, of all of them, whatever the
-    // buffer holds), and the largest of them
+    // a tile's logits from its products: their keys' steps, and the mask (behind the last tile, of all of them, whatever the
+    // buffer holds)
     const auto logits = [&](uint32_t j, f32x16& x) __attribute__((always_inline)) {
         if constexpr (HALF) {
 #pragma unroll
@@ -520,24 +540,19 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
                 for (int c = 0; c < 4; ++c) x[4 * w + c] *= ks[c];
             }
         }
-        const uint32_t t0 = start_of(j);
-        if (j >= j1 || !all_seen(t0)) {
-            Sight sees = sight_of(t0);
+        if (!wave_sees(j)) {
+            Sight sees = sight_of(start_of(j));
             if (j >= j1) sees.past = -1;
 #pragma unroll
             for (int c = 0; c < 16; ++c) x[c] = sees(8 * (c / 4) + c % 4) ? x[c] : kNegInf;
         }
-        float y = x[0];
-#pragma unroll
-        for (int c = 1; c < 16; ++c) y = fmaxf(y, x[c]);
-        top = y * f;
     };
     // Values of a buffer (8 bits: their steps) that are not finite, in a tile that some row sees only part of: a row that
     // sees one is NaN in its channel, which is noted here (bit 16 n + 4 j + c of the lane's channels), and it becomes 0.
     // (Every wave comes by.)
     uint64_t lost = 0;
     const auto take_out = [&](uint32_t j) __attribute__((always_inline)) {
-        const uint32_t buf = j & 3;
+        const uint32_t buf = (j - j0) & 3;
         uint8_t* vt = sh.kv[1][buf];
         const Sight sees = sight_of(start_of(j));
 #pragma unroll 1
@@ -583,25 +598,43 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
     };
 
     // ---- One tile's part of the pipeline: the products of the next tile's keys (into `next`), this one's weights (from
-    // `now`, into `w`) and the values of the one before (weighted by `before`) are independent, and go side by side: a
-    // product of each kind beside two weights (four with 64 channels). What a step reads from LDS was asked for one
-    // step before. (The barriers keep the compiler from asking for everything at once, which spills 100 registers.)
-    const auto turn = [&](uint32_t j, f32x16& now, f32x16& next, Weights& before, Weights& w) __attribute__((always_inline)) {
+    // `now`, into `w`) and the values of the one before (weighted by `before`) are independent, and go side by side: two
+    // products beside two weights (four with 64 channels), first those of keys, so that the next tile's largest logit is
+    // found beside those of values. What two products read from LDS was asked for two products before (`op`: that of the
+    // first two). (The barriers keep the compiler from asking for everything at once, which spills 100 registers.)
+    const auto first_keys = [&](uint32_t buf, u32x4 (&op)[4]) __attribute__((always_inline)) {
+        op[0] = keys(buf, 0);
+        op[1] = keys(buf, 1);
+    };
+    const auto turn = [&](uint32_t j, auto keys_in, auto values_in, f32x16& now, f32x16& next, Weights& before, Weights& w,
+                          u32x4 (&op)[4]) __attribute__((always_inline)) {
+        constexpr uint32_t kb = decltype(keys_in)::value, vb = decltype(values_in)::value;
+        constexpr int PAIRS = 8 / KS;  // of weights beside two products
+        const uint32_t sb = j & 7;
+        u32x2 vs[2][HALF ? PAIRS : 1];
+        const auto steps_of = [&](int k, u32x2 (&x)[HALF ? PAIRS : 1]) {
+            if constexpr (HALF) {
+#pragma unroll
+                for (int c = 0; c < PAIRS; ++c) {
+                    const int v = PAIRS * k + c;  // tokens of elements 2 v, 2 v + 1 of 16
+                    x[c] = *reinterpret_cast<const u32x2*>(&sh.steps[1][sb][8 * (v / 2) + 4 * hi + 2 * (v % 2)]);
+                }
+            }
+        };
         // (steps count for their tile's weights, values when they are added)
-        if (__builtin_expect(HALF ? sh.odd[j & 7] == j + 1 : sh.odd[(j - 1) & 7] == j && j > j0, 0)) {
-            if (mixed(HALF ? j : j - 1)) take_out(HALF ? j : j - 1);
+        const uint32_t odd = HALF ? j : j - 1;
+        if (__builtin_expect(!block_sees(odd), 0)) {
+            if (j >= j0 + !HALF && j < j1 + !HALF && sh.odd[odd & 7] == odd + 1) take_out(odd);
         }
         bool move = top > m + kSlack;
         // steps of the values are brought into binary16's range by 2^-E; those that the row sees count for E
         float big = 0.0f;
         if constexpr (HALF) {
-            const uint32_t t0 = start_of(j);
-            if (j >= j1) {
-            } else if (all_seen(t0)) {
+            if (wave_sees(j)) {
                 const float2 y = *reinterpret_cast<const float2*>(sh.big[j & 7]);
                 big = fmaxf(y.x, y.y);
-            } else {
-                const Sight sees = sight_of(t0);
+            } else if (j < j1) {
+                const Sight sees = sight_of(start_of(j));
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const f32x4 y = *reinterpret_cast<const f32x4*>(&sh.steps[1][j & 7][8 * v + 4 * hi]);
@@ -613,7 +646,7 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
         }
         if (__ballot(move) != 0) {
             // (the weights before are relative to m as it was)
-            add_values((j - 1) & 3, before);
+            add_values(vb, before);
 #pragma unroll
             for (int k = 0; k < 2; ++k) before[k] = 0;
             const auto larger = [](float a, float c) { return fmaxf(a, c); };
@@ -634,31 +667,27 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) next[i] = 0.0f;
-        constexpr int PAIRS = 8 / KS;  // of weights in a step
-        const uint32_t kb = (j + 1) & 3, vb = (j - 1) & 3, sb = j & 7;
-        u32x4 a[2], y[2];
-        u32x2 vs[2][HALF ? PAIRS : 1];
-        const auto steps_of = [&](int k, u32x2 (&x)[HALF ? PAIRS : 1]) {
-            if constexpr (HALF) {
-#pragma unroll
-                for (int c = 0; c < PAIRS; ++c) {
-                    const int v = PAIRS * k + c;  // tokens of elements 2 v, 2 v + 1 of 16
-                    x[c] = *reinterpret_cast<const u32x2*>(&sh.steps[1][sb][8 * (v / 2) + 4 * hi + 2 * (v % 2)]);
-                }
-            }
-        };
-        a[0] = keys(kb, 0);
-        y[0] = values(vb, 0, 0);
         steps_of(0, vs[0]);
+        float largest = kNegInf;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-            if (k + 1 < KS) {
-                a[(k + 1) & 1] = keys(kb, k + 1);
-                y[(k + 1) & 1] = values(vb, (k + 1) / CB, (k + 1) % CB);
-                steps_of(k + 1, vs[(k + 1) & 1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int q = 2 * k + 2 + x;  // of KS products of keys, then KS of values
+                if (q < KS)
+                    op[q % 4] = keys(kb, q);
+                else if (q < 2 * KS)
+                    op[q % 4] = values(vb, (q - KS) / CB, (q - KS) % CB);
             }
-            next = mfma<FMT>(a[k & 1], qf[k], next);
-            o[k % CB] = mfma<FMT>(y[k & 1], before[k / CB], o[k % CB]);
+            if (k + 1 < KS) steps_of(k + 1, vs[(k + 1) & 1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int q = 2 * k + x, v = q - KS;
+                if (q < KS)
+                    next = mfma<FMT>(op[q % 4], qf[q % KS], next);
+                else
+                    o[v % CB] = mfma<FMT>(op[q % 4], before[v / CB & 1], o[v % CB]);
+            }
 #pragma unroll
             for (int x = 0; x < PAIRS; ++x) {
                 const int v = PAIRS * k + x;
@@ -675,9 +704,16 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
             asm volatile("" : "+v"(l));
 #pragma unroll
             for (int x = 0; x < PAIRS; ++x) asm volatile("" : "+v"(w[(PAIRS * k + x) / 4][(PAIRS * k + x) % 4]));
+            constexpr int LEFT = KS / 2 - 1;  // steps behind the first with values: the next logits are there
+            if (k > KS / 2) {
+#pragma unroll
+                for (int c = 16 * (k - KS / 2 - 1) / LEFT; c < 16 * (k - KS / 2) / LEFT; ++c) largest = fmaxf(largest, next[c]);
+                asm volatile("" : "+v"(largest));
+            }
             __builtin_amdgcn_sched_barrier(0);
+            if (k == KS / 2) logits(j + 1, next);
         }
-        logits(j + 1, next);
+        top = largest * f;
     };
 
     // ---- Two tiles, j and j + 1, between barriers: keys j + 1, j + 2 and values j - 1, j are there, keys j + 3, j + 4 and
@@ -685,36 +721,53 @@ __global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p
     if (j0 < j1) {
         Run ahead = run_of(j0 + 1);
         if (FMT != kPageBf16) {  // (their registers are needed again)
-            put(0, first);
-            put(1, first);
+            put(0, first, 0);
+            put(1, first, 0);
         }
-        ask(0, ahead);
+        ask(0, ahead, 1 + second);
         arrive();
-        if (FMT == kPageBf16) put(1, first);
-        put(0, ahead);
+        if (FMT == kPageBf16) put(1, first, 0);
+        put(0, ahead, 1 + second);
         Run then = run_of(j0 + 3);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 16; ++i) s0[i] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) s0 = mfma<FMT>(keys(j0 & 3, k), qf[k], s0);
+        for (int k = 0; k < KS; ++k) s0 = mfma<FMT>(keys(0, k), qf[k], s0);
         logits(j0, s0);
-        for (uint32_t j = j0; j < j1; j += 2) {
-            ask(1, ahead);
-            ask(0, then);
+        top = kNegInf;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) top = fmaxf(top, s0[c]);
+        top *= f;
+        u32x4 op[4];
+        // four tiles a turn of the loop, so that their buffers are known when this is compiled
+        const auto two = [&](uint32_t j, auto first_buffer) __attribute__((always_inline)) {
+            constexpr uint32_t B = decltype(first_buffer)::value;
+            first_keys((B + 1) & 3, op);
+            ask(1, ahead, (B + 1 + second) & 3);
+            ask(0, then, (B + 3 + second) & 3);
             const Run behind = ahead;
             ahead = then;
             then = run_of(j + 5);
-            turn(j, s0, s1, w1, w0);
-            turn(j + 1, s1, s0, w0, w1);
+            turn(j, std::integral_constant<uint32_t, (B + 1) & 3>{}, std::integral_constant<uint32_t, (B + 3) & 3>{}, s0, s1, w1, w0, op);
+            first_keys((B + 2) & 3, op);
+            turn(j + 1, std::integral_constant<uint32_t, (B + 2) & 3>{}, std::integral_constant<uint32_t, B>{}, s1, s0, w0, w1, op);
             arrive();
-            put(1, behind);
-            put(0, ahead);
+            put(1, behind, (B + 1 + second) & 3);
+            put(0, ahead, (B + 3 + second) & 3);
             __syncthreads();
+        };
+        for (uint32_t j = j0;;) {
+            two(j, std::integral_constant<uint32_t, 0>{});
+            j += 2;
+            if (j >= j1) break;
+            two(j, std::integral_constant<uint32_t, 2>{});
+            j += 2;
+            if (j >= j1) break;
         }
         if ((j1 - j0) % 2 == 0) {  // (else the last tile's values went beside a tile that is none)
-            if (!HALF && sh.odd[(j1 - 1) & 7] == j1 && mixed(j1 - 1)) take_out(j1 - 1);
-            add_values((j1 - 1) & 3, w1);
+            if (!HALF && !block_sees(j1 - 1) && sh.odd[(j1 - 1) & 7] == j1) take_out(j1 - 1);
+            add_values((j1 - 1 - j0) & 3, w1);
         }
     }
 
