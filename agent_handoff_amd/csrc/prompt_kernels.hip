@@ -239,7 +239,7 @@ __device__ __forceinline__ Item item_of(const PromptParams& p, uint32_t at) {
 }
 
 template <int FMT, int D>
-__global__ __launch_bounds__(kWaves* kWave, 2) void prompt_kernel(PromptParams p) {
+__global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(PromptParams p) {
     fetch_arguments<sizeof(PromptParams)>();
     constexpr bool HALF = half_products(FMT);
     constexpr int KS = D / 16, CB = D / 32;  // steps of a key product, blocks of channels
