@@ -106,6 +106,11 @@ struct AttendPlan {
 };
 // tail: pages behind a pool (all parts are joined, none is written as output).
 AttendPlan page_attend_plan(uint32_t n_seqs, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens, bool tail);
+// Many new tokens, few of each sequence.
+AttendPlan many_attend_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens,
+                            uint32_t window, uint32_t sinks);
+// Workspace of any such call with up to `rows` query rows of all sequences and a kv head.
+uint64_t many_attend_room(uint32_t n_seqs, uint64_t rows, uint32_t H, uint32_t d, uint64_t max_tokens);
 AttendPlan pool_attend_plan(uint32_t H, uint32_t n_agents, uint32_t Hq, uint32_t d, uint32_t T, bool tail);
 
 // Tokens that a call over at most max_tokens counts for a sequence, at most: with a
@@ -137,6 +142,9 @@ struct AttendArgs {
     uint32_t L, T, layer;
     // pages (table != nullptr)
     TailArgs tail;
+    // many new tokens of each sequence, over pages alone (starts != nullptr)
+    const int32_t* starts;
+    uint32_t tokens;
 };
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
 
@@ -145,6 +153,7 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
 // tokens; `blocks` bounds how many a kv head has, which the host does not know.
 constexpr uint32_t kPromptRows = 64;  // of the smallest block
 struct PromptPlan {
+    bool few;         // few new tokens of each sequence: taken by launch_attend
     uint32_t more;    // shares that a kv head's blocks may have beyond one each
     uint64_t blocks;
     uint64_t bytes;   // of the workspace: what the call uses,

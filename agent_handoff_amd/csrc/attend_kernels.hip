@@ -58,7 +58,7 @@
 namespace kvc {
 namespace {
 
-constexpr int kDevBadHeader = 1, kDevBadPage = 32, kDevBadLength = 64;  // KVC_DEV_*
+constexpr int kDevBadHeader = 1, kDevBadPage = 32, kDevBadLength = 64, kDevBadStart = 128;  // KVC_DEV_*
 constexpr int kFmtBf16 = kPageBf16, kFmtInt8 = kPageInt8, kFmtFp8 = kPageFp8, kFmtFp4 = kPageFp4, kFmtPool = 3;
 // Products in binary16 (codes of 8 bits, levels) or in bf16 (which holds a 4-bit code times its power of two exactly).
 constexpr bool half_products(int fmt) { return fmt != kFmtBf16 && fmt != kFmtFp4; }
@@ -70,6 +70,9 @@ constexpr float kSlack = 3.0f;
 constexpr int kWeightExp = 12;
 constexpr int kMinExp = -100;  // steps below 2^-100 are taken with this exponent
 constexpr float kNegInf = -__builtin_inff();
+// What a kernel is compiled for: one new token of each sequence that sees all of it; or a window and sinks; or many new
+// tokens, each of which sees those up to its own (with a window or without).
+constexpr int kOneSeesAll = 0, kOneWindow = 1, kMany = 2;
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -110,8 +113,14 @@ struct Source {
         uint32_t sinks;
     };
     uint32_t layer;
-    uint32_t more;  // shares of `each` blocks, the first `more` of them one larger
-    uint64_t each;
+    union {
+        uint32_t more;    // shares of `each` blocks, the first `more` of them one larger
+        uint32_t tokens;  // many new tokens: query rows, of
+    };
+    union {
+        uint64_t each;
+        const int32_t* starts;  // sequence b: starts[b] to starts[b + 1] - 1
+    };
     // pages
     const uint8_t* pages;
     const int32_t* table;
@@ -129,6 +138,10 @@ __device__ __forceinline__ f32x4 mfma_half(const u32x4& a, const u32x4& b, const
 __device__ __forceinline__ f32x4 mfma_bf16(const u32x4& a, const u32x4& b, const f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                    0, 0, 0);
+}
+// Ones in each half that holds a bf16 that is not finite.
+__device__ __forceinline__ uint32_t infinite(uint32_t v) {
+    return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 template <int FMT>
 __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
@@ -262,11 +275,12 @@ struct Seen {
     uint32_t len, hid0, hid1;
     uint32_t cut, gap;  // token t stands for t + gap from `cut` on
 };
-template <bool WIN>
-__device__ __forceinline__ Seen seen_of(const Source& p, uint32_t len) {
+// (of many new tokens: what any of them sees)
+template <int MODE>
+__device__ __forceinline__ Seen seen_of(const Source& p, uint32_t len, uint32_t tokens = 1) {
     Seen s{len, 0, 0, 0, 0};
-    if (!WIN) return s;
-    const uint32_t lo = len > p.window ? len - p.window : 0;
+    if (MODE == kOneSeesAll || (MODE == kMany && p.window == 0)) return s;
+    const uint32_t back = p.window + tokens - 1, lo = len > back ? len - back : 0;
     s.hid0 = p.sinks < lo ? p.sinks : lo;
     s.cut = (s.hid0 + 15) & ~15u;
     s.gap = (lo & ~15u) > s.cut ? (lo & ~15u) - s.cut : 0;
@@ -276,6 +290,33 @@ __device__ __forceinline__ Seen seen_of(const Source& p, uint32_t len) {
 }
 // Blocks of a length; an empty sequence has one, without tokens.
 __device__ __forceinline__ uint32_t blocks_of(uint32_t len) { return len <= kBlock ? 1 : (len + kBlock - 1) / kBlock; }
+
+// The new tokens of sequence b (many new tokens), none where its starts are wrong.
+struct Fresh {
+    uint32_t first, count;
+    bool bad;
+};
+__device__ __forceinline__ Fresh fresh_of(const Source& p, uint32_t b) {
+    const int32_t a = p.starts[b], e = p.starts[b + 1];
+    const bool bad = a < 0 || e < a || (uint32_t)e > p.tokens;
+    return Fresh{bad ? 0u : (uint32_t)a, bad ? 0u : (uint32_t)(e - a), bad};
+}
+// Row blocks of a kv head for so many new tokens; and the place of a sequence's first in the list of units (those of
+// the sequences before it, rounded up one by one, are no more).
+template <int RT>
+__device__ __forceinline__ uint32_t row_blocks_of(uint32_t count, uint32_t group) {
+    return (count * group + 16 * RT - 1) / (16 * RT);
+}
+template <int RT>
+__device__ __forceinline__ uint64_t first_unit(uint32_t b, uint32_t first, uint32_t group, uint32_t H) {
+    return (uint64_t)(first * group / (16 * RT) + b) * H;
+}
+
+// Which tokens a query row sees, counted from where its lane's tokens of a run begin.
+struct Sight {
+    int32_t past, left, sunk_to;
+    __device__ __forceinline__ bool operator()(int32_t c) const { return (c <= past) & ((c > left) | (c < sunk_to)); }
+};
 
 // Query row r (of the unit's rows) -> sequence and query head.
 template <int FMT>
@@ -389,15 +430,27 @@ __device__ __forceinline__ uint32_t scan_threads(uint32_t v, uint32_t* sums, uin
 }
 
 // The share of workgroup w.
-template <int FMT, int D, int RT, bool WIN>
+template <int FMT, int D, int RT, int MODE>
 __device__ __forceinline__ void attend_share(const Common& p, const Source& src, uint32_t w, Shared<D, RT>& sh) {
     constexpr int KS = D / 32;   // key product steps
     constexpr int NC = D / 16;   // channels of a lane, value products
     constexpr bool HALF = half_products(FMT);
+    constexpr bool MANY = MODE == kMany, WIN = MODE != kOneSeesAll;
+    constexpr int RE = MANY ? RT : 1;  // exponents taken out of the weights: of a row, where rows see different tokens
     using R = Raw<FMT, D>;
     const uint32_t lane = lane_id(), c = lane & 15, g = lane >> 4;
     const uint32_t wave = wave_uniform(threadIdx.x / kWave);
-    const uint32_t per_seq = p.H * src.row_blocks;  // units of a sequence
+    const uint32_t per_seq = MANY ? p.H : p.H * src.row_blocks;  // units of a sequence (that share a row block)
+    // what a sequence adds to the list of blocks, over `per_seq`
+    const auto weight_of = [&](uint32_t s) {
+        const int32_t given = src.lens[s];
+        const uint32_t len = clamp_length(src, given);
+        if (!MANY) return blocks_of(seen_of<MODE>(src, len).len);
+        const Fresh x = fresh_of(src, s);
+        if (w == 0 && p.status && (x.bad || bad_length(src, given)))
+            atomicOr(p.status, (x.bad ? kDevBadStart : 0) | (bad_length(src, given) ? kDevBadLength : 0));
+        return row_blocks_of<RT>(x.count, p.group) * blocks_of(seen_of<MODE>(src, len, x.count).len);
+    };
 
     // ---- this workgroup's blocks: `left` of them, from block `off` of unit (b, hr)
     uint32_t b = 0, hr = 0, off = 0;
@@ -441,7 +494,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         uint32_t part;
         if (p.n <= kWave) {
             // a sequence a lane, in every wave for itself
-            const uint32_t v = lane < p.n ? blocks_of(seen_of<WIN>(src, clamp_length(src, src.lens[lane])).len) : 0;
+            const uint32_t v = lane < p.n ? weight_of(lane) : 0;
             const uint32_t up = scan_lanes(v);
             if (!share((uint64_t)__builtin_amdgcn_readlane(up, 63) * per_seq)) return;
             divmod_u64(x0, per_seq, q64, part);
@@ -453,7 +506,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             const uint32_t run = (p.n + kWaves * kWave - 1) / (kWaves * kWave);
             const uint32_t s0 = threadIdx.x * run, s1 = s0 + run < p.n ? s0 + run : p.n;
             uint32_t v = 0, all;
-            for (uint32_t s = s0; s < s1; ++s) v += blocks_of(seen_of<WIN>(src, clamp_length(src, src.lens[s])).len);
+            for (uint32_t s = s0; s < s1; ++s) v += weight_of(s);
             const uint32_t at0 = scan_threads(v, sh.sums, all);
             if (!share((uint64_t)wave_uniform(all) * per_seq)) return;
             divmod_u64(x0, per_seq, q64, part);
@@ -461,7 +514,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             if (q >= at0 && q - at0 < v) {
                 uint32_t at = at0, s = s0, nb = 0;
                 for (; s < s1; ++s) {
-                    nb = blocks_of(seen_of<WIN>(src, clamp_length(src, src.lens[s])).len);
+                    nb = weight_of(s);
                     if (q - at < nb) break;
                     at += nb;
                 }
@@ -474,18 +527,46 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             before = wave_uniform(sh.found[1]);
             mine = wave_uniform(sh.found[2]);
         }
+        if (MANY) {
+            const uint32_t count = fresh_of(src, b).count;
+            mine /= row_blocks_of<RT>(count, p.group);
+        }
         divmod_u64(x0 - (uint64_t)before * per_seq, mine, q64, off);
         hr = (uint32_t)q64;
     }
 
     uint64_t first = x0 - off;  // the unit's first block
     for (uint32_t nb = 0; left != 0; off = 0, ++hr, first += nb) {
-        if (FMT != kFmtPool && hr == per_seq) {
-            hr = 0;
-            ++b;
+        Fresh fresh{};
+        uint32_t row_blocks = src.row_blocks, rows = src.rows;
+        if constexpr (MANY) {
+            for (;; hr = 0, ++b) {
+                if (b >= p.n) return;
+                fresh = fresh_of(src, b);
+                fresh.first = wave_uniform(fresh.first);
+                fresh.count = wave_uniform(fresh.count);
+                row_blocks = row_blocks_of<RT>(fresh.count, p.group);
+                rows = fresh.count * p.group;
+                if (hr < p.H * row_blocks) break;
+            }
+        } else {
+            if (FMT != kFmtPool && hr == per_seq) {
+                hr = 0;
+                ++b;
+            }
+            if (FMT == kFmtPool ? hr >= per_seq : b >= p.n) break;
         }
-        if (FMT == kFmtPool ? hr >= per_seq : b >= p.n) break;
-        const uint32_t h = hr / src.row_blocks, rb = hr % src.row_blocks;
+        const uint64_t unit = MANY ? first_unit<RT>(b, fresh.first, p.group, p.H) + hr : b * per_seq + hr;
+        const uint32_t h = hr / row_blocks, rb = hr % row_blocks;
+        // query row r of the unit's
+        const auto place_of = [&](uint32_t r, uint32_t& at, uint32_t& qh) {
+            if (MANY) {
+                at = fresh.first + r / p.group;
+                qh = h * p.group + r % p.group;
+            } else {
+                row_of<FMT>(p, b, h, r, at, qh);
+            }
+        };
 
         // everything that can be asked for at once: the queries (row 16 rt + c,
         // channels as the key loads have them), the length, the first page numbers
@@ -494,7 +575,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         for (int rt = 0; rt < RT; ++rt) {
             const uint32_t r = (rb * RT + rt) * 16 + c;
             uint32_t seq, qh;
-            row_of<FMT>(p, b, h, r < src.rows ? r : 0, seq, qh);
+            place_of(r < rows ? r : 0, seq, qh);
             const uint8_t* qp = reinterpret_cast<const uint8_t*>(p.q.data + (uint64_t)seq * p.q.ts + (uint64_t)qh * p.q.hs);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
@@ -518,10 +599,24 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             given = src.lens[b];
             if (!WIN) page = load_pages(off * kBlock);
         }
-        seen = seen_of<WIN>(src, FMT == kFmtPool ? src.T : wave_uniform(clamp_length(src, given)));
+        const uint32_t length = FMT == kFmtPool ? src.T : wave_uniform(clamp_length(src, given));
+        seen = seen_of<MODE>(src, length, MANY ? fresh.count : 1);
+        // many new tokens: each row's position, and the tokens that all of them see
+        int32_t pos[MANY ? RT : 1];
+        uint32_t all_from = seen.hid1, all_to = seen.len;
+        if constexpr (MANY) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const uint32_t r = (rb * RT + rt) * 16 + c;
+                pos[rt] = (int32_t)length - (int32_t)fresh.count + (int32_t)((r < rows ? r : 0) / p.group);
+            }
+            const uint32_t last = src.window && length > src.window ? length - src.window : 0;
+            all_from = last > seen.gap ? last - seen.gap : 0;
+            all_to = length + 1 > fresh.count + seen.gap ? length + 1 - fresh.count - seen.gap : 0;
+        }
         if (WIN) page = load_pages(off * kBlock);
         const uint32_t len = seen.len;
-        if (FMT != kFmtPool && hr == 0 && off == 0 && threadIdx.x == 0 && bad_length(src, given) && p.status)
+        if (FMT != kFmtPool && !MANY && hr == 0 && off == 0 && threadIdx.x == 0 && bad_length(src, given) && p.status)
             atomicOr(p.status, kDevBadLength);
         nb = blocks_of(len);
         const uint32_t take = nb - off < left ? nb - off : (uint32_t)left;
@@ -628,7 +723,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             // a row that is none is a zero; the factor of a row's logits is kept
             // >= 0, so that the largest product is the largest logit: a negative
             // scale turns the queries' signs
-            const bool live = (rb * RT + rt) * 16 + c < src.rows;
+            const bool live = (rb * RT + rt) * 16 + c < rows;
             qscale[rt] = fabsf(p.scale_log2);
             if (HALF) {
                 ushort2_t top = 0;
@@ -676,9 +771,14 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         // running state
         f32x4 o[RT][NC];
         float m[RT], mu[RT], l[RT];
-        int E = kMinExp;  // exponent taken out of the weights (HALF)
-        float elimit = __builtin_amdgcn_ldexpf(1.0f, kMinExp);  // 2^E, which no step so far has reached
-        float wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - kMinExp);
+        int E[RE];  // exponent taken out of the weights (HALF)
+        float elimit[RE], wmul[RE];  // 2^E, which no step so far has reached; 2^(kWeightExp - E)
+#pragma unroll
+        for (int e = 0; e < RE; ++e) {
+            E[e] = kMinExp;
+            elimit[e] = __builtin_amdgcn_ldexpf(1.0f, kMinExp);
+            wmul[e] = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - kMinExp);
+        }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             m[rt] = kNegInf;
@@ -853,6 +953,26 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             }
             if (t_next < end) load(t_next, it + 1, x);
 
+            // many new tokens: which of the lane's 8 tokens a row sees
+            uint32_t sight[MANY ? RT : 1];
+            const auto row_sees = [&](int rt, int j) { return (sight[MANY ? rt : 0] >> j & 1) != 0; };
+            if (MANY && PART) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    uint32_t bits = 0;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int32_t t = (int32_t)(real(t0 + 16 * i) + 4 * g);
+                        Sight z;
+                        z.past = pos[MANY ? rt : 0] - t;
+                        z.left = src.window ? z.past - (int32_t)src.window : -0x7FFFFFFF;
+                        z.sunk_to = src.window ? (int32_t)src.sinks - t : 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) bits |= z(j) ? 1u << (4 * i + j) : 0u;
+                    }
+                    sight[MANY ? rt : 0] = bits;
+                }
+            }
             // logits (in powers of two), their maxima, and the steps' largest
             float y[RT][8], top[RT];
             bool move = false;
@@ -878,29 +998,37 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             for (int rt = 0; rt < RT; ++rt) {
                 if (PART) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) y[rt][j] = counts(t0, j) ? y[rt][j] : kNegInf;
+                    for (int j = 0; j < 8; ++j) y[rt][j] = (MANY ? row_sees(rt, j) : counts(t0, j)) ? y[rt][j] : kNegInf;
                 }
                 top[rt] = y[rt][0];
 #pragma unroll
                 for (int j = 1; j < 8; ++j) top[rt] = fmaxf(top[rt], y[rt][j]);
                 move |= top[rt] > m[rt] + kSlack;
             }
-            float big = 0.0f;
+            float big[RE];
             if (HALF) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) big = fmaxf(big, vs[j]);
-                move |= big >= elimit;
+                for (int e = 0; e < RE; ++e) {
+                    big[e] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) big[e] = fmaxf(big[e], MANY && PART && !row_sees(e, j) ? 0.0f : vs[j]);
+                    move |= big[e] >= elimit[e];
+                }
             }
             if (__ballot(move) != 0) {
                 const auto larger = [](float a, float b) { return fmaxf(a, b); };
-                float shrink = 1.0f;
-                if (HALF) {
-                    big = over_groups(big, larger);
-                    const int e = __builtin_amdgcn_frexp_expf(big), ne = big >= elimit ? e : E;
-                    shrink = __builtin_amdgcn_ldexpf(1.0f, E - ne);
-                    E = ne;
-                    elimit = __builtin_amdgcn_ldexpf(1.0f, E);
-                    wmul = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - E);
+                float shrink[RE];
+#pragma unroll
+                for (int i = 0; i < RE; ++i) {
+                    shrink[i] = 1.0f;
+                    if (HALF) {
+                        big[i] = over_groups(big[i], larger);
+                        const int e = __builtin_amdgcn_frexp_expf(big[i]), ne = big[i] >= elimit[i] ? e : E[i];
+                        shrink[i] = __builtin_amdgcn_ldexpf(1.0f, E[i] - ne);
+                        E[i] = ne;
+                        elimit[i] = __builtin_amdgcn_ldexpf(1.0f, ne);
+                        wmul[i] = __builtin_amdgcn_ldexpf(1.0f, kWeightExp - ne);
+                    }
                 }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
@@ -910,12 +1038,44 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                     mu[rt] = nm == kNegInf ? 0.0f : nm;
                     l[rt] *= a;
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) o[rt][n] *= a * shrink;
+                    for (int n = 0; n < NC; ++n) o[rt][n] *= a * shrink[MANY ? rt : 0];
                 }
             }
-            if (HALF) {
+            if (HALF && !MANY) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) vs[j] *= wmul;
+                for (int j = 0; j < 8; ++j) vs[j] *= wmul[0];
+            }
+            if constexpr (MANY && !HALF) {
+                // a value that is not finite, seen by some rows and not by others: what it reaches is NaN, by a product of
+                // what is not finite with who sees it, and it becomes 0, which a weight of 0 leaves at 0
+                uint32_t bad = 0;
+                if (PART) {
+#pragma unroll
+                    for (int n = 0; n < NC; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) bad |= infinite(vf[n][j]);
+                }
+                if (__builtin_expect(PART && __ballot(bad != 0) != 0, 0)) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        u32x4 who;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) who[j] = (row_sees(rt, 2 * j) ? 0x3F80u : 0) | (row_sees(rt, 2 * j + 1) ? 0x3F800000u : 0);
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) {
+                            u32x4 what;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) what[j] = infinite(vf[n][j]) & 0x3F803F80u;
+                            const f32x4 hit = mfma_bf16(what, who, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) o[rt][n][r] = hit[r] > 0.0f ? __builtin_nanf("") : o[rt][n][r];
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NC; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) vf[n][j] &= ~infinite(vf[n][j]);
+                }
             }
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
@@ -926,7 +1086,8 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                     // by the token, not by its logit: -inf * 0 has no sign
                     if (PART && !WIN) e = counts(t0, j) ? e : 0.0f;
                     l[rt] += e;
-                    w[j] = HALF ? e * vs[j] : e;
+                    w[j] = !HALF ? e : MANY ? e * (vs[j] * wmul[MANY ? rt : 0]) : e * vs[j];
+                    if (HALF && MANY && PART) w[j] = row_sees(rt, j) ? w[j] : 0.0f;  // (a step of NaN)
                 }
                 if (HALF) {
                     u32x4 pf;
@@ -959,7 +1120,8 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             uint32_t it = 0, t0 = base + wave * kTile;
             if (WIN) {
                 for (; t0 < stop; t0 += kBlock, ++it) {
-                    const bool all = t0 + kTile <= stop && (t0 + kTile <= seen.hid0 || t0 >= seen.hid1);
+                    const bool all = MANY ? t0 + kTile <= stop && t0 + kTile <= all_to && t0 >= all_from
+                                          : t0 + kTile <= stop && (t0 + kTile <= seen.hid0 || t0 >= seen.hid1);
                     tile(!all, t0, t0 + kBlock < stop ? t0 + kBlock : end, it, x);
                 }
             } else {
@@ -976,7 +1138,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
 
         // ---- join the waves: m and l first, then the sums
         const bool whole = take == nb;
-        const uint32_t slot = whole ? (src.whole ? 0 : 2 * src.W) + b * per_seq + hr : off ? 2 * w : 2 * w + 1;
+        const uint32_t slot = whole ? (src.whole ? 0 : 2 * src.W) + (uint32_t)unit : off ? 2 * w : 2 * w + 1;
         if (off == 0 && threadIdx.x == 0 && !(src.whole && p.direct)) {
             // parts: up to the workgroup whose share has the unit's last block
             uint32_t parts = p.direct ? 0 : 1;
@@ -990,7 +1152,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                     divmod_u64(last - large, (uint32_t)each, at, rest);
                 parts = (uint32_t)at + (last < large ? 0 : more) - w + 1;
             }
-            src.info[b * per_seq + hr] = make_uint2(slot, parts);
+            src.info[unit] = make_uint2(slot, parts);
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -1007,7 +1169,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
 #pragma unroll
             for (int v = 1; v < kWaves; ++v) M = fmaxf(M, sh.ml[v][rt * 16 + c][0]);
             float a = exp2_fast(m[rt] - (M == kNegInf ? 0.0f : M));
-            if (HALF) a *= __builtin_amdgcn_ldexpf(1.0f, E - kWeightExp);
+            if (HALF) a *= __builtin_amdgcn_ldexpf(1.0f, E[MANY ? rt : 0] - kWeightExp);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -1045,10 +1207,10 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
 #pragma unroll
                 for (int n = 0; n < NC; ++n) y[n] *= k;
             }
-            if (r < src.rows) {
+            if (r < rows) {
                 if (whole && p.direct) {
                     uint32_t seq, qh;
-                    row_of<FMT>(p, b, h, r, seq, qh);
+                    place_of(r, seq, qh);
                     // a row without tokens: zeros, and ln 0
                     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                     uint16_t* to = p.out.data + (uint64_t)seq * p.out.ts + (uint64_t)qh * p.out.hs + ch;
@@ -1076,11 +1238,11 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
     }
 }
 
-template <int FMT, int D, int RT, bool WIN>
+template <int FMT, int D, int RT, int MODE>
 __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_kernel(Common p, Source src) {
     fetch_arguments<sizeof(Common) + sizeof(Source)>();
     __shared__ Shared<D, RT> sh;
-    attend_share<FMT, D, RT, WIN>(p, src, blockIdx.x, sh);
+    attend_share<FMT, D, RT, MODE>(p, src, blockIdx.x, sh);
 }
 
 // A pool's workgroups and those of the tails behind it, in one launch.
@@ -1093,9 +1255,9 @@ __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_b
         Shared<D, 1> b;
     } sh;
     if (blockIdx.x < pool.W)
-        attend_share<kFmtPool, D, RT, false>(p, pool, blockIdx.x, sh.a);
+        attend_share<kFmtPool, D, RT, kOneSeesAll>(p, pool, blockIdx.x, sh.a);
     else
-        attend_share<FMT, D, 1, false>(p, tail, blockIdx.x - pool.W, sh.b);
+        attend_share<FMT, D, 1, kOneSeesAll>(p, tail, blockIdx.x - pool.W, sh.b);
 }
 
 // Joins the parts of a row: V waves a row, which take its parts in turn, d / 64
@@ -1108,7 +1270,7 @@ struct JoinParams {
     uint32_t sources;
 };
 
-template <int D, int V>
+template <int D, int V, bool MANY>
 __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p) {
     fetch_arguments<sizeof(JoinParams)>();
     constexpr int C = D / 64, U = 8;
@@ -1117,9 +1279,28 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
     const uint32_t lane = lane_id();
     const uint32_t wave = wave_uniform(threadIdx.x / kWave), w = wave % V;
     const uint32_t row = blockIdx.x * RPB + wave / V;
-    if (row >= p.c.n * p.c.Hq) return;
-    const uint32_t seq = row / p.c.Hq, qh = row % p.c.Hq;
-    const uint32_t h = qh / p.c.group, i = qh % p.c.group;
+    if (row >= (MANY ? p.src[0].tokens : p.c.n) * p.c.Hq) return;
+    const uint32_t seq = row / p.c.Hq, qh = row % p.c.Hq;  // many new tokens: `seq` is a token
+    const uint32_t h = qh / p.c.group;
+    uint32_t i = qh % p.c.group, row_blocks = p.src[0].row_blocks;
+    uint64_t unit0 = 0;
+    if constexpr (MANY) {
+        // the last sequence that starts at or before the token: of 64 that are evenly apart, then of those between two
+        uint32_t b = 0, range = p.c.n;
+        while (range > 1) {
+            const uint32_t each = (range + kWave - 1) / kWave, at = b + lane * each;
+            const bool before = lane * each < range && p.src[0].starts[at] <= (int32_t)seq;
+            const uint32_t k = __builtin_popcountll(__ballot(before));
+            if (k == 0) return;
+            b += (k - 1) * each;
+            range = (k - 1) * each + each < range ? each : range - (k - 1) * each;
+        }
+        const Fresh x = fresh_of(p.src[0], b);
+        if (seq - x.first >= x.count) return;  // of no sequence
+        i += (seq - x.first) * p.c.group;
+        unit0 = p.rt[0] == 1 ? first_unit<1>(b, x.first, p.c.group, p.c.H) : first_unit<2>(b, x.first, p.c.group, p.c.H);
+        row_blocks = p.rt[0] == 1 ? row_blocks_of<1>(x.count, p.c.group) : row_blocks_of<2>(x.count, p.c.group);
+    }
     // this row's place in each source: its part k at from[s] + stride[s] * slot,
     // and the part's maximum and sum `ml` floats behind it
     const float* from[2] = {};
@@ -1131,7 +1312,10 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
         const Source& x = p.src[s];
         const uint32_t tile = 16 * p.rt[s], r = x.pool ? seq * p.c.group + i : i, at = r % tile;
         // (a long pool's numbers could be worked out here: 0.6 us more than the load)
-        info[s] = scalar_load<u32x2>(x.info + (x.pool ? 0 : seq * p.c.H * x.row_blocks) + h * x.row_blocks + r / tile);
+        if (MANY)
+            info[s] = scalar_load<u32x2>(x.info + unit0 + h * row_blocks + r / tile);
+        else
+            info[s] = scalar_load<u32x2>(x.info + (x.pool ? 0 : seq * p.c.H * x.row_blocks) + h * x.row_blocks + r / tile);
         stride[s] = tile * (D + 2);
         from[s] = x.part + at * D;
         ml[s] = (tile - at) * D + at * 2;
@@ -1271,22 +1455,27 @@ AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens,
     return plan_of(units_of_rows, rows, max_tokens, d, rows > one_tile && enough ? 2 : 1, direct);
 }
 
-template <int FMT, int D>
-hipError_t launch_pages(uint32_t rt, bool window, uint32_t grid, const Common& p, const Source& s, hipStream_t stream) {
-    auto f = rt == 1 ? attend_kernel<FMT, D, 1, false> : attend_kernel<FMT, D, 2, false>;
-    if constexpr (FMT != kFmtPool)
-        if (window) f = rt == 1 ? attend_kernel<FMT, D, 1, true> : attend_kernel<FMT, D, 2, true>;
-    return launch_kernel(f, dim3(grid), dim3(kWaves * kWave), stream, p, s);
+template <int FMT, int D, int MODE>
+hipError_t launch_pages(uint32_t rt, uint32_t grid, const Common& p, const Source& s, hipStream_t stream) {
+    return launch_kernel(rt == 1 ? attend_kernel<FMT, D, 1, MODE> : attend_kernel<FMT, D, 2, MODE>, dim3(grid),
+                         dim3(kWaves * kWave), stream, p, s);
 }
-template <int D>
-hipError_t launch_pages_of(uint32_t format, uint32_t rt, bool window, uint32_t grid, const Common& p, const Source& s,
+template <int D, int MODE>
+hipError_t launch_pages_as(uint32_t format, uint32_t rt, uint32_t grid, const Common& p, const Source& s,
                            hipStream_t stream) {
     switch (format) {
-        case kPageBf16: return launch_pages<kFmtBf16, D>(rt, window, grid, p, s, stream);
-        case kPageInt8: return launch_pages<kFmtInt8, D>(rt, window, grid, p, s, stream);
-        case kPageFp8: return launch_pages<kFmtFp8, D>(rt, window, grid, p, s, stream);
-        default: return launch_pages<kFmtFp4, D>(rt, window, grid, p, s, stream);
+        case kPageBf16: return launch_pages<kFmtBf16, D, MODE>(rt, grid, p, s, stream);
+        case kPageInt8: return launch_pages<kFmtInt8, D, MODE>(rt, grid, p, s, stream);
+        case kPageFp8: return launch_pages<kFmtFp8, D, MODE>(rt, grid, p, s, stream);
+        default: return launch_pages<kFmtFp4, D, MODE>(rt, grid, p, s, stream);
     }
+}
+template <int D>
+hipError_t launch_pages_of(int mode, uint32_t format, uint32_t rt, uint32_t grid, const Common& p, const Source& s,
+                           hipStream_t stream) {
+    return mode == kMany        ? launch_pages_as<D, kMany>(format, rt, grid, p, s, stream)
+           : mode == kOneWindow ? launch_pages_as<D, kOneWindow>(format, rt, grid, p, s, stream)
+                                : launch_pages_as<D, kOneSeesAll>(format, rt, grid, p, s, stream);
 }
 template <int FMT, int D>
 hipError_t launch_both(uint32_t rt, uint32_t grid, const Common& p, const Source& a, const Source& b, hipStream_t stream) {
@@ -1325,6 +1514,32 @@ AttendPlan pool_attend_plan(uint32_t H, uint32_t n_agents, uint32_t Hq, uint32_t
     return make_plan(H, n_agents * (Hq / H), T, d, 16, !tail);
 }
 
+// Many new tokens: up to 32 rows of a sequence and kv head (its new tokens times the heads that share it) a unit.
+AttendPlan many_attend_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens,
+                            uint32_t window, uint32_t sinks) {
+    AttendPlan a{};
+    const uint64_t rows = (uint64_t)n_tokens * (Hq / H);
+    a.rt = rows > 16ull * n_seqs ? 2 : 1;
+    a.row_blocks = 1;
+    a.units = (rows / (16 * a.rt) + n_seqs) * H;  // at most
+    // (a sequence's rows see the tokens of one row, and with a window as many more as it has new ones)
+    const uint64_t seen = window ? seen_tokens(max_tokens, (uint64_t)window + n_tokens, sinks) : max_tokens;
+    a.blocks = a.units * ((seen + kBlock - 1) / kBlock);
+    const uint64_t places = 256ull * waves_per_simd(d, a.rt);
+    a.W = a.blocks / kMinBlocks < places ? a.blocks / kMinBlocks : places;
+    if (a.W < 1) a.W = 1;
+    a.slots = 2 * a.W;
+    a.room = a.bytes(d);
+    return a;
+}
+
+uint64_t many_attend_room(uint32_t n_seqs, uint64_t rows, uint32_t H, uint32_t d, uint64_t max_tokens) {
+    const uint64_t units = (rows / 16 + n_seqs) * H, places = 256ull * waves_per_simd(d, 1);
+    uint64_t w = units * ((max_tokens + kBlock - 1) / kBlock) / kMinBlocks;
+    w = w < 1 ? 1 : w < places ? w : places;
+    return align_up(2 * w * 32 * (d + 2) * 4 + units * 8, 256);
+}
+
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     Common p{};
     p.q = a.q;
@@ -1355,8 +1570,9 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     }
     if (has_pages) {
         const PageLayout& lay = a.tail.lay;
-        page_plan = page_attend_plan(a.n, a.H, a.Hq, a.d,
-                                     seen_tokens((uint64_t)a.tail.table_cols * lay.P, a.tail.window, a.tail.sinks), has_pool);
+        const uint64_t most = (uint64_t)a.tail.table_cols * lay.P;
+        page_plan = a.starts ? many_attend_plan(a.n, a.tokens, a.H, a.Hq, a.d, most, a.tail.window, a.tail.sinks)
+                             : page_attend_plan(a.n, a.H, a.Hq, a.d, seen_tokens(most, a.tail.window, a.tail.sinks), has_pool);
         ws += place_source(pages, page_plan, a.d, ws);
         pages.pages = a.tail.pages;
         pages.table = a.tail.table;
@@ -1364,6 +1580,10 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
         pages.lens = a.tail.lens;
         pages.window = a.tail.window;
         pages.sinks = a.tail.sinks;
+        if (a.starts) {
+            pages.starts = a.starts;
+            pages.tokens = a.tokens;
+        }
         pages.table_cols = a.tail.table_cols;
         pages.num_pages = lay.num_pages;
         pages.page_shift = 31 - __builtin_clz(lay.P);
@@ -1376,12 +1596,13 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
         e = a.d == 64 ? launch_both_of<64>(a.tail.lay.format, pool_plan.rt, grid, p, pool, pages, stream)
                       : launch_both_of<128>(a.tail.lay.format, pool_plan.rt, grid, p, pool, pages, stream);
     } else if (has_pool) {
-        e = a.d == 64 ? launch_pages<kFmtPool, 64>(pool_plan.rt, false, pool.W, p, pool, stream)
-                      : launch_pages<kFmtPool, 128>(pool_plan.rt, false, pool.W, p, pool, stream);
+        e = a.d == 64 ? launch_pages<kFmtPool, 64, kOneSeesAll>(pool_plan.rt, pool.W, p, pool, stream)
+                      : launch_pages<kFmtPool, 128, kOneSeesAll>(pool_plan.rt, pool.W, p, pool, stream);
     } else {
         const uint32_t format = a.tail.lay.format;
-        e = a.d == 64 ? launch_pages_of<64>(format, page_plan.rt, a.tail.window != 0, pages.W, p, pages, stream)
-                      : launch_pages_of<128>(format, page_plan.rt, a.tail.window != 0, pages.W, p, pages, stream);
+        const int mode = a.starts ? kMany : a.tail.window ? kOneWindow : kOneSeesAll;
+        e = a.d == 64 ? launch_pages_of<64>(mode, format, page_plan.rt, pages.W, p, pages, stream)
+                      : launch_pages_of<128>(mode, format, page_plan.rt, pages.W, p, pages, stream);
     }
     const AttendPlan& first = has_pool ? pool_plan : page_plan;
     if (e != hipSuccess || (p.direct && first.whole)) return e;
@@ -1392,17 +1613,19 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream) {
     j.src[1] = pages;
     j.rt[1] = has_pages ? page_plan.rt : 1;
     j.sources = p.direct ? 1 : 2;
-    const uint64_t rows = (uint64_t)a.n * a.Hq;
+    const uint64_t rows = (uint64_t)(a.starts ? a.tokens : a.n) * a.Hq;
     // One wave joins a row of few parts, four one of many. A call with one and with four, us: pages of 1, 4, 8, 15
     // and 32 sequences of 4096 tokens (W / units 64, 16, 8, 4, 2) 10.4 and 10.0, 13.4 and 13.1, 18.3 and 18.6, 28.8
     // and 29.2, 48.0 and 48.7; a pool of 8192 tokens for 4 agents (32) 12.2 and 10.7, of 131071 over 2 kv heads (256) 32.9
     // and 19.9. It goes by the mean: of 100 sequences (5) one of 40000 tokens among 99 of 100 takes 31.2, with four 16.4.
     const bool few = first.whole || first.W <= 6 * first.units;
-    if (few)
-        return launch_kernel(a.d == 64 ? attend_join_kernel<64, 1> : attend_join_kernel<128, 1>,
-                             dim3((uint32_t)((rows + 3) / 4)), dim3(kBlockThreads), stream, j);
-    return launch_kernel(a.d == 64 ? attend_join_kernel<64, 4> : attend_join_kernel<128, 4>, dim3((uint32_t)rows),
-                         dim3(kBlockThreads), stream, j);
+    const dim3 grid((uint32_t)(few ? (rows + 3) / 4 : rows));
+    const auto join = [&](auto one, auto four) { return launch_kernel(few ? one : four, grid, dim3(kBlockThreads), stream, j); };
+    if (a.starts)
+        return a.d == 64 ? join(attend_join_kernel<64, 1, true>, attend_join_kernel<64, 4, true>)
+                         : join(attend_join_kernel<128, 1, true>, attend_join_kernel<128, 4, true>);
+    return a.d == 64 ? join(attend_join_kernel<64, 1, false>, attend_join_kernel<64, 4, false>)
+                     : join(attend_join_kernel<128, 1, false>, attend_join_kernel<128, 4, false>);
 }
 
 }  // namespace kvc

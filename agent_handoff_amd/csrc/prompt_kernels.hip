@@ -864,6 +864,8 @@ hipError_t launch_of(uint32_t format, const PromptParams& p, uint32_t grid, hipS
 
 // Workgroups of 4 waves that the GPU holds at once.
 constexpr uint64_t kPlaces = 512;
+// Up to so many rows of a sequence and kv head, at the mean, a call is memory's: the kernel for one new token takes them.
+constexpr uint64_t kFewRows = 32;
 
 }  // namespace
 
@@ -881,10 +883,34 @@ PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t 
     const uint64_t each = (uint64_t)kRows * (d + 2) * 4;
     if (a.more) a.bytes = align_up(2 * a.more * H * each, 256);
     if (can) a.room = align_up(2 * ((kPlaces + H - 1) / H) * H * each, 256);
+    const uint64_t rows = n_tokens * group, few = rows < kFewRows * n_seqs ? rows : kFewRows * n_seqs;
+    const AttendPlan many = many_attend_plan(n_seqs, n_tokens, H, Hq, d, max_tokens, window, sinks);
+    // (what its kernel counts with 32 bits, wherever the sequences start)
+    a.few = rows <= few && (uint64_t)n_seqs * (rows / 16 + 1) * (max_tokens / 128 + 1) < 1ull << 31;
+    if (a.few) a.bytes = many.bytes(d);
+    const uint64_t room = many_attend_room(n_seqs, few, H, d, max_tokens);
+    if (room > a.room) a.room = room;
     return a;
 }
 
 hipError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& plan, hipStream_t stream) {
+    if (plan.few) {
+        AttendArgs b{};
+        b.n = a.n;
+        b.H = a.H;
+        b.Hq = a.Hq;
+        b.d = a.d;
+        b.q = a.q;
+        b.out = a.out;
+        b.scale = a.scale;
+        b.lse = a.lse;
+        b.ws = a.ws;
+        b.status = a.status;
+        b.tail = a.tail;
+        b.starts = a.starts;
+        b.tokens = a.rows;
+        return launch_attend(b, stream);
+    }
     PromptParams p{};
     const PageLayout& lay = a.tail.lay;
     p.q = a.q;
