@@ -864,13 +864,19 @@ hipError_t launch_of(uint32_t format, const PromptParams& p, uint32_t grid, hipS
 
 // Workgroups of 4 waves that the GPU holds at once.
 constexpr uint64_t kPlaces = 512;
-// Up to so many rows of a sequence and kv head, at the mean, a call is memory's: the kernel for one new token takes them.
-constexpr uint64_t kFewRows = 32;
+// Few new tokens of each sequence (their rows, times the heads that share a kv head, in the mean of all): a call is then
+// memory's, and the kernel for one new token takes them, 32 rows at a time. 15 sequences behind 8192 tokens (8 kv heads of
+// 128), that kernel and the one here, us: 32 rows e4m3 78 and 138, 64 rows 109 and 152, 4 bits 89 and 130, bf16 176 and
+// 148, 96 rows e4m3 153 and 166, 128 rows 188 and 181; one sequence of 32 rows behind 4000 tokens 17 and 41, behind 400
+// 14 and 22, and, with a second launch that joins what it shared out, behind 100 13 and 12 (15 sequences 20 and 13).
+// (Rows that belong to no sequence count as well: a quarter more.)
+constexpr uint64_t few_rows(uint32_t format) { return format == kPageBf16 ? 40 : 80; }
+constexpr uint64_t kFewTokens = 256;
 
 }  // namespace
 
-PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens,
-                       uint32_t window, uint32_t sinks) {
+PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint32_t format,
+                       uint64_t max_tokens, uint32_t window, uint32_t sinks) {
     const uint64_t group = Hq / H;
     PromptPlan a{};
     a.blocks = n_tokens * group / kRows + n_seqs;
@@ -883,10 +889,10 @@ PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t 
     const uint64_t each = (uint64_t)kRows * (d + 2) * 4;
     if (a.more) a.bytes = align_up(2 * a.more * H * each, 256);
     if (can) a.room = align_up(2 * ((kPlaces + H - 1) / H) * H * each, 256);
-    const uint64_t rows = n_tokens * group, few = rows < kFewRows * n_seqs ? rows : kFewRows * n_seqs;
+    const uint64_t rows = n_tokens * group, most = few_rows(format) * n_seqs, few = rows < most ? rows : most;
     const AttendPlan many = many_attend_plan(n_seqs, n_tokens, H, Hq, d, max_tokens, window, sinks);
     // (what its kernel counts with 32 bits, wherever the sequences start)
-    a.few = rows <= few && (uint64_t)n_seqs * (rows / 16 + 1) * (max_tokens / 128 + 1) < 1ull << 31;
+    a.few = rows <= most && max_tokens > kFewTokens && (uint64_t)n_seqs * (rows / 16 + 1) * (max_tokens / 128 + 1) < 1ull << 31;
     if (a.few) a.bytes = many.bytes(d);
     const uint64_t room = many_attend_room(n_seqs, few, H, d, max_tokens);
     if (room > a.room) a.room = room;

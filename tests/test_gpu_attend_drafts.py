@@ -1,5 +1,6 @@
 """GPU parity of attention of few new tokens of each sequence (drafts to be verified, the last tokens of a prompt), which
-kvpage_attend_prompt takes another way than long prompts: against the formula in 64 bits."""
+kvpage_attend_prompt takes another way than long prompts (where tables hold more than 256 tokens a sequence): against
+the formula in 64 bits."""
 
 import numpy as np
 import pytest
@@ -20,12 +21,13 @@ NONE = 0x7FC0
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("heads, group, page, new, lens", [
     (1, 1, 16, [1], [1]),
-    (2, 4, 16, [5, 0, 8, 1], [500, 40, 8, 700]),      # one row tile and two
+    (2, 4, 16, [5, 0, 8, 1], [500, 40, 8, 700]),
     (3, 7, 64, [4, 2], [2000, 64]),                   # a token's rows in two units
     (1, 1, 32, [31, 33], [31, 1500]),
+    (2, 4, 16, [4, 2, 3], [500, 40, 800]),            # one row tile (the others: two)
     (1, 4, 16, [60, 1, 1, 1, 1, 1, 1, 1, 1], [90, 1, 200, 17, 300, 16, 33, 40, 1000]),  # several row blocks of one
     (1, 16, 256, [2], [513]),
-    (4, 2, 16, [3] * 20, list(range(3, 23))),
+    (4, 2, 16, [3] * 20, list(range(3, 22)) + [300]),
 ])
 def test_drafts(fmt, d, heads, group, page, new, lens):
     _case(fmt, d, heads, group, page, new, lens, 0, 0, layout="heads" if group == 4 else "fused" if group == 7 else "tokens")
@@ -41,8 +43,8 @@ def test_windows_over_drafts(fmt, d, window, sinks):
 
 @pytest.mark.parametrize("fmt", ALL_FORMATS)
 def test_more_drafts_than_tokens(fmt):
-    _case(fmt, 64, 2, 2, 16, [10, 5, 7], [4, 0, 150], 0, 0, before=3, behind=7)
-    _case(fmt, 128, 1, 4, 16, [6, 5, 7], [4, 0, 40], 9, 2, before=1)
+    _case(fmt, 64, 2, 2, 16, [10, 5, 7], [4, 0, 350], 0, 0, before=3, behind=7)
+    _case(fmt, 128, 1, 4, 16, [6, 5, 7], [4, 0, 400], 9, 2, before=1)
 
 
 @pytest.mark.parametrize("fmt", ALL_FORMATS)
@@ -55,7 +57,7 @@ def test_scales_of_drafts(fmt):
 def test_drafts_of_many_sequences(n):
     rng = np.random.default_rng(n)
     new = [int(x) for x in rng.integers(0, 7, n)]
-    lens = [m + int(x) for m, x in zip(new, rng.integers(0, 200, n))]
+    lens = [m + int(x) for m, x in zip(new, rng.integers(0, 400, n))]
     _case(ka.KVC_PAGE_INT8, 64, 1, 4, 16, new, lens, 0, 0, before=2, behind=1)
     _case(ka.KVC_PAGE_BF16, 64, 1, 4, 16, new, lens, 30, 2)
 
@@ -66,21 +68,21 @@ def test_drafts_of_many_sequences(n):
 def test_non_finite_tokens_reach_the_drafts_that_see_them(fmt, d, what):
     """A row is not finite exactly where it sees a token that is not: the others are as if that token were any other."""
     rng = np.random.default_rng(61)
-    heads, group, page, m, n, window = 2, 2, 16, 12, 200, 60
-    spec = (20, heads, page, d, fmt)
+    heads, group, page, m, n, window = 2, 2, 16, 12, 400, 60
+    spec = (40, heads, page, d, fmt)
     store, table = store_of(rng, spec, [n])
     dev = store.dev()
     x = np.full((1, heads, d), 0x3F80, np.uint16)
     y = x.copy()
     y[0, 1, d - 1] = 0x7F80 if what == "value inf" else NONE
-    bad = [134, 194]  # at the windows' first tokens, and among the drafts
+    bad = [334, 394]  # at the windows' first tokens, and among the drafts
     for t in bad:
         slot = torch.tensor([int(table[0, t // page]) * page + t % page], device=DEV)
         ka.kvpage_write(spec, dev, to_dev(y if what == "key" else x), to_dev(x if what == "key" else y), slot)
     torch.cuda.synchronize()
     store.host[:] = dev.cpu().numpy()
     q = bits(rng, (m, heads * group, d))
-    for win, sinks in ((0, 0), (window, 2), (window, 150)):
+    for win, sinks in ((0, 0), (window, 2), (window, 350)):
         out, lse = _attend(spec, dev, q, [0, m], table, [n], win, sinks)
         o, l = host_f64(out), host_f64(lse)
         see = rows_see(m, n, win, sinks)
@@ -104,13 +106,13 @@ def test_drafted_values_of_very_different_sizes(fmt):
     """Steps that grow by 2^60 along the drafts: a row that does not see the large ones keeps its own bits."""
     rng = np.random.default_rng(62)
     d, n, m = 64, 60, 30
-    spec = (4, 1, 16, d, fmt)
+    spec = (20, 1, 16, d, fmt)
     store = Store(spec)
     k, v = bits(rng, (n, 1, d)), bits(rng, (n, 1, d))
     e = (v >> 7 & 255).astype(int) + np.round(np.linspace(-30, 30, n)).astype(int)[:, None, None]
     v = ((v & 0x807F) | (e << 7)).astype(np.uint16)
     put_all(store.host, spec, k, v, np.arange(n))
-    table = np.arange(4, dtype=np.int32)[None]
+    table = np.arange(20, dtype=np.int32)[None]
     q = bits(rng, (m, 1, d))
     out, lse = _attend(spec, store.dev(), q, [0, m], table, [n])
     kk, vv = sequence(store, table, 0, n)
@@ -123,8 +125,8 @@ def test_drafted_values_of_very_different_sizes(fmt):
 
 def test_bad_pages_lengths_and_starts_of_drafts_are_reported():
     rng = np.random.default_rng(63)
-    spec = (30, 1, 16, 64, ka.KVC_PAGE_INT8)
-    new, lens = [5, 3, 7, 1], [100, 50, 30, 80]
+    spec = (40, 1, 16, 64, ka.KVC_PAGE_INT8)
+    new, lens = [5, 3, 7, 1], [300, 50, 30, 80]
     starts = np.concatenate([[0], np.cumsum(new)]).tolist()
     store, table = store_of(rng, spec, lens)
     dev, q = store.dev(), bits(rng, (16, 2, 64))
@@ -135,9 +137,9 @@ def test_bad_pages_lengths_and_starts_of_drafts_are_reported():
     out, lse = _attend(spec, dev, q, starts, wrong, lens, st=st)
     assert int(st) == ka.KVC_DEV_BAD_PAGE and torch.equal(out[5:15], ref[5:15]) and torch.equal(lse[5:15], ref_lse[5:15])
     full = np.where(table < 0, 0, table)
-    for length in (-1, 113, -(1 << 31), (1 << 31) - 1):
+    for length in (-1, 305, -(1 << 31), (1 << 31) - 1):
         st = status()
-        out, lse = _attend(spec, dev, q, starts, full, [100, length, 30, 80], st=st)
+        out, lse = _attend(spec, dev, q, starts, full, [300, length, 30, 80], st=st)
         assert int(st) == ka.KVC_DEV_BAD_LENGTH
         keep = list(range(5)) + list(range(8, 16))
         assert torch.equal(out[keep], ref[keep]) and torch.equal(lse[keep], ref_lse[keep])
