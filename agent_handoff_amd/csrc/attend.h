@@ -159,8 +159,8 @@ struct PromptPlan {
     uint64_t bytes;   // of the workspace: what the call uses,
     uint64_t room;    // and what serves every smaller call too
 };
-PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint32_t format,
-                       uint64_t max_tokens, uint32_t window, uint32_t sinks);
+PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens,
+                       uint32_t window, uint32_t sinks);
 struct PromptArgs {
     uint32_t n, rows, H, Hq, d;  // sequences, query rows (tokens), kv heads, query heads, channels
     RowsDev q, out;

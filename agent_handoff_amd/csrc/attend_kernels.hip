@@ -51,6 +51,7 @@
 #include "attend.h"
 #include "codebook.h"
 #include "kernels_common.h"
+#include "lds_fetch.h"
 #include "page_codes.h"
 
 #include <type_traits>
@@ -139,10 +140,8 @@ __device__ __forceinline__ f32x4 mfma_bf16(const u32x4& a, const u32x4& b, const
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                    0, 0, 0);
 }
-// Ones in each half that holds a bf16 that is not finite.
-__device__ __forceinline__ uint32_t infinite(uint32_t v) {
-    return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-}
+// The top bit of each half that holds a bf16 that is not finite.
+__device__ __forceinline__ uint32_t infinite(uint32_t v) { return ((v & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 template <int FMT>
 __device__ __forceinline__ f32x4 mfma(const u32x4& a, const u32x4& b, const f32x4& c) {
     return half_products(FMT) ? mfma_half(a, b, c) : mfma_bf16(a, b, c);
@@ -242,6 +241,14 @@ __device__ __forceinline__ void load_words(const uint8_t* a, uint32_t (&w)[W]) {
     } else {
         w[0] = *reinterpret_cast<const uint32_t*>(a);
     }
+}
+
+__device__ __forceinline__ void take_steps(const uint8_t* from, float* to) {
+    const float4 a = *reinterpret_cast<const float4*>(from);
+    to[0] = a.x;
+    to[1] = a.y;
+    to[2] = a.z;
+    to[3] = a.w;
 }
 
 // What no workgroup of a launch writes, at an address that is the same in all
@@ -368,14 +375,50 @@ __device__ __forceinline__ void fwht_row(float (&y)[C], uint32_t lane) {
 // workgroups a CU holds.
 constexpr int waves_per_simd(int d, int rt) { return d == 64 ? (rt == 1 ? 3 : 2) : 2; }
 
+// Tiles on their way to a wave lie in its registers, or in LDS, which a wave fills for itself. In LDS they cost more
+// instructions, but leave room for a second row tile and for tiles further ahead: 8-bit and 16-bit pages with two row tiles
+// (15 sequences of 5 drafts behind 8192 tokens, 8 kv heads of 128, 20 rows: e4m3 74 and 65 us, bf16 125 and 120). With
+// one row tile int8 52 and 55, bf16 98 and 97; 4 bits 61 and 69, with two 54 and 58.
+constexpr bool through_lds(int fmt, int rt) { return rt == 2 && fmt != kFmtPool && fmt != kFmtFp4; }
+
+// A tile: rows of keys, of values, then the steps of both. The keys' chunks of 16 bytes change places inside a row by
+// the token, so that 16 lanes with one chunk of 16 tokens meet in no bank.
+template <int FMT, int D, int RT>
+struct Ring {
+    static constexpr uint32_t kRow = page_code_bytes(FMT, D), kCodes = kTile * kRow;
+    static constexpr uint32_t kBytes = 2 * kCodes + 2 * kTile * page_step_bytes(FMT, D);
+    static constexpr uint32_t kRunLoads = kRow / 64;  // of 16 tokens
+    static constexpr uint32_t kLoads = 4 * kRunLoads + (page_step_bytes(FMT, D) ? 1 : 0);
+    static constexpr uint32_t kRoom = 160 * 1024 / waves_per_simd(D, RT) - 2048;  // the rest of Shared is smaller
+    static constexpr uint32_t kDepth = kRoom / (kWaves * kBytes);
+    static_assert(kDepth >= 1 && kLoads * (kDepth - 1) < 64);
+    static __device__ __forceinline__ uint32_t turn(uint32_t token) {
+        return kRow == 256 ? token & 15 : kRow == 128 ? token >> 1 & 7 : token >> 2 & 3;
+    }
+    uint8_t tile[kWaves][kDepth][kBytes];
+};
+struct NoRing {};
+
 // LDS of a workgroup. (Without its alignment, accesses of four floats come out in pairs.)
-template <int D, int RT>
+template <int FMT, int D, int RT>
 struct Shared {
     alignas(16) float ml[kWaves][RT * 16][2];
-    alignas(16) float os[RT][kWaves][16][D + 4];
+    union {
+        alignas(16) float os[RT][kWaves][16][D + 4];
+        alignas(16) std::conditional_t<through_lds(FMT, RT), Ring<FMT, D, RT>, NoRing> ring;
+    };
     uint32_t sums[kWaves];
     uint32_t found[3];  // sequence, blocks before it, its blocks
 };
+
+// Tiles that are on their way at once.
+template <int FMT, int D, int RT>
+constexpr uint32_t ahead_of() {
+    if constexpr (through_lds(FMT, RT))
+        return Ring<FMT, D, RT>::kDepth;
+    else
+        return 1;
+}
 
 // Over the four lanes that hold a query row (lane % 16), in all of them: rows of 16
 // lanes change places, then halves.
@@ -431,11 +474,12 @@ __device__ __forceinline__ uint32_t scan_threads(uint32_t v, uint32_t* sums, uin
 
 // The share of workgroup w.
 template <int FMT, int D, int RT, int MODE>
-__device__ __forceinline__ void attend_share(const Common& p, const Source& src, uint32_t w, Shared<D, RT>& sh) {
+__device__ __forceinline__ void attend_share(const Common& p, const Source& src, uint32_t w, Shared<FMT, D, RT>& sh) {
     constexpr int KS = D / 32;   // key product steps
     constexpr int NC = D / 16;   // channels of a lane, value products
     constexpr bool HALF = half_products(FMT);
     constexpr bool MANY = MODE == kMany, WIN = MODE != kOneSeesAll;
+    constexpr bool RING = through_lds(FMT, RT);
     constexpr int RE = MANY ? RT : 1;  // exponents taken out of the weights: of a row, where rows see different tokens
     using R = Raw<FMT, D>;
     const uint32_t lane = lane_id(), c = lane & 15, g = lane >> 4;
@@ -666,7 +710,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                         x.vs[i] = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
                     }
                 }
-            } else {
+            } else if constexpr (!RING) {
                 constexpr uint32_t ROW = page_code_bytes(FMT, D);
                 const uint32_t P = 1u << src.page_shift;
 #pragma unroll
@@ -695,23 +739,85 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
 #pragma unroll
                         for (int j = 0; j < 4; ++j) load_words(vb + (4 * g + j) * ROW + c * (ROW / 16), x.v[4 * i + j]);
                         if (FMT != kFmtBf16) {
-                            const float4 a = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(kl + 4 * g) * 4);
-                            const float4 w = *reinterpret_cast<const float4*>(pb + src.steps + (uint64_t)(vl + 4 * g) * 4);
-                            x.ks[4 * i] = a.x;
-                            x.ks[4 * i + 1] = a.y;
-                            x.ks[4 * i + 2] = a.z;
-                            x.ks[4 * i + 3] = a.w;
-                            x.vs[4 * i] = w.x;
-                            x.vs[4 * i + 1] = w.y;
-                            x.vs[4 * i + 2] = w.z;
-                            x.vs[4 * i + 3] = w.w;
+                            take_steps(pb + src.steps + (uint64_t)(kl + 4 * g) * 4, &x.ks[4 * i]);
+                            take_steps(pb + src.steps + (uint64_t)(vl + 4 * g) * 4, &x.vs[4 * i]);
                         }
+                    }
+                }
+            } else {
+                using Way = Ring<FMT, D, RT>;
+                constexpr uint32_t ROW = Way::kRow, STEP = page_step_bytes(FMT, D), N = Way::kRunLoads;
+                const uint32_t P = 1u << src.page_shift;
+                uint8_t* to = sh.ring.tile[wave][it % Way::kDepth];
+                const uint8_t *k[2], *v[2], *steps[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t pg = __builtin_amdgcn_readlane(my_page, (2 * it + i) & 63);
+                    const uint8_t* pb = src.pages + (uint64_t)pg * src.page_bytes;
+                    const uint32_t kl = h * P + (real(t0 + 16 * i) & (P - 1));  // row inside the page
+                    k[i] = pb + (uint64_t)kl * ROW;
+                    v[i] = pb + (uint64_t)(kl + p.H * P) * ROW;
+                    steps[i] = pb + src.steps + (uint64_t)kl * STEP;
+                }
+                // (what was read of the buffer has arrived)
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                uint32_t ko[N], vo[N];
+#pragma unroll
+                for (uint32_t u = 0; u < N; ++u) {
+                    constexpr uint32_t CPR = ROW / 16;  // chunks of a row
+                    ko[u] = lane / CPR * ROW + (lane % CPR ^ Way::turn(u * (64 / CPR) + lane / CPR)) * 16;
+                    vo[u] = lane * 16;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) fetch16<N>(k[i], ko, to + 16 * i * ROW);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) fetch16<N>(v[i], vo, to + Way::kCodes + 16 * i * ROW);
+                // keys' steps of both runs, then values'
+                if constexpr (STEP != 0)
+                    fetch_lane4((lane & 16 ? steps[1] : steps[0]) + (lane & 32 ? (uint64_t)p.H * P * STEP : 0) + lane % 16 * 4,
+                                to + 2 * Way::kCodes);
+            }
+        };
+        // a tile's keys, and its values and steps, out of LDS; it is waited for while `behind` tiles may be on their way
+        const auto take_keys = [&](uint32_t it, uint32_t behind, R& x) {
+            if constexpr (RING) {
+                using Way = Ring<FMT, D, RT>;
+                wait_loads<Way::kLoads, Way::kDepth - 1>(behind);
+                const uint8_t* at = sh.ring.tile[wave][it % Way::kDepth];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (uint32_t s = 0; s < (uint32_t)R::KL; ++s)
+                        x.k[i][s] = *reinterpret_cast<const uint4*>(at + (16 * i + c) * Way::kRow + ((4 * s + g) ^ Way::turn(c)) * 16);
+            }
+        };
+        const auto take_values = [&](uint32_t it, R& x) {
+            if constexpr (RING) {
+                using Way = Ring<FMT, D, RT>;
+                const uint8_t* at = sh.ring.tile[wave][it % Way::kDepth] + Way::kCodes;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        load_words(at + (16 * i + 4 * g + j) * Way::kRow + c * (Way::kRow / 16), x.v[4 * i + j]);
+                    if constexpr (FMT != kFmtBf16) {
+                        const uint8_t* steps = at + Way::kCodes;
+                        take_steps(steps + (16 * i + 4 * g) * 4, &x.ks[4 * i]);
+                        take_steps(steps + (kTile + 16 * i + 4 * g) * 4, &x.vs[4 * i]);
                     }
                 }
             }
         };
         R x;
-        if (begin + wave * kTile < end) load(begin + wave * kTile, 0, x);
+        // the first tiles from `base` on: as many as there is room for
+        constexpr uint32_t kAhead = ahead_of<FMT, D, RT>();
+        const auto load_first = [&](uint32_t base) {
+            const uint32_t stop = FMT == kFmtPool || end - base <= kPageRun ? end : base + kPageRun;
+#pragma unroll
+            for (uint32_t u = 0; u < kAhead; ++u)
+                if (base + wave * kTile + u * kBlock < stop) load(base + wave * kTile + u * kBlock, u, x);
+        };
+        load_first(begin);
         // looked at before anything is written: the loads do not depend on it
         const bool header = FMT != kFmtPool || pool_header_ok(src, p.H, D);
 
@@ -796,11 +902,11 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             const uint32_t t = t0 + (j < 4 ? 0 : 16) + 4 * g + (j & 3);
             return WIN ? t < end && (t < seen.hid0 || t >= seen.hid1) : t < end;
         };
-        // One tile: its loads are in x; those of the next one (at t_next, if
-        // below end) go out as soon as x has been widened. PART: some of its tokens
-        // do not count.
-        const auto tile = [&](auto part, uint32_t t0, uint32_t t_next, uint32_t it, R& x) {
-            const bool PART = part;  // known when this is compiled, but for a window
+        // One tile: its loads are in x, or on their way to LDS; those of a later one (if it lies before `stop`) go
+        // out as soon as x has been widened, or read. PART: some of its tokens do not count.
+        const auto tile = [&](auto part, uint32_t t0, uint32_t stop, uint32_t it, R& x) {
+            constexpr bool PART = decltype(part)::value;
+            take_keys(it, (stop - t0 - 1) / kBlock, x);
             f32x4 s[RT][2];
             {
                 u32x4 kf[2][KS];
@@ -838,6 +944,8 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             // value operands: token pairs of one channel
             u32x4 vf[NC];
             float vs[8], ks[8];
+            take_values(it, x);
+            if (RING && t0 + kAhead * kBlock < stop) load(t0 + kAhead * kBlock, it + kAhead, x);
             if constexpr (FMT == kFmtPool) {
                 constexpr uint32_t l0 = level_bytes(0, 0), l1 = level_bytes(4, 0);
                 constexpr uint32_t h0 = level_bytes(0, 8), h1 = level_bytes(4, 8);
@@ -951,7 +1059,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                     }
                 }
             }
-            if (t_next < end) load(t_next, it + 1, x);
+            if (!RING && t0 + kBlock < stop) load(t0 + kBlock, it + 1, x);
 
             // many new tokens: which of the lane's 8 tokens a row sees
             uint32_t sight[MANY ? RT : 1];
@@ -1056,25 +1164,31 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                         for (int j = 0; j < 4; ++j) bad |= infinite(vf[n][j]);
                 }
                 if (__builtin_expect(PART && __ballot(bad != 0) != 0, 0)) {
+                    u32x4 who[RT];
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        u32x4 who;
+                    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) who[j] = (row_sees(rt, 2 * j) ? 0x3F80u : 0) | (row_sees(rt, 2 * j + 1) ? 0x3F800000u : 0);
+                        for (int j = 0; j < 4; ++j)
+                            who[rt][j] = ((sight[MANY ? rt : 0] >> 2 * j & 1) | (sight[MANY ? rt : 0] >> (2 * j + 1) & 1) << 16) * 0x3F80u;
 #pragma unroll
-                        for (int n = 0; n < NC; ++n) {
-                            u32x4 what;
+                    for (int n = 0; n < NC; ++n) {
+                        u32x4 what;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) what[j] = infinite(vf[n][j]) & 0x3F803F80u;
-                            const f32x4 hit = mfma_bf16(what, who, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t z = vf[n][j];
+                            asm("" : "+v"(z));  // (found again here: kept, it would take 32 registers)
+                            const uint32_t ones = infinite(z) >> 15;
+                            what[j] = ones * 0x3F80u;
+                            vf[n][j] = z & ~(ones * 0xFFFFu);
+                        }
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) {
+                            const f32x4 hit = mfma_bf16(what, who[rt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
                             for (int r = 0; r < 4; ++r) o[rt][n][r] = hit[r] > 0.0f ? __builtin_nanf("") : o[rt][n][r];
                         }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-#pragma unroll
-                    for (int n = 0; n < NC; ++n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) vf[n][j] &= ~infinite(vf[n][j]);
                 }
             }
 #pragma unroll
@@ -1114,20 +1228,19 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             if (base != begin) {  // the next page numbers (the pool needs none: one round)
                 page = load_pages(base);
                 take_pages(base);
-                if (base + wave * kTile < end) load(base + wave * kTile, 0, x);
+                load_first(base);
             }
             const uint32_t stop = FMT == kFmtPool || end - base <= kPageRun ? end : base + kPageRun;
             uint32_t it = 0, t0 = base + wave * kTile;
             if (WIN) {
-                for (; t0 < stop; t0 += kBlock, ++it) {
-                    const bool all = MANY ? t0 + kTile <= stop && t0 + kTile <= all_to && t0 >= all_from
-                                          : t0 + kTile <= stop && (t0 + kTile <= seen.hid0 || t0 >= seen.hid1);
-                    tile(!all, t0, t0 + kBlock < stop ? t0 + kBlock : end, it, x);
-                }
+                // tiles that all rows see the whole of lie side by side, others before and behind them
+                const uint32_t full = all_to < stop ? all_to : stop, masked = all_from < stop ? all_from : stop;
+                for (; t0 < masked; t0 += kBlock, ++it) tile(std::true_type{}, t0, stop, it, x);
+                for (; t0 + kTile <= full; t0 += kBlock, ++it) tile(std::false_type{}, t0, stop, it, x);
+                for (; t0 < stop; t0 += kBlock, ++it) tile(std::true_type{}, t0, stop, it, x);
             } else {
-                for (; t0 + kTile <= stop; t0 += kBlock, ++it)
-                    tile(std::false_type{}, t0, t0 + kBlock < stop ? t0 + kBlock : end, it, x);
-                if (t0 < stop) tile(std::true_type{}, t0, end, it, x);
+                for (; t0 + kTile <= stop; t0 += kBlock, ++it) tile(std::false_type{}, t0, stop, it, x);
+                if (t0 < stop) tile(std::true_type{}, t0, stop, it, x);
             }
             if (FMT == kFmtPool) break;
         }
@@ -1241,7 +1354,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
 template <int FMT, int D, int RT, int MODE>
 __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_kernel(Common p, Source src) {
     fetch_arguments<sizeof(Common) + sizeof(Source)>();
-    __shared__ Shared<D, RT> sh;
+    __shared__ Shared<FMT, D, RT> sh;
     attend_share<FMT, D, RT, MODE>(p, src, blockIdx.x, sh);
 }
 
@@ -1251,8 +1364,8 @@ __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_b
                                                                                            Source tail) {
     fetch_arguments<sizeof(Common) + 2 * sizeof(Source)>();
     __shared__ union {
-        Shared<D, RT> a;
-        Shared<D, 1> b;
+        Shared<kFmtPool, D, RT> a;
+        Shared<FMT, D, 1> b;
     } sh;
     if (blockIdx.x < pool.W)
         attend_share<kFmtPool, D, RT, kOneSeesAll>(p, pool, blockIdx.x, sh.a);

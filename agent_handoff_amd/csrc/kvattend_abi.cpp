@@ -446,8 +446,8 @@ int kvpage_attend_window(const kvc_pages* spec, const void* pages, size_t pages_
 size_t kvpage_attend_prompt_workspace_bytes(const kvc_pages* spec, uint32_t n_seqs, uint32_t n_tokens,
                                             uint32_t q_heads, uint32_t max_tokens, uint32_t window, uint32_t sinks) {
     if (!prompt_ok(spec, n_seqs, n_tokens, q_heads) || max_tokens >= (1u << 31)) return 0;
-    return (size_t)kvc::prompt_plan(n_seqs, n_tokens, spec->num_kv_heads, q_heads, spec->head_dim, spec->format, max_tokens,
-                                    window, sinks).room;
+    return (size_t)kvc::prompt_plan(n_seqs, n_tokens, spec->num_kv_heads, q_heads, spec->head_dim, max_tokens, window,
+                                    sinks).room;
 }
 
 int kvpage_attend_prompt(const kvc_pages* spec, const void* pages, size_t pages_bytes, uint32_t n_seqs,
@@ -463,7 +463,7 @@ int kvpage_attend_prompt(const kvc_pages* spec, const void* pages, size_t pages_
     const int rc = check_tail(spec, pages, pages_bytes, n_seqs, table, table_cols, table_stride, lens);
     if (rc != KVC_OK) return rc;
     const uint32_t d = spec->head_dim;
-    const kvc::PromptPlan plan = kvc::prompt_plan(n_seqs, n_tokens, spec->num_kv_heads, q_heads, d, spec->format,
+    const kvc::PromptPlan plan = kvc::prompt_plan(n_seqs, n_tokens, spec->num_kv_heads, q_heads, d,
                                                   (uint64_t)table_cols * spec->page_tokens, window, sinks);
     if (ws_bytes < plan.bytes) return KVC_E_SIZE;
     View qv, ov;

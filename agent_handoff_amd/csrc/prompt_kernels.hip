@@ -14,6 +14,7 @@
 // gives four tokens of one channel to a lane, so V stays in LDS as it is in memory.
 #include "attend.h"
 #include "kernels_common.h"
+#include "lds_fetch.h"
 #include "page_codes.h"
 
 #include <type_traits>
@@ -39,7 +40,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-#define KVC_LDS __attribute__((address_space(3)))
 
 struct PromptParams {
     RowsDev q, out;
@@ -97,34 +97,6 @@ __device__ __forceinline__ uint32_t place_k(uint32_t token, uint32_t chunk) {
 template <int D>
 __device__ __forceinline__ uint32_t place_v(uint32_t token, uint32_t chunk) {
     return token * (2 * D) + ((chunk ^ (D == 128 ? (token & 3) << 2 : (token >> 1 & 1) << 2)) << 4);
-}
-
-// N times 16 bytes of each lane from memory to LDS: from base (the same in all lanes) + off[u] + 1024 u to lds + 1024 u
-// + 16 * lane. Written out: behind the builtin the compiler waits for it before the next read of LDS, of whichever
-// buffer. Here it knows of nothing; arrive() waits. (No register is written but M0, which nothing else here uses; what
-// reads it comes a wait state behind its write.)
-template <int N>
-__device__ __forceinline__ void fetch16(const uint8_t* base, const uint32_t (&off)[N], uint8_t* lds) {
-    const uint64_t from = (uint64_t)base;
-    const uint64_t at = (uint64_t)wave_uniform((uint32_t)(from >> 32)) << 32 | wave_uniform((uint32_t)from);
-    const uint32_t to = wave_uniform((uint32_t)(uint64_t)(KVC_LDS uint8_t*)lds);
-    static_assert(N == 2 || N == 4);
-    if constexpr (N == 4)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
-                     "global_load_lds_dwordx4 %2, %1\n\t"
-                     "global_load_lds_dwordx4 %3, %1 offset:1024\n\t"
-                     "global_load_lds_dwordx4 %4, %1 offset:2048\n\t"
-                     "global_load_lds_dwordx4 %5, %1 offset:3072"
-                     :
-                     : "s"(to), "s"(at), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3])
-                     : "memory");
-    else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
-                     "global_load_lds_dwordx4 %2, %1\n\t"
-                     "global_load_lds_dwordx4 %3, %1 offset:1024"
-                     :
-                     : "s"(to), "s"(at), "v"(off[0]), "v"(off[1])
-                     : "memory");
 }
 
 // LDS: tile j of keys, and of values, is in buffer (j - the share's first) % 4. The steps of both (8 bits) come with the keys and are read
@@ -866,17 +838,16 @@ hipError_t launch_of(uint32_t format, const PromptParams& p, uint32_t grid, hipS
 constexpr uint64_t kPlaces = 512;
 // Few new tokens of each sequence (their rows, times the heads that share a kv head, in the mean of all): a call is then
 // memory's, and the kernel for one new token takes them, 32 rows at a time. 15 sequences behind 8192 tokens (8 kv heads of
-// 128), that kernel and the one here, us: 32 rows e4m3 78 and 138, 64 rows 109 and 152, 4 bits 89 and 130, bf16 176 and
-// 148, 96 rows e4m3 153 and 166, 128 rows 188 and 181; one sequence of 32 rows behind 4000 tokens 17 and 41, behind 400
-// 14 and 22, and, with a second launch that joins what it shared out, behind 100 13 and 12 (15 sequences 20 and 13).
-// (Rows that belong to no sequence count as well: a quarter more.)
-constexpr uint64_t few_rows(uint32_t format) { return format == kPageBf16 ? 40 : 80; }
+// 128), that kernel and the one here, us: 32 rows e4m3 66 and 138, 64 rows 99 and 152, bf16 148 and 148; one sequence of 32
+// rows behind 4000 tokens 17 and 41, behind 400 14 and 22, and, with a second launch that joins what it shared out,
+// behind 100 13 and 12 (15 sequences 20 and 13). (Rows that belong to no sequence count as well: a quarter more.)
+constexpr uint64_t kFewRows = 80;
 constexpr uint64_t kFewTokens = 256;
 
 }  // namespace
 
-PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint32_t format,
-                       uint64_t max_tokens, uint32_t window, uint32_t sinks) {
+PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens,
+                       uint32_t window, uint32_t sinks) {
     const uint64_t group = Hq / H;
     PromptPlan a{};
     a.blocks = n_tokens * group / kRows + n_seqs;
@@ -889,7 +860,7 @@ PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t 
     const uint64_t each = (uint64_t)kRows * (d + 2) * 4;
     if (a.more) a.bytes = align_up(2 * a.more * H * each, 256);
     if (can) a.room = align_up(2 * ((kPlaces + H - 1) / H) * H * each, 256);
-    const uint64_t rows = n_tokens * group, most = few_rows(format) * n_seqs, few = rows < most ? rows : most;
+    const uint64_t rows = n_tokens * group, most = kFewRows * n_seqs, few = rows < most ? rows : most;
     const AttendPlan many = many_attend_plan(n_seqs, n_tokens, H, Hq, d, max_tokens, window, sinks);
     // (what its kernel counts with 32 bits, wherever the sequences start)
     a.few = rows <= most && max_tokens > kFewTokens && (uint64_t)n_seqs * (rows / 16 + 1) * (max_tokens / 128 + 1) < 1ull << 31;
