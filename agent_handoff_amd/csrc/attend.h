@@ -154,8 +154,8 @@ hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
 constexpr uint32_t kPromptRows = 64;  // of the smallest block
 struct PromptPlan {
     bool few;         // few new tokens of each sequence: taken by launch_attend
-    uint32_t more;    // shares that a kv head's blocks may have beyond one each
-    uint64_t blocks;
+    uint32_t shares;  // workgroups that share out a kv head's tiles evenly (0: each takes a block)
+    uint64_t blocks;  // of a kv head, at most
     uint64_t bytes;   // of the workspace: what the call uses,
     uint64_t room;    // and what serves every smaller call too
 };

@@ -30,6 +30,7 @@ constexpr uint32_t kRun = 16;      // tokens that lie in one page: a wave fetche
 constexpr float kSlack = 3.0f;     // m moves when a tile's maximum passes it by this (powers of two)
 constexpr int kWeightExp = 12;     // binary16 weights: the largest stays below 2^(12 + 3 + 1)
 constexpr uint32_t kMinShare = 16;  // tiles of a share, at least
+constexpr uint32_t kBegin = 6;      // to begin and end a block takes as long as so many tiles
 constexpr float kNegInf = -__builtin_inff();
 constexpr bool half_products(int fmt) { return fmt == kPageInt8 || fmt == kPageFp8; }
 
@@ -51,9 +52,10 @@ struct PromptParams {
     uint32_t n, rows, H, Hq, group;
     uint32_t table_cols, num_pages, page_shift;
     uint32_t window, sinks;
-    uint32_t more;  // workgroups that a kv head has for shares beyond one of each block (0: no block is cut up)
+    uint32_t shares;  // of the tiles of a kv head, one a workgroup (0: a block a workgroup, none is cut up)
     float scale_log2;
-    float* part;  // of each share of a block that is cut up: sums [rows of a block][d], then {m, l} of each row
+    float* part;  // of a share's part of a block that is cut up: sums [rows of a block][d], then {m, l} of each row
+    uint2* info;  // of each block: its first share and its parts, 0 where it is not cut up
 };
 
 template <int FMT>
@@ -127,109 +129,222 @@ __device__ __forceinline__ Range range_of(const PromptParams& p, int32_t pos_lo,
     return r;
 }
 
-// A sequence's new tokens and length, and the positions of the first and last row of one of its blocks.
+// A sequence's new tokens and length. Sequences are taken from the last to the first (`i` counts them so), and a
+// sequence's blocks too, so that the longest of a prompt come first.
 struct Sequence {
     uint32_t b, first, m;  // first: its first row
     int32_t len;
-    uint32_t blocks, shares;
+    uint32_t blocks;
     __device__ __forceinline__ int32_t pos_of(uint32_t row, uint32_t group) const { return len - (int32_t)m + (int32_t)(row / group); }
 };
-
-// Which item of work (`at`, of one kv head) this is: sequence, block, share, and the place of its partial results if
-// the sequence's blocks are cut up. Every workgroup finds that for itself, a lane a sequence. Sequences and their blocks
-// are taken from the last to the first, so that the longest of a prompt come first. Blocks of a sequence are cut into
-// so many shares that none has more than `each` tiles, where all of them together have at most `more` shares
-// beyond one of each block.
-struct Item {
-    bool found;
-    Sequence s;
-    uint32_t block, share;
-    uint32_t slot;  // of the block's first share
-};
-template <bool JOIN>
-__device__ __forceinline__ Item item_of(const PromptParams& p, uint32_t at) {
-    const uint32_t lane = lane_id();
-    Item x{};
-    const auto sequence = [&](uint32_t base, uint32_t& tiles) {
-        Sequence s{};
-        tiles = 0;
-        if (base + lane >= p.n) return s;
-        s.b = p.n - 1 - base - lane;
-        const int32_t a = p.starts[s.b], e = p.starts[s.b + 1], given = p.lens[s.b];
-        const bool bad = a < 0 || e < a || (uint32_t)e > p.rows;
-        const uint32_t most = p.table_cols << p.page_shift;
-        s.len = given < 0 ? 0 : (uint32_t)given > most ? (int32_t)most : given;
-        if (!JOIN && p.status && (bad || s.len != given))
-            atomicOr(p.status, (bad ? kDevBadStart : 0) | (s.len != given ? kDevBadLength : 0));
-        s.first = a;
-        s.m = bad ? 0 : e - a;
-        s.blocks = (s.m * p.group + kRows - 1) / kRows;
-        s.shares = 1;
-        if (p.more && s.blocks) tiles = range_of(p, s.pos_of((s.blocks - 1) * kRows, p.group), s.len - 1).tiles;
-        return s;
-    };
-    uint32_t tiles, each = 0;
-    Sequence s = sequence(0, tiles);
-    if (p.more) {
-        uint64_t all = 0;
-        for (uint32_t base = 0;;) {
-            // (below 2^36: fewer than 2^11 blocks, of 2^25 tiles)
-            const uint64_t t = (uint64_t)s.blocks * tiles;
-            const uint32_t low = scan_lanes((uint32_t)t & 4095), high = scan_lanes((uint32_t)(t >> 12));
-            all += (uint32_t)__builtin_amdgcn_readlane(low, 63) + ((uint64_t)(uint32_t)__builtin_amdgcn_readlane(high, 63) << 12);
-            base += kWave;
-            if (base >= p.n) break;
-            s = sequence(base, tiles);
-        }
-        all = (all + p.more - 1) / p.more;
-        each = all < kMinShare ? kMinShare : all > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)all;
-        if (p.n > kWave) s = sequence(0, tiles);
-    }
-    uint32_t before = 0, slots = 0;
-    for (uint32_t base = 0;;) {
-        if (p.more && tiles) s.shares = (tiles - 1) / each + 1;
-        const uint32_t items = s.blocks * s.shares, mine = JOIN ? s.blocks : items;
-        const uint32_t up = scan_lanes(mine), up_slots = scan_lanes(s.shares > 1 ? items : 0);
-        const uint32_t all = __builtin_amdgcn_readlane(up, 63);
-        if (at < before + all) {
-            const int l = __builtin_popcountll(__ballot(before + up <= at));
-            const auto of = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane(v, l); };
-            x.found = true;
-            x.s = Sequence{of(s.b), of(s.first), of(s.m), (int32_t)of(s.len), of(s.blocks), of(s.shares)};
-            const uint32_t back = before + of(up) - 1 - at;  // from the sequence's last item
-            x.block = JOIN ? back : back / x.s.shares;
-            x.share = JOIN ? 0 : back % x.s.shares;
-            x.slot = slots + of(up_slots) - x.s.blocks * x.s.shares + x.block * x.s.shares;
-            return x;
-        }
-        before += all;
-        slots += __builtin_amdgcn_readlane(up_slots, 63);
-        base += kWave;
-        if (base >= p.n) return x;
-        s = sequence(base, tiles);
-    }
+template <bool REPORT>
+__device__ __forceinline__ Sequence sequence_at(const PromptParams& p, uint32_t i) {
+    Sequence s{};
+    if (i >= p.n) return s;
+    s.b = p.n - 1 - i;
+    const int32_t a = p.starts[s.b], e = p.starts[s.b + 1], given = p.lens[s.b];
+    const bool bad = a < 0 || e < a || (uint32_t)e > p.rows;
+    const uint32_t most = p.table_cols << p.page_shift;
+    s.len = given < 0 ? 0 : (uint32_t)given > most ? (int32_t)most : given;
+    if (REPORT && p.status && (bad || s.len != given))
+        atomicOr(p.status, (bad ? kDevBadStart : 0) | (s.len != given ? kDevBadLength : 0));
+    s.first = a;
+    s.m = bad ? 0 : e - a;
+    s.blocks = (s.m * p.group + kRows - 1) / kRows;
+    return s;
+}
+__device__ __forceinline__ Sequence uniform(const Sequence& s, int lane) {
+    const auto of = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane(v, lane); };
+    return Sequence{of(s.b), of(s.first), of(s.m), (int32_t)of(s.len), of(s.blocks)};
+}
+// Tiles that a block sees; one that sees none has an empty one, so that its rows are written.
+__device__ __forceinline__ uint32_t tiles_of(const PromptParams& p, const Sequence& s, uint32_t block) {
+    const uint32_t row0 = block * kRows, left = s.m * p.group - row0;
+    const uint32_t t = range_of(p, s.pos_of(row0, p.group), s.pos_of(row0 + (left < kRows ? left : kRows) - 1, p.group)).tiles;
+    return t ? t : 1;
 }
 
-template <int FMT, int D>
+// Where few blocks would leave workgroups idle, or wait for the longest, all tiles of a kv head are shared out evenly: the
+// blocks stand in a row, and each workgroup takes as many tiles as the others, from where the one before it ends. What
+// blocks of a sequence see grows evenly, so the row has the last with the first, the last but one with the second, ...:
+// each such pair counts as long as the first pair is (the one in the middle, of an odd number, half as long; with what
+// it takes to begin a block), and how far into a pair a share begins or ends is taken in proportion.
+struct Pairs {
+    uint32_t len, last;  // of a pair, and of the last one
+    uint64_t all;        // of all
+};
+__device__ __forceinline__ Pairs pairs_of(const PromptParams& p, const Sequence& s) {
+    Pairs x{};
+    if (s.blocks == 0) return x;
+    x.len = tiles_of(p, s, 0) + tiles_of(p, s, s.blocks - 1) + 2 * kBegin;
+    x.last = s.blocks % 2 ? (x.len + 1) / 2 : x.len;
+    x.all = (uint64_t)((s.blocks - 1) / 2) * x.len + x.last;
+    return x;
+}
+// A pair's blocks and their tiles (`low` of a middle one: none).
+struct Pair {
+    uint32_t high, low, tiles_high, tiles_low, len;
+    // tiles up to `at` of the pair's length
+    __device__ __forceinline__ uint32_t tiles_to(uint32_t at) const {
+        uint64_t q;
+        uint32_t r;
+        divmod_u64((uint64_t)at * (tiles_high + tiles_low), len, q, r);
+        return (uint32_t)q;
+    }
+};
+__device__ __forceinline__ Pair pair_at(const PromptParams& p, const Sequence& s, const Pairs& x, uint32_t q) {
+    Pair r;
+    r.high = s.blocks - 1 - q;
+    r.low = q;
+    r.tiles_high = tiles_of(p, s, r.high);
+    r.tiles_low = r.low < r.high ? tiles_of(p, s, r.low) : 0;
+    r.len = q == (s.blocks - 1) / 2 ? x.last : x.len;
+    return r;
+}
+
+// Over the wave's lanes up to this one, of numbers below 2^50.
+__device__ __forceinline__ uint64_t scan_lanes64(uint64_t v) {
+    return scan_lanes((uint32_t)v & 0xFFFFF) + ((uint64_t)scan_lanes((uint32_t)(v >> 20)) << 20);
+}
+__device__ __forceinline__ uint64_t read_lane64(uint64_t v, int lane) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(v >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((uint32_t)v, lane);
+}
+// The first sequence with which the sum of `of` passes `at`, and the sums before it: a wave finds it, a lane a sequence.
+// `at` comes from the sum of all, which is known at once where the lanes hold every sequence.
+struct Found {
+    bool any;
+    Sequence s;
+    uint32_t i;
+    uint64_t at, before;
+};
+template <class F, class A>
+__device__ __forceinline__ Found find_sequence(const PromptParams& p, F of, A place) {
+    uint64_t all = 0, mine = 0, up = 0;
+    Sequence s{};
+    for (uint32_t base = 0; base < p.n; base += kWave) {
+        s = sequence_at<true>(p, base + lane_id());
+        mine = of(s);
+        up = scan_lanes64(mine);
+        all += read_lane64(up, 63);
+    }
+    const uint64_t at = place(all);
+    if (at >= all) return Found{};
+    uint64_t before = 0;
+    for (uint32_t base = 0;; base += kWave) {
+        if (p.n > kWave) {
+            s = sequence_at<false>(p, base + lane_id());
+            mine = of(s);
+            up = scan_lanes64(mine);
+        }
+        const uint64_t these = read_lane64(up, 63);
+        if (at < before + these) {
+            const int l = __builtin_popcountll(__ballot(before + up <= at));
+            return Found{true, uniform(s, l), base + l, at, before + read_lane64(up - mine, l)};
+        }
+        before += these;
+    }
+}
+// A block's place in the list of all (those of the sequences before it, rounded up one by one, are no more).
+__device__ __forceinline__ uint32_t first_block(const PromptParams& p, uint32_t b, uint32_t first) { return first * p.group / kRows + b; }
+
+// SHARED: the tiles of all blocks are shared out.
+template <int FMT, int D, bool SHARED>
 __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(PromptParams p) {
     fetch_arguments<sizeof(PromptParams)>();
     constexpr bool HALF = half_products(FMT);
     constexpr int KS = D / 16, CB = D / 32;  // steps of a key product, blocks of channels
     __shared__ Tiles<FMT, D> sh;
-    const uint32_t lane = lane_id(), wave = wave_uniform(threadIdx.x / kWave);
+    const uint32_t h = blockIdx.x % p.H, share = blockIdx.x / p.H;
+    Sequence sq;
+    Pairs pairs{};
+    uint32_t index = 0, block = 0, half = 0;
+    uint64_t at = 0, left = 0;  // where the share is in its sequence's row of blocks, and how much of it is left
+    uint64_t each = 0;
+    if constexpr (SHARED) {
+        const Found f = find_sequence(p, [&](const Sequence& s) { return pairs_of(p, s).all; }, [&](uint64_t all) {
+            uint32_t r;
+            divmod_u64(all + p.shares - 1, p.shares, each, r);
+            each = each < kMinShare ? kMinShare : each;
+            left = all - share * each < each ? all - share * each : each;
+            return share * each;
+        });
+        if (!f.any) return;
+        sq = f.s;
+        index = f.i;
+        at = f.at - f.before;
+        pairs = pairs_of(p, sq);
+    } else {
+        const Found f = find_sequence(p, [](const Sequence& s) { return (uint64_t)s.blocks; }, [&](uint64_t) { return share; });
+        if (!f.any) return;
+        sq = f.s;
+        block = f.s.blocks - 1 - (share - (uint32_t)f.before);
+    }
+    for (bool again = false;; again = true) {
+    uint32_t part0 = 0, part1 = 0xFFFFFFFFu;  // tiles of the block, of
+    uint32_t tiles = 0;
+    if constexpr (SHARED) {
+        if (left == 0) return;
+        if (at == pairs.all) {
+            do sq = uniform(sequence_at<false>(p, ++index), 0);
+            while (sq.blocks == 0);
+            pairs = pairs_of(p, sq);
+            at = 0;
+        }
+        uint64_t q;
+        uint32_t a;
+        divmod_u64(at, pairs.len, q, a);
+        const Pair x = pair_at(p, sq, pairs, (uint32_t)q);
+        const uint32_t e = x.len - a < left ? x.len : a + (uint32_t)left, from = x.tiles_to(a), to = x.tiles_to(e);
+        if (half == 0) {
+            block = x.high;
+            tiles = x.tiles_high;
+            part0 = from < tiles ? from : tiles;
+            part1 = to < tiles ? to : tiles;
+        } else {
+            block = x.low;
+            tiles = x.tiles_low;
+            part0 = from > x.tiles_high ? from - x.tiles_high : 0;
+            part1 = to > x.tiles_high ? to - x.tiles_high : 0;
+        }
+        if (part0 == 0 && part1 != 0 && threadIdx.x == 0) {
+            // the share that begins a block counts the shares that go on with it
+            const uint32_t all = half ? x.tiles_high + x.tiles_low : x.tiles_high;
+            uint64_t end = e;
+            uint32_t parts = part1 < tiles ? 1 : 0;
+            for (uint32_t reached = to; reached < all; ++parts) {
+                end += each;
+                reached = end < x.len ? x.tiles_to((uint32_t)end) : x.tiles_high + x.tiles_low;
+            }
+            p.info[(uint64_t)(first_block(p, sq.b, sq.first) + block) * p.H + h] = make_uint2(share, parts);
+        }
+        half ^= 1;
+        if (half == 0) {
+            at += e - a;
+            left -= e - a;
+        }
+        if (part0 >= part1) {
+            // a share too short for a tile of a block that it is inside of
+            if (part0 > 0 && part0 < tiles) {
+                float* to = p.part + ((uint64_t)(2 * share) * p.H + h) * (kRows * (D + 2)) + kRows * D;
+                if (threadIdx.x < kRows) *reinterpret_cast<float2*>(to + 2 * threadIdx.x) = make_float2(kNegInf, 0.0f);
+            }
+            continue;
+        }
+    }
+    const bool cut = SHARED && part1 - part0 < tiles;
+    if (again) __syncthreads();  // the block before is out of LDS
+    // (new to the compiler for each block, or it would keep whatever follows from them alone: 40 registers)
+    uint32_t thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));
+    const uint32_t lane = thread % kWave, wave = wave_uniform(thread / kWave);
     const uint32_t col = lane & 31, hi = lane >> 5;
-
-    const uint32_t h = blockIdx.x % p.H;
-    const Item item = item_of<false>(p, blockIdx.x / p.H);
-    if (!item.found) return;
-    const Sequence& sq = item.s;
-    const uint32_t row0 = item.block * kRows;
+    const uint32_t row0 = block * kRows;
     const uint32_t nrows = sq.m * p.group - row0 < kRows ? sq.m * p.group - row0 : kRows;
     const int32_t block_lo = sq.pos_of(row0, p.group);
     const Range see = range_of(p, block_lo, sq.pos_of(row0 + nrows - 1, p.group));
     const auto start_of = [&](uint32_t i) { return (i < see.tiles0 ? i : i - see.tiles0 + see.from) * kTokens; };
-    const uint32_t j0 = (uint32_t)((uint64_t)see.tiles * item.share / sq.shares),
-                   j1 = (uint32_t)((uint64_t)see.tiles * (item.share + 1) / sq.shares);
+    const uint32_t j0 = part0, j1 = part1 < see.tiles ? part1 : see.tiles;
 
     // ---- this lane's row; a lane without one takes the block's last, which is not written
     const uint32_t my_row = wave * 32 + col;
@@ -421,9 +536,9 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(
     const uint32_t second = wave / 2;  // the wave's run is of the second of two tiles
     ask(0, first, 0);
     ask(1, first, 0);
-    if (threadIdx.x < 8) sh.odd[threadIdx.x] = 0;
+    if (thread < 8) sh.odd[thread] = 0;
     // the first turn adds the values of a tile before the first, with weights of 0
-    for (uint32_t at = threadIdx.x * 16; at < Tiles<FMT, D>::kBytes; at += kWaves * kWave * 16)
+    for (uint32_t at = thread * 16; at < Tiles<FMT, D>::kBytes; at += kWaves * kWave * 16)
         *reinterpret_cast<u32x4*>(sh.kv[1][3] + at) = u32x4{0, 0, 0, 0};
 
     // ---- queries
@@ -544,12 +659,12 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(
         }
         __syncthreads();
         if constexpr (HALF) {
-            if (threadIdx.x < kTokens) {
-                float& x = sh.steps[1][j & 7][threadIdx.x];
+            if (thread < kTokens) {
+                float& x = sh.steps[1][j & 7][thread];
                 x = __builtin_isnan(x) ? 0.0f : x;
             }
         } else {
-            for (uint32_t at = threadIdx.x * 16; at < Tiles<FMT, D>::kBytes; at += kWaves * kWave * 16) {
+            for (uint32_t at = thread * 16; at < Tiles<FMT, D>::kBytes; at += kWaves * kWave * 16) {
                 u32x4 y = *reinterpret_cast<u32x4*>(vt + at);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -756,17 +871,19 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(
 #pragma unroll
         for (int n = 0; n < CB; ++n) o[n] *= down;
     }
-    if (sq.shares > 1) {
-        if (!has_row) return;
-        float* to = p.part + ((uint64_t)(item.slot + item.share) * p.H + h) * (kRows * (D + 2));
+    if (cut) {
+        // a share's first piece continues a block, or its last begins one
+        if (has_row) {
+            float* to = p.part + ((uint64_t)(2 * share + (part0 == 0)) * p.H + h) * (kRows * (D + 2));
 #pragma unroll
-        for (int n = 0; n < CB; ++n)
+            for (int n = 0; n < CB; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<f32x4*>(to + my_row * D + 32 * n + 8 * j + 4 * hi) =
-                    f32x4{o[n][4 * j], o[n][4 * j + 1], o[n][4 * j + 2], o[n][4 * j + 3]};
-        if (hi == 0) *reinterpret_cast<float2*>(to + kRows * D + 2 * my_row) = make_float2(m, l);
-        return;
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<f32x4*>(to + my_row * D + 32 * n + 8 * j + 4 * hi) =
+                        f32x4{o[n][4 * j], o[n][4 * j + 1], o[n][4 * j + 2], o[n][4 * j + 3]};
+            if (hi == 0) *reinterpret_cast<float2*>(to + kRows * D + 2 * my_row) = make_float2(m, l);
+        }
+        continue;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     if (p.lse && has_row && hi == 0) p.lse[(uint64_t)(sq.first + tok) * p.Hq + qh] = (m + log2f(l)) * 0.69314718055994531f;
@@ -790,47 +907,73 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(
             *reinterpret_cast<u32x4*>(p.out.data + (uint64_t)(sq.first + to_tok) * p.out.ts + (uint64_t)to_head * p.out.hs + 8 * piece) =
                 *reinterpret_cast<const u32x4*>(mine + r * LINE + 16 * piece);
     }
+    if constexpr (!SHARED) return;
+    }
 }
 
-// Joins the shares of a block's rows: a workgroup a block, four channels a lane.
+// Joins what shares have of a block that is cut up: a workgroup some of its rows, four channels a lane.
+constexpr uint32_t kJoinRows = 16;
 template <int D>
 __global__ __launch_bounds__(kBlockThreads) void prompt_join_kernel(PromptParams p) {
     fetch_arguments<sizeof(PromptParams)>();
-    constexpr uint32_t LPR = D / 4, RPB = kBlockThreads / LPR;
-    const uint32_t h = blockIdx.x % p.H;
-    const Item item = item_of<true>(p, blockIdx.x / p.H);
-    if (!item.found || item.s.shares == 1) return;
-    const uint32_t row0 = item.block * kRows, all = item.s.m * p.group;
-    const uint32_t nrows = all - row0 < kRows ? all - row0 : kRows, shares = item.s.shares;
-    const uint64_t each = (uint64_t)p.H * (kRows * (D + 2));
-    const float* from = p.part + ((uint64_t)item.slot * p.H + h) * (kRows * (D + 2));
+    constexpr uint32_t LPR = D / 4, RPB = kBlockThreads / LPR, GROUPS = kRows / kJoinRows;
+    const uint32_t h = blockIdx.x % p.H, group = blockIdx.x / p.H % GROUPS, place = blockIdx.x / p.H / GROUPS;
+    const u32x2 info = *(const __attribute__((address_space(4))) u32x2*)(uint64_t)(p.info + (uint64_t)place * p.H + h);
+    // the last sequence whose blocks' places begin at or before this one: of 64 that are evenly apart, then of those between two
+    uint32_t b = 0, range = p.n;
+    for (;;) {
+        const uint32_t each = (range + kWave - 1) / kWave, at = lane_id() * each;
+        const bool before = at < range && first_block(p, b + at, p.starts[b + at]) <= place;
+        const uint32_t k = __builtin_popcountll(__ballot(before));
+        if (k == 0) return;
+        b += (k - 1) * each;
+        range = range - (k - 1) * each < each ? range - (k - 1) * each : each;
+        if (range <= 1) break;
+    }
+    const Sequence sq = uniform(sequence_at<false>(p, p.n - 1 - b), 0);
+    const uint32_t block = place - first_block(p, b, sq.first), row0 = block * kRows + group * kJoinRows, all = sq.m * p.group;
+    if (block >= sq.blocks || row0 >= all) return;
+    const uint32_t parts = info.y;
+    if (parts == 0) return;  // written already
+    // part 0 is the last piece of its share, the others the first of theirs
+    const auto part_of = [&](uint32_t i) {
+        return p.part + ((uint64_t)(i ? 2 * (info.x + i) : 2 * info.x + 1) * p.H + h) * (kRows * (D + 2));
+    };
     const uint32_t c = threadIdx.x % LPR * 4;
-    for (uint32_t r = threadIdx.x / LPR; r < nrows; r += RPB) {
+#pragma unroll
+    for (uint32_t k = 0; k < kJoinRows / RPB; ++k) {
+        const uint32_t r = group * kJoinRows + k * RPB + threadIdx.x / LPR, row = block * kRows + r;
+        if (row >= all) return;
         float M = kNegInf;
-        for (uint32_t s = 0; s < shares; ++s) M = fmaxf(M, from[s * each + kRows * D + 2 * r]);
+#pragma unroll 4
+        for (uint32_t i = 0; i < parts; ++i) M = fmaxf(M, part_of(i)[kRows * D + 2 * r]);
         const float Mu = M == kNegInf ? 0.0f : M;
         float total = 0.0f;
         f32x4 y = 0.0f;
-        for (uint32_t s = 0; s < shares; ++s) {
-            const float2 ml = *reinterpret_cast<const float2*>(from + s * each + kRows * D + 2 * r);
-            const float a = __builtin_amdgcn_exp2f(ml.x - Mu);
-            total = fmaf(ml.y, a, total);
-            y += *reinterpret_cast<const f32x4*>(from + s * each + r * D + c) * a;
+#pragma unroll 4
+        for (uint32_t i = 0; i < parts; ++i) {
+            const float* from = part_of(i);
+            const float2 ml = *reinterpret_cast<const float2*>(from + kRows * D + 2 * r);
+            f32x4 v = *reinterpret_cast<const f32x4*>(from + r * D + c);
+            const float w = __builtin_amdgcn_exp2f(ml.x - Mu);
+            if (ml.x == kNegInf) v = 0.0f;  // (a part without tiles has no sums)
+            total = fmaf(ml.y, w, total);
+            y += v * w;
         }
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-        const uint32_t tok = item.s.first + (row0 + r) / p.group, qh = h * p.group + (row0 + r) % p.group;
+        const uint32_t tok = sq.first + row / p.group, qh = h * p.group + row % p.group;
         *reinterpret_cast<u32x2*>(p.out.data + (uint64_t)tok * p.out.ts + (uint64_t)qh * p.out.hs + c) =
             u32x2{pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv)};
         if (p.lse && c == 0) p.lse[(uint64_t)tok * p.Hq + qh] = (M + log2f(total)) * 0.69314718055994531f;
     }
 }
 
-template <int D>
+template <int D, bool SHARED>
 hipError_t launch_of(uint32_t format, const PromptParams& p, uint32_t grid, hipStream_t stream) {
-    const auto f = format == kPageBf16   ? prompt_kernel<kPageBf16, D>
-                   : format == kPageInt8 ? prompt_kernel<kPageInt8, D>
-                   : format == kPageFp8  ? prompt_kernel<kPageFp8, D>
-                                         : prompt_kernel<kPageFp4, D>;
+    const auto f = format == kPageBf16   ? prompt_kernel<kPageBf16, D, SHARED>
+                   : format == kPageInt8 ? prompt_kernel<kPageInt8, D, SHARED>
+                   : format == kPageFp8  ? prompt_kernel<kPageFp8, D, SHARED>
+                                         : prompt_kernel<kPageFp4, D, SHARED>;
     return launch_kernel(f, dim3(grid), dim3(kWaves * kWave), stream, p);
 }
 
@@ -855,11 +998,13 @@ PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t 
     // with a window, a block's rows see the tokens of one row and as many more as the block has tokens
     const uint64_t seen = window ? seen_tokens(max_tokens, (uint64_t)window + kRows / group, sinks) : max_tokens;
     const bool can = seen > kMinShare * kTokens;
-    if (can && H * a.blocks < 4 * kPlaces) a.more = (uint32_t)((kPlaces + H - 1) / H);
-    // a block that is cut up has two shares at least: no more than 2 more of them
-    const uint64_t each = (uint64_t)kRows * (d + 2) * 4;
-    if (a.more) a.bytes = align_up(2 * a.more * H * each, 256);
-    if (can) a.room = align_up(2 * ((kPlaces + H - 1) / H) * H * each, 256);
+    const uint64_t shares = (kPlaces + H - 1) / H;
+    if (can && H * a.blocks < 4 * kPlaces) a.shares = (uint32_t)shares;
+    // a share leaves two parts of blocks at most
+    const uint64_t parts = align_up(2 * shares * H * (kRows * (d + 2) * 4), 256);
+    const uint64_t info = align_up(a.blocks * H * 8, 256);
+    if (a.shares) a.bytes = parts + info;
+    if (can) a.room = parts + align_up((a.blocks < 4 * kPlaces / H + 1 ? a.blocks : 4 * kPlaces / H + 1) * H * 8, 256);
     const uint64_t rows = n_tokens * group, most = kFewRows * n_seqs, few = rows < most ? rows : most;
     const AttendPlan many = many_attend_plan(n_seqs, n_tokens, H, Hq, d, max_tokens, window, sinks);
     // (what its kernel counts with 32 bits, wherever the sequences start)
@@ -911,14 +1056,18 @@ hipError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& plan, hip
     p.page_shift = 31 - __builtin_clz(lay.P);
     p.window = a.tail.window;
     p.sinks = a.tail.sinks;
-    p.more = plan.more;
+    p.shares = plan.shares;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.part = static_cast<float*>(a.ws);
-    const uint32_t grid = (uint32_t)((plan.blocks + plan.more) * a.H);
-    const hipError_t e = a.d == 64 ? launch_of<64>(lay.format, p, grid, stream) : launch_of<128>(lay.format, p, grid, stream);
-    if (e != hipSuccess || !plan.more) return e;
+    // behind the parts
+    p.info = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.ws) + align_up(2ull * plan.shares * a.H * (kRows * (a.d + 2) * 4), 256));
+    const uint32_t grid = (uint32_t)((plan.shares ? plan.shares : plan.blocks) * a.H);
+    if (!plan.shares)
+        return a.d == 64 ? launch_of<64, false>(lay.format, p, grid, stream) : launch_of<128, false>(lay.format, p, grid, stream);
+    const hipError_t e = a.d == 64 ? launch_of<64, true>(lay.format, p, grid, stream) : launch_of<128, true>(lay.format, p, grid, stream);
+    if (e != hipSuccess) return e;
     const auto join = a.d == 64 ? prompt_join_kernel<64> : prompt_join_kernel<128>;
-    return launch_kernel(join, dim3((uint32_t)(plan.blocks * a.H)), dim3(kBlockThreads), stream, p);
+    return launch_kernel(join, dim3((uint32_t)(plan.blocks * a.H * (kRows / kJoinRows))), dim3(kBlockThreads), stream, p);
 }
 
 }  // namespace kvc
