@@ -30,7 +30,7 @@ constexpr uint32_t kRun = 16;      // tokens that lie in one page: a wave fetche
 constexpr float kSlack = 3.0f;     // m moves when a tile's maximum passes it by this (powers of two)
 constexpr int kWeightExp = 12;     // binary16 weights: the largest stays below 2^(12 + 3 + 1)
 constexpr uint32_t kMinShare = 16;  // tiles of a share, at least
-constexpr uint32_t kBegin = 6;      // to begin and end a block takes as long as so many tiles
+constexpr uint32_t kBegin = 8;      // to begin and end a block takes as long as so many tiles
 constexpr float kNegInf = -__builtin_inff();
 constexpr bool half_products(int fmt) { return fmt == kPageInt8 || fmt == kPageFp8; }
 
@@ -54,7 +54,7 @@ struct PromptParams {
     uint32_t window, sinks;
     uint32_t shares;  // of the tiles of a kv head, one a workgroup (0: a block a workgroup, none is cut up)
     float scale_log2;
-    float* part;  // of a share's part of a block that is cut up: sums [rows of a block][d], then {m, l} of each row
+    float* part;  // of a share's part of a block that is cut up: sums, as lanes hold them, then {m, l} of each row
     uint2* info;  // of each block: its first share and its parts, 0 where it is not cut up
 };
 
@@ -879,7 +879,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(
             for (int n = 0; n < CB; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<f32x4*>(to + my_row * D + 32 * n + 8 * j + 4 * hi) =
+                    *reinterpret_cast<f32x4*>(to + ((n * kWaves + wave) * 4 + j) * (4 * kWave) + 4 * lane) =
                         f32x4{o[n][4 * j], o[n][4 * j + 1], o[n][4 * j + 2], o[n][4 * j + 3]};
             if (hi == 0) *reinterpret_cast<float2*>(to + kRows * D + 2 * my_row) = make_float2(m, l);
         }
@@ -911,13 +911,12 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(
     }
 }
 
-// Joins what shares have of a block that is cut up: a workgroup some of its rows, four channels a lane.
-constexpr uint32_t kJoinRows = 16;
+// Joins what shares have of a block that is cut up: a workgroup 32 channels, whose lanes hold what those of the shares held.
 template <int D>
 __global__ __launch_bounds__(kBlockThreads) void prompt_join_kernel(PromptParams p) {
     fetch_arguments<sizeof(PromptParams)>();
-    constexpr uint32_t LPR = D / 4, RPB = kBlockThreads / LPR, GROUPS = kRows / kJoinRows;
-    const uint32_t h = blockIdx.x % p.H, group = blockIdx.x / p.H % GROUPS, place = blockIdx.x / p.H / GROUPS;
+    constexpr uint32_t CB = D / 32;
+    const uint32_t h = blockIdx.x % p.H, n = blockIdx.x / p.H % CB, place = blockIdx.x / p.H / CB;
     const u32x2 info = *(const __attribute__((address_space(4))) u32x2*)(uint64_t)(p.info + (uint64_t)place * p.H + h);
     // the last sequence whose blocks' places begin at or before this one: of 64 that are evenly apart, then of those between two
     uint32_t b = 0, range = p.n;
@@ -931,41 +930,53 @@ __global__ __launch_bounds__(kBlockThreads) void prompt_join_kernel(PromptParams
         if (range <= 1) break;
     }
     const Sequence sq = uniform(sequence_at<false>(p, p.n - 1 - b), 0);
-    const uint32_t block = place - first_block(p, b, sq.first), row0 = block * kRows + group * kJoinRows, all = sq.m * p.group;
-    if (block >= sq.blocks || row0 >= all) return;
-    const uint32_t parts = info.y;
-    if (parts == 0) return;  // written already
+    const uint32_t block = place - first_block(p, b, sq.first);
+    if (block >= sq.blocks || info.y == 0) return;  // none, or written already
+    const uint32_t lane = lane_id(), wave = threadIdx.x / kWave, hi = lane >> 5, r = wave * 32 + lane % 32;
+    const uint32_t row = block * kRows + r, parts = info.y;
+    if (row >= sq.m * p.group) return;  // (with its neighbour, which holds the row's other channels)
     // part 0 is the last piece of its share, the others the first of theirs
     const auto part_of = [&](uint32_t i) {
         return p.part + ((uint64_t)(i ? 2 * (info.x + i) : 2 * info.x + 1) * p.H + h) * (kRows * (D + 2));
     };
-    const uint32_t c = threadIdx.x % LPR * 4;
+    float M = kNegInf;
+#pragma unroll 4
+    for (uint32_t i = 0; i < parts; ++i) M = fmaxf(M, part_of(i)[kRows * D + 2 * r]);
+    const float Mu = M == kNegInf ? 0.0f : M;
+    float total = 0.0f;
+    f32x4 y[4];
 #pragma unroll
-    for (uint32_t k = 0; k < kJoinRows / RPB; ++k) {
-        const uint32_t r = group * kJoinRows + k * RPB + threadIdx.x / LPR, row = block * kRows + r;
-        if (row >= all) return;
-        float M = kNegInf;
-#pragma unroll 4
-        for (uint32_t i = 0; i < parts; ++i) M = fmaxf(M, part_of(i)[kRows * D + 2 * r]);
-        const float Mu = M == kNegInf ? 0.0f : M;
-        float total = 0.0f;
-        f32x4 y = 0.0f;
-#pragma unroll 4
-        for (uint32_t i = 0; i < parts; ++i) {
-            const float* from = part_of(i);
-            const float2 ml = *reinterpret_cast<const float2*>(from + kRows * D + 2 * r);
-            f32x4 v = *reinterpret_cast<const f32x4*>(from + r * D + c);
-            const float w = __builtin_amdgcn_exp2f(ml.x - Mu);
+    for (int j = 0; j < 4; ++j) y[j] = 0.0f;
+#pragma unroll 2
+    for (uint32_t i = 0; i < parts; ++i) {
+        const float* from = part_of(i);
+        const float2 ml = *reinterpret_cast<const float2*>(from + kRows * D + 2 * r);
+        const float w = __builtin_amdgcn_exp2f(ml.x - Mu);
+        total = fmaf(ml.y, w, total);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f32x4 v = *reinterpret_cast<const f32x4*>(from + ((n * kWaves + wave) * 4 + j) * (4 * kWave) + 4 * lane);
             if (ml.x == kNegInf) v = 0.0f;  // (a part without tiles has no sums)
-            total = fmaf(ml.y, w, total);
-            y += v * w;
+            y[j] += v * w;
         }
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-        const uint32_t tok = sq.first + row / p.group, qh = h * p.group + row % p.group;
-        *reinterpret_cast<u32x2*>(p.out.data + (uint64_t)tok * p.out.ts + (uint64_t)qh * p.out.hs + c) =
-            u32x2{pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv)};
-        if (p.lse && c == 0) p.lse[(uint64_t)tok * p.Hq + qh] = (M + log2f(total)) * 0.69314718055994531f;
     }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const uint32_t tok = sq.first + row / p.group, qh = h * p.group + row % p.group;
+    uint16_t* to = p.out.data + (uint64_t)tok * p.out.ts + (uint64_t)qh * p.out.hs + 32 * n;
+    // two lanes hold channels 8 j + 4 hi to + 3: one takes all of j, the other of j + 1
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        u32x4 z;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const auto q = __builtin_amdgcn_permlane32_swap(pack_bf16x2(y[j][2 * c] * inv, y[j][2 * c + 1] * inv),
+                                                            pack_bf16x2(y[j + 1][2 * c] * inv, y[j + 1][2 * c + 1] * inv), false, false);
+            z[c] = q[0];
+            z[2 + c] = q[1];
+        }
+        *reinterpret_cast<u32x4*>(to + 8 * (j + hi)) = z;
+    }
+    if (p.lse && n == 0 && hi == 0) p.lse[(uint64_t)tok * p.Hq + qh] = (M + log2f(total)) * 0.69314718055994531f;
 }
 
 template <int D, bool SHARED>
@@ -1067,7 +1078,7 @@ hipError_t launch_attend_prompt(const PromptArgs& a, const PromptPlan& plan, hip
     const hipError_t e = a.d == 64 ? launch_of<64, true>(lay.format, p, grid, stream) : launch_of<128, true>(lay.format, p, grid, stream);
     if (e != hipSuccess) return e;
     const auto join = a.d == 64 ? prompt_join_kernel<64> : prompt_join_kernel<128>;
-    return launch_kernel(join, dim3((uint32_t)(plan.blocks * a.H * (kRows / kJoinRows))), dim3(kBlockThreads), stream, p);
+    return launch_kernel(join, dim3((uint32_t)(plan.blocks * a.H * (a.d / 32))), dim3(kBlockThreads), stream, p);
 }
 
 }  // namespace kvc
