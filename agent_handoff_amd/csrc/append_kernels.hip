@@ -56,6 +56,7 @@ __global__ __launch_bounds__(kBlockThreads) void append_kernel(AppendParams p) {
     constexpr uint32_t LPV = D / 16;
     constexpr uint32_t VPB = kBlockThreads / LPV;  // vectors at a time
     __shared__ float cs[TW][kMaxPairs], sn[TW][kMaxPairs];
+    __shared__ int64_t slots[TW];
     __shared__ uint4 turn_about[FMT == kPageFp4 ? kBlockThreads * 2 : 1];
     const uint32_t tok0 = blockIdx.x * TW;
     const uint32_t ntok = p.n - tok0 < TW ? p.n - tok0 : TW;
@@ -66,6 +67,15 @@ __global__ __launch_bounds__(kBlockThreads) void append_kernel(AppendParams p) {
     // the lane's two chunks of 8 channels: of a value always 16 in a row
     const uint32_t oa = turned && p.pairing == 0 ? 8 * i : 16 * i;
     const uint32_t ob = turned && p.pairing == 0 ? p.n_pairs + 8 * i : 16 * i + 8;
+    kvc_u32x4 wq[2] = {}, wk[2] = {};
+    if (p.q_weight) {
+        wq[0] = *reinterpret_cast<const kvc_u32x4*>(p.q_weight + oa);
+        wq[1] = *reinterpret_cast<const kvc_u32x4*>(p.q_weight + ob);
+    }
+    if (p.k_weight) {
+        wk[0] = *reinterpret_cast<const kvc_u32x4*>(p.k_weight + oa);
+        wk[1] = *reinterpret_cast<const kvc_u32x4*>(p.k_weight + ob);
+    }
     uint32_t t = 0, h = threadIdx.x / LPV;
     const auto settle = [&]() {
         while (h >= heads && t < ntok) {
@@ -87,6 +97,7 @@ __global__ __launch_bounds__(kBlockThreads) void append_kernel(AppendParams p) {
     };
     settle();
     load();
+    if (threadIdx.x < ntok) slots[threadIdx.x] = p.slots[tok0 + threadIdx.x];
     for (uint32_t j = threadIdx.x; j < TW * kMaxPairs; j += kBlockThreads) {
         const uint32_t jt = j / kMaxPairs, pair = j % kMaxPairs;
         if (jt < ntok && pair < p.n_pairs) {
@@ -104,8 +115,7 @@ __global__ __launch_bounds__(kBlockThreads) void append_kernel(AppendParams p) {
         const uint32_t head = is_q ? h : is_v ? h - p.Hq - p.Hk : h - p.Hq;
         const uint32_t t_now = t;
         uint4 ya = make_uint4(xa.x, xa.y, xa.z, xa.w), yb = make_uint4(xb.x, xb.y, xb.z, xb.w);
-        int64_t slot = 0;
-        if (!is_q) slot = p.slots[tok0 + t];
+        const int64_t slot = slots[t];
         h += VPB;
         settle();
         load();
@@ -113,18 +123,17 @@ __global__ __launch_bounds__(kBlockThreads) void append_kernel(AppendParams p) {
             float a[8], b[8];
             unpack8(ya, a);
             unpack8(yb, b);
-            const uint16_t* weight = is_q ? p.q_weight : p.k_weight;
-            if (weight) {
+            if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
                 float ss = 0.0f;
 #pragma unroll
                 for (int u = 0; u < 8; ++u) ss = fmaf(a[u], a[u], fmaf(b[u], b[u], ss));
                 ss = sum_lanes<LPV>(ss);
                 const float inv = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
                 float w[8];
-                unpack8(*reinterpret_cast<const uint4*>(weight + oa), w);
+                { const kvc_u32x4 z = is_q ? wq[0] : wk[0]; unpack8(make_uint4(z.x, z.y, z.z, z.w), w); }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) a[u] = a[u] * inv * w[u];
-                unpack8(*reinterpret_cast<const uint4*>(weight + ob), w);
+                { const kvc_u32x4 z = is_q ? wq[1] : wk[1]; unpack8(make_uint4(z.x, z.y, z.z, z.w), w); }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) b[u] = b[u] * inv * w[u];
             }
