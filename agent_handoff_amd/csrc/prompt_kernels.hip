@@ -30,6 +30,8 @@ constexpr uint32_t kRun = 16;      // tokens that lie in one page: a wave fetche
 constexpr float kSlack = 3.0f;     // m moves when a tile's maximum passes it by this (powers of two)
 constexpr int kWeightExp = 12;     // binary16 weights: the largest stays below 2^(12 + 3 + 1)
 constexpr uint32_t kMinShare = 16;  // tiles of a share, at least
+constexpr uint32_t kCus = 256;
+constexpr uint32_t workgroups(uint32_t d) { return d == 64 ? 3 : 2; }  // of a CU: registers bound them
 constexpr uint32_t kBegin = 8;      // to begin and end a block takes as long as so many tiles
 constexpr float kNegInf = -__builtin_inff();
 constexpr bool half_products(int fmt) { return fmt == kPageInt8 || fmt == kPageFp8; }
@@ -245,12 +247,42 @@ __device__ __forceinline__ Found find_sequence(const PromptParams& p, F of, A pl
         before += these;
     }
 }
+// Where share k of `count` begins in `all` tiles. A CU's first workgroup goes before its second, which goes before its
+// third (a SIMD takes its oldest wave first), so that with equal shares the later ones end by themselves: four chunked
+// prompts, int8, shares of 76 tiles, after 136 and 158 us. Long shares are given out in that order, in proportions of 18
+// to 16 to 14 (the call with bf16 pages 123 -> 116 us); short ones are equal, as are then most blocks or their halves,
+// of which fewer are cut up (one prompt of 2000 tokens, shares of 39 tiles: 64 us, in those proportions 72).
+constexpr uint32_t kLongShare = 64;
+struct Bounds {
+    uint64_t all;
+    uint32_t count, row;  // row: shares of a kv head with which each CU has one workgroup
+    uint32_t less;        // of 18, with each further workgroup of a CU
+    __device__ __forceinline__ uint32_t weight_to(uint32_t k) const {
+        return 18 * k - less * ((k > row ? k - row : 0) + (k > 2 * row ? k - 2 * row : 0));
+    }
+    __device__ __forceinline__ uint64_t operator()(uint32_t k) const {
+        if (k >= count) return all;
+        uint64_t q;
+        uint32_t r;
+        if (less == 0) {
+            divmod_u64(all + count - 1, count, q, r);
+            return q * k < all ? q * k : all;
+        }
+        divmod_u64(all * weight_to(k), weight_to(count), q, r);
+        return q;
+    }
+};
+__device__ __forceinline__ Bounds bounds_of(const PromptParams& p, uint64_t all) {
+    const uint64_t most = all / kMinShare;
+    const uint32_t count = most < 1 ? 1 : most < p.shares ? (uint32_t)most : p.shares;
+    return Bounds{all, count, kCus / p.H ? kCus / p.H : 1, all >= (uint64_t)kLongShare * count ? 2u : 0u};
+}
 // A block's place in the list of all (those of the sequences before it, rounded up one by one, are no more).
 __device__ __forceinline__ uint32_t first_block(const PromptParams& p, uint32_t b, uint32_t first) { return first * p.group / kRows + b; }
 
 // SHARED: the tiles of all blocks are shared out.
 template <int FMT, int D, bool SHARED>
-__global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(PromptParams p) {
+__global__ __launch_bounds__(kWaves* kWave, workgroups(D)) void prompt_kernel(PromptParams p) {
     fetch_arguments<sizeof(PromptParams)>();
     constexpr bool HALF = half_products(FMT);
     constexpr int KS = D / 16, CB = D / 32;  // steps of a key product, blocks of channels
@@ -260,14 +292,13 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(
     Pairs pairs{};
     uint32_t index = 0, block = 0, half = 0;
     uint64_t at = 0, left = 0;  // where the share is in its sequence's row of blocks, and how much of it is left
-    uint64_t each = 0;
+    Bounds bounds{};
     if constexpr (SHARED) {
         const Found f = find_sequence(p, [&](const Sequence& s) { return pairs_of(p, s).all; }, [&](uint64_t all) {
-            uint32_t r;
-            divmod_u64(all + p.shares - 1, p.shares, each, r);
-            each = each < kMinShare ? kMinShare : each;
-            left = all - share * each < each ? all - share * each : each;
-            return share * each;
+            bounds = bounds_of(p, all);
+            const uint64_t x0 = bounds(share);
+            left = bounds(share + 1) - x0;
+            return x0;
         });
         if (!f.any) return;
         sq = f.s;
@@ -310,10 +341,10 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 3 : 2) void prompt_kernel(
         if (part0 == 0 && part1 != 0 && threadIdx.x == 0) {
             // the share that begins a block counts the shares that go on with it
             const uint32_t all = half ? x.tiles_high + x.tiles_low : x.tiles_high;
-            uint64_t end = e;
             uint32_t parts = part1 < tiles ? 1 : 0;
+            const uint64_t mine = bounds(share + 1);  // e, in the row of all
             for (uint32_t reached = to; reached < all; ++parts) {
-                end += each;
+                const uint64_t end = e + (bounds(share + 1 + parts) - mine);
                 reached = end < x.len ? x.tiles_to((uint32_t)end) : x.tiles_high + x.tiles_low;
             }
             p.info[(uint64_t)(first_block(p, sq.b, sq.first) + block) * p.H + h] = make_uint2(share, parts);
@@ -988,8 +1019,11 @@ hipError_t launch_of(uint32_t format, const PromptParams& p, uint32_t grid, hipS
     return launch_kernel(f, dim3(grid), dim3(kWaves * kWave), stream, p);
 }
 
-// Workgroups of 4 waves that the GPU holds at once.
-constexpr uint64_t kPlaces = 512;
+// Workgroups of 4 waves that the GPU holds at once. Tiles are shared out up to 5/4 as many blocks: more balance one another,
+// and beginning a piece of a block costs what eight tiles cost. Blocks shared out and not, us: 504 blocks of 512 places (one
+// prompt of 2000 tokens, 8 kv heads of 128, 4 heads each, bf16) 64 and 80, 600 93 and 98, 752 125 and 96, 1500 361 and
+// 309; where contexts differ, 712 (chunks of four prompts, int8) 215 and 244.
+constexpr uint64_t places_of(uint32_t d) { return kCus * workgroups(d); }
 // Few new tokens of each sequence (their rows, times the heads that share a kv head, in the mean of all): a call is then
 // memory's, and the kernel for one new token takes them, 32 rows at a time. 15 sequences behind 8192 tokens (8 kv heads of
 // 128), that kernel and the one here, us: 32 rows e4m3 66 and 138, 64 rows 99 and 152, bf16 148 and 148; one sequence of 32
@@ -1009,13 +1043,13 @@ PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t 
     // with a window, a block's rows see the tokens of one row and as many more as the block has tokens
     const uint64_t seen = window ? seen_tokens(max_tokens, (uint64_t)window + kRows / group, sinks) : max_tokens;
     const bool can = seen > kMinShare * kTokens;
-    const uint64_t shares = (kPlaces + H - 1) / H;
-    if (can && H * a.blocks < 4 * kPlaces) a.shares = (uint32_t)shares;
+    const uint64_t places = places_of(d), shares = (places + H - 1) / H, few_blocks = 5 * places / 4;
+    if (can && H * a.blocks < few_blocks) a.shares = (uint32_t)shares;
     // a share leaves two parts of blocks at most
     const uint64_t parts = align_up(2 * shares * H * (kRows * (d + 2) * 4), 256);
     const uint64_t info = align_up(a.blocks * H * 8, 256);
     if (a.shares) a.bytes = parts + info;
-    if (can) a.room = parts + align_up((a.blocks < 4 * kPlaces / H + 1 ? a.blocks : 4 * kPlaces / H + 1) * H * 8, 256);
+    if (can) a.room = parts + align_up((a.blocks < few_blocks / H + 1 ? a.blocks : few_blocks / H + 1) * H * 8, 256);
     const uint64_t rows = n_tokens * group, most = kFewRows * n_seqs, few = rows < most ? rows : most;
     const AttendPlan many = many_attend_plan(n_seqs, n_tokens, H, Hq, d, max_tokens, window, sinks);
     // (what its kernel counts with 32 bits, wherever the sequences start)
