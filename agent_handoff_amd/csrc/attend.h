@@ -149,9 +149,9 @@ struct AttendArgs {
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
 
 // Attention of many new tokens. The query rows of a sequence and kv head (tokens x
-// the heads that share it) are taken in blocks, one a workgroup and share of the
-// tokens; `blocks` bounds how many a kv head has, which the host does not know.
-constexpr uint32_t kPromptRows = 64;  // of the smallest block
+// the heads that share it) are taken in blocks; `blocks` bounds how many a kv head
+// has, which the host does not know.
+constexpr uint32_t kPromptRows = 64;  // a call's limit counts blocks of so many rows
 struct PromptPlan {
     bool few;         // few new tokens of each sequence: taken by launch_attend
     uint32_t shares;  // workgroups that share out a kv head's tiles evenly (0: each takes a block)
