@@ -550,6 +550,8 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         if (p.n <= kWave) {
             // a sequence a lane, in every wave for itself
             const uint32_t v = lane < p.n ? weight_of(lane) : 0;
+            // (wrong starts could give rows many times over: nothing is done)
+            if (MANY && __ballot(lane < p.n && fresh_of(src, lane).bad) != 0) return;
             const uint32_t up = scan_lanes(v);
             if (!share((uint64_t)__builtin_amdgcn_readlane(up, 63) * per_seq)) return;
             divmod_u64(x0, per_seq, q64, part);
@@ -561,7 +563,12 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             const uint32_t run = (p.n + kWaves * kWave - 1) / (kWaves * kWave);
             const uint32_t s0 = threadIdx.x * run, s1 = s0 + run < p.n ? s0 + run : p.n;
             uint32_t v = 0, all;
-            for (uint32_t s = s0; s < s1; ++s) v += weight_of(s);
+            bool bad = false;
+            for (uint32_t s = s0; s < s1; ++s) {
+                v += weight_of(s);
+                if (MANY) bad |= fresh_of(src, s).bad;
+            }
+            if (MANY && __syncthreads_or(bad)) return;
             const uint32_t at0 = scan_threads(v, sh.sums, all);
             if (!share((uint64_t)wave_uniform(all) * per_seq)) return;
             divmod_u64(x0, per_seq, q64, part);
@@ -1445,6 +1452,8 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
         ml[s] = (tile - at) * D + at * 2;
     }
     const bool header = !p.src[0].pool || pool_header_ok(p.src[0], p.c.H, D);
+    // (starts were wrong, and no workgroup wrote it)
+    if (MANY && (info[0].x >= 2 * p.src[0].W || info[0].y > p.src[0].W || info[0].x + 2 * info[0].y > 2 * p.src[0].W + 2)) return;
     const uint32_t n0 = info[0].y, n = n0 + info[1].y;
     if (n == 0 || !header) return;  // written already, or never to be
     // this wave's parts w, w + V, ...: a lane has the place, maximum and sum of one of

@@ -151,7 +151,7 @@ __device__ __forceinline__ Range range_of(const PromptParams& p, int32_t pos_lo,
 // A sequence's new tokens and length. Sequences are taken from the last to the first (`i` counts them so), and a
 // sequence's blocks too, so that the longest of a prompt come first.
 struct Sequence {
-    uint32_t b, first, m;  // first: its first row
+    uint32_t b, first, m;  // first: its first row (~0: its starts are wrong)
     int32_t len;
     uint32_t blocks;
     __device__ __forceinline__ int32_t pos_of(uint32_t row, uint32_t group) const { return len - (int32_t)m + (int32_t)(row / group); }
@@ -167,7 +167,7 @@ __device__ __forceinline__ Sequence sequence_at(const PromptParams& p, uint32_t 
     s.len = given < 0 ? 0 : (uint32_t)given > most ? (int32_t)most : given;
     if (REPORT && p.status && (bad || s.len != given))
         atomicOr(p.status, (bad ? kDevBadStart : 0) | (s.len != given ? kDevBadLength : 0));
-    s.first = a;
+    s.first = bad ? ~0u : (uint32_t)a;
     s.m = bad ? 0 : e - a;
     s.blocks = (s.m * p.group + kRows - 1) / kRows;
     return s;
@@ -176,6 +176,7 @@ __device__ __forceinline__ Sequence uniform(const Sequence& s, int lane) {
     const auto of = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane(v, lane); };
     return Sequence{of(s.b), of(s.first), of(s.m), (int32_t)of(s.len), of(s.blocks)};
 }
+__device__ __forceinline__ uint64_t uniform(uint64_t x) { return (uint64_t)wave_uniform((uint32_t)(x >> 32)) << 32 | wave_uniform((uint32_t)x); }
 // Tiles that a block sees; one that sees none has an empty one, so that its rows are written.
 __device__ __forceinline__ uint32_t tiles_of(const PromptParams& p, const Sequence& s, uint32_t block) {
     const uint32_t row0 = block * kRows, left = s.m * p.group - row0;
@@ -230,7 +231,8 @@ __device__ __forceinline__ uint64_t read_lane64(uint64_t v, int lane) {
            (uint32_t)__builtin_amdgcn_readlane((uint32_t)v, lane);
 }
 // The first sequence with which the sum of `of` passes `at`, and the sums before it: a wave finds it, a lane a sequence.
-// `at` comes from the sum of all, which is known at once where the lanes hold every sequence.
+// `at` comes from the sum of all, which is known at once where the lanes hold every sequence. Where starts are wrong
+// there is none: rows could be given many times over.
 struct Found {
     bool any;
     Sequence s;
@@ -240,13 +242,16 @@ struct Found {
 template <class F, class A>
 __device__ __forceinline__ Found find_sequence(const PromptParams& p, F of, A place) {
     uint64_t all = 0, mine = 0, up = 0;
+    bool bad = false;
     Sequence s{};
     for (uint32_t base = 0; base < p.n; base += kWave) {
         s = sequence_at<true>(p, base + lane_id());
+        bad |= s.first == ~0u;
         mine = of(s);
         up = scan_lanes64(mine);
         all += read_lane64(up, 63);
     }
+    if (__ballot(bad) != 0) all = 0;
     const uint64_t at = place(all);
     if (at >= all) return Found{};
     uint64_t before = 0;
@@ -329,6 +334,16 @@ __global__ __launch_bounds__(kWaves* kWave, workgroups(D)) void prompt_kernel(Pr
         block = f.s.blocks - 1 - (share - (uint32_t)f.before);
     }
     for (bool again = false;; again = true) {
+    if constexpr (SHARED) {
+        // the same in all lanes, which the compiler does not see (20 vector registers)
+        at = uniform(at);
+        left = uniform(left);
+        bounds = Bounds{uniform(bounds.all), wave_uniform(bounds.count), bounds.row, wave_uniform(bounds.less)};
+        pairs = Pairs{wave_uniform(pairs.len), wave_uniform(pairs.last), uniform(pairs.all)};
+        sq = uniform(sq, 0);
+        index = wave_uniform(index);
+        half = wave_uniform(half);
+    }
     uint32_t part0 = 0, part1 = 0xFFFFFFFFu;  // tiles of the block, of
     uint32_t tiles = 0;
     if constexpr (SHARED) {
@@ -980,6 +995,7 @@ __global__ __launch_bounds__(kBlockThreads) void prompt_join_kernel(PromptParams
     const Sequence sq = uniform(sequence_at<false>(p, p.n - 1 - b), 0);
     const uint32_t block = place - first_block(p, b, sq.first);
     if (block >= sq.blocks || info.y == 0) return;  // none, or written already
+    if (info.x >= p.shares || info.y > p.shares - info.x) return;  // (starts were wrong: no share wrote it)
     const uint32_t lane = lane_id(), wave = threadIdx.x / kWave, hi = lane >> 5, r = wave * 32 + lane % 32;
     const uint32_t row = block * kRows + r, parts = info.y;
     if (row >= sq.m * p.group) return;  // (with its neighbour, which holds the row's other channels)
@@ -1066,11 +1082,11 @@ PromptPlan prompt_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t 
     const uint64_t parts = align_up(2 * shares * H * (kRows * (d + 2) * 4), 256);
     const uint64_t info = align_up(a.blocks * H * 8, 256);
     if (a.shares) a.bytes = parts + info;
-    if (can) a.room = parts + align_up((a.blocks < few_blocks / H + 1 ? a.blocks : few_blocks / H + 1) * H * 8, 256);
+    if (can && H < few_blocks) a.room = parts + align_up((a.blocks < few_blocks / H + 1 ? a.blocks : few_blocks / H + 1) * H * 8, 256);
     const uint64_t rows = n_tokens * group, most = kFewRows * n_seqs, few = rows < most ? rows : most;
     const AttendPlan many = many_attend_plan(n_seqs, n_tokens, H, Hq, d, max_tokens, window, sinks);
-    // (what its kernel counts with 32 bits, wherever the sequences start)
-    a.few = rows <= most && max_tokens > kFewTokens && (uint64_t)n_seqs * (rows / 16 + 1) * (max_tokens / 128 + 1) < 1ull << 31;
+    // (what its kernels count with 32 bits, wherever the sequences start, and a wave's threads of each row)
+    a.few = rows <= most && max_tokens > kFewTokens && rows * H < 1ull << 24 && (uint64_t)n_seqs * (rows / 16 + 1) * (max_tokens / 128 + 1) < 1ull << 31;
     if (a.few) a.bytes = many.bytes(d);
     const uint64_t room = many_attend_room(n_seqs, few, H, d, max_tokens);
     if (room > a.room) a.room = room;
