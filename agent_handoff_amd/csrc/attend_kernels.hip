@@ -1443,17 +1443,19 @@ __global__ __launch_bounds__(kBlockThreads) void attend_join_kernel(JoinParams p
         const Source& x = p.src[s];
         const uint32_t tile = 16 * p.rt[s], r = x.pool ? seq * p.c.group + i : i, at = r % tile;
         // (a long pool's numbers could be worked out here: 0.6 us more than the load)
-        if (MANY)
-            info[s] = scalar_load<u32x2>(x.info + unit0 + h * row_blocks + r / tile);
-        else
+        if (MANY) {
+            // (where starts were wrong no workgroup wrote it, and it may hold anything)
+            const u32x2 z = scalar_load<u32x2>(x.info + unit0 + h * row_blocks + r / tile);
+            const bool ok = (z.x < 2 * x.W) & (z.y <= x.W) & (z.x + 2 * z.y <= 2 * x.W + 2);
+            info[s] = u32x2{ok ? z.x : 0, ok ? z.y : 0};
+        } else {
             info[s] = scalar_load<u32x2>(x.info + (x.pool ? 0 : seq * p.c.H * x.row_blocks) + h * x.row_blocks + r / tile);
+        }
         stride[s] = tile * (D + 2);
         from[s] = x.part + at * D;
         ml[s] = (tile - at) * D + at * 2;
     }
     const bool header = !p.src[0].pool || pool_header_ok(p.src[0], p.c.H, D);
-    // (starts were wrong, and no workgroup wrote it)
-    if (MANY && (info[0].x >= 2 * p.src[0].W || info[0].y > p.src[0].W || info[0].x + 2 * info[0].y > 2 * p.src[0].W + 2)) return;
     const uint32_t n0 = info[0].y, n = n0 + info[1].y;
     if (n == 0 || !header) return;  // written already, or never to be
     // this wave's parts w, w + V, ...: a lane has the place, maximum and sum of one of
