@@ -19,10 +19,10 @@
 // weights and the values of the one before, which are independent, two products beside two weights. Keys and
 // values lie in a ring of four tiles in LDS, filled by loads that nothing waits for but the end of
 // two tiles (bf16), or widened on their way (8 bits: binary16, where codes are exact; 4 bits: bf16, the same). One prompt of 8192
-// tokens (8 kv heads of 128, 4 heads each): bf16 558 us, 985 TFLOP/s of what the mask leaves, of a SIMD's cycles
+// tokens (8 kv heads of 128, 4 heads each): bf16 546 us, 1007 TFLOP/s of what the mask leaves, of a SIMD's cycles
 // the matrix core 53 %, the VALU 52 %, at 1.9 GHz: the clock falls as power allows (a build with 12 %
-// more cycles took 1 % longer). e4m3 705, int8 733, 4 bits 586 us: steps of 8 bits cost a product each for logits and
-// weights, and codes their widening. Heads of 64, with as many exponentials for half the products: 332 us.
+// more cycles took 1 % longer). e4m3 686, int8 713, 4 bits 559 us: steps of 8 bits cost a product each for logits and
+// weights, and codes their widening. Heads of 64, with as many exponentials for half the products: 318 us.
 // Measured and left out: tiles of 64 tokens (7 to 20 % longer), 256 rows a
 // workgroup, operands asked for four products ahead.
 //
