@@ -23,16 +23,16 @@ __device__ __forceinline__ void fetch16(const uint8_t* base, const uint32_t (&of
     if constexpr (N == 4)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
                      "global_load_lds_dwordx4 %2, %1\n\t"
-                     "global_load_lds_dwordx4 %3, %1 offset:1024\n\t"
-                     "global_load_lds_dwordx4 %4, %1 offset:2048\n\t"
-                     "global_load_lds_dwordx4 %5, %1 offset:3072"
+                     "global_load_lds_dwordx4 %3, %1 offset:0x400\n\t"
+                     "global_load_lds_dwordx4 %4, %1 offset:0x800\n\t"
+                     "global_load_lds_dwordx4 %5, %1 offset:0xc00"
                      :
                      : "s"(to), "s"(at), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3])
                      : "memory");
     else if constexpr (N == 2)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
                      "global_load_lds_dwordx4 %2, %1\n\t"
-                     "global_load_lds_dwordx4 %3, %1 offset:1024"
+                     "global_load_lds_dwordx4 %3, %1 offset:0x400"
                      :
                      : "s"(to), "s"(at), "v"(off[0]), "v"(off[1])
                      : "memory");
