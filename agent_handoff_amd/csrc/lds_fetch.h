@@ -1,7 +1,10 @@
 // lds_fetch.h - loads from memory to LDS (device side). Written out: behind the builtin the compiler waits for all of
 // them before the next read of LDS, of whichever buffer. Here it knows of none, and the kernels wait themselves, with
 // wait_loads() (loads that the compiler knows of only make its own waits, and these, longer than they need be). No
-// register is written but M0, which nothing else in these kernels uses; what reads it comes a wait state behind its write.
+// register is written but M0, which nothing else in these kernels uses (the compiler keeps it for itself and takes no note
+// of it); what reads it comes a wait state behind its write. The compiler does not look into the text for hazards: a scalar
+// address that a vector instruction wrote (v_readfirstlane) may be read five wait states later at the earliest, and the
+// instruction before the text may be that write, so the text begins with them.
 #pragma once
 
 #include "kernels_common.h"
@@ -21,7 +24,7 @@ __device__ __forceinline__ void fetch16(const uint8_t* base, const uint32_t (&of
     const uint32_t to = lds_place(lds);
     static_assert(N == 1 || N == 2 || N == 4);
     if constexpr (N == 4)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\t"
                      "global_load_lds_dwordx4 %2, %1\n\t"
                      "global_load_lds_dwordx4 %3, %1 offset:0x400\n\t"
                      "global_load_lds_dwordx4 %4, %1 offset:0x800\n\t"
@@ -30,14 +33,14 @@ __device__ __forceinline__ void fetch16(const uint8_t* base, const uint32_t (&of
                      : "s"(to), "s"(at), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3])
                      : "memory");
     else if constexpr (N == 2)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\t"
                      "global_load_lds_dwordx4 %2, %1\n\t"
                      "global_load_lds_dwordx4 %3, %1 offset:0x400"
                      :
                      : "s"(to), "s"(at), "v"(off[0]), "v"(off[1])
                      : "memory");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\t"
                      "global_load_lds_dwordx4 %2, %1"
                      :
                      : "s"(to), "s"(at), "v"(off[0])
