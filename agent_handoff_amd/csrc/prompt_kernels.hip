@@ -870,6 +870,7 @@ __global__ __launch_bounds__(kWaves* kWave, workgroups(D)) void prompt_kernel(Pr
     // values j + 1, j + 2 on their way
     if (j0 < j1) {
         Run ahead = run_of(j0 + 1);
+        __syncthreads();  // `odd` is cleared, by one wave for all
         if (FMT != kPageBf16) {  // (their registers are needed again)
             put(0, first, 0);
             put(1, first, 0);
