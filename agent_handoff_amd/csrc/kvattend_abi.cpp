@@ -331,8 +331,9 @@ int kvc_norm_rotate(uint32_t n_tokens, uint32_t q_heads, uint32_t kv_heads, uint
     a.k_in = rows_dev(vi[1]);
     a.q_out = rows_dev(vo[0]);
     a.k_out = rows_dev(vo[1]);
-    a.q_weight = q_weight;
-    a.k_weight = k_weight;
+    // (weights without heads are not checked, and kernels load what they are given)
+    a.q_weight = q_heads ? q_weight : nullptr;
+    a.k_weight = kv_heads ? k_weight : nullptr;
     a.eps = eps;
     a.positions = positions;
     a.inv_freq = inv_freq;
@@ -403,7 +404,7 @@ int kvpage_append(const kvc_pages* spec, void* pages, size_t pages_bytes, uint32
     a.k_in = rows_dev(in[1]);
     a.v_in = rows_dev(in[2]);
     a.q_out = rows_dev(out);
-    a.q_weight = q_weight;
+    a.q_weight = q_heads ? q_weight : nullptr;  // (as above)
     a.k_weight = k_weight;
     a.eps = eps;
     a.positions = positions;

@@ -93,7 +93,7 @@ enum {
  *                  NULL, if n_pairs is 0)
  *   inv_freq       host, n_pairs floats; n_pairs a multiple of 8, at most head_dim / 2
  *   q_out, k_out   rows; the same as q_in / k_in turns in place
- * kv_heads may be 0 (then k_in, k_out are not used), and so may q_heads.
+ * kv_heads may be 0 (then k_in, k_out, k_weight are not used), and so may q_heads.
  * Errors: KVC_E_NULL, KVC_E_SHAPE, KVC_E_RANGE (pairing, n_pairs, eps),
  * KVC_E_ALIGN, KVC_E_ALIAS, KVC_E_HIP. */
 int kvc_norm_rotate(uint32_t n_tokens, uint32_t q_heads, uint32_t kv_heads, uint32_t head_dim,
@@ -146,7 +146,7 @@ int kvpage_read(const kvc_pages* spec, const void* pages, size_t pages_bytes, ui
  * bf16, but not kept) and of v. The bytes of q_out and of the pages are those of the
  * two calls.
  *   q_in, k_in, v_in  rows of n_tokens x q_heads and twice n_tokens x num_kv_heads;
- *                  n_tokens <= 2^26 - 4. q_heads may be 0 (q_in, q_out are not used)
+ *                  n_tokens <= 2^26 - 4. q_heads may be 0 (q_in, q_out, q_weight are not used)
  *   q_out          rows; the same as q_in turns in place
  *   slots          as for kvpage_write; a token with a negative slot (padding) or one
  *                  outside the cache has its queries turned all the same
