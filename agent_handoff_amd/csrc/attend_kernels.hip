@@ -387,10 +387,18 @@ __device__ __forceinline__ void fwht_row(float (&y)[C], uint32_t lane) {
 constexpr int waves_per_simd(int d, int rt) { return d == 64 ? (rt == 1 ? 3 : 2) : 2; }
 
 // Tiles on their way to a wave lie in its registers, or in LDS, which a wave fills for itself. In LDS they cost more
-// instructions, but leave room for a second row tile and for tiles further ahead: 8-bit and 16-bit pages with two row tiles
-// (15 sequences of 5 drafts behind 8192 tokens, 8 kv heads of 128, 20 rows: e4m3 74 and 65 us, bf16 125 and 120). With
-// one row tile int8 52 and 55, bf16 98 and 97; 4 bits 61 and 69, with two 54 and 58.
-constexpr bool through_lds(int fmt, int rt) { return rt == 2 && fmt != kFmtPool && fmt != kFmtFp4; }
+// instructions, but leave registers for a second row tile of heads of 128, where bf16's spill otherwise, and 8 bits' too
+// if there is a window or each row has a position of its own. (8 kv heads of 128, us in registers and in LDS. One new token,
+// 40 rows: bf16, 15 sequences of 400 tokens 14.5 and 12.8, 4 of 2000 21.8 and 17.1, 64 of 1000 103 and 92, 32 of 8000 300
+// and 310; e4m3 10.7 and 11.3, 18.1 and 18.5, 52.4 and 53.5, 155 and 164. Windows: bf16, 4 sequences of 1024 tokens 27.5
+// and 20.0, 32 of 4096 164 and 159; e4m3 22.0 and 20.1, 64 of 1000 56.6 and 54.1, 32 of 4096 89.8 and 92.0. 15 sequences of 5
+// drafts behind 8192 tokens: bf16 135 and 104, e4m3 73.0 and 66.0. Heads of 64, whose registers suffice, e4m3: 64 sequences of
+// 1000 tokens, 20 rows, 19.7 and 23.7; those drafts 39.2 and 42.9.) With one row tile int8 52 and 55, bf16 98 and 97;
+// 4 bits 61 and 69, with two 54 and 58.
+constexpr bool through_lds(int fmt, int d, int rt, int mode) {
+    const bool bits8 = fmt == kFmtInt8 || fmt == kFmtFp8;
+    return rt == 2 && d == 128 && (fmt == kFmtBf16 || (bits8 && mode != kOneSeesAll));
+}
 
 // A tile: rows of keys, of values, then the steps of both. The keys' chunks of 16 bytes change places inside a row by
 // the token, so that 16 lanes with one chunk of 16 tokens meet in no bank.
@@ -411,21 +419,21 @@ struct Ring {
 struct NoRing {};
 
 // LDS of a workgroup. (Without its alignment, accesses of four floats come out in pairs.)
-template <int FMT, int D, int RT>
+template <int FMT, int D, int RT, int MODE>
 struct Shared {
     alignas(16) float ml[kWaves][RT * 16][2];
     union {
         alignas(16) float os[RT][kWaves][16][D + 4];
-        alignas(16) std::conditional_t<through_lds(FMT, RT), Ring<FMT, D, RT>, NoRing> ring;
+        alignas(16) std::conditional_t<through_lds(FMT, D, RT, MODE), Ring<FMT, D, RT>, NoRing> ring;
     };
     uint32_t sums[kWaves];
     uint32_t found[3];  // sequence, blocks before it, its blocks
 };
 
 // Tiles that are on their way at once.
-template <int FMT, int D, int RT>
+template <int FMT, int D, int RT, int MODE>
 constexpr uint32_t ahead_of() {
-    if constexpr (through_lds(FMT, RT))
+    if constexpr (through_lds(FMT, D, RT, MODE))
         return Ring<FMT, D, RT>::kDepth;
     else
         return 1;
@@ -485,12 +493,12 @@ __device__ __forceinline__ uint32_t scan_threads(uint32_t v, uint32_t* sums, uin
 
 // The share of workgroup w.
 template <int FMT, int D, int RT, int MODE>
-__device__ __forceinline__ void attend_share(const Common& p, const Source& src, uint32_t w, Shared<FMT, D, RT>& sh) {
+__device__ __forceinline__ void attend_share(const Common& p, const Source& src, uint32_t w, Shared<FMT, D, RT, MODE>& sh) {
     constexpr int KS = D / 32;   // key product steps
     constexpr int NC = D / 16;   // channels of a lane, value products
     constexpr bool HALF = half_products(FMT);
     constexpr bool MANY = MODE == kMany, WIN = MODE != kOneSeesAll;
-    constexpr bool RING = through_lds(FMT, RT);
+    constexpr bool RING = through_lds(FMT, D, RT, MODE);
     constexpr int RE = MANY ? RT : 1;  // exponents taken out of the weights: of a row, where rows see different tokens
     using R = Raw<FMT, D>;
     const uint32_t lane = lane_id(), c = lane & 15, g = lane >> 4;
@@ -828,7 +836,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         };
         R x;
         // the first tiles from `base` on: as many as there is room for
-        constexpr uint32_t kAhead = ahead_of<FMT, D, RT>();
+        constexpr uint32_t kAhead = ahead_of<FMT, D, RT, MODE>();
         const auto load_first = [&](uint32_t base) {
             const uint32_t stop = FMT == kFmtPool || end - base <= kPageRun ? end : base + kPageRun;
 #pragma unroll
@@ -924,6 +932,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
         // out as soon as x has been widened, or read. PART: some of its tokens do not count.
         const auto tile = [&](auto part, uint32_t t0, uint32_t stop, uint32_t it, R& x) {
             constexpr bool PART = decltype(part)::value;
+            constexpr bool LAST = PART && !WIN;  // none lies behind it
             take_keys(it, (stop - t0 - 1) / kBlock, x);
             f32x4 s[RT][2];
             {
@@ -963,7 +972,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
             u32x4 vf[NC];
             float vs[8], ks[8];
             take_values(it, x);
-            if (RING && t0 + kAhead * kBlock < stop) load(t0 + kAhead * kBlock, it + kAhead, x);
+            if (RING && !LAST && t0 + kAhead * kBlock < stop) load(t0 + kAhead * kBlock, it + kAhead, x);
             if constexpr (FMT == kFmtPool) {
                 constexpr uint32_t l0 = level_bytes(0, 0), l1 = level_bytes(4, 0);
                 constexpr uint32_t h0 = level_bytes(0, 8), h1 = level_bytes(4, 8);
@@ -1077,7 +1086,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
                     }
                 }
             }
-            if (!RING && t0 + kBlock < stop) load(t0 + kBlock, it + 1, x);
+            if (!RING && !LAST && t0 + kBlock < stop) load(t0 + kBlock, it + 1, x);
 
             // many new tokens: which of the lane's 8 tokens a row sees
             uint32_t sight[MANY ? RT : 1];
@@ -1372,7 +1381,7 @@ __device__ __forceinline__ void attend_share(const Common& p, const Source& src,
 template <int FMT, int D, int RT, int MODE>
 __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_kernel(Common p, Source src) {
     fetch_arguments<sizeof(Common) + sizeof(Source)>();
-    __shared__ Shared<FMT, D, RT> sh;
+    __shared__ Shared<FMT, D, RT, MODE> sh;
     attend_share<FMT, D, RT, MODE>(p, src, blockIdx.x, sh);
 }
 
@@ -1382,8 +1391,8 @@ __global__ __launch_bounds__(kWaves* kWave, waves_per_simd(D, RT)) void attend_b
                                                                                            Source tail) {
     fetch_arguments<sizeof(Common) + 2 * sizeof(Source)>();
     __shared__ union {
-        Shared<kFmtPool, D, RT> a;
-        Shared<FMT, D, 1> b;
+        Shared<kFmtPool, D, RT, kOneSeesAll> a;
+        Shared<FMT, D, 1, kOneSeesAll> b;
     } sh;
     if (blockIdx.x < pool.W)
         attend_share<kFmtPool, D, RT, kOneSeesAll>(p, pool, blockIdx.x, sh.a);
