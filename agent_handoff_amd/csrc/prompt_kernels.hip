@@ -301,6 +301,20 @@ __device__ __forceinline__ Bounds bounds_of(const PromptParams& p, uint64_t all)
 }
 // A block's place in the list of all (those of the sequences before it, rounded up one by one, are no more).
 __device__ __forceinline__ uint32_t first_block(const PromptParams& p, uint32_t b, uint32_t first) { return first * p.group / kRows + b; }
+// The last sequence whose blocks' places begin at or before this one: of 64 that are evenly apart, then of those between
+// two. (n: none. Wrong starts give some sequence, or none.)
+__device__ __forceinline__ uint32_t sequence_of(const PromptParams& p, uint32_t place) {
+    uint32_t b = 0, range = p.n;
+    for (;;) {
+        const uint32_t each = (range + kWave - 1) / kWave, at = lane_id() * each;
+        const bool before = at < range && first_block(p, b + at, p.starts[b + at]) <= place;
+        const uint32_t k = __builtin_popcountll(__ballot(before));
+        if (k == 0) return p.n;
+        b += (k - 1) * each;
+        range = range - (k - 1) * each < each ? range - (k - 1) * each : each;
+        if (range <= 1) return b;
+    }
+}
 
 // SHARED: the tiles of all blocks are shared out.
 template <int FMT, int D, bool SHARED>
@@ -327,6 +341,16 @@ __global__ __launch_bounds__(kWaves* kWave, workgroups(D)) void prompt_kernel(Pr
         index = f.i;
         at = f.at - f.before;
         pairs = pairs_of(p, sq);
+    } else if (p.n > kWave) {
+        // by places: with all sequences counted by each workgroup, a call of 16384 sequences of one token (8 kv heads) takes 30
+        // ms, by places 2.4, and the former grows with their square. There are as many places as sequences at least, so each
+        // sequence is looked at for what is wrong with it.
+        if (h == 0 && share < p.n) (void)sequence_at<true>(p, share);
+        const uint32_t place = p.rows * p.group / kRows + p.n - 1 - share, b = sequence_of(p, place);
+        if (b >= p.n) return;
+        sq = uniform(sequence_at<false>(p, p.n - 1 - b), 0);
+        block = place - first_block(p, b, sq.first);
+        if (block >= sq.blocks) return;
     } else {
         const Found f = find_sequence(p, [](const Sequence& s) { return (uint64_t)s.blocks; }, [&](uint64_t) { return share; });
         if (!f.any) return;
@@ -982,17 +1006,8 @@ __global__ __launch_bounds__(kBlockThreads) void prompt_join_kernel(PromptParams
     constexpr uint32_t CB = D / 32;
     const uint32_t h = blockIdx.x % p.H, n = blockIdx.x / p.H % CB, place = blockIdx.x / p.H / CB;
     const u32x2 info = *(const __attribute__((address_space(4))) u32x2*)(uint64_t)(p.info + (uint64_t)place * p.H + h);
-    // the last sequence whose blocks' places begin at or before this one: of 64 that are evenly apart, then of those between two
-    uint32_t b = 0, range = p.n;
-    for (;;) {
-        const uint32_t each = (range + kWave - 1) / kWave, at = lane_id() * each;
-        const bool before = at < range && first_block(p, b + at, p.starts[b + at]) <= place;
-        const uint32_t k = __builtin_popcountll(__ballot(before));
-        if (k == 0) return;
-        b += (k - 1) * each;
-        range = range - (k - 1) * each < each ? range - (k - 1) * each : each;
-        if (range <= 1) break;
-    }
+    const uint32_t b = sequence_of(p, place);
+    if (b >= p.n) return;
     const Sequence sq = uniform(sequence_at<false>(p, p.n - 1 - b), 0);
     const uint32_t block = place - first_block(p, b, sq.first);
     if (block >= sq.blocks || info.y == 0) return;  // none, or written already
