@@ -32,11 +32,11 @@
 // the bytes of 8 bits, but as many instructions for as many tokens (a SIMD's VALU is busy half of the time).
 // A window: a sequence's tokens are counted without the gap between its sinks and its
 // window, cut out in whole runs of 16, so nothing between is read (int8, 32 sequences of up to 16384 tokens, window
-// 4096: 48 us, 5.0 TB/s; one of 5000 tokens, window 1024: 10 us of latency and 4 of joining, where the length has to
+// 4096: 49 us, 4.9 TB/s; one of 5000 tokens, window 1024: 10 us of latency and 4 of joining, where the length has to
 // be known before the table is read).
 // Few new tokens of each sequence: its rows are tokens times heads, each with a position of its
 // own, which masks single tiles at the ends; what bounds it is still memory (15 sequences of 5 drafts behind 8192
-// tokens, e4m3, 20 rows: 58 us, 4.5 TB/s).
+// tokens, e4m3, 20 rows: 60 us, 4.3 TB/s).
 //
 // Tried and left out: keeping two tiles of loads in registers (spills, or the same
 // time; in LDS, see through_lds); sharing widened tokens among the waves through LDS (a quarter fewer
@@ -393,8 +393,8 @@ constexpr int waves_per_simd(int d, int rt) { return d == 64 ? (rt == 1 ? 3 : 2)
 // and 310; e4m3 10.7 and 11.3, 18.1 and 18.5, 52.4 and 53.5, 155 and 164. Windows: bf16, 4 sequences of 1024 tokens 27.5
 // and 20.0, 32 of 4096 164 and 159; e4m3 22.0 and 20.1, 64 of 1000 56.6 and 54.1, 32 of 4096 89.8 and 92.0. 15 sequences of 5
 // drafts behind 8192 tokens: bf16 135 and 104, e4m3 73.0 and 66.0. Heads of 64, whose registers suffice, e4m3: 64 sequences of
-// 1000 tokens, 20 rows, 19.7 and 23.7; those drafts 39.2 and 42.9.) With one row tile int8 52 and 55, bf16 98 and 97;
-// 4 bits 61 and 69, with two 54 and 58.
+// 1000 tokens, 20 rows, 19.7 and 23.7; those drafts 39.2 and 42.9. 4 bits, those drafts with heads of 128: 54 and 58.) One row
+// tile needs no room: 32 windows of 4096 int8 52 and 55, bf16 98 and 97, 32 sequences of up to 16384 in 4 bits 61 and 69.
 constexpr bool through_lds(int fmt, int d, int rt, int mode) {
     const bool bits8 = fmt == kFmtInt8 || fmt == kFmtFp8;
     return rt == 2 && d == 128 && (fmt == kFmtBf16 || (bits8 && mode != kOneSeesAll));
@@ -1588,12 +1588,11 @@ AttendPlan make_plan(uint64_t units_of_rows, uint32_t rows, uint64_t max_tokens,
                      bool direct) {
     // Two row tiles of a wave share the widening of the tokens, but start and
     // join later: taken where every workgroup has a block to do. A call with two and
-    // with one, over the same inputs again and again (which the 256 MB cache then holds; a
-    // pool of 131071 tokens that it does not hold takes 78), us: pool of 15 agents, 60 rows, heads of 128:
-    // 131071 tokens 70 and 103, 4096 with tails 15.2 and 18.0, 1024 11.5 and 9.7. Pages, 8
-    // sequences of 8192, 2 kv heads: heads of 64, 17 rows int8 12.4 and 13.0, bf16 12.0 and
-    // 15.6; heads of 128, int8 32 rows 19.9 and 17.0, 48 rows 21.6 and 25.3, bf16 27.3
-    // and 37.3 (where 44 vector registers are spilled).
+    // with one, us: pool of 15 agents, 60 rows, heads of 128: 131071 tokens 81 and 110, 4096 with tails 15.1 and 18.2,
+    // 1024 12.3 and 10.0. Pages, 8 sequences of 8192, 2 kv heads: heads of 64, 17 rows int8 13.0 and 14.1, bf16 13.9 and
+    // 16.5; heads of 128, 32 rows int8 19.4 and 17.5, bf16 21.1 and 19.2, 33 rows 21.0 and 25.4, 21.4 and 36.6. Not taken
+    // yet: two tiles for 17 to 32 rows of heads of 128 in larger calls (15 sequences of 4096, 8 kv heads, 17 rows: int8 38.0
+    // and 48.5, bf16 56.0 and 80.8; 32 rows: 40.7 and 49.8, 58.0 and 81.8).
     const uint64_t most_blocks = (max_tokens + kBlock - 1) / kBlock;
     const bool enough = units_of_rows * ((rows + 31) / 32) * most_blocks >= 256ull * waves_per_simd(d, 2);
     return plan_of(units_of_rows, rows, max_tokens, d, rows > one_tile && enough ? 2 : 1, direct);
@@ -1658,7 +1657,10 @@ AttendPlan pool_attend_plan(uint32_t H, uint32_t n_agents, uint32_t Hq, uint32_t
     return make_plan(H, n_agents * (Hq / H), T, d, 16, !tail);
 }
 
-// Many new tokens: up to 32 rows of a sequence and kv head (its new tokens times the heads that share it) a unit.
+// Many new tokens: up to 32 rows of a sequence and kv head (its new tokens times the heads that share it) a unit. Two row
+// tiles from 17 rows in the mean on: 15 sequences with drafts behind 8192 tokens, 8 kv heads, with two and with one, us:
+// heads of 128, 20 rows e4m3 66.6 and 85.9, bf16 104 and 151, 16 rows 65.2 and 60.3, 103 and 101; heads of 64, 20 rows
+// 39.4 and 50.1, 57.2 and 79.8, 16 rows 38.4 and 35.2, 56.0 and 54.0.
 AttendPlan many_attend_plan(uint32_t n_seqs, uint32_t n_tokens, uint32_t H, uint32_t Hq, uint32_t d, uint64_t max_tokens,
                             uint32_t window, uint32_t sinks) {
     AttendPlan a{};

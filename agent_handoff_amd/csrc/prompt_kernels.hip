@@ -19,10 +19,12 @@
 // weights and the values of the one before, which are independent, two products beside two weights. Keys and
 // values lie in a ring of four tiles in LDS, filled by loads that nothing waits for but the end of
 // two tiles (bf16), or widened on their way (8 bits: binary16, where codes are exact; 4 bits: bf16, the same). One prompt of 8192
-// tokens (8 kv heads of 128, 4 heads each): bf16 546 us, 1007 TFLOP/s of what the mask leaves, of a SIMD's cycles
-// the matrix core 53 %, the VALU 52 %, at 1.9 GHz: the clock falls as power allows (a build with 12 %
-// more cycles took 1 % longer). e4m3 686, int8 713, 4 bits 559 us: steps of 8 bits cost a product each for logits and
-// weights, and codes their widening. Heads of 64, with as many exponentials for half the products: 318 us.
+// tokens (8 kv heads of 128, 4 heads each): bf16 541 to 573 us from card to card and by what runs beside it, 960 to 1016
+// TFLOP/s of what the mask leaves, of a SIMD's cycles the matrix core 53 %, the VALU 52 %, at 1.9 GHz: the clock falls as
+// power allows (a build with 12 % more cycles took 1 % longer). Back to back on a card where bf16 takes 572: e4m3 722, int8
+// 745, 4 bits 590 us: steps of 8 bits cost a product each for logits and weights, and codes their widening. Heads of 64, with
+// as many exponentials for half the products: 333 us. Vector registers spilled: where tiles are shared out 23 (e4m3) and 24
+// (int8), with heads of 64 38, 50, 23 (4 bits) and 9 (bf16); where not, with heads of 64, 18, 20, 2 and 0.
 // Measured and left out: tiles of 64 tokens (7 to 20 % longer), 256 rows a
 // workgroup, operands asked for four products ahead.
 //
@@ -1074,10 +1076,12 @@ hipError_t launch_of(uint32_t format, const PromptParams& p, uint32_t grid, hipS
 // 309; where contexts differ, 712 (chunks of four prompts, int8) 215 and 244.
 constexpr uint64_t places_of(uint32_t d) { return kCus * workgroups(d); }
 // Few new tokens of each sequence (their rows, times the heads that share a kv head, in the mean of all): a call is then
-// memory's, and the kernel for one new token takes them, 32 rows at a time. 15 sequences behind 8192 tokens (8 kv heads of
-// 128), that kernel and the one here, us: 32 rows e4m3 66 and 138, 64 rows 99 and 152, bf16 148 and 148; one sequence of 32
-// rows behind 4000 tokens 17 and 41, behind 400 14 and 22, and, with a second launch that joins what it shared out,
-// behind 100 13 and 12 (15 sequences 20 and 13). (Rows that belong to no sequence count as well: a quarter more.)
+// memory's, and the kernel for one new token takes them, 32 rows at a time. That kernel and the one here, us, 8 kv heads of
+// 128: 15 sequences behind 8192 tokens, 32 rows e4m3 56 and 112, bf16 106 and 112, 64 rows 98 and 116, 160 and 115, 80 rows 134
+// and 120, 239 and 118; 4 such sequences, 64 rows 29 and 63, 34 and 52, 80 rows 46 and 65, 73 and 53; one of 32 rows behind
+// 4000 tokens e4m3 15 and 32, behind 400 12 and 20, and, with a second launch that joins what it shared out, behind 100 13 and
+// 11. (Rows that belong to no sequence count as well: a quarter more.) So 80 is too many for bf16 where there are more
+// than a few sequences (60 behind 2000, 64 rows: 207 and 98); a rule that knows the format and the sequences is not here yet.
 constexpr uint64_t kFewRows = 80;
 constexpr uint64_t kFewTokens = 256;
 

@@ -252,7 +252,8 @@ size_t kvpage_attend_prompt_workspace_bytes(const kvc_pages* spec, uint32_t n_se
  * The same call gives the same bits. Weights are rounded once, to bf16 (2^-8; bf16 and
  * KVC_PAGE_FP4 pages) or, times the step, to binary16 (2^-11; 8-bit formats): a row sums
  * over many tokens, and the rounding errors do not add up as the weights do. (Calls with
- * few new tokens of each sequence run as kvpage_attend does, with its roundings.) The
+ * few new tokens of each sequence in the mean run as kvpage_attend does, with its
+ * roundings: a sequence's bits may differ with the others of its call.) The
  * softmax's sums are those of the weights before that. Products and sums are
  * binary32. Logits in powers of two (scale * q . k * log2 e) have to stay below 2^24 in
  * size, 8-bit key steps that are not 0 between 2^-90 and 2^90. A NaN in a key or value,
