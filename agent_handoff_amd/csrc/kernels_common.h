@@ -52,22 +52,29 @@ __device__ __forceinline__ float signed_by_mask(uint64_t mask, float m) {
     return r;
 }
 
-// acc * 2 + (bit `lane` of mask): appends one code bit per lane (the mask is
-// a wave-wide compare result) in a single add-with-carry.
-__device__ __forceinline__ uint32_t shift_in_bit(uint32_t acc, uint64_t mask) {
-    uint32_t r;
+// The compiler looks for no hazards inside of these texts. gfx950 needs two wait states between a vector instruction's
+// write of a scalar register and a vector instruction's read of it, carry and mask included; so the masks of three
+// words go in, and come out, together, where two of the instructions are the third's wait.
+
+// acc * 2 + (bit `lane` of mask) of three words: appends one code bit each per lane (the masks are
+// wave-wide compare results) in a single add-with-carry.
+__device__ __forceinline__ void shift_in_bits(uint32_t (&acc)[3], uint64_t m0, uint64_t m1, uint64_t m2) {
     uint64_t carry_out;
-    asm("v_addc_co_u32_e64 %0, %1, %2, %2, %3" : "=v"(r), "=s"(carry_out) : "v"(acc), "s"(mask));
-    return r;
+    asm("s_nop 1\n\t"
+        "v_addc_co_u32_e64 %2, %3, %2, %2, %6\n\t"
+        "v_addc_co_u32_e64 %1, %3, %1, %1, %5\n\t"
+        "v_addc_co_u32_e64 %0, %3, %0, %0, %4"
+        : "+&v"(acc[0]), "+&v"(acc[1]), "+&v"(acc[2]), "=&s"(carry_out)
+        : "s"(m0), "s"(m1), "s"(m2));
 }
 
-// w * 2, returning the lanes' former top bits as a wave mask (carry out).
-__device__ __forceinline__ uint64_t shift_out_bit(uint32_t& w) {
-    uint32_t r;
-    uint64_t mask;
-    asm("v_add_co_u32_e64 %0, %1, %2, %2" : "=v"(r), "=s"(mask) : "v"(w));
-    w = r;
-    return mask;
+// w * 2 of three words, returning the lanes' former top bits as wave masks (carry out). The last may be read by a
+// vector instruction right behind, the others by scalar ones.
+__device__ __forceinline__ void shift_out_bits(uint32_t (&w)[3], uint64_t& m0, uint64_t& m1, uint64_t& m2) {
+    asm("v_add_co_u32_e64 %2, %5, %2, %2\n\t"
+        "v_add_co_u32_e64 %0, %3, %0, %0\n\t"
+        "v_add_co_u32_e64 %1, %4, %1, %1"
+        : "+&v"(w[0]), "+&v"(w[1]), "+&v"(w[2]), "=&s"(m0), "=&s"(m1), "=&s"(m2));
 }
 
 // Cross-lane butterfly step on 8 registers in one instruction each:

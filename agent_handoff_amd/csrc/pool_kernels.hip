@@ -208,9 +208,7 @@ __device__ __forceinline__ void code_slot(const float (&y)[C], float r, uint32_t
     const bool b1 = z >= t1;
     const float a0 = (b1 == b2) ? kTh7 : kTh5;
     const float t0 = b2 ? a0 : -a0;
-    pl[0] = shift_in_bit(pl[0], __builtin_amdgcn_ballot_w64(z >= t0));
-    pl[1] = shift_in_bit(pl[1], __builtin_amdgcn_ballot_w64(b1));
-    pl[2] = shift_in_bit(pl[2], __builtin_amdgcn_ballot_w64(b2));
+    shift_in_bits(pl, __builtin_amdgcn_ballot_w64(z >= t0), __builtin_amdgcn_ballot_w64(b1), __builtin_amdgcn_ballot_w64(b2));
 }
 
 template <int C, int... Is>
@@ -919,9 +917,8 @@ __global__ __launch_bounds__(kBlockThreads) void pool_decode_kernel(DecodeParams
     float y[C];
 #pragma unroll
     for (int i = C - 1; i >= 0; --i) {
-        const uint64_t w0 = shift_out_bit(pw[0]);
-        const uint64_t w1 = shift_out_bit(pw[1]);
-        const uint64_t w2 = shift_out_bit(pw[2]);
+        uint64_t w0, w1, w2;
+        shift_out_bits(pw, w0, w1, w2);
         // level index within the half: (b1, b0) for b2 = 1, complemented for b2 = 0
         const uint64_t m1 = ~(w1 ^ w2), m0 = ~(w0 ^ w2);
         const float lo = select_by_mask(m0, c0, c1);
